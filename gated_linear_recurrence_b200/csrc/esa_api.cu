@@ -14,6 +14,7 @@
 
 #include "esa.h"
 #include "esa_fused_launch.h"
+#include "esa_host.h"
 #include "esa_launch.h"
 
 namespace {
@@ -283,6 +284,28 @@ int fused_impl(const void *x, const void *W, const void *W_O, void *z, void *y, 
 }
 
 }  // namespace
+
+namespace esa {
+
+int check_current_device() { return check_device(); }
+
+int sm_count() {
+  static std::atomic<int> cache[64];   // 0 unknown
+  int dev = -1, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
+    cudaGetLastError();
+    return 148;
+  }
+  if (dev < 64 && (sms = cache[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+    cudaGetLastError();
+    return 148;
+  }
+  if (dev < 64) cache[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+
+}  // namespace esa
 
 extern "C" {
 

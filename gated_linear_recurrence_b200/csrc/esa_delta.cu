@@ -1,0 +1,187 @@
+// esa_delta.cu -- C ABI of the gated delta rule (declared in include/esa.h):
+// argument checks, the workspace, and the order of the kernels.
+#include "esa_delta.h"
+
+#include <climits>
+
+#include "esa.h"
+#include "esa_host.h"
+
+using namespace esa;
+
+namespace {
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// What the forward keeps for the backward (u), then the backward's scratch.
+struct DeltaLayout {
+  size_t u = 0, du = 0, dk = 0, dq = 0, gain = 0, end = 0, total = 0;
+};
+
+DeltaLayout delta_layout(const DeltaShape &s, bool keep) {
+  DeltaLayout lo;
+  const size_t n = static_cast<size_t>(s.B) * s.T * s.H;
+  size_t o = 0;
+  if (keep) {
+    const size_t rows = up256(n * s.D * sizeof(float));
+    lo.u = o; o += rows;
+    lo.du = o; o += rows;
+    lo.dk = o; o += rows;
+    lo.dq = o; o += rows;
+    lo.gain = o; o += up256(n * sizeof(float));
+    lo.end = o; o += up256(static_cast<size_t>(s.B) * s.H * (s.D / 16) * sizeof(float));
+  }
+  lo.total = o;
+  return lo;
+}
+
+int elem(int dtype) { return dtype == ESA_F32 ? 4 : 2; }
+
+int check_shape(int B, int T, int H, int D, int dtype) {
+  if (B < 0 || T < 0 || H < 1 || D < 1) return ESA_ERR_ARG;
+  if (dtype < ESA_F32 || dtype > ESA_E4M3) return ESA_ERR_ARG;
+  if (dtype == ESA_E4M3 || (D != 32 && D != 64 && D != 128)) return ESA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(H) * D > INT_MAX / 2) return ESA_ERR_ARG;
+  if (static_cast<long long>(B) * H > INT_MAX / 8) return ESA_ERR_ARG;         // blocks of a launch
+  if (static_cast<long long>(B) * T > (1ll << 33) / H) return ESA_ERR_ARG;     // eight rows a block
+  return ESA_OK;
+}
+
+int check_rows(long long ld, long long least, int dtype) {
+  if (ld < least || ld > INT_MAX) return ESA_ERR_ARG;
+  return (ld * elem(dtype)) % 16 ? ESA_ERR_ALIGN : ESA_OK;
+}
+
+int check_scale(float s) { return s == s && s < 3.0e38f && s > -3.0e38f ? ESA_OK : ESA_ERR_ARG; }
+
+// Shape, strides and the five inputs of a sequence call.
+int check_inputs(const DeltaShape &s, int dtype, const void *q, const void *k, const void *v, const void *a,
+                 const void *b) {
+  int rc = check_shape(s.B, s.T, s.H, s.D, dtype);
+  if (rc) return rc;
+  if ((rc = check_scale(s.scale))) return rc;
+  const long long C = static_cast<long long>(s.H) * s.D;
+  if ((rc = check_rows(s.ld_qk, C, dtype)) || (rc = check_rows(s.ld_v, C, dtype))) return rc;
+  if (s.ld_g < s.H || s.ld_g > INT_MAX) return ESA_ERR_ARG;
+  if (s.B > 0 && s.T > 0 && (!q || !k || !v || !a || !b)) return ESA_ERR_ARG;
+  for (const void *p : {q, k, v})
+    if (p && !aligned_to(p, 16)) return ESA_ERR_ALIGN;
+  for (const void *p : {a, b})
+    if (p && !aligned_to(p, elem(dtype))) return ESA_ERR_ALIGN;
+  return ESA_OK;
+}
+
+size_t state_bytes(const DeltaShape &s) { return static_cast<size_t>(s.B) * s.H * s.D * s.D * sizeof(float); }
+
+// The state (or its gradient) of no tokens.
+int copy_state(float *out, const float *in, const DeltaShape &s, cudaStream_t st) {
+  if (!out || out == in) return ESA_OK;
+  return in ? runtime_status(cudaMemcpyAsync(out, in, state_bytes(s), cudaMemcpyDeviceToDevice, st))
+            : runtime_status(cudaMemsetAsync(out, 0, state_bytes(s), st));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t esa_delta_workspace_size(int B, int T, int H, int D, int dtype, int keep) {
+  if (check_shape(B, T, H, D, dtype) != ESA_OK || (keep != 0 && keep != 1)) return 0;
+  return delta_layout(DeltaShape{B, T, H, D, 0, 0, 0, 1.0f}, keep != 0).total + 256;
+}
+
+int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, long long ld_v, const void *a,
+                  const void *b, long long ld_g, void *y, float *S_final, int B, int T, int H, int D, float scale,
+                  const float *S_init, int dtype, int keep, void *workspace, size_t workspace_bytes, void *stream) {
+  const DeltaShape s{B, T, H, D, ld_qk, ld_v, ld_g, scale};
+  int rc = check_inputs(s, dtype, q, k, v, a, b);
+  if (rc) return rc;
+  if (keep != 0 && keep != 1) return ESA_ERR_ARG;
+  if (B > 0 && T > 0 && !y) return ESA_ERR_ARG;
+  for (const void *p : {static_cast<const void *>(y), static_cast<const void *>(S_final),
+                        static_cast<const void *>(S_init), static_cast<const void *>(workspace)})
+    if (p && !aligned_to(p, 16)) return ESA_ERR_ALIGN;
+  if (!workspace || workspace_bytes < esa_delta_workspace_size(B, T, H, D, dtype, keep)) return ESA_ERR_WORKSPACE;
+  if ((rc = check_current_device())) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (B == 0) return ESA_OK;
+  if (T == 0) return copy_state(S_final, S_init, s, st);
+  const DeltaLayout lo = delta_layout(s, keep != 0);
+  SweepArgs p{};
+  p.s = s;
+  p.q = q; p.k = k; p.v = v; p.a = a; p.b = b;
+  p.S_in = S_init;
+  p.S_out = S_final;
+  p.y = y;
+  p.u = keep ? reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + lo.u) : nullptr;
+  return launch_sweep(kSweepFwd, dtype, p, st);
+}
+
+int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, long long ld_v, const void *a,
+                  const void *b, long long ld_g, const void *dy, const float *dS_final, void *dq, void *dk, void *dv,
+                  void *da, void *db, float *dS_init, int B, int T, int H, int D, float scale, const float *S_init,
+                  int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+  const DeltaShape s{B, T, H, D, ld_qk, ld_v, ld_g, scale};
+  int rc = check_inputs(s, dtype, q, k, v, a, b);
+  if (rc) return rc;
+  if (B > 0 && T > 0 && (!dy || !dq || !dk || !dv || !da || !db)) return ESA_ERR_ARG;
+  for (const void *p : {dy, static_cast<const void *>(dS_final), static_cast<const void *>(dq),
+                        static_cast<const void *>(dk), static_cast<const void *>(dv),
+                        static_cast<const void *>(dS_init), static_cast<const void *>(S_init),
+                        static_cast<const void *>(workspace)})
+    if (p && !aligned_to(p, 16)) return ESA_ERR_ALIGN;
+  for (const void *p : {static_cast<const void *>(da), static_cast<const void *>(db)})
+    if (p && !aligned_to(p, elem(dtype))) return ESA_ERR_ALIGN;
+  if (!workspace || workspace_bytes < esa_delta_workspace_size(B, T, H, D, dtype, 1)) return ESA_ERR_WORKSPACE;
+  if ((rc = check_current_device())) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (B == 0) return ESA_OK;
+  if (T == 0) return copy_state(dS_init, dS_final, s, st);
+  const DeltaLayout lo = delta_layout(s, true);
+  unsigned char *base = static_cast<unsigned char *>(workspace);
+  SweepArgs p{};
+  p.s = s;
+  p.q = q; p.k = k; p.v = v; p.dy = dy; p.a = a; p.b = b;
+  p.u = reinterpret_cast<float *>(base + lo.u);
+  p.du = reinterpret_cast<float *>(base + lo.du);
+  p.dk = reinterpret_cast<float *>(base + lo.dk);
+  p.dq = reinterpret_cast<float *>(base + lo.dq);
+  p.end = reinterpret_cast<float *>(base + lo.end);
+  p.S_in = dS_final;
+  p.S_out = dS_init;
+  if ((rc = launch_sweep(kSweepDu, dtype, p, st))) return rc;
+  p.S_out = nullptr;
+  if ((rc = launch_sweep(kSweepDk, dtype, p, st))) return rc;
+  p.S_in = S_init;
+  p.dS_final = dS_final;
+  if ((rc = launch_sweep(kSweepDq, dtype, p, st))) return rc;
+  FinishArgs f{};
+  f.s = s;
+  f.q = q; f.v = v; f.a = a; f.b = b;
+  f.u = p.u; f.du = p.du; f.dkf = p.dk; f.dqf = p.dq; f.end = p.end;
+  f.gain = reinterpret_cast<float *>(base + lo.gain);
+  f.dq = dq; f.dk = dk; f.dv = dv; f.da = da; f.db = db;
+  return launch_delta_finish(dtype, f, st);
+}
+
+int esa_delta_step(const void *q_t, const void *k_t, const void *v_t, const void *a_t, const void *b_t, float *S,
+                   void *y_t, int B, int H, int D, float scale, int dtype, void *stream) {
+  int rc = check_shape(B, 1, H, D, dtype);
+  if (rc) return rc;
+  const long long C = static_cast<long long>(H) * D;
+  const DeltaShape s{B, 1, H, D, C, C, H, scale};
+  if ((rc = check_inputs(s, dtype, q_t, k_t, v_t, a_t, b_t))) return rc;
+  if (B > 0 && (!S || !y_t)) return ESA_ERR_ARG;
+  for (const void *p : {static_cast<const void *>(S), static_cast<const void *>(y_t)})
+    if (p && !aligned_to(p, 16)) return ESA_ERR_ALIGN;
+  if ((rc = check_current_device())) return rc;
+  if (B == 0) return ESA_OK;
+  SweepArgs p{};
+  p.s = s;
+  p.q = q_t; p.k = k_t; p.v = v_t; p.a = a_t; p.b = b_t;
+  p.S_in = S;
+  p.S_out = S;
+  p.y = y_t;
+  return launch_sweep(kSweepFwd, dtype, p, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

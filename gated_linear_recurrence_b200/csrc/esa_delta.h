@@ -1,0 +1,44 @@
+// esa_delta.h -- host-side interface between the gated delta rule's C ABI and
+// its kernels.  Internal to the library.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+
+namespace esa {
+
+// Shape and element strides of a call: row (b, t) of q and k starts at
+// (b T + t) ld_qk, of v at (b T + t) ld_v, of a and b at (b T + t) ld_g.
+struct DeltaShape {
+  int B, T, H, D;
+  long long ld_qk, ld_v, ld_g;
+  float scale;
+};
+
+// One token-by-token sweep (see esa_delta_sweep.cuh for the four kinds).
+struct SweepArgs {
+  DeltaShape s;
+  const void *q, *k, *v, *dy, *a, *b;   // I/O type
+  const float *S_in;                    // state (or its gradient) before the first token visited; NULL = zeros
+  float *S_out;                         // after the last one; NULL = not written
+  const float *dS_final;                // forward row sweep: joined with the final state
+  void *y;                              // forward sweep's output, I/O type
+  float *u, *du, *dk, *dq, *end;        // float32 scratch, [B,T,H,D] and [B,H,D/16]
+};
+
+// Kinds of sweep.
+enum { kSweepFwd = 0, kSweepDu = 1, kSweepDk = 2, kSweepDq = 3 };
+
+int launch_sweep(int kind, int dtype, const SweepArgs &a, cudaStream_t st);
+
+struct FinishArgs {
+  DeltaShape s;
+  const void *q, *v, *a, *b;
+  const float *u, *du, *dkf, *dqf, *end;
+  float *gain;   // [B,H,T]
+  void *dq, *dk, *dv, *da, *db;
+};
+int launch_delta_finish(int dtype, const FinishArgs &a, cudaStream_t st);
+
+}  // namespace esa

@@ -104,6 +104,21 @@ def load_library():
         lib.esa_fused_layer_fwd.restype = I
         lib.esa_step.argtypes = [P, P, P, P, P, I, I, I, I, I, P]
         lib.esa_step.restype = I
+        F = ctypes.c_float
+        lib.esa_delta_workspace_size.argtypes = [I, I, I, I, I, I]
+        lib.esa_delta_workspace_size.restype = S
+        lib.esa_delta_fwd.argtypes = [P, P, L, P, L, P, P, L, P, P, I, I, I, I, F, P, I, I, P, S, P]
+        lib.esa_delta_fwd.restype = I
+        lib.esa_delta_bwd.argtypes = [P, P, L, P, L, P, P, L, P, P, P, P, P, P, P, P, I, I, I, I, F, P, I, P, S, P]
+        lib.esa_delta_bwd.restype = I
+        lib.esa_delta_step.argtypes = [P, P, P, P, P, P, P, I, I, I, F, I, P]
+        lib.esa_delta_step.restype = I
+        lib.esa_norm_workspace_size.argtypes = [L, I, I, I]
+        lib.esa_norm_workspace_size.restype = S
+        lib.esa_norm_fwd.argtypes = [P, L, P, L, P, P, P, P, P, L, I, F, I, I, P]
+        lib.esa_norm_fwd.restype = I
+        lib.esa_norm_bwd.argtypes = [P, L, P, L, P, P, P, L, P, P, P, L, I, I, I, P, S, P]
+        lib.esa_norm_bwd.restype = I
         lib.esa_check.argtypes = [P, P]
         lib.esa_check.restype = I
         lib.esa_workspace_init.argtypes = [P, S, P]

@@ -342,6 +342,101 @@ int esa_step(const void *a_t, const void *v_t, const void *q_t, float *E, void *
              int B, int H, int D, int mode, int dtype, void *stream);
 
 /*
+ * ---- The gated delta rule -------------------------------------------------
+ * The recurrence with a matrix state per head.  With alpha_t = sigmoid(a_t)
+ * (the gate of the diagonal recurrence above, one per head) and
+ * beta_t = sigmoid(b_t) (the write strength), S [D key][D value]:
+ *     u_t = beta_t (v_t - alpha_t S_{t-1}^T k_t),
+ *     S_t = alpha_t S_{t-1} + k_t u_t^T,
+ *     y_t = scale S_t^T q_t.
+ * Keys are used as given: with |k_t| <= 1 the recurrence never grows (the
+ * caller normalises them); logits below -80 count as -80.  No counterpart on
+ * the pages.
+ *   q, k      rows of H*D elements, ld_qk elements apart: (b, t) at b T + t.
+ *   v         the same with ld_v.  ld >= H*D, and ld times the element size a
+ *             multiple of 16 bytes (else ESA_ERR_ARG / ESA_ERR_ALIGN), so that
+ *             column blocks of a projection output can be read in place.
+ *   a, b      logits, rows of H elements, ld_g >= H apart; aligned to their
+ *             element only.
+ *   y, dy, dq, dk, dv [B,T,H,D] and da, db [B,T,H] contiguous, I/O dtype.
+ *   S_init, S_final, dS_final, dS_init  [B,H,D,D] contiguous float32, each
+ *             NULL when absent (zeros) or not wanted.
+ * dtype ESA_F32, ESA_F16 or ESA_BF16, D of 32, 64 or 128 (else
+ * ESA_ERR_UNSUPPORTED).  The state and all sums are float32.
+ */
+
+/* Bytes of workspace for esa_delta_fwd (keep = 0: the forward alone; 1: also
+ * what esa_delta_bwd reads and its scratch).  0 on a bad argument.  The
+ * workspace needs no initialisation and can be reused by any later call; two
+ * calls that may overlap need two. */
+size_t esa_delta_workspace_size(int B, int T, int H, int D, int dtype, int keep);
+
+/* Forward over a whole sequence.  keep = 1 leaves what the backward needs in
+ * the workspace: run nothing else on it before the matching esa_delta_bwd. */
+int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, long long ld_v, const void *a,
+                  const void *b, long long ld_g, void *y, float *S_final, int B, int T, int H, int D, float scale,
+                  const float *S_init, int dtype, int keep, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Backward: gradients of sum(dy . y) + sum(dS_final . S_final) with respect to
+ * q, k, v, a, b and S_init.  The inputs and the workspace are those of the
+ * matching esa_delta_fwd with keep = 1, unchanged since.  With dS the gradient
+ * of S_t from later tokens, dS += scale q_t dy_t^T, then
+ *     du = dS^T k,  dv = beta du,  dk = dS u - alpha beta S_{t-1} du,
+ *     dq = scale S_t dy,  db = (du.u)(1 - beta),
+ *     da = (<dS, S_t> - beta v.du)(1 - alpha),  dS <- alpha (dS - beta k du^T).
+ */
+int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, long long ld_v, const void *a,
+                  const void *b, long long ld_g, const void *dy, const float *dS_final, void *dq, void *dk, void *dv,
+                  void *da, void *db, float *dS_init, int B, int T, int H, int D, float scale, const float *S_init,
+                  int dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token: q_t, k_t, v_t, y_t [B,H,D] and a_t, b_t [B,H] contiguous; S
+ * [B,H,D,D] float32 is read and overwritten.  Needs no workspace. */
+int esa_delta_step(const void *q_t, const void *k_t, const void *v_t, const void *a_t, const void *b_t, float *S,
+                   void *y_t, int B, int H, int D, float scale, int dtype, void *stream);
+
+/*
+ * ---- Layer norm -------------------------------------------------------------
+ * The norm in front of a mixer ("Entangled State Attention v2.0", the model
+ * example: norm, mixer, residual), over the last axis of `rows` rows of N:
+ *     h = x + residual (rounded to the I/O dtype),
+ *     y = (h - mean) rstd w + c,  rstd = 1 / sqrt(mean((h - mean)^2) + eps).
+ *   x, residual  rows ld_x / ld_res elements apart (>= N); residual NULL: h = x.
+ *   weight, bias [N] in wdtype (dtype itself or ESA_F32), NULL: ones / zeros.
+ *   y, h      [rows, N] contiguous outputs; h is written when residual is
+ *             given (it may be x or residual itself), ignored otherwise.
+ *   stats     [rows, 2] float32 output (mean, rstd) for esa_norm_bwd, or NULL.
+ * N <= 16384, rows < 2^31 (else ESA_ERR_UNSUPPORTED / ESA_ERR_ARG); dtype
+ * ESA_F32, ESA_F16, ESA_BF16.  Pointers are aligned to their element at least;
+ * rows that all start on 16 bytes are read in 16-byte units.
+ */
+int esa_norm_fwd(const void *x, long long ld_x, const void *residual, long long ld_res, const void *weight,
+                 const void *bias, void *y, void *h, float *stats, long long rows, int N, float eps, int dtype,
+                 int wdtype, void *stream);
+
+/* Bytes of workspace for esa_norm_bwd's weight and bias sums (0 on a bad
+ * argument); needs no initialisation. */
+size_t esa_norm_workspace_size(long long rows, int N, int dtype, int wdtype);
+
+/*
+ * Backward: with n = (h - mean) rstd and g = dy w,
+ *     dx = rstd (g - mean(g) - n mean(g n)) + dh,
+ *     dweight = sum over rows of dy n,  dbias = sum over rows of dy.
+ *   h, stats  the forward's (h is x when it had no residual); rows ld_h apart.
+ *   dh        gradient that reaches h through the residual stream, or NULL.
+ *   dx        [rows, N] contiguous: the gradient of x and of residual alike;
+ *             may be dh or dy when that has contiguous rows.
+ *   dweight, dbias [N] in wdtype, NULL when not wanted; with both NULL the
+ *             workspace is not used.  Their sums have one order, so they do
+ *             not change from run to run.
+ */
+int esa_norm_bwd(const void *dy, long long ld_dy, const void *h, long long ld_h, const void *weight,
+                 const float *stats, const void *dh, long long ld_dh, void *dx, void *dweight, void *dbias,
+                 long long rows, int N, int dtype, int wdtype, void *workspace, size_t workspace_bytes,
+                 void *stream);
+
+/*
  * Synchronise `stream`, then read and clear the device status word in
  * `workspace`.  Returns ESA_OK; ESA_ERR_WORKSPACE if the workspace is not
  * initialised (a scan on it did nothing); ESA_ERR_TIMEOUT if a bounded wait

@@ -1,0 +1,330 @@
+"""The gated delta rule on the GPU against the float64 definition."""
+import pytest
+import torch
+
+from gated_linear_recurrence_b200 import (EsaError, PreparedDeltaStep, esa_delta_bwd, esa_delta_fwd, esa_delta_step,
+                                          esa_delta_workspace_size)
+from tests._delta_reference import HALF, PER_TOKEN, assert_within, delta_reference
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+NAMES = ("q", "k", "v", "a", "b")
+
+
+def draw(dt, B, T, H, D, seed=0, a_mean=3.0, state=True):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)   # noqa: E731
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True).clamp(min=1e-30)   # noqa: E731
+    x = {"q": unit(r(B, T, H, D)), "k": unit(r(B, T, H, D)) * 0.99, "v": r(B, T, H, D), "a": r(B, T, H) + a_mean,
+         "b": r(B, T, H), "dy": r(B, T, H, D)}
+    x = {n: t.to(DT[dt]).cuda() for n, t in x.items()}
+    S0 = 0.3 * r(B, H, D, D).cuda() if state else None
+    dS = 0.1 * r(B, H, D, D).cuda() if state else None
+    return x, S0, dS
+
+
+def ins(x):
+    return [x[n] for n in NAMES]
+
+
+def check(x, out, ref, T, D, gradients=True, half_p=0.0):
+    """`half_p`: further roundings of intermediates, in the 2-norm and per element of the largest value."""
+    a, n = PER_TOKEN * max(T, 1), PER_TOKEN * max(T, 1) ** 0.5
+    for name in ("y", "S"):
+        if out.get(name) is not None:
+            extra = half_p if out[name].dtype != torch.float32 else 0.0
+            assert_within(name, out[name], ref[name], a + extra, n + extra)
+    if gradients:
+        for name in ("dq", "dk", "dv", "db", "dS0"):
+            if out.get(name) is not None:
+                extra = half_p if out[name].dtype != torch.float32 else 0.0
+                assert_within(name, out[name], ref[name], 2 * a + extra, 2 * n + extra)
+        # da is (1 - alpha) times a sum of q.dq - v.dv over the later tokens, which cancel where alpha is small: its
+        # error goes by the terms' sizes, each off by what dq and dv are off by before their rounding
+        terms = (x["q"].cpu().double() * ref["dq"]).sum(-1).abs() + (x["v"].cpu().double() * ref["dv"]).sum(-1).abs()
+        top = float(terms.max()) + float(ref["da"].abs().max())
+        extra = half_p if out["da"].dtype != torch.float32 else 0.0
+        off = (out["da"].cpu().double() - ref["da"]).abs()
+        half = HALF[out["da"].dtype]
+        assert torch.isfinite(off).all() and bool((off <= half * ref["da"].abs() + (2 * a + extra) * top + 1e-30).all()), \
+            f"da: off by {float(off.max()):.3e} of {top:.3e}"
+
+
+def run(x, S0, dS, scale, **kw):
+    y, S, ws = esa_delta_fwd(*ins(x), scale=scale, S_init=S0, **kw)
+    dq, dk, dv, da, db, dS0 = esa_delta_bwd(*ins(x), x["dy"], ws, scale=scale, S_init=S0, dS_final=dS,
+                                            want_dS_init=S0 is not None)
+    return dict(y=y, S=S, dq=dq, dk=dk, dv=dv, da=da, db=db, dS0=dS0)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("B,T,H", [(1, 1, 1), (2, 2, 3), (1, 15, 2), (2, 16, 1), (1, 17, 2), (2, 63, 2), (1, 64, 1),
+                                   (1, 65, 2), (2, 131, 3)])
+def test_forward_and_backward(cuda_device, dt, D, B, T, H):
+    x, S0, dS = draw(dt, B, T, H, D, seed=T)
+    out = run(x, S0, dS, D ** -0.5)
+    # 16-bit outputs of the chunked kernels: three 16-bit roundings of intermediates, of half a float16 step each
+    check(x, out, delta_reference(*ins(x), D ** -0.5, S0, x["dy"], dS), T, D, half_p=3 * 2.0 ** -11)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_without_states(cuda_device, dt):
+    x, _, _ = draw(dt, 2, 70, 2, 64, seed=5, state=False)
+    out = run(x, None, None, 1.0)
+    check(x, out, delta_reference(*ins(x), 1.0, None, x["dy"], None), 70, 64, half_p=3 * 2.0 ** -11)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("T", [1, 90])
+def test_inference_call_and_many_heads(cuda_device, D, T):
+    """Enough heads for whole-head blocks; keep=False; no final state wanted."""
+    x, S0, _ = draw("f16", 4, T, 80, D, seed=9)
+    y, S, ws = esa_delta_fwd(*ins(x), S_init=S0, keep=False, want_S_final=False)
+    assert S is None
+    full = run(x, S0, None, None)
+    assert torch.equal(y, full["y"])
+    pick = slice(1, 2)
+    ref = delta_reference(*(t[pick, :, :4] for t in ins(x)), D ** -0.5, S0[pick, :4])
+    check(x, {"y": y[pick, :, :4], "S": full["S"][pick, :4]}, ref, T, D, gradients=False, half_p=3 * 2.0 ** -11)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_steps_equal_the_sequence(cuda_device, D):
+    T = 21
+    x, S0, _ = draw("f32", 3, T, 2, D, seed=2)
+    y, S, _ = esa_delta_fwd(*ins(x), S_init=S0)
+    St = S0.clone()
+    ys = []
+    for t in range(T):
+        ys.append(esa_delta_step(*(z[:, t].contiguous() for z in ins(x)), St))
+    # the same operations in the same order
+    assert torch.equal(torch.stack(ys, 1), y) and torch.equal(St, S)
+
+
+def test_prepared_step_and_graph(cuda_device):
+    x, S0, _ = draw("bf16", 2, 3, 4, 64, seed=4)
+    toks = [[z[:, t].contiguous() for z in ins(x)] for t in range(3)]
+    want_S, want = S0.clone(), []
+    for t in range(3):
+        want.append(esa_delta_step(*toks[t], want_S).clone())
+    buf = [z.clone() for z in toks[0]]
+    S = S0.clone()
+    step = PreparedDeltaStep(*buf, S)
+    for t in range(3):
+        for z, w in zip(buf, toks[t]):
+            z.copy_(w)
+        assert torch.equal(step(), want[t])
+    assert torch.equal(S, want_S)
+    S.copy_(S0)
+    st = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(st):
+        step = PreparedDeltaStep(*buf, S)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=st):
+            y = step()
+    S.copy_(S0)
+    for t in range(3):
+        for z, w in zip(buf, toks[t]):
+            z.copy_(w)
+        g.replay()
+        assert torch.equal(y, want[t])
+    assert torch.equal(S, want_S)
+
+
+@pytest.mark.parametrize("T", [5, 130])
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_split_sequence(cuda_device, T, D):
+    """Two calls with the state handed over equal one call."""
+    x, S0, _ = draw("f32", 2, T, 2, D, seed=6)
+    y, S, _ = esa_delta_fwd(*ins(x), S_init=S0)
+    c = T // 3
+    y1, S1, _ = esa_delta_fwd(*(z[:, :c].contiguous() for z in ins(x)), S_init=S0)
+    y2, S2, _ = esa_delta_fwd(*(z[:, c:].contiguous() for z in ins(x)), S_init=S1)
+    assert_within("y", torch.cat([y1, y2], 1), y.double().cpu(), 2 * PER_TOKEN * T, 2 * PER_TOKEN * T ** 0.5)
+    assert_within("S", S2, S.double().cpu(), 2 * PER_TOKEN * T, 2 * PER_TOKEN * T ** 0.5)
+
+
+def test_strided_rows_and_outputs_given(cuda_device):
+    B, T, H, D = 2, 77, 2, 64
+    C = H * D
+    x, S0, dS = draw("bf16", B, T, H, D, seed=8)
+    P = torch.full((B, T, 3 * C + 8 + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    q, k, v = (P[..., i * C:(i + 1) * C].view(B, T, H, D) for i in range(3))
+    a, b = P[..., 3 * C + 1:3 * C + 1 + H], P[..., 3 * C + 5:3 * C + 5 + H]
+    for dst, n in zip((q, k, v, a, b), NAMES):
+        dst.copy_(x[n])
+    base = run(x, S0, dS, 0.3)
+    y = torch.empty(B, T, H, D, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(esa_delta_workspace_size(B, T, H, D, torch.bfloat16), dtype=torch.uint8, device="cuda")
+    y2, S, ws2 = esa_delta_fwd(q, k, v, a, b, scale=0.3, S_init=S0, y=y, workspace=ws)
+    assert y2 is y and ws2 is ws and torch.equal(y, base["y"]) and torch.equal(S, base["S"])
+    g = esa_delta_bwd(q, k, v, a, b, x["dy"], ws, scale=0.3, S_init=S0, dS_final=dS)
+    for n, t in zip(("dq", "dk", "dv", "da", "db", "dS0"), g):
+        assert torch.equal(t, base[n]), n
+    # the column blocks' neighbours are read only
+    assert bool((P[..., 3 * C:3 * C + 1] == 7).all()) and bool((P[..., 3 * C + 8:] == 7).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("which", ["forget", "keep", "no_write", "overwrite", "reset_inside", "far_below", "infinite"])
+def test_gate_extremes(cuda_device, which, D):
+    B, T, H = 1, 150, 2
+    x, S0, dS = draw("bf16", B, T, H, D, seed=11)
+    if which == "forget":
+        x["a"].fill_(-30.0)
+    elif which == "keep":
+        x["a"].fill_(30.0)
+    elif which == "no_write":
+        x["b"].fill_(-30.0)
+    elif which == "overwrite":
+        x["b"].fill_(30.0)
+    elif which == "reset_inside":
+        x["a"].fill_(6.0)
+        x["a"][:, 40] = -60.0
+        x["a"][:, 100] = -1000.0
+    elif which == "far_below":
+        x["a"].fill_(-1.0e4)
+        x["b"][:, ::2] = -1.0e4
+    else:
+        x["a"][:, 20] = float("-inf")
+        x["a"][:, 30:] = float("inf")
+        x["b"][:, 60:] = float("inf")
+    out = run(x, S0, dS, D ** -0.5)
+    check(x, out, delta_reference(*ins(x), D ** -0.5, S0, x["dy"], dS), T, D, half_p=3 * 2.0 ** -11)
+
+
+@pytest.mark.parametrize("scale_v,scale_k", [(1.0e3, 1.0), (1.0e-4, 1.0), (1.0, 1.0e-3), (1.0, 0.0), (0.0, 1.0)])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_sizes_of_values(cuda_device, dt, scale_v, scale_k):
+    B, T, H, D = 1, 140, 2, 128
+    x, _, _ = draw(dt, B, T, H, D, seed=12)
+    x["v"] = x["v"] * scale_v
+    x["k"] = x["k"] * scale_k
+    out = run(x, None, None, D ** -0.5)
+    ref = delta_reference(*ins(x), D ** -0.5, None, x["dy"], None)
+    check(x, out, ref, T, D, half_p=3 * 2.0 ** -11)
+
+
+def test_repeated_key(cuda_device):
+    """The same key at every token: the chunk matrix is as far from the identity as it gets."""
+    B, T, H, D = 1, 200, 1, 128
+    x, S0, dS = draw("bf16", B, T, H, D, seed=13, a_mean=8.0)
+    x["k"].copy_(x["k"][:, :1].expand_as(x["k"]))
+    x["b"].fill_(4.0)
+    out = run(x, S0, dS, D ** -0.5)
+    check(x, out, delta_reference(*ins(x), D ** -0.5, S0, x["dy"], dS), T, D, half_p=3 * 2.0 ** -11)
+
+
+def test_no_tokens_and_no_batch(cuda_device):
+    S0 = torch.randn(2, 3, 32, 32, device="cuda")
+    z = torch.empty(2, 0, 3, 32, device="cuda")
+    g = torch.empty(2, 0, 3, device="cuda")
+    y, S, ws = esa_delta_fwd(z, z, z, g, g, S_init=S0)
+    assert y.shape == z.shape and torch.equal(S, S0)
+    _, S, _ = esa_delta_fwd(z, z, z, g, g)
+    assert not S.any()
+    *_, dS0 = esa_delta_bwd(z, z, z, g, g, z, ws, S_init=S0, dS_final=S0)
+    assert torch.equal(dS0, S0)
+    z, g = torch.empty(0, 4, 3, 32, device="cuda"), torch.empty(0, 4, 3, device="cuda")
+    y, S, ws = esa_delta_fwd(z, z, z, g, g)
+    assert y.numel() == 0 and S.numel() == 0
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("f16", 128), ("f32", 32)])
+def test_same_results_every_time_and_two_streams(cuda_device, dt, D):
+    x, S0, dS = draw(dt, 2, 200, 4, D, seed=14)
+    x2, S02, dS2 = draw(dt, 2, 200, 4, D, seed=15)
+    first, second = run(x, S0, dS, 0.1), run(x2, S02, dS2, 0.1)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            a = run(x, S0, dS, 0.1)
+        with torch.cuda.stream(s2):
+            b = run(x2, S02, dS2, 0.1)
+        torch.cuda.synchronize()
+        for n in first:
+            assert torch.equal(a[n], first[n]) and torch.equal(b[n], second[n]), n
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_graph_of_forward_and_backward(cuda_device, D):
+    x, S0, dS = draw("bf16", 1, 129, 2, D, seed=16)
+    want = run(x, S0, dS, 0.2)
+    st = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(st):
+        run(x, S0, dS, 0.2)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=st):
+            out = run(x, S0, dS, 0.2)
+    for t in out.values():
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for n in want:
+        assert torch.equal(out[n], want[n]), n
+
+
+def test_nothing_written_outside(cuda_device):
+    """Canary rows around every output stay as they were."""
+    B, T, H, D = 1, 67, 2, 128
+    x, S0, dS = draw("f16", B, T, H, D, seed=17)
+
+    def guarded(shape, dtype):
+        n = 1
+        for s in shape:
+            n *= s
+        flat = torch.full((n + 512,), 3.0, dtype=dtype, device="cuda")
+        return flat, flat[256:256 + n].view(shape)
+
+    h, f = torch.float16, torch.float32
+    bufs = {n: guarded(s, t) for n, s, t in (("y", (B, T, H, D), h), ("S", (B, H, D, D), f), ("dq", (B, T, H, D), h),
+                                             ("dk", (B, T, H, D), h), ("dv", (B, T, H, D), h), ("da", (B, T, H), h),
+                                             ("db", (B, T, H), h), ("dS0", (B, H, D, D), f))}
+    need = esa_delta_workspace_size(B, T, H, D, torch.float16)
+    wflat = torch.full((need + 512,), 171, dtype=torch.uint8, device="cuda")
+    ws = wflat[256:256 + need]
+    out = {n: t[1] for n, t in bufs.items()}
+    esa_delta_fwd(*ins(x), S_init=S0, y=out["y"], S_final=out["S"], workspace=ws)
+    esa_delta_bwd(*ins(x), x["dy"], ws, S_init=S0, dS_final=dS, dq=out["dq"], dk=out["dk"], dv=out["dv"],
+                  da=out["da"], db=out["db"], dS_init=out["dS0"])
+    torch.cuda.synchronize()
+    for n, (flat, _) in bufs.items():
+        assert bool((flat[:256] == 3).all()) and bool((flat[-256:] == 3).all()), n
+    assert bool((wflat[:256] == 171).all()) and bool((wflat[-256:] == 171).all())
+    check(x, out, delta_reference(*ins(x), D ** -0.5, S0, x["dy"], dS), T, D, half_p=3 * 2.0 ** -11)
+
+
+def test_refusals(cuda_device):
+    x, S0, _ = draw("bf16", 1, 8, 2, 64, seed=18)
+    q, k, v, a, b = ins(x)
+    with pytest.raises(ValueError):
+        esa_delta_fwd(q, k[:, :4], v, a, b)
+    with pytest.raises(ValueError):
+        esa_delta_fwd(q, k.float(), v, a, b)
+    with pytest.raises(ValueError):
+        esa_delta_fwd(q, k, v, a[..., :1], b)
+    with pytest.raises(ValueError):
+        esa_delta_fwd(q.transpose(1, 2).contiguous().transpose(1, 2), k, v, a, b)
+    with pytest.raises(ValueError):
+        esa_delta_fwd(q, k, v, a, b, S_init=S0.half())
+    with pytest.raises(ValueError):
+        esa_delta_fwd(q, k, v, a, b, y=torch.empty_like(q).float())
+    with pytest.raises(TypeError):
+        esa_delta_fwd(*(t.to(torch.float8_e4m3fn) for t in (q, k, v, a, b)))
+    with pytest.raises(ValueError):
+        esa_delta_fwd(*(t[..., :16].contiguous() for t in (q, k, v)), a, b)
+    with pytest.raises(EsaError):
+        esa_delta_fwd(q, k, v, a, b, scale=float("nan"))
+    with pytest.raises(EsaError):
+        esa_delta_fwd(q, k, v, a, b, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        esa_delta_bwd(q, k, v, a, b, x["dy"], None)
+    with pytest.raises(EsaError):   # rows that do not start on 16 bytes
+        wide = torch.zeros(1, 8, 2 * 64 + 4, dtype=torch.bfloat16, device="cuda")
+        w = wide[..., :128].view(1, 8, 2, 64)
+        esa_delta_fwd(w, w, v, a, b)
