@@ -1,6 +1,7 @@
 // esa_delta.cu -- C ABI of the gated delta rule (declared in include/esa.h):
 // argument checks, the workspace, and the order of the kernels.
 #include "esa_delta.h"
+#include "esa_delta_chunk.h"
 
 #include <climits>
 
@@ -13,10 +14,43 @@ namespace {
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Sequences of 16-bit types of at least this many tokens go through the
+// chunked kernels, shorter ones and float32 token by token.
+constexpr int kChunkMinT = 17;
+bool chunked(const DeltaShape &s, int dtype) { return dtype != ESA_F32 && s.T >= kChunkMinT; }
+
 // What the forward keeps for the backward (u), then the backward's scratch.
 struct DeltaLayout {
   size_t u = 0, du = 0, dk = 0, dq = 0, gain = 0, end = 0, total = 0;
 };
+
+// The chunk arrays, laid out from `base`; `*total` gets their size.
+ChunkArrays chunk_arrays(unsigned char *base, const DeltaShape &s, bool keep, size_t *total) {
+  ChunkArrays w{};
+  w.nc = (s.T + kChunk - 1) / kChunk;
+  const size_t n = static_cast<size_t>(s.B) * s.H * w.nc;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    unsigned char *p = base + o;
+    o += up256(bytes);
+    return p;
+  };
+  const size_t rec = s.D == 32 ? ChunkRecord<32>::bytes : s.D == 64 ? ChunkRecord<64>::bytes : ChunkRecord<128>::bytes;
+  w.rec = take(n * rec);
+  if (keep) {
+    const size_t D = s.D, groups = up256(n * (D / 16) * sizeof(float));
+    w.u16 = reinterpret_cast<__half *>(take(n * 64 * D * 2));
+    w.r16 = reinterpret_cast<__half *>(take(n * 64 * D * 2));
+    w.s16 = reinterpret_cast<__half *>(take(n * D * D * 2));
+    w.ds16 = reinterpret_cast<__half *>(take(n * D * D * 2));
+    w.su = reinterpret_cast<float *>(take(groups));
+    w.sr = reinterpret_cast<float *>(take(groups));
+    w.ss = reinterpret_cast<float *>(take(groups));
+    w.sds = reinterpret_cast<float *>(take(groups));
+  }
+  *total = o;
+  return w;
+}
 
 DeltaLayout delta_layout(const DeltaShape &s, bool keep) {
   DeltaLayout lo;
@@ -86,7 +120,13 @@ extern "C" {
 
 size_t esa_delta_workspace_size(int B, int T, int H, int D, int dtype, int keep) {
   if (check_shape(B, T, H, D, dtype) != ESA_OK || (keep != 0 && keep != 1)) return 0;
-  return delta_layout(DeltaShape{B, T, H, D, 0, 0, 0, 1.0f}, keep != 0).total + 256;
+  const DeltaShape s{B, T, H, D, 0, 0, 0, 1.0f};
+  size_t total = 0;
+  if (chunked(s, dtype)) {
+    chunk_arrays(nullptr, s, keep != 0, &total);
+    return total + 256;
+  }
+  return delta_layout(s, keep != 0).total + 256;
 }
 
 int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, long long ld_v, const void *a,
@@ -105,6 +145,19 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (B == 0) return ESA_OK;
   if (T == 0) return copy_state(S_final, S_init, s, st);
+  if (chunked(s, dtype)) {
+    ChunkArgs c{};
+    size_t total;
+    c.s = s;
+    c.w = chunk_arrays(static_cast<unsigned char *>(workspace), s, keep != 0, &total);
+    c.q = q; c.k = k; c.v = v; c.a = a; c.b = b;
+    c.y = y;
+    c.S_in = S_init;
+    c.S_out = S_final;
+    c.keep = keep != 0;
+    if ((rc = launch_chunk_prep(dtype, c, st))) return rc;
+    return launch_chunk_fwd(dtype, c, st);
+  }
   const DeltaLayout lo = delta_layout(s, keep != 0);
   SweepArgs p{};
   p.s = s;
@@ -136,8 +189,21 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (B == 0) return ESA_OK;
   if (T == 0) return copy_state(dS_init, dS_final, s, st);
-  const DeltaLayout lo = delta_layout(s, true);
   unsigned char *base = static_cast<unsigned char *>(workspace);
+  if (chunked(s, dtype)) {
+    ChunkArgs c{};
+    size_t total;
+    c.s = s;
+    c.w = chunk_arrays(base, s, true, &total);
+    c.q = q; c.k = k; c.v = v; c.a = a; c.b = b; c.dy = dy;
+    c.dq = dq; c.dk = dk; c.dv = dv; c.da = da; c.db = db;
+    c.S_in = dS_final;
+    c.S_out = dS_init;
+    c.keep = true;
+    if ((rc = launch_chunk_bwd(dtype, c, st))) return rc;
+    return launch_chunk_grad(dtype, c, st);
+  }
+  const DeltaLayout lo = delta_layout(s, true);
   SweepArgs p{};
   p.s = s;
   p.q = q; p.k = k; p.v = v; p.dy = dy; p.a = a; p.b = b;

@@ -1,0 +1,401 @@
+// esa_delta_chain.cu -- second kernel of the chunked gated delta rule: the
+// state carried from chunk to chunk, and the outputs (sm_100a).
+//
+// Value channels do not mix, so a warp carries 16 of them through the whole
+// sequence by itself: S^T (16 value channels x D key channels) stays in its
+// registers as float32 accumulators, and every product of a chunk has the
+// warp's 16 channels as its 16 rows, so that the accumulators of one product
+// are the A operand of the next (esa_mma.cuh) and no shared memory, tensor
+// memory round trip or barrier lies on the chain
+//     X = S^T K^T,   R = beta (V^T - e^G X),   U = R T^T,   S^T <- e^{G_last} S^T + (e^{G_last - G} U) K.
+// The B operands -- K, Q, T, P of the chunk -- are the same for all warps of a
+// head; they are copied to shared memory one chunk ahead (cp.async, two
+// buffers).  The output is Y^T = scale (e^G S^T Q^T + U P^T) from the same
+// fragments.
+//
+// Rounding.  What enters the state keeps float32 accuracy: S, R, U and T are
+// operands in two float16 terms each (22 bits, esa_mma.cuh), K is exact, sums
+// are float32.  The output's own product takes S, U and P in one float16 term
+// (2^-12 of a value on average) when the output is bfloat16 (2^-9), and S and
+// U in two when it is float16, P in one.
+//
+// A chunk costs a warp 400 mma at D = 128 (130 of them off the chain).  The
+// issue rate of mma.sync (8 clocks per m16n8k16 and SM quarter, measured 550
+// TFLOP/s) bounds it with two warps per quarter, the latency of the dependent
+// steps with one.  tcgen05 would have four times the rate but takes 128 rows:
+// the whole head in one SM, with the state converted through tensor memory
+// three times a chunk; with few heads (the usual case of a long prompt) that
+// leaves most SMs idle, where 16-row warps spread a head over eight.
+#include <type_traits>
+
+#include "esa_delta_chunk.h"
+#include "esa_delta_sweep.cuh"
+#include "esa_mma.cuh"
+
+#include "esa.h"
+#include "esa_host.h"
+
+namespace esa {
+namespace {
+
+template <int D, int W>
+struct ChainSmem {
+  using R = ChunkRecord<D>;
+  static constexpr int kRow = 32 * W;   // bytes of a value row of the block
+  static constexpr int v = R::pl, stage = v + 64 * kRow;
+  static constexpr int total = 2 * stage;
+};
+
+// First token (or 64) from which each of the thread's two rows is not finite,
+// agreed over the row's four lanes; those entries become zero.
+__device__ __forceinline__ void cut_rows(float (&R)[8][4], int t4, int (&first)[2]) {
+  first[0] = first[1] = 64;
+#pragma unroll
+  for (int nt = 7; nt >= 0; --nt)
+#pragma unroll
+    for (int e = 3; e >= 0; --e)
+      if (!(fabsf(R[nt][e]) <= 3.4028235e38f)) first[e >> 1] = min(first[e >> 1], 8 * nt + 2 * t4 + (e & 1));
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    first[r] = min(first[r], __shfl_xor_sync(0xffffffffu, first[r], 1));
+    first[r] = min(first[r], __shfl_xor_sync(0xffffffffu, first[r], 2));
+  }
+#pragma unroll
+  for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (8 * nt + 2 * t4 + (e & 1) >= first[e >> 1]) R[nt][e] = 0.0f;
+}
+
+template <typename T, int D, int W, bool KEEP>
+__global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p) {
+  using L = ChainSmem<D, W>;
+  using R = ChunkRecord<D>;
+  constexpr int NT = D / 8;                                // accumulator tiles of the state
+  constexpr bool kTwo = std::is_same<T, __half>::value;    // two terms in the output's product
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+  constexpr int SL = D / (16 * W);
+  const int head = blockIdx.x / SL, slice = blockIdx.x - head * SL;
+  const int b = head / p.s.H, h = head - b * p.s.H;
+  const int dv0 = slice * 16 * W;             // first value channel of the block
+  const int dvw = dv0 + 16 * warp;            // and of this warp
+  const int nc = p.w.nc;
+  const long long c0 = static_cast<long long>(head) * nc;
+  const long long row0 = static_cast<long long>(b) * p.s.T;
+  const T *v = static_cast<const T *>(p.v) + h * D + dv0;
+  T *y = static_cast<T *>(p.y) + h * D + dvw + 8 * (lane & 1);
+  const long long ldy = static_cast<long long>(p.s.H) * D;
+  const uint32_t s0 = smem_u32(smem);
+  const uint32_t vofs = tile_off<L::kRow>(lane & 15, 2 * warp + (lane >> 4));          // this warp's columns, fragments
+  const uint32_t vrow = tile_off<L::kRow>(lane >> 1, 2 * warp + (lane & 1));           // the same, 32-byte rows
+
+  auto fetch = [&](int n, int buf) {
+    const uint32_t s = s0 + buf * L::stage;
+    copy_linear<R::pl, W * 32>(s, p.w.rec + (c0 + n) * R::bytes);
+    const int len = min(kChunk, p.s.T - n * kChunk);
+    const T *src = v + (row0 + n * kChunk) * p.s.ld_v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // 64 rows of 2 W units, W 32 threads
+      const int e = threadIdx.x + i * W * 32, r = e / (2 * W), u = e % (2 * W);
+      const bool on = r < len;
+      cp_async16_zfill(s + L::v + tile_off<L::kRow>(r, u), on ? src + r * p.s.ld_v + u * 8 : v, on);
+    }
+    sweep::cp_async_commit();
+  };
+
+  // S^T times a power of two, 1 / sinv: each chunk leaves it in the scale in
+  // which it added to it.
+  float S[NT][4];
+  float scur = 1.0f, sinv = 1.0f;
+  if (p.S_in != nullptr) {
+    const float *Si = p.S_in + static_cast<long long>(head) * D * D;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[nt][e] = Si[(8 * nt + 2 * t4 + (e & 1)) * D + dvw + g + (e >> 1) * 8];
+  } else {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[nt][e] = 0.0f;
+  }
+
+  fetch(0, 0);
+#pragma unroll 1
+  for (int n = 0; n < nc; ++n) {
+    const int buf = n & 1;
+    if (n + 1 < nc) {
+      fetch(n + 1, buf ^ 1);
+      sweep::cp_async_wait<1>();
+    } else {
+      sweep::cp_async_wait<0>();
+    }
+    __syncthreads();
+    const uint32_t st = s0 + buf * L::stage;
+    const LaneOff<D * 2> ofd(lane, st);        // tiles of keys and queries
+    const LaneOff<128> of64(lane, st);         // T and P
+    const unsigned char *sb = smem + buf * L::stage;
+    const float *tok = reinterpret_cast<const float *>(sb + R::tok) + 2 * t4;
+    const float4 fac = *reinterpret_cast<const float4 *>(sb + R::fac);
+    const long long c = c0 + n;
+
+    // X = S^T K^T and the output's S^T Q^T
+    float X[8][4], Y[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) X[i][e] = Y[i][e] = 0.0f;
+    float top = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) top = max_tile(S[nt], top);
+    const float tops = warp_max(top);
+    const Pow2 ps = pow2_scale(tops);
+    const float xinv = ps.inv * sinv;
+    if (KEEP && lane == 0) p.w.ss[c * (D / 16) + (dvw >> 4)] = tops > 0.0f ? xinv : 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t hi[4], lo[4];
+      split_a(S[2 * ks], S[2 * ks + 1], splat(ps.s), splat(ps.s), hi, lo);
+      if constexpr (KEEP) {
+        __half *o = p.w.s16 + c * (D * D) + (dvw + g) * D + 16 * ks + 2 * t4;
+        *reinterpret_cast<uint32_t *>(o) = hi[0];
+        *reinterpret_cast<uint32_t *>(o + 8) = hi[2];
+        *reinterpret_cast<uint32_t *>(o + 8 * D) = hi[1];
+        *reinterpret_cast<uint32_t *>(o + 8 * D + 8) = hi[3];
+      }
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t bk[4], bq[4];
+        ldsm4(bk, ofd.at(np, ks) + R::k);
+        ldsm4(bq, ofd.at(np, ks) + R::q);
+        mma_f16(X[2 * np], hi, bk[0], bk[2]);
+        mma_f16(X[2 * np + 1], hi, bk[1], bk[3]);
+        mma_f16(Y[2 * np], hi, bq[0], bq[2]);
+        mma_f16(Y[2 * np + 1], hi, bq[1], bq[3]);
+        mma_f16(X[2 * np], lo, bk[0], bk[2]);
+        mma_f16(X[2 * np + 1], lo, bk[1], bk[3]);
+        if constexpr (kTwo) {
+          mma_f16(Y[2 * np], lo, bq[0], bq[2]);
+          mma_f16(Y[2 * np + 1], lo, bq[1], bq[3]);
+        }
+      }
+    }
+    // R = beta V^T - (beta e^G) X, in place of X
+    float2 chk = make_float2(0.0f, 0.0f);
+    top = 0.0f;
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      uint32_t vv[4];
+      ldsm4t(vv, st + L::v + vofs + 16 * np * L::kRow);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int nt = 2 * np + half;
+        const float2 be = *reinterpret_cast<const float2 *>(tok + kTokBeta * 64 + 8 * nt);
+        const float2 tx = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 8 * nt), splat(-xinv));
+        const float2 r0 = fma2(tx, row_lo(X[nt]), mul2(be, unpack_io<T>(vv[half])));
+        const float2 r1 = fma2(tx, row_hi(X[nt]), mul2(be, unpack_io<T>(vv[2 + half])));
+        chk = fma2(r0, splat(0.0f), fma2(r1, splat(0.0f), chk));
+        set_lo(X[nt], r0);
+        set_hi(X[nt], r1);
+        top = max_tile(X[nt], top);
+      }
+    }
+    // A value, key or state that is not finite poisons its channel from that
+    // token on; zero there keeps it from reaching earlier tokens of the chunk
+    // through the zeros above the diagonals of T and P.
+    int first[2] = {64, 64};
+    const bool cut = __any_sync(0xffffffffu, !(chk.x + chk.y == 0.0f));
+    if (cut) {
+      cut_rows(X, t4, first);
+      top = 0.0f;
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt) top = max_tile(X[nt], top);
+    }
+    const Pow2 pr = pow2_scale(warp_max(top));
+    // U = R T^T: T_ij = 0 for j > i, in blocks of 16
+    float U[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) U[i][e] = 0.0f;
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+      uint32_t hi[4], lo[4];
+      split_a(X[2 * kb], X[2 * kb + 1], splat(pr.s), splat(pr.s), hi, lo);
+#pragma unroll
+      for (int np = kb; np < 4; ++np) {
+        uint32_t bh[4], bl[4];
+        ldsm4(bh, of64.at(np, kb) + R::th);
+        ldsm4(bl, of64.at(np, kb) + R::tl);
+        mma_f16(U[2 * np], hi, bh[0], bh[2]);
+        mma_f16(U[2 * np + 1], hi, bh[1], bh[3]);
+        mma_f16(U[2 * np], lo, bh[0], bh[2]);
+        mma_f16(U[2 * np + 1], lo, bh[1], bh[3]);
+        mma_f16(U[2 * np], hi, bl[0], bl[2]);
+        mma_f16(U[2 * np + 1], hi, bl[1], bl[3]);
+      }
+    }
+    // U is uf times the sums; U e^{G_last - G} / key scale into X
+    const float uf = pr.inv * fac.y;
+    top = 0.0f;
+    float topl = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      const float2 tl = *reinterpret_cast<const float2 *>(tok + kTokL * 64 + 8 * nt);
+      top = max_tile(U[nt], top);
+      set_lo(X[nt], mul2(row_lo(U[nt]), tl));
+      set_hi(X[nt], mul2(row_hi(U[nt]), tl));
+      topl = max_tile(X[nt], topl);
+    }
+    top = warp_max(top);
+    const Pow2 pu = pow2_scale(top), pl = pow2_scale(warp_max(topl));
+    // S^T <- e^{G_last} S^T + X K in the scale that suits X, unless that would
+    // lift the state by more than 2^36 over its own
+    const float asc = fminf(pl.s * (1.0f / uf), tops > 0.0f ? ps.s * scur * 68719476736.0f : __int_as_float(0x7f800000));
+    {
+      const float2 sc = splat(fac.x * (asc * sinv));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) scale_tile(S[nt], sc);
+      scur = asc;
+      sinv = 1.0f / asc;
+    }
+    const float xs = asc * uf;
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+      uint32_t hi[4], lo[4];
+      split_a(X[2 * kb], X[2 * kb + 1], splat(xs), splat(xs), hi, lo);
+#pragma unroll
+      for (int np = 0; np < D / 16; ++np) {
+        uint32_t bk[4];
+        ldsm4t(bk, ofd.at(kb, np) + R::k);
+        mma_f16(S[2 * np], hi, bk[0], bk[1]);
+        mma_f16(S[2 * np + 1], hi, bk[2], bk[3]);
+        mma_f16(S[2 * np], lo, bk[0], bk[1]);
+        mma_f16(S[2 * np + 1], lo, bk[2], bk[3]);
+      }
+    }
+    // Y = (scale e^G) S^T Q^T + scale U P^T; the first product joins the
+    // second's sum, its tokens' factors over the second's
+    const float uinv = pu.inv * uf, yf = p.s.scale * fac.z * uinv;
+    {
+      const float r = yf != 0.0f ? xinv / yf : 0.0f;
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt)
+        scale_tile(Y[nt], mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 8 * nt), splat(r)));
+    }
+    if (KEEP && lane == 0) p.w.su[c * (D / 16) + (dvw >> 4)] = top > 0.0f ? uinv : 0.0f;
+    uint32_t uh[4][4];
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+      uint32_t ul[4];
+      if constexpr (kTwo) split_a(U[2 * kb], U[2 * kb + 1], splat(pu.s), splat(pu.s), uh[kb], ul);
+      else single_a(U[2 * kb], U[2 * kb + 1], splat(pu.s), splat(pu.s), uh[kb]);
+#pragma unroll
+      for (int np = kb; np < 4; ++np) {
+        uint32_t bp[4];
+        ldsm4(bp, of64.at(np, kb) + R::ph);
+        mma_f16(Y[2 * np], uh[kb], bp[0], bp[2]);
+        mma_f16(Y[2 * np + 1], uh[kb], bp[1], bp[3]);
+        if constexpr (kTwo) {
+          mma_f16(Y[2 * np], ul, bp[0], bp[2]);
+          mma_f16(Y[2 * np + 1], ul, bp[1], bp[3]);
+        }
+      }
+    }
+    if (cut) {   // rows that are not finite from token `first` on
+      const float nan = __int_as_float(0x7fc00000);
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (8 * nt + 2 * t4 + (e & 1) >= first[e >> 1]) Y[nt][e] = nan;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (first[e >> 1] < 64) S[nt][e] = nan;
+    }
+    // Transpose through this warp's own columns of the value tile (read above) and store rows of 32 bytes.
+    const int len = min(kChunk, p.s.T - n * kChunk);
+    const uint32_t vw = st + L::v + vofs;
+    const unsigned char *vr = sb + L::v + vrow;
+    __syncwarp();
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      const float2 a = mul2(row_lo(Y[2 * np]), splat(yf)), bb = mul2(row_lo(Y[2 * np + 1]), splat(yf));
+      const float2 cc = mul2(row_hi(Y[2 * np]), splat(yf)), d = mul2(row_hi(Y[2 * np + 1]), splat(yf));
+      const uint32_t o[4] = {pack_io<T>(a.x, a.y), pack_io<T>(bb.x, bb.y), pack_io<T>(cc.x, cc.y), pack_io<T>(d.x, d.y)};
+      stsm4t(vw + 16 * np * L::kRow, o);
+    }
+    __syncwarp();
+    T *yr = y + (row0 + n * kChunk + (lane >> 1)) * ldy;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (16 * i + (lane >> 1) < len)
+        *reinterpret_cast<uint4 *>(yr + 16 * i * ldy) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
+    if constexpr (KEEP) {
+      __syncwarp();
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        const uint32_t o[4] = {uh[kb][0], uh[kb][2], uh[kb][1], uh[kb][3]};
+        stsm4t(vw + 16 * kb * L::kRow, o);
+      }
+      __syncwarp();
+      __half *ur = p.w.u16 + (c * 64 + (lane >> 1)) * D + dvw + 8 * (lane & 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(ur + 16 * i * D) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
+    }
+    __syncthreads();   // the next turn's copies overwrite this buffer
+  }
+  if (p.S_out != nullptr) {
+    float *So = p.S_out + static_cast<long long>(head) * D * D;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) So[(8 * nt + 2 * t4 + (e & 1)) * D + dvw + g + (e >> 1) * 8] = S[nt][e] * sinv;
+  }
+}
+
+template <typename T, int D, int W, bool KEEP>
+int run(const ChunkArgs &a, cudaStream_t st) {
+  using L = ChainSmem<D, W>;
+  auto kern = delta_chain_fwd_kernel<T, D, W, KEEP>;
+  const int rc = runtime_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total));
+  if (rc) return rc;
+  kern<<<static_cast<unsigned>(a.s.B) * a.s.H * (D / (16 * W)), W * 32, L::total, st>>>(a);
+  return runtime_status(cudaGetLastError());
+}
+
+template <typename T, int D, int W>
+int by_keep(const ChunkArgs &a, cudaStream_t st) {
+  return a.keep ? run<T, D, W, true>(a, st) : run<T, D, W, false>(a, st);
+}
+
+template <typename T, int D>
+int by_warps(const ChunkArgs &a, cudaStream_t st) {
+  if constexpr (D == 128)
+    if (chain_splits(a.s.B * a.s.H)) return by_keep<T, D, 4>(a, st);
+  return by_keep<T, D, D / 16>(a, st);
+}
+
+template <typename T>
+int by_d(const ChunkArgs &a, cudaStream_t st) {
+  switch (a.s.D) {
+    case 32: return by_warps<T, 32>(a, st);
+    case 64: return by_warps<T, 64>(a, st);
+    case 128: return by_warps<T, 128>(a, st);
+    default: return ESA_ERR_UNSUPPORTED;
+  }
+}
+
+}  // namespace
+
+bool chain_splits(int heads) { return 2ll * heads <= sm_count(); }
+
+int launch_chunk_fwd(int dtype, const ChunkArgs &a, cudaStream_t st) {
+  return dtype == ESA_F16 ? by_d<__half>(a, st) : by_d<__nv_bfloat16>(a, st);
+}
+
+}  // namespace esa

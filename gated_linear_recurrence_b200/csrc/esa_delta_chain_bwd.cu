@@ -1,0 +1,333 @@
+// esa_delta_chain_bwd.cu -- the backward of the chunked gated delta rule, first
+// kernel: the gradient of the state carried from the last chunk to the first
+// (sm_100a).
+//
+// As in the forward chain (esa_delta_chain.cu) a warp carries 16 value
+// channels, here of dS^T, in its registers.  For a chunk, with dS the gradient
+// of the state leaving it and P, T as in the first kernel,
+//   dU^T = e^{G_last - G} (dS^T K^T) + scale dO^T P,
+//   du^T = dU^T T                                  (the gradient of u: T^T is applied to dU),
+//   dS^T <- e^{G_last} dS^T - (beta e^G du^T) K + scale (e^G dO^T) Q,
+// and dv = beta du.  What enters dS keeps float32 accuracy (two float16 terms,
+// K, Q and dO exact), because dS_init is float32.  dS and du are left for the
+// second kernel (esa_delta_grad.cu) in float16, one power of two per 16
+// channels.
+//
+// 484 mma a chunk and warp at D = 128, bound as the forward chain is.
+#include <type_traits>
+
+#include "esa_delta_chunk.h"
+#include "esa_delta_sweep.cuh"
+#include "esa_mma.cuh"
+
+#include "esa.h"
+#include "esa_host.h"
+
+namespace esa {
+namespace {
+
+template <int D, int W>
+struct ChainBwdSmem {
+  using R = ChunkRecord<D>;
+  static constexpr int kRow = 32 * W;
+  static constexpr int dy = R::bytes, stage = dy + 64 * kRow, total = 2 * stage;
+};
+
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p) {
+  using L = ChainBwdSmem<D, W>;
+  using R = ChunkRecord<D>;
+  constexpr int NT = D / 8;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+  constexpr int SL = D / (16 * W);
+  const int head = blockIdx.x / SL, slice = blockIdx.x - head * SL;
+  const int b = head / p.s.H, h = head - b * p.s.H;
+  const int dv0 = slice * 16 * W, dvw = dv0 + 16 * warp;
+  const int nc = p.w.nc;
+  const long long c0 = static_cast<long long>(head) * nc;
+  const long long row0 = static_cast<long long>(b) * p.s.T;
+  const long long ldc = static_cast<long long>(p.s.H) * D;
+  const T *dy = static_cast<const T *>(p.dy) + h * D + dv0;
+  T *dv = static_cast<T *>(p.dv) + h * D + dvw + 8 * (lane & 1);
+  const uint32_t s0 = smem_u32(smem);
+  const uint32_t vofs = tile_off<L::kRow>(lane & 15, 2 * warp + (lane >> 4));
+  const uint32_t vrow = tile_off<L::kRow>(lane >> 1, 2 * warp + (lane & 1));
+
+  auto fetch = [&](int n, int buf) {
+    const uint32_t s = s0 + buf * L::stage;
+    copy_linear<R::bytes, W * 32>(s, p.w.rec + (c0 + n) * R::bytes);
+    const int len = min(kChunk, p.s.T - n * kChunk);
+    const T *src = dy + (row0 + n * kChunk) * ldc;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = threadIdx.x + i * W * 32, r = e / (2 * W), u = e % (2 * W);
+      const bool on = r < len;
+      cp_async16_zfill(s + L::dy + tile_off<L::kRow>(r, u), on ? src + r * ldc + u * 8 : dy, on);
+    }
+    sweep::cp_async_commit();
+  };
+
+  float S[NT][4];   // dS^T times scur
+  float scur = 1.0f, sinv = 1.0f;
+  if (p.S_in != nullptr) {
+    const float *Si = p.S_in + static_cast<long long>(head) * D * D;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[nt][e] = Si[(8 * nt + 2 * t4 + (e & 1)) * D + dvw + g + (e >> 1) * 8];
+  } else {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[nt][e] = 0.0f;
+  }
+
+  fetch(nc - 1, 0);
+#pragma unroll 1
+  for (int it = 0; it < nc; ++it) {
+    const int n = nc - 1 - it, buf = it & 1;
+    if (n > 0) {
+      fetch(n - 1, buf ^ 1);
+      sweep::cp_async_wait<1>();
+    } else {
+      sweep::cp_async_wait<0>();
+    }
+    __syncthreads();
+    const uint32_t st = s0 + buf * L::stage;
+    const LaneOff<D * 2> ofd(lane, st);
+    const LaneOff<128> of64(lane, st);
+    const unsigned char *sb = smem + buf * L::stage;
+    const float *tok = reinterpret_cast<const float *>(sb + R::tok) + 2 * t4;
+    const float4 fac = *reinterpret_cast<const float4 *>(sb + R::fac);
+    const long long c = c0 + n;
+
+    // X = dS^T K^T
+    float X[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) X[i][e] = 0.0f;
+    float top = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) top = max_tile(S[nt], top);
+    const float tops = warp_max(top);
+    const Pow2 ps = pow2_scale(tops);
+    const float xinv = ps.inv * sinv;
+    if (lane == 0) p.w.sds[c * (D / 16) + (dvw >> 4)] = tops > 0.0f ? xinv : 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t hi[4], lo[4];
+      split_a(S[2 * ks], S[2 * ks + 1], splat(ps.s), splat(ps.s), hi, lo);
+      __half *o = p.w.ds16 + c * (D * D) + (dvw + g) * D + 16 * ks + 2 * t4;
+      *reinterpret_cast<uint32_t *>(o) = hi[0];
+      *reinterpret_cast<uint32_t *>(o + 8) = hi[2];
+      *reinterpret_cast<uint32_t *>(o + 8 * D) = hi[1];
+      *reinterpret_cast<uint32_t *>(o + 8 * D + 8) = hi[3];
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t bk[4];
+        ldsm4(bk, ofd.at(np, ks) + R::k);
+        mma_f16(X[2 * np], hi, bk[0], bk[2]);
+        mma_f16(X[2 * np + 1], hi, bk[1], bk[3]);
+        mma_f16(X[2 * np], lo, bk[0], bk[2]);
+        mma_f16(X[2 * np + 1], lo, bk[1], bk[3]);
+      }
+    }
+    // dO^T as an A operand, scaled to float16
+    uint32_t od[4][4];
+    top = 0.0f;
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+      uint32_t r[4];
+      ldsm4t(r, st + L::dy + vofs + 16 * kb * L::kRow);
+      od[kb][0] = r[0]; od[kb][1] = r[2]; od[kb][2] = r[1]; od[kb][3] = r[3];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = unpack_io<T>(od[kb][e]);
+        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+      }
+    }
+    const Pow2 pd = pow2_scale(warp_max(top));
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) od[kb][e] = pack2(mul2(unpack_io<T>(od[kb][e]), splat(pd.s)));
+    // dU^T = zf (X r + dO^T P); without an output gradient's share (scale 0) P is left out
+    const float zf0 = p.s.scale * fac.z * pd.inv;
+    const bool with = zf0 != 0.0f;
+    const float zf = with ? zf0 : 1.0f;
+    {
+      const float2 r = splat(xinv / zf);
+#pragma unroll
+      for (int nt = 0; nt < 8; ++nt)
+        scale_tile(X[nt], mul2(*reinterpret_cast<const float2 *>(tok + kTokL * 64 + 8 * nt), r));
+    }
+    if (with) {
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+        for (int np = 0; np <= kb; ++np) {
+          uint32_t bh[4], bl[4];
+          ldsm4t(bh, of64.at(kb, np) + R::ph);
+          ldsm4t(bl, of64.at(kb, np) + R::pl);
+          mma_f16(X[2 * np], od[kb], bh[0], bh[1]);
+          mma_f16(X[2 * np + 1], od[kb], bh[2], bh[3]);
+          mma_f16(X[2 * np], od[kb], bl[0], bl[1]);
+          mma_f16(X[2 * np + 1], od[kb], bl[2], bl[3]);
+        }
+    }
+    // du^T = dU^T T
+    top = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) top = max_tile(X[nt], top);
+    const Pow2 pr = pow2_scale(warp_max(top));
+    float U[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) U[i][e] = 0.0f;
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+      uint32_t hi[4], lo[4];
+      split_a(X[2 * kb], X[2 * kb + 1], splat(pr.s), splat(pr.s), hi, lo);
+#pragma unroll
+      for (int np = 0; np <= kb; ++np) {
+        uint32_t bh[4], bl[4];
+        ldsm4t(bh, of64.at(kb, np) + R::th);
+        ldsm4t(bl, of64.at(kb, np) + R::tl);
+        mma_f16(U[2 * np], hi, bh[0], bh[1]);
+        mma_f16(U[2 * np + 1], hi, bh[2], bh[3]);
+        mma_f16(U[2 * np], lo, bh[0], bh[1]);
+        mma_f16(U[2 * np + 1], lo, bh[2], bh[3]);
+        mma_f16(U[2 * np], hi, bl[0], bl[1]);
+        mma_f16(U[2 * np + 1], hi, bl[2], bl[3]);
+      }
+    }
+    // du is rf times the sums.  -beta e^G du / key scale into X; the largest of that and of scale e^G dO / query scale
+    const float rf = pr.inv * zf * fac.y;
+    top = 0.0f;
+    float topx = 0.0f, topo = 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt) {
+      const float2 tx = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 8 * nt), splat(-rf));
+      top = max_tile(U[nt], top);
+      set_lo(X[nt], mul2(row_lo(U[nt]), tx));
+      set_hi(X[nt], mul2(row_hi(U[nt]), tx));
+      topx = max_tile(X[nt], topx);
+    }
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = mul2(unpack_h2(od[kb][e]), mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8 * (e >> 1)), splat(pd.inv)));
+        topo = fmaxf(topo, fmaxf(fabsf(x.x), fabsf(x.y)));
+      }
+    top = warp_max(top);
+    const Pow2 pu = pow2_scale(top), pl = pow2_scale(warp_max(fmaxf(topx, topo)));
+    const float asc = fminf(pl.s, tops > 0.0f ? ps.s * scur * 68719476736.0f : __int_as_float(0x7f800000));
+    {
+      const float2 sc = splat(fac.x * (asc * sinv));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) scale_tile(S[nt], sc);
+      scur = asc;
+      sinv = 1.0f / asc;
+    }
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+      uint32_t hi[4], lo[4], qh[4], ql[4];
+      split_a(X[2 * kb], X[2 * kb + 1], splat(asc), splat(asc), hi, lo);
+      const float os = pd.inv * asc;
+      const float2 y0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb), splat(os));
+      const float2 y1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8), splat(os));
+      split2(mul2(unpack_h2(od[kb][0]), y0), qh[0], ql[0]);
+      split2(mul2(unpack_h2(od[kb][1]), y0), qh[1], ql[1]);
+      split2(mul2(unpack_h2(od[kb][2]), y1), qh[2], ql[2]);
+      split2(mul2(unpack_h2(od[kb][3]), y1), qh[3], ql[3]);
+#pragma unroll
+      for (int np = 0; np < D / 16; ++np) {
+        uint32_t bk[4], bq[4];
+        ldsm4t(bk, ofd.at(kb, np) + R::k);
+        ldsm4t(bq, ofd.at(kb, np) + R::q);
+        mma_f16(S[2 * np], hi, bk[0], bk[1]);
+        mma_f16(S[2 * np + 1], hi, bk[2], bk[3]);
+        mma_f16(S[2 * np], lo, bk[0], bk[1]);
+        mma_f16(S[2 * np + 1], lo, bk[2], bk[3]);
+        mma_f16(S[2 * np], qh, bq[0], bq[1]);
+        mma_f16(S[2 * np + 1], qh, bq[2], bq[3]);
+        mma_f16(S[2 * np], ql, bq[0], bq[1]);
+        mma_f16(S[2 * np + 1], ql, bq[2], bq[3]);
+      }
+    }
+    // dv = beta du, and du itself, through this warp's own columns of the dy tile
+    const int len = min(kChunk, p.s.T - n * kChunk);
+    const uint32_t vw = st + L::dy + vofs;
+    const unsigned char *vr = sb + L::dy + vrow;
+    __syncwarp();
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      const float2 b0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokBeta * 64 + 16 * np), splat(rf));
+      const float2 b1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokBeta * 64 + 16 * np + 8), splat(rf));
+      const float2 a = mul2(row_lo(U[2 * np]), b0), bb = mul2(row_lo(U[2 * np + 1]), b1);
+      const float2 cc = mul2(row_hi(U[2 * np]), b0), d = mul2(row_hi(U[2 * np + 1]), b1);
+      const uint32_t o[4] = {pack_io<T>(a.x, a.y), pack_io<T>(bb.x, bb.y), pack_io<T>(cc.x, cc.y), pack_io<T>(d.x, d.y)};
+      stsm4t(vw + 16 * np * L::kRow, o);
+    }
+    __syncwarp();
+    T *dr = dv + (row0 + n * kChunk + (lane >> 1)) * ldc;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (16 * i + (lane >> 1) < len)
+        *reinterpret_cast<uint4 *>(dr + 16 * i * ldc) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
+    __syncwarp();
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      uint32_t r[4];
+      single_a(U[2 * np], U[2 * np + 1], splat(pu.s), splat(pu.s), r);
+      const uint32_t o[4] = {r[0], r[2], r[1], r[3]};
+      stsm4t(vw + 16 * np * L::kRow, o);
+    }
+    __syncwarp();
+    __half *ur = p.w.r16 + (c * 64 + (lane >> 1)) * D + dvw + 8 * (lane & 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4 *>(ur + 16 * i * D) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
+    if (lane == 0) p.w.sr[c * (D / 16) + (dvw >> 4)] = top > 0.0f ? pu.inv * rf : 0.0f;
+    __syncthreads();
+  }
+  if (p.S_out != nullptr) {
+    float *So = p.S_out + static_cast<long long>(head) * D * D;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) So[(8 * nt + 2 * t4 + (e & 1)) * D + dvw + g + (e >> 1) * 8] = S[nt][e] * sinv;
+  }
+}
+
+template <typename T, int D, int W>
+int run(const ChunkArgs &a, cudaStream_t st) {
+  using L = ChainBwdSmem<D, W>;
+  auto kern = delta_chain_bwd_kernel<T, D, W>;
+  const int rc = runtime_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total));
+  if (rc) return rc;
+  kern<<<static_cast<unsigned>(a.s.B) * a.s.H * (D / (16 * W)), W * 32, L::total, st>>>(a);
+  return runtime_status(cudaGetLastError());
+}
+
+template <typename T>
+int by_d(const ChunkArgs &a, cudaStream_t st) {
+  switch (a.s.D) {
+    case 32: return run<T, 32, 2>(a, st);
+    case 64: return run<T, 64, 4>(a, st);
+    case 128: return chain_splits(a.s.B * a.s.H) ? run<T, 128, 4>(a, st) : run<T, 128, 8>(a, st);
+    default: return ESA_ERR_UNSUPPORTED;
+  }
+}
+
+}  // namespace
+
+int launch_chunk_bwd(int dtype, const ChunkArgs &a, cudaStream_t st) {
+  return dtype == ESA_F16 ? by_d<__half>(a, st) : by_d<__nv_bfloat16>(a, st);
+}
+
+}  // namespace esa

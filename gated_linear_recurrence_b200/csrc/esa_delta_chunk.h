@@ -1,0 +1,73 @@
+// esa_delta_chunk.h -- the chunked gated delta rule: its arrays in the
+// workspace and the launches.  Internal to the library.
+//
+// A head's sequence is cut into chunks of 64 tokens (the last one padded with
+// tokens that neither write nor forget).  Chunk c = head * nc + n, head =
+// b H + h, has a record of ChunkRecord<D>::bytes bytes, written by the first
+// kernel in the order and with the swizzle in which later kernels hold it in
+// shared memory, so that a copy of it is linear:
+//   tok    [kTokRows][64] float32  per-token factors (rows below)
+//   fac    [4] float32             e^{G_last}, 1/scale of T, 1/scale of P, unused
+//   k, q   [64][D] float16         keys and queries, each row scaled by a power of two (exact)
+//   th, tl [64][64] float16        two terms of T = (1 + M)^-1, scaled by one power of two
+//   ph, pl [64][64] float16        two terms of P_ij = e^{Gi-Gj} q_i.k_j (j <= i), scaled likewise
+//   g      [2][64] float32         running sums of log alpha, two terms
+// and, kept for the backward or written by it,
+//   u16, r16   [64][D] float16     u and du (token rows), one power of two per 16 channels
+//   s16, ds16  [D][D] float16      state entering the chunk and gradient of the state leaving it
+//                                  (row: value channel), one power of two per 16 rows
+//   su, sr, ss, sds [D/16] float32 inverses of those powers of two (0 for a group of zeros)
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+
+#include "esa_delta.h"
+
+namespace esa {
+
+constexpr int kChunk = 64;
+enum { kTokBeta = 0, kTokX = 1, kTokL = 2, kTokY = 3, kTokK = 4, kTokQ = 5, kTokRows = 6 };
+//   kTokBeta  beta (NaN where the key is not finite: the token poisons what follows it)
+//   kTokX     beta e^G / key scale          (what the state's prediction K16 S is multiplied by)
+//   kTokL     e^{G_last - G} / key scale    (what u is multiplied by before it is added to the state)
+//   kTokY     scale e^G / query scale       (NaN where the query is not finite)
+//   kTokK, kTokQ  1 / key scale, 1 / query scale
+
+template <int D>
+struct ChunkRecord {
+  static constexpr int tok = 0, fac = kTokRows * 64 * 4, k = fac + 128, q = k + 64 * D * 2, th = q + 64 * D * 2,
+                       tl = th + 8192, ph = tl + 8192, pl = ph + 8192, g = pl + 8192, bytes = g + 512;
+};
+
+struct ChunkArrays {
+  unsigned char *rec;
+  __half *u16, *r16, *s16, *ds16;
+  float *su, *sr, *ss, *sds;
+  int nc;
+};
+
+struct ChunkArgs {
+  DeltaShape s;
+  ChunkArrays w;
+  const void *q, *k, *v, *a, *b, *dy;
+  void *y, *dq, *dk, *dv, *da, *db;
+  const float *S_in;   // S_init, or dS_final for the backward chain
+  float *S_out;        // S_final, or dS_init
+  bool keep;
+};
+
+int launch_chunk_prep(int dtype, const ChunkArgs &a, cudaStream_t st);
+int launch_chunk_fwd(int dtype, const ChunkArgs &a, cudaStream_t st);
+int launch_chunk_bwd(int dtype, const ChunkArgs &a, cudaStream_t st);    // dv, dS_init, du
+int launch_chunk_grad(int dtype, const ChunkArgs &a, cudaStream_t st);   // dq, dk, da, db
+
+// Whether the two chain kernels cut a head of 128 channels over two blocks of
+// four warps: while that gives no SM more than one block, every warp has an SM
+// quarter to itself (16 heads: 129 us a pass of 32 chunks against 205 with
+// eight warps in one SM; 128 heads: 263 against 215 the other way).
+bool chain_splits(int heads);
+
+}  // namespace esa

@@ -1,0 +1,184 @@
+// esa_mma.cuh -- warp-level helpers of the chunked gated delta rule: matrix
+// fragments in registers, swizzled shared-memory tiles, and the splitting of
+// float32 values into scaled float16 terms (sm_100a).
+//
+// Fragments are those of mma.m16n8k16: with g = lane / 4 and t = lane % 4, an
+// accumulator holds (row g, columns 2t, 2t+1) and (row g + 8, the same); an A
+// operand holds rows g and g + 8 of columns 2t, 2t+1 and 2t+8, 2t+9.  So two
+// neighbouring accumulators are the A operand of the next product without any
+// exchange between lanes.
+//
+// A float32 value x is kept as two float16 terms of x s, with s a power of two
+// that brings the largest |x| of its group to [2^12, 2^13): hi = fp16(x s),
+// lo = fp16(x s - hi).  The two carry 22 bits (an absolute error of at most
+// 2^-37 of the group's largest value for its small elements), and a product
+// with an exact float16 operand is two mma with one accumulator.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "esa_common.cuh"
+
+namespace esa {
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+// Byte offset of 16-byte unit `c` of row `row` in a tile of RB-byte rows.  The
+// units are permuted so that the 8 rows of one matrix of an ldmatrix fall
+// into different banks.
+template <int RB>
+__device__ __forceinline__ uint32_t tile_off(int row, int c) {
+  if constexpr (RB >= 128) return row * RB + ((c ^ (row & 7)) << 4);
+  else if constexpr (RB == 64) return row * RB + ((c ^ ((row >> 1) & 3)) << 4);
+  else return row * RB + ((c ^ ((row >> 2) & 1)) << 4);
+}
+
+// Address for ldmatrix.x4 of the 16 x 16 block at (row0, col0): matrices in
+// the order (rows 0-7, cols 0-7), (rows 8-15, cols 0-7), (rows 0-7, cols
+// 8-15), (rows 8-15, cols 8-15) -- the order of an A operand (plain), or of
+// an A operand's transpose when loaded with .trans and read as [0,2,1,3].
+template <int RB>
+__device__ __forceinline__ uint32_t block_addr(uint32_t tile, int row0, int col0, int lane) {
+  return tile + tile_off<RB>(row0 + (lane & 15), (col0 >> 3) + (lane >> 4));
+}
+
+__device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+__device__ __forceinline__ uint32_t pack_h2(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Pair of I/O elements packed in 32 bits -> floats, and back.
+template <typename T> __device__ __forceinline__ float2 unpack_io(uint32_t v);
+template <> __device__ __forceinline__ float2 unpack_io<__half>(uint32_t v) { return unpack_h2(v); }
+template <> __device__ __forceinline__ float2 unpack_io<__nv_bfloat16>(uint32_t v) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v));
+}
+template <typename T> __device__ __forceinline__ uint32_t pack_io(float x, float y);
+template <> __device__ __forceinline__ uint32_t pack_io<__half>(float x, float y) { return pack_h2(x, y); }
+template <> __device__ __forceinline__ uint32_t pack_io<__nv_bfloat16>(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Power of two that brings `top` (>= 0) to [2^12, 2^13), and its inverse;
+// 1 for zero, and bounded so that both are normal numbers.
+struct Pow2 {
+  float s, inv;
+};
+__device__ __forceinline__ Pow2 pow2_scale(float top) {
+  int e = static_cast<int>(__float_as_uint(top) >> 23) - 12;      // biased exponent of top / 2^12
+  e = top > 0.0f ? max(1, min(e, 253)) : 127;
+  return {__uint_as_float(static_cast<uint32_t>(254 - e) << 23), __uint_as_float(static_cast<uint32_t>(e) << 23)};
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// hi and lo terms of an already scaled pair.  hi - x is one mixed-precision
+// subtraction (exact), its sign goes into the second conversion.
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
+  hi = pack_h2(x.x, x.y);
+  unsigned short h0, h1;
+  float d0, d1;
+  asm("mov.b32 {%0, %1}, %2;" : "=h"(h0), "=h"(h1) : "r"(hi));
+  asm("sub.rn.f32.f16 %0, %1, %2;" : "=f"(d0) : "h"(h0), "f"(x.x));
+  asm("sub.rn.f32.f16 %0, %1, %2;" : "=f"(d1) : "h"(h1), "f"(x.y));
+  lo = pack_h2(-d0, -d1);
+}
+
+// An accumulator tile's two rows, as pairs.
+__device__ __forceinline__ float2 row_lo(const float (&c)[4]) { return make_float2(c[0], c[1]); }
+__device__ __forceinline__ float2 row_hi(const float (&c)[4]) { return make_float2(c[2], c[3]); }
+__device__ __forceinline__ void set_lo(float (&c)[4], float2 x) { c[0] = x.x; c[1] = x.y; }
+__device__ __forceinline__ void set_hi(float (&c)[4], float2 x) { c[2] = x.x; c[3] = x.y; }
+__device__ __forceinline__ void scale_tile(float (&c)[4], float2 s) {
+  set_lo(c, mul2(row_lo(c), s));
+  set_hi(c, mul2(row_hi(c), s));
+}
+__device__ __forceinline__ float max_tile(const float (&c)[4], float top) {
+  top = fmaxf(fmaxf(top, fabsf(c[0])), fabsf(c[1]));
+  return fmaxf(fmaxf(top, fabsf(c[2])), fabsf(c[3]));
+}
+
+// A operand (hi and lo terms, or hi alone) of columns 16 k .. 16 k + 15 from
+// the accumulators of tiles 2 k and 2 k + 1, whose columns are multiplied by
+// s0 and s1 first.
+__device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], float2 s0, float2 s1,
+                                        uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  split2(mul2(row_lo(c0), s0), hi[0], lo[0]);
+  split2(mul2(row_hi(c0), s0), hi[1], lo[1]);
+  split2(mul2(row_lo(c1), s1), hi[2], lo[2]);
+  split2(mul2(row_hi(c1), s1), hi[3], lo[3]);
+}
+__device__ __forceinline__ uint32_t pack2(float2 x) { return pack_h2(x.x, x.y); }
+__device__ __forceinline__ void single_a(const float (&c0)[4], const float (&c1)[4], float2 s0, float2 s1,
+                                         uint32_t (&hi)[4]) {
+  hi[0] = pack2(mul2(row_lo(c0), s0));
+  hi[1] = pack2(mul2(row_hi(c0), s0));
+  hi[2] = pack2(mul2(row_lo(c1), s1));
+  hi[3] = pack2(mul2(row_hi(c1), s1));
+}
+
+// A lane's offsets for ldmatrix.x4 of 16 x 16 blocks of a tile of RB-byte
+// rows: block (16 i, 16 j) is at off[j % 4] + 128 (j / 4) + 16 i RB, so a whole
+// chunk's fragment loads are a few registers and immediate offsets.
+template <int RB>
+struct LaneOff {
+  static constexpr int N = RB >= 128 ? 4 : RB / 32;
+  uint32_t o[N];
+  __device__ __forceinline__ explicit LaneOff(int lane, uint32_t base = 0) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = base + tile_off<RB>(lane & 15, 2 * j + (lane >> 4));
+  }
+  __device__ __forceinline__ uint32_t at(int i, int j) const { return o[j % N] + 128 * (j / 4) + 16 * i * RB; }
+};
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async16_s(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Copy BYTES contiguous bytes to shared memory with all THREADS threads.
+template <int BYTES, int THREADS>
+__device__ __forceinline__ void copy_linear(uint32_t dst, const unsigned char *src) {
+  constexpr int U = BYTES / 16;
+  const uint32_t d = dst + threadIdx.x * 16;
+  const unsigned char *s = src + threadIdx.x * 16;
+#pragma unroll
+  for (int i = 0; i < U / THREADS; ++i) cp_async16_s(d + i * THREADS * 16, s + i * THREADS * 16);
+  if constexpr (U % THREADS != 0)
+    if (threadIdx.x < U % THREADS) cp_async16_s(d + U / THREADS * THREADS * 16, s + U / THREADS * THREADS * 16);
+}
+
+}  // namespace esa
