@@ -38,15 +38,12 @@ ChunkArrays chunk_arrays(unsigned char *base, const DeltaShape &s, bool keep, si
   const size_t rec = s.D == 32 ? ChunkRecord<32>::bytes : s.D == 64 ? ChunkRecord<64>::bytes : ChunkRecord<128>::bytes;
   w.rec = take(n * rec);
   if (keep) {
-    const size_t D = s.D, groups = up256(n * (D / 16) * sizeof(float));
+    const size_t D = s.D;
     w.u16 = reinterpret_cast<__half *>(take(n * 64 * D * 2));
     w.r16 = reinterpret_cast<__half *>(take(n * 64 * D * 2));
     w.s16 = reinterpret_cast<__half *>(take(n * D * D * 2));
     w.ds16 = reinterpret_cast<__half *>(take(n * D * D * 2));
-    w.su = reinterpret_cast<float *>(take(groups));
-    w.sr = reinterpret_cast<float *>(take(groups));
-    w.ss = reinterpret_cast<float *>(take(groups));
-    w.sds = reinterpret_cast<float *>(take(groups));
+    w.slice = reinterpret_cast<float *>(take(n * 32 * sizeof(float)));
   }
   *total = o;
   return w;

@@ -134,7 +134,8 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     __syncthreads();
     const uint32_t st = s0 + buf * L::stage;
     const LaneOff<D * 2> ofd(lane, st);        // tiles of keys and queries
-    const LaneOff<128> of64(lane, st);         // T and P
+    const LaneOffB<D * 2> ofb(lane, st);       // the same as [token][channel] B operands
+    const LaneOffB<128> of64(lane, st);        // T and P
     const unsigned char *sb = smem + buf * L::stage;
     const float *tok = reinterpret_cast<const float *>(sb + R::tok) + 2 * t4;
     const float4 fac = *reinterpret_cast<const float4 *>(sb + R::fac);
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     const float tops = warp_max(top);
     const Pow2 ps = pow2_scale(tops);
     const float xinv = ps.inv * sinv;
-    if (KEEP && lane == 0) p.w.ss[c * (D / 16) + (dvw >> 4)] = tops > 0.0f ? xinv : 0.0f;
+    if (KEEP && lane == 0) p.w.slice[c * 32 + kSliceS + (dvw >> 4)] = tops > 0.0f ? xinv : 0.0f;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint32_t hi[4], lo[4];
@@ -167,17 +168,17 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
         uint32_t bk[4], bq[4];
-        ldsm4(bk, ofd.at(np, ks) + R::k);
-        ldsm4(bq, ofd.at(np, ks) + R::q);
-        mma_f16(X[2 * np], hi, bk[0], bk[2]);
-        mma_f16(X[2 * np + 1], hi, bk[1], bk[3]);
-        mma_f16(Y[2 * np], hi, bq[0], bq[2]);
-        mma_f16(Y[2 * np + 1], hi, bq[1], bq[3]);
-        mma_f16(X[2 * np], lo, bk[0], bk[2]);
-        mma_f16(X[2 * np + 1], lo, bk[1], bk[3]);
+        ldsm4(bk, ofb.at(np, ks) + R::k);
+        ldsm4(bq, ofb.at(np, ks) + R::q);
+        mma_f16(X[2 * np], hi, bk[0], bk[1]);
+        mma_f16(X[2 * np + 1], hi, bk[2], bk[3]);
+        mma_f16(Y[2 * np], hi, bq[0], bq[1]);
+        mma_f16(Y[2 * np + 1], hi, bq[2], bq[3]);
+        mma_f16(X[2 * np], lo, bk[0], bk[1]);
+        mma_f16(X[2 * np + 1], lo, bk[2], bk[3]);
         if constexpr (kTwo) {
-          mma_f16(Y[2 * np], lo, bq[0], bq[2]);
-          mma_f16(Y[2 * np + 1], lo, bq[1], bq[3]);
+          mma_f16(Y[2 * np], lo, bq[0], bq[1]);
+          mma_f16(Y[2 * np + 1], lo, bq[2], bq[3]);
         }
       }
     }
@@ -228,12 +229,12 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
         uint32_t bh[4], bl[4];
         ldsm4(bh, of64.at(np, kb) + R::th);
         ldsm4(bl, of64.at(np, kb) + R::tl);
-        mma_f16(U[2 * np], hi, bh[0], bh[2]);
-        mma_f16(U[2 * np + 1], hi, bh[1], bh[3]);
-        mma_f16(U[2 * np], lo, bh[0], bh[2]);
-        mma_f16(U[2 * np + 1], lo, bh[1], bh[3]);
-        mma_f16(U[2 * np], hi, bl[0], bl[2]);
-        mma_f16(U[2 * np + 1], hi, bl[1], bl[3]);
+        mma_f16(U[2 * np], hi, bh[0], bh[1]);
+        mma_f16(U[2 * np + 1], hi, bh[2], bh[3]);
+        mma_f16(U[2 * np], lo, bh[0], bh[1]);
+        mma_f16(U[2 * np + 1], lo, bh[2], bh[3]);
+        mma_f16(U[2 * np], hi, bl[0], bl[1]);
+        mma_f16(U[2 * np + 1], hi, bl[2], bl[3]);
       }
     }
     // U is uf times the sums; U e^{G_last - G} / key scale into X
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       for (int nt = 0; nt < 8; ++nt)
         scale_tile(Y[nt], mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 8 * nt), splat(r)));
     }
-    if (KEEP && lane == 0) p.w.su[c * (D / 16) + (dvw >> 4)] = top > 0.0f ? uinv : 0.0f;
+    if (KEEP && lane == 0) p.w.slice[c * 32 + kSliceU + (dvw >> 4)] = top > 0.0f ? uinv : 0.0f;
     uint32_t uh[4][4];
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
@@ -295,11 +296,11 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       for (int np = kb; np < 4; ++np) {
         uint32_t bp[4];
         ldsm4(bp, of64.at(np, kb) + R::ph);
-        mma_f16(Y[2 * np], uh[kb], bp[0], bp[2]);
-        mma_f16(Y[2 * np + 1], uh[kb], bp[1], bp[3]);
+        mma_f16(Y[2 * np], uh[kb], bp[0], bp[1]);
+        mma_f16(Y[2 * np + 1], uh[kb], bp[2], bp[3]);
         if constexpr (kTwo) {
-          mma_f16(Y[2 * np], ul, bp[0], bp[2]);
-          mma_f16(Y[2 * np + 1], ul, bp[1], bp[3]);
+          mma_f16(Y[2 * np], ul, bp[0], bp[1]);
+          mma_f16(Y[2 * np + 1], ul, bp[2], bp[3]);
         }
       }
     }

@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     __syncthreads();
     const uint32_t st = s0 + buf * L::stage;
     const LaneOff<D * 2> ofd(lane, st);
+    const LaneOffB<D * 2> ofb(lane, st);
     const LaneOff<128> of64(lane, st);
     const unsigned char *sb = smem + buf * L::stage;
     const float *tok = reinterpret_cast<const float *>(sb + R::tok) + 2 * t4;
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     const float tops = warp_max(top);
     const Pow2 ps = pow2_scale(tops);
     const float xinv = ps.inv * sinv;
-    if (lane == 0) p.w.sds[c * (D / 16) + (dvw >> 4)] = tops > 0.0f ? xinv : 0.0f;
+    if (lane == 0) p.w.slice[c * 32 + kSliceDs + (dvw >> 4)] = tops > 0.0f ? xinv : 0.0f;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint32_t hi[4], lo[4];
@@ -127,11 +128,11 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
         uint32_t bk[4];
-        ldsm4(bk, ofd.at(np, ks) + R::k);
-        mma_f16(X[2 * np], hi, bk[0], bk[2]);
-        mma_f16(X[2 * np + 1], hi, bk[1], bk[3]);
-        mma_f16(X[2 * np], lo, bk[0], bk[2]);
-        mma_f16(X[2 * np + 1], lo, bk[1], bk[3]);
+        ldsm4(bk, ofb.at(np, ks) + R::k);
+        mma_f16(X[2 * np], hi, bk[0], bk[1]);
+        mma_f16(X[2 * np + 1], hi, bk[2], bk[3]);
+        mma_f16(X[2 * np], lo, bk[0], bk[1]);
+        mma_f16(X[2 * np + 1], lo, bk[2], bk[3]);
       }
     }
     // dO^T as an A operand, scaled to float16
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<uint4 *>(ur + 16 * i * D) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
-    if (lane == 0) p.w.sr[c * (D / 16) + (dvw >> 4)] = top > 0.0f ? pu.inv * rf : 0.0f;
+    if (lane == 0) p.w.slice[c * 32 + kSliceR + (dvw >> 4)] = top > 0.0f ? pu.inv * rf : 0.0f;
     __syncthreads();
   }
   if (p.S_out != nullptr) {

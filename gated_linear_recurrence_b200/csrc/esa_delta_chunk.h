@@ -16,7 +16,7 @@
 //   u16, r16   [64][D] float16     u and du (token rows), one power of two per 16 channels
 //   s16, ds16  [D][D] float16      state entering the chunk and gradient of the state leaving it
 //                                  (row: value channel), one power of two per 16 rows
-//   su, sr, ss, sds [D/16] float32 inverses of those powers of two (0 for a group of zeros)
+//   slice      [4][8] float32      inverses of those powers of two (0 for a group of zeros)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -42,10 +42,12 @@ struct ChunkRecord {
                        tl = th + 8192, ph = tl + 8192, pl = ph + 8192, g = pl + 8192, bytes = g + 512;
 };
 
+enum { kSliceU = 0, kSliceR = 8, kSliceS = 16, kSliceDs = 24 };   // rows of `slice`
+
 struct ChunkArrays {
   unsigned char *rec;
   __half *u16, *r16, *s16, *ds16;
-  float *su, *sr, *ss, *sds;
+  float *slice;
   int nc;
 };
 

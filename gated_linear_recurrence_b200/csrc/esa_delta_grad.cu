@@ -10,16 +10,21 @@
 //   db = (du.u)(1 - beta),
 //   da_i = (1 - alpha_i)(c + sum_{s >= i} (q_s.dq_s - beta_s v_s.du_s)),
 //   c = <dS, S leaving> = e^{G_last} <dS, S> + sum_j k_j.(e^{G_last - G_j} u_j dS^T).
-// Sums of the gate's gradient start anew in every chunk, from c.
+// The triangular system gives beta_i v_i = u_i + sum_j M_ij u_j + beta_i e^{Gi} S^T k_i,
+// so beta_i v_i.du_i = u_i.du_i - k_i.(N K - beta e^G du S^T)_i comes from terms
+// that are at hand and v is not read.  <dS, S> is the diagonal of dS S^T, 16
+// rows at a time, on the tensor cores too.  Sums of the gate's gradient start
+// anew in every chunk, from c.
 //
 // These are outputs in 16 bits: S, dS, U, du, dP and N are operands in one
 // float16 term each (2^-12 of a value on average, against 2^-9 for a bfloat16
-// output and 2^-12 for a float16 one).  Tiles whose rows or channel groups
-// have powers of two of their own are brought to one per tile first.
+// output and 2^-12 for a float16 one).
 //
-// One block of 8 warps per chunk and head: warp (m, half) has 16 tokens and
-// half of the channels.  About 2,500 mma at D = 128 against 190 KB read and
-// written, so memory traffic and mma bound it alike.
+// A persistent block takes chunk after chunk.  Warp (m, cw) has 16 tokens and
+// a share of the channels.  U, du and dO of the next chunk are copied while
+// this one is computed (two buffers), its S and dS as soon as this one's have
+// been used, then its K and Q; so copies of 190 KB a chunk (D = 128) run under
+// 2,500 mma.
 #include "esa_delta_chunk.h"
 #include "esa_delta_sweep.cuh"
 #include "esa_mma.cuh"
@@ -30,23 +35,17 @@
 namespace esa {
 namespace {
 
-constexpr int kThreads = 256;
-
 template <int D>
-struct GradSmem {
+struct GradShape {
+  static constexpr int threads = D == 128 ? 512 : 256;
+  static constexpr int CW = threads / 128;          // shares of the channels
   static constexpr int row = 64 * D * 2, mat = D * D * 2;
-  static constexpr int k = 0, q = row, u = 2 * row, r = 3 * row, o = 4 * row, s = 5 * row, ds = s + mat, dp = ds + mat,
-                       n = dp + 8192, vec = n + 8192, total = vec + 13 * 64 * 4 + 128;
+  static constexpr int hdr = ChunkRecord<D>::k + 512 + 128;   // per-token factors, running sums, slice scales
+  static constexpr int k = 0, q = row, s = 2 * row, ds = s + mat, dp = ds + mat, n = dp + 8192, buf = n + 8192,
+                       u = 0, r = row, o = 2 * row, h = 3 * row, stage = 3 * row + hdr, vec = buf + 2 * stage,
+                       total = vec + (64 + 64 + 3 * CW * 64 + 64) * 4;
 };
 
-// Rows of 16-byte units of a plain [rows][D] float16 array into a swizzled tile.
-template <int D>
-__device__ __forceinline__ void fetch_tile(uint32_t dst, const __half *src, int rows) {
-  constexpr int U = D / 8;
-  for (int i = threadIdx.x; i < rows * U; i += kThreads) cp_async16_s(dst + tile_off<D * 2>(i / U, i % U), src + i * 8);
-}
-
-// Multiply unit (row, unit) of a tile by f, a power of two of at most 1.
 __device__ __forceinline__ void scale_unit(unsigned char *p, float f) {
   uint4 v = *reinterpret_cast<uint4 *>(p);
   __half2 *h = reinterpret_cast<__half2 *>(&v);
@@ -55,396 +54,446 @@ __device__ __forceinline__ void scale_unit(unsigned char *p, float f) {
   for (int i = 0; i < 4; ++i) h[i] = __hmul2(h[i], s);
   *reinterpret_cast<uint4 *>(p) = v;
 }
-
-// Largest of n (<= 64) positive factors, seen by every thread.
-__device__ __forceinline__ float factor_top(const float *f, int n) {
-  float x = 0.0f;
-  for (int i = threadIdx.x & 31; i < n; i += 32) x = fmaxf(x, f[i]);
-  x = warp_max(x);
-  return x > 0.0f ? x : 1.0f;
+__device__ __forceinline__ void scale_frag(uint32_t (&a)[4], float f) {
+  const __half2 s = __float2half2_rn(f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&a[i]), s);
+    a[i] = *reinterpret_cast<const uint32_t *>(&x);
+  }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) delta_grad_kernel(ChunkArgs p) {
-  using L = GradSmem<D>;
+__global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(ChunkArgs p, int chunks) {
+  using L = GradShape<D>;
   using R = ChunkRecord<D>;
-  constexpr int NH = D / 16;      // accumulator tiles of half the channels
-  constexpr int SLC = D / 16;     // channel groups
+  constexpr int kThreads = L::threads, CW = L::CW;
+  constexpr int NH = D / (8 * CW);   // accumulator tiles of a share of the channels
+  constexpr int NPA = 4 / CW;        // 16-column blocks of dP and N a warp forms
+  constexpr int KS = D / 16;
   extern __shared__ __align__(128) unsigned char smem[];
   float *vec = reinterpret_cast<float *>(smem + L::vec);
-  float *G = vec, *Gl = vec + 64, *beta = vec + 128, *kf = vec + 192, *qf = vec + 256, *oinv = vec + 320;
-  float *qdq = vec + 384, *wk = vec + 512, *vdu = vec + 640, *udu = vec + 704, *red = vec + 768;   // qdq, wk: two halves
+  float *oinv = vec, *udu = vec + 64, *qdq = vec + 128, *wk = qdq + CW * 64, *zk = wk + CW * 64, *red = zk + CW * 64;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  const long long c = blockIdx.x;
-  const int head = static_cast<int>(c / p.w.nc), n = static_cast<int>(c - static_cast<long long>(head) * p.w.nc);
-  const int b = head / p.s.H, h = head - b * p.s.H;
-  const int t0 = n * kChunk, len = min(kChunk, p.s.T - t0);
-  const long long row = static_cast<long long>(b) * p.s.T + t0, ldc = static_cast<long long>(p.s.H) * D;
-  const unsigned char *rec = p.w.rec + c * R::bytes;
+  const int m = warp & 3, cw = warp >> 2;
+  const long long ldc = static_cast<long long>(p.s.H) * D;
   const uint32_t s0 = smem_u32(smem);
-  const float *tokg = reinterpret_cast<const float *>(rec + R::tok);
 
-  copy_linear<2 * L::row, kThreads>(s0 + L::k, rec + R::k);   // keys and queries, swizzled already
-  fetch_tile<D>(s0 + L::u, p.w.u16 + c * (64 * D), 64);
-  fetch_tile<D>(s0 + L::r, p.w.r16 + c * (64 * D), 64);
-  sweep::cp_async_commit();
-  fetch_tile<D>(s0 + L::s, p.w.s16 + c * (D * D), D);
-  sweep::cp_async_commit();
-  fetch_tile<D>(s0 + L::ds, p.w.ds16 + c * (D * D), D);
-  sweep::cp_async_commit();
-
-  const float *su = p.w.su + c * SLC, *sr = p.w.sr + c * SLC, *ss = p.w.ss + c * SLC, *sds = p.w.sds + c * SLC;
-  const float uinv = factor_top(su, SLC), rinv = factor_top(sr, SLC), sinv = factor_top(ss, SLC), dsinv = factor_top(sds, SLC);
-  const float ktop = factor_top(tokg + kTokK * 64, 64), qtop = factor_top(tokg + kTokQ * 64, 64);
-  const float last = *reinterpret_cast<const float *>(rec + R::fac);
-  if (tid < 64) {
-    const float *gg = reinterpret_cast<const float *>(rec + R::g);
-    G[tid] = gg[tid];
-    Gl[tid] = gg[64 + tid];
-    beta[tid] = tokg[kTokBeta * 64 + tid];
-    kf[tid] = tokg[kTokK * 64 + tid];
-    qf[tid] = tokg[kTokQ * 64 + tid];
-  }
-  {   // dO, each row to float16 with its own power of two; 8 rows a warp
-    constexpr int LPR = D / 8, RPI = 32 / LPR;
-    const int sub = lane % LPR;
-    const T *dy = static_cast<const T *>(p.dy) + row * ldc + h * D + sub * 8;
+  auto place = [&](int c, int &b, int &h, int &t0) {
+    const int head = c / p.w.nc;
+    b = head / p.s.H;
+    h = head - b * p.s.H;
+    t0 = (c - head * p.w.nc) * kChunk;
+  };
+  auto fetch_rows = [&](int c, int buf) {   // U, du, dO and the header
+    if (c < chunks) {
+      const uint32_t st = s0 + L::buf + buf * L::stage;
+      copy_rows<D * 2, 64, kThreads>(st + L::u, p.w.u16 + static_cast<long long>(c) * (64 * D));
+      copy_rows<D * 2, 64, kThreads>(st + L::r, p.w.r16 + static_cast<long long>(c) * (64 * D));
+      int b, h, t0;
+      place(c, b, h, t0);
+      constexpr int U = D / 8, STEP = kThreads / U;
+      const int r = tid / U, u = tid % U, len = min(kChunk, p.s.T - t0);
+      const T *dy = static_cast<const T *>(p.dy) + (static_cast<long long>(b) * p.s.T + t0) * ldc + h * D + u * 8;
 #pragma unroll
-    for (int i = 0; i < 8 / RPI + (RPI > 8); ++i) {
-      const int rr = 8 * warp + i * RPI + lane / LPR;
-      uint4 raw = make_uint4(0, 0, 0, 0);
-      if (rr < len) raw = *reinterpret_cast<const uint4 *>(dy + rr * ldc);
-      const uint32_t *w = reinterpret_cast<const uint32_t *>(&raw);
-      float2 x[4];
-      float top = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[j] = unpack_io<T>(w[j]);
-        top = fmaxf(top, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
+      for (int i = 0; i < (64 + STEP - 1) / STEP; ++i) {
+        const int rr = r + i * STEP;
+        if (STEP <= 64 || rr < 64)
+          cp_async16_zfill(st + L::o + tile_off<D * 2>(rr, u), rr < len ? dy + rr * ldc : static_cast<const T *>(p.dy), rr < len);
       }
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const Pow2 ps = pow2_scale(top);
-      uint4 ov;
-      uint32_t *ow = reinterpret_cast<uint32_t *>(&ov);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) ow[j] = pack2(mul2(x[j], splat(ps.s)));
-      *reinterpret_cast<uint4 *>(smem + L::o + tile_off<D * 2>(rr, sub)) = ov;
-      if (sub == 0) oinv[rr] = ps.inv;
+      const unsigned char *rec = p.w.rec + static_cast<long long>(c) * R::bytes;
+      if (tid < R::k / 16) cp_async16_s(st + L::h + tid * 16, rec + tid * 16);
+      else if (tid >= 128 && tid < 160) cp_async16_s(st + L::h + R::k + (tid - 128) * 16, rec + R::g + (tid - 128) * 16);
+      else if (tid >= 160 && tid < 168)
+        cp_async16_s(st + L::h + R::k + 512 + (tid - 160) * 16, p.w.slice + static_cast<long long>(c) * 32 + (tid - 160) * 4);
     }
-  }
-  sweep::cp_async_wait<2>();
-  __syncthreads();
-  {   // one power of two per tile
-    constexpr int U = D / 8;
-    for (int i = tid; i < 64 * U; i += kThreads) {
-      const int rr = i / U, uu = i % U;
-      const uint32_t o = tile_off<D * 2>(rr, uu);
-      scale_unit(smem + L::k + o, kf[rr] / ktop);
-      scale_unit(smem + L::q + o, qf[rr] / qtop);
-      scale_unit(smem + L::u + o, su[uu >> 1] / uinv);
-      scale_unit(smem + L::r + o, sr[uu >> 1] / rinv);
+    sweep::cp_async_commit();
+  };
+  auto fetch_states = [&](int c) {
+    if (c < chunks) {
+      copy_rows<D * 2, D, kThreads>(s0 + L::s, p.w.s16 + static_cast<long long>(c) * (D * D));
+      copy_rows<D * 2, D, kThreads>(s0 + L::ds, p.w.ds16 + static_cast<long long>(c) * (D * D));
     }
-  }
-  __syncthreads();
+    sweep::cp_async_commit();
+  };
+  auto fetch_keys = [&](int c) {
+    if (c < chunks) copy_linear<2 * L::row, kThreads>(s0 + L::k, p.w.rec + static_cast<long long>(c) * R::bytes + R::k);
+    sweep::cp_async_commit();
+  };
 
-  const int m = warp & 3, half = warp >> 2;
   const LaneOff<D * 2> ofd(lane, s0);
+  const LaneOffB<D * 2> ofb(lane, s0);
   const LaneOff<128> of64(lane, s0);
   const int i0 = 16 * m + g;   // this thread's token rows: i0, i0 + 8
-  {   // dP and N: columns 32 half .. 32 half + 31
-    float P[4][4], N[4][4];
+  int it = 0;
+  fetch_rows(blockIdx.x, 0);
+  fetch_states(blockIdx.x);
+  fetch_keys(blockIdx.x);
+#pragma unroll 1
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x, ++it) {
+    const int buf = it & 1, next = c + gridDim.x;
+    int b, h, t0;
+    place(c, b, h, t0);
+    const int len = min(kChunk, p.s.T - t0);
+    const long long row = static_cast<long long>(b) * p.s.T + t0;
+    const uint32_t bo = L::buf + buf * L::stage;
+    unsigned char *sb = smem + bo;
+    const float *tok = reinterpret_cast<const float *>(sb + L::h);
+    const float *G = reinterpret_cast<const float *>(sb + L::h + R::k), *Gl = G + 64;
+    sweep::cp_async_wait<2>();   // rows of this chunk
+    __syncthreads();
+    fetch_rows(next, buf ^ 1);
+    // dO, each row to float16 with its own power of two
+    {
+      constexpr int U = D / 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 64 * U / kThreads; ++i) {
+        const int e = tid + i * kThreads, rr = e / U;
+        unsigned char *at = sb + L::o + tile_off<D * 2>(rr, e % U);
+        uint4 raw = *reinterpret_cast<const uint4 *>(at);
+        uint32_t *w = reinterpret_cast<uint32_t *>(&raw);
+        float top = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) P[i][e] = N[i][e] = 0.0f;
-    if (2 * half <= m) {
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = unpack_io<T>(w[j]);
+          top = fmaxf(fmaxf(top, fabsf(x.x)), fabsf(x.y));
+        }
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t ao[4], ar[4];
-        ldsm4(ao, ofd.at(0, ks) + L::o + 16 * m * D * 2);
-        ldsm4(ar, ofd.at(0, ks) + L::r + 16 * m * D * 2);
+        for (int o = U / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const Pow2 ps = pow2_scale(top);
 #pragma unroll
-        for (int np = 0; np < 2; ++np) {
-          if (2 * half + np > m) continue;
-          uint32_t bu[4];
-          ldsm4(bu, ofd.at(np, ks) + L::u + 32 * half * D * 2);
-          mma_f16(P[2 * np], ao, bu[0], bu[2]);
-          mma_f16(P[2 * np + 1], ao, bu[1], bu[3]);
-          mma_f16(N[2 * np], ar, bu[0], bu[2]);
-          mma_f16(N[2 * np + 1], ar, bu[1], bu[3]);
+        for (int j = 0; j < 4; ++j) w[j] = pack2(mul2(unpack_io<T>(w[j]), splat(ps.s)));
+        *reinterpret_cast<uint4 *>(at) = raw;
+        if (e % U == 0) oinv[rr] = ps.inv;
+      }
+    }
+    // slice scales: the largest of each kind, and what each slice has of it (1 almost always)
+    float part, uinv, rinv, sinv, dsinv;
+    bool flat;
+    {
+      const float v = (lane & 7) < KS ? reinterpret_cast<const float *>(sb + L::h + R::k + 512)[lane] : 0.0f;
+      float t = v;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+      if (!(t > 0.0f)) t = 1.0f;
+      part = v > 0.0f ? v / t : 1.0f;
+      flat = __all_sync(0xffffffffu, part == 1.0f);
+      uinv = __shfl_sync(0xffffffffu, t, kSliceU);
+      rinv = __shfl_sync(0xffffffffu, t, kSliceR);
+      sinv = __shfl_sync(0xffffffffu, t, kSliceS);
+      dsinv = __shfl_sync(0xffffffffu, t, kSliceDs);
+    }
+    float ktop, qtop;
+    bool flatk;
+    {
+      const float k0 = tok[kTokK * 64 + lane], k1 = tok[kTokK * 64 + 32 + lane];
+      const float q0 = tok[kTokQ * 64 + lane], q1 = tok[kTokQ * 64 + 32 + lane];
+      ktop = warp_max(fmaxf(k0, k1));
+      qtop = warp_max(fmaxf(q0, q1));
+      if (!(ktop > 0.0f)) ktop = 1.0f;
+      if (!(qtop > 0.0f)) qtop = 1.0f;
+      flatk = __all_sync(0xffffffffu, (k0 == ktop || k0 == 0.0f) && (k1 == ktop || k1 == 0.0f) &&
+                                          (q0 == qtop || q0 == 0.0f) && (q1 == qtop || q1 == 0.0f));
+    }
+    __syncthreads();
+
+    const float be0 = tok[kTokBeta * 64 + i0], be1 = tok[kTokBeta * 64 + i0 + 8];
+    {   // dP and N: 16-column blocks NPA cw ..
+      float P[2 * NPA][4], N[2 * NPA][4];
+#pragma unroll
+      for (int i = 0; i < 2 * NPA; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) P[i][e] = N[i][e] = 0.0f;
+      if (NPA * cw <= m) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t ao[4], ar[4];
+          ldsm4(ao, ofd.at(0, ks) + bo + L::o + 16 * m * D * 2);
+          ldsm4(ar, ofd.at(0, ks) + bo + L::r + 16 * m * D * 2);
+          if (!flat) {
+            const float fu = __shfl_sync(0xffffffffu, part, kSliceU + ks);
+            scale_frag(ao, fu);
+            scale_frag(ar, fu * __shfl_sync(0xffffffffu, part, kSliceR + ks));
+          }
+#pragma unroll
+          for (int np = 0; np < NPA; ++np) {
+            if (NPA * cw + np > m) continue;
+            uint32_t bu[4];
+            ldsm4(bu, ofb.at(np, ks) + bo + L::u + 16 * NPA * cw * D * 2);
+            mma_f16(P[2 * np], ao, bu[0], bu[1]);
+            mma_f16(P[2 * np + 1], ao, bu[2], bu[3]);
+            mma_f16(N[2 * np], ar, bu[0], bu[1]);
+            mma_f16(N[2 * np + 1], ar, bu[2], bu[3]);
+          }
         }
       }
-    }
-    // in the factors under which both enter dK: dP qtop, N ktop
-    float top = 0.0f;
-    float fp[2], fn[2], gi[2], gli[2];
+      // in the factors under which both enter dK: dP qtop, N ktop
+      float top = 0.0f;
+      const float ru = rinv * uinv;
+      float fp[2], fn[2], gi[2], gli[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      fp[e] = p.s.scale * oinv[i0 + 8 * e] * uinv * qtop;
-      fn[e] = -beta[i0 + 8 * e] * rinv * uinv * ktop;
-      gi[e] = G[i0 + 8 * e];
-      gli[e] = Gl[i0 + 8 * e];
-    }
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = i0 + (e >> 1) * 8, j = 32 * half + 8 * nt + 2 * t4 + (e & 1);
-        float d = 0.0f;
-        if (j <= i) d = expf((gi[e >> 1] - G[j]) + (gli[e >> 1] - Gl[j]));
-        P[nt][e] = j <= i ? P[nt][e] * (d * fp[e >> 1]) : 0.0f;
-        N[nt][e] = j < i ? N[nt][e] * (d * fn[e >> 1]) : 0.0f;
-        top = fmaxf(top, fmaxf(fabsf(P[nt][e]), fabsf(N[nt][e])));
+      for (int e = 0; e < 2; ++e) {
+        fp[e] = p.s.scale * oinv[i0 + 8 * e] * uinv * qtop;
+        fn[e] = -(e ? be1 : be0) * ru * ktop;
+        gi[e] = G[i0 + 8 * e];
+        gli[e] = Gl[i0 + 8 * e];
       }
-    top = warp_max(top);
-    if (lane == 0) red[warp] = top;
+#pragma unroll
+      for (int nt = 0; nt < 2 * NPA; ++nt) {
+        const int j0 = 16 * NPA * cw + 8 * nt + 2 * t4;
+        const float2 gj = *reinterpret_cast<const float2 *>(G + j0), glj = *reinterpret_cast<const float2 *>(Gl + j0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = i0 + (e >> 1) * 8, j = j0 + (e & 1);
+          // 16-bit results: the exponential's error of a few 2^-23 times the exponent does not show
+          const float d = __expf((gi[e >> 1] - (e & 1 ? gj.y : gj.x)) + (gli[e >> 1] - (e & 1 ? glj.y : glj.x)));
+          if (i == j) udu[i] = N[nt][e] * ru;
+          P[nt][e] = j <= i ? P[nt][e] * (d * fp[e >> 1]) : 0.0f;
+          N[nt][e] = j < i ? N[nt][e] * (d * fn[e >> 1]) : 0.0f;
+        }
+        top = max_tile(P[nt], max_tile(N[nt], top));
+      }
+      top = warp_max(top);
+      if (lane == 0) red[warp] = top;
+      __syncthreads();
+      top = red[lane & (kThreads / 32 - 1)];
+      const Pow2 pp = pow2_scale(warp_max(top));
+      if (tid == 0) red[32] = pp.inv;
+#pragma unroll
+      for (int nt = 0; nt < 2 * NPA; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const uint32_t o = tile_off<128>(i0 + (e >> 1) * 8, 2 * NPA * cw + nt) + 4 * t4;
+          *reinterpret_cast<uint32_t *>(smem + L::dp + o) = pack_h2(P[nt][e] * pp.s, P[nt][e + 1] * pp.s);
+          *reinterpret_cast<uint32_t *>(smem + L::n + o) = pack_h2(N[nt][e] * pp.s, N[nt][e + 1] * pp.s);
+        }
+    }
+    sweep::cp_async_wait<2>();   // S and dS
     __syncthreads();
-    top = red[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) top = fmaxf(top, red[i]);
-    const Pow2 pp = pow2_scale(top);
-    if (tid == 0) red[8] = pp.inv;
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const uint32_t o = tile_off<128>(i0 + (e >> 1) * 8, 4 * half + nt) + 4 * t4;
-        *reinterpret_cast<uint32_t *>(smem + L::dp + o) = pack_h2(P[nt][e] * pp.s, P[nt][e + 1] * pp.s);
-        *reinterpret_cast<uint32_t *>(smem + L::n + o) = pack_h2(N[nt][e] * pp.s, N[nt][e + 1] * pp.s);
-      }
-  }
-  // v.du and du.u of each token, four threads a row
-  {
-    const int rr = tid >> 2, part = tid & 3;
-    const T *v = static_cast<const T *>(p.v) + (row + rr) * p.s.ld_v + h * D;
-    float a = 0.0f, bb = 0.0f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int uu = part + 4 * i;
-      const uint32_t o = tile_off<D * 2>(rr, uu);
-      const uint4 du = *reinterpret_cast<const uint4 *>(smem + L::r + o), uv = *reinterpret_cast<const uint4 *>(smem + L::u + o);
-      uint4 vv = make_uint4(0, 0, 0, 0);
-      if (rr < len) vv = *reinterpret_cast<const uint4 *>(v + uu * 8);
-      const uint32_t *x = reinterpret_cast<const uint32_t *>(&du), *y = reinterpret_cast<const uint32_t *>(&uv),
-                     *z = reinterpret_cast<const uint32_t *>(&vv);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 d2 = unpack_h2(x[j]), u2 = unpack_h2(y[j]), v2 = unpack_io<T>(z[j]);
-        a = fmaf(d2.x, v2.x, fmaf(d2.y, v2.y, a));
-        bb = fmaf(d2.x, u2.x, fmaf(d2.y, u2.y, bb));
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      bb += __shfl_xor_sync(0xffffffffu, bb, o);
-    }
-    if (part == 0) {
-      vdu[rr] = a * rinv * beta[rr];
-      udu[rr] = bb * rinv * uinv;
-    }
-  }
-  sweep::cp_async_wait<0>();
-  __syncthreads();
-  float inner = 0.0f;   // <dS, S>, this thread's share
-  {
-    constexpr int U = D / 8;
-    for (int i = tid; i < D * U; i += kThreads) {
-      const int rr = i / U, uu = i % U;
-      const uint32_t o = tile_off<D * 2>(rr, uu);
-      scale_unit(smem + L::s + o, ss[rr >> 4] / sinv);
-      scale_unit(smem + L::ds + o, sds[rr >> 4] / dsinv);
-      const uint4 x = *reinterpret_cast<const uint4 *>(smem + L::s + o), y = *reinterpret_cast<const uint4 *>(smem + L::ds + o);
-      const uint32_t *xw = reinterpret_cast<const uint32_t *>(&x), *yw = reinterpret_cast<const uint32_t *>(&y);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 a = unpack_h2(xw[j]), bb = unpack_h2(yw[j]);
-        inner = fmaf(a.x, bb.x, fmaf(a.y, bb.y, inner));
-      }
-    }
-  }
-  inner = head_sum<32>(inner);
-  if (lane == 0) red[16 + warp] = inner;
-  __syncthreads();
 
-  float Qa[NH][4], Ka[NH][4], X[NH][4];
-  const uint32_t cofs = D >= 128 ? 128 * half : 0;             // first column of this half, in swizzled units of 64 columns
-  const int cj = D >= 128 ? 0 : half * (D / 32);               // or as a 16-column block index
-  auto zero = [&] {
+    float Q[NH][4], K[NH][4], X[NH][4];
 #pragma unroll
     for (int i = 0; i < NH; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) X[i][e] = 0.0f;
-  };
-  // X = A B^T with A the token rows of a tile and B stored [value channel][key channel]
-  auto rows_by_state = [&](int a_tile, int s_tile) {
-    zero();
+      for (int e = 0; e < 4; ++e) Q[i][e] = K[i][e] = X[i][e] = 0.0f;
+    // Block index of this warp's channels: NH / 2 blocks from b0 on.  The
+    // offsets of LaneOff repeat every four blocks, so with a share of two
+    // blocks the warp's parity of pairs picks which of them it uses.
+    const bool odd = (NH / 2 == 2) && (cw & 1);
+    const uint32_t far = D == 128 ? (cw >> 1) * 128u : 0u;
+    auto cols = [&](int kb, int np) -> uint32_t {
+      if constexpr (NH / 2 == 2) return (odd ? ofd.at(kb, 2 + np) : ofd.at(kb, np)) + far;
+      else return cw ? ofd.at(kb, 1) : ofd.at(kb, 0);   // D = 32: one block a share
+    };
+    // dO S^T, du S^T and U dS^T; S and dS are stored [value channel][key channel]
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t a[4];
-      ldsm4(a, ofd.at(0, ks) + a_tile + 16 * m * D * 2);
+    for (int ks = 0; ks < KS; ++ks) {
+      uint32_t ao[4], ar[4], au[4];
+      ldsm4(ao, ofd.at(0, ks) + bo + L::o + 16 * m * D * 2);
+      ldsm4(ar, ofd.at(0, ks) + bo + L::r + 16 * m * D * 2);
+      ldsm4(au, ofd.at(0, ks) + bo + L::u + 16 * m * D * 2);
+      if (!flat) {
+        const float fs = __shfl_sync(0xffffffffu, part, kSliceS + ks);
+        scale_frag(ao, fs);
+        scale_frag(ar, fs * __shfl_sync(0xffffffffu, part, kSliceR + ks));
+        scale_frag(au, __shfl_sync(0xffffffffu, part, kSliceU + ks) * __shfl_sync(0xffffffffu, part, kSliceDs + ks));
+      }
 #pragma unroll
       for (int np = 0; np < NH / 2; ++np) {
-        uint32_t bs[4];
-        if constexpr (D >= 128) ldsm4t(bs, ofd.at(ks, np) + s_tile + cofs);
-        else ldsm4t(bs, (cj == 0 ? ofd.at(ks, np) : ofd.at(ks, np + D / 32)) + s_tile);
-        mma_f16(X[2 * np], a, bs[0], bs[1]);
-        mma_f16(X[2 * np + 1], a, bs[2], bs[3]);
+        uint32_t bs[4], bd[4];
+        ldsm4t(bs, cols(ks, np) + L::s);
+        ldsm4t(bd, cols(ks, np) + L::ds);
+        mma_f16(Q[2 * np], ao, bs[0], bs[1]);
+        mma_f16(Q[2 * np + 1], ao, bs[2], bs[3]);
+        mma_f16(K[2 * np], ar, bs[0], bs[1]);
+        mma_f16(K[2 * np + 1], ar, bs[2], bs[3]);
+        mma_f16(X[2 * np], au, bd[0], bd[1]);
+        mma_f16(X[2 * np + 1], au, bd[2], bd[3]);
       }
     }
-  };
-  // X += A B with A a 64 x 64 tile's rows (or its transpose's) and B the token rows of a tile
-  auto mat_by_rows = [&](int a_tile, bool transposed, int b_tile) {
+    if (warp < KS) {   // <dS, S> of 16 rows: the diagonal of dS S^T
+      float d[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[i][e] = 0.0f;
+#pragma unroll
+      for (int kb = 0; kb < KS; ++kb) {
+        uint32_t a[4], bs[4];
+        ldsm4(a, ofd.at(0, kb) + L::ds + 16 * warp * D * 2);
+        ldsm4(bs, ofb.at(0, kb) + L::s + 16 * warp * D * 2);
+        mma_f16(d[0], a, bs[0], bs[1]);
+        mma_f16(d[1], a, bs[2], bs[3]);
+      }
+      float x = 0.0f;
+      if (2 * t4 == g) x = d[0][0] + d[1][2];
+      if (2 * t4 + 1 == g) x = d[0][1] + d[1][3];
+      x = head_sum<32>(x);
+      if (!flat) x *= __shfl_sync(0xffffffffu, part, kSliceS + warp) * __shfl_sync(0xffffffffu, part, kSliceDs + warp);
+      if (lane == 0) red[16 + warp] = x;
+    }
+    __syncthreads();             // S and dS have been used
+    fetch_states(next);
+    sweep::cp_async_wait<2>();   // K and Q
+    __syncthreads();
+    if (!flatk) {                // one power of two for all rows
+      constexpr int U = D / 8;
+      for (int i = tid; i < 64 * U; i += kThreads) {
+        const uint32_t o = tile_off<D * 2>(i / U, i % U);
+        scale_unit(smem + L::k + o, tok[kTokK * 64 + i / U] / ktop);
+        scale_unit(smem + L::q + o, tok[kTokQ * 64 + i / U] / qtop);
+      }
+      __syncthreads();
+    }
+    const float pinv = red[32], ps = 1.0f / pinv;
+    const float fq = pinv * (ktop / qtop);
+    {   // the sums so far, in the units of what joins them
+      const float e0 = expf(G[i0] + Gl[i0]), e1 = expf(G[i0 + 8] + Gl[i0 + 8]);
+      const float fs = p.s.scale * sinv * (1.0f / fq), fk = -rinv * sinv * ps;
+      const float q0 = fs * e0 * oinv[i0], q1 = fs * e1 * oinv[i0 + 8], k0 = fk * be0 * e0, k1 = fk * be1 * e1;
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {
+        set_lo(Q[i], mul2(row_lo(Q[i]), splat(q0)));
+        set_hi(Q[i], mul2(row_hi(Q[i]), splat(q1)));
+        set_lo(K[i], mul2(row_lo(K[i]), splat(k0)));
+        set_hi(K[i], mul2(row_hi(K[i]), splat(k1)));
+      }
+    }
+    // Q += dP K, K += N K
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
-      if (transposed ? kb < m : kb > m) continue;
-      uint32_t a[4];
-      if (!transposed) {
-        ldsm4(a, of64.at(0, kb) + a_tile + 16 * m * 128);
-      } else {
-        uint32_t r[4];
-        ldsm4t(r, s0 + a_tile + tile_off<128>(16 * kb + (lane & 15), 2 * m + (lane >> 4)));
-        a[0] = r[0]; a[1] = r[2]; a[2] = r[1]; a[3] = r[3];
-      }
+      if (kb > m) continue;
+      uint32_t ap[4], an[4];
+      ldsm4(ap, of64.at(0, kb) + L::dp + 16 * m * 128);
+      ldsm4(an, of64.at(0, kb) + L::n + 16 * m * 128);
 #pragma unroll
       for (int np = 0; np < NH / 2; ++np) {
-        uint32_t bs[4];
-        if constexpr (D >= 128) ldsm4t(bs, ofd.at(kb, np) + b_tile + cofs);
-        else ldsm4t(bs, (cj == 0 ? ofd.at(kb, np) : ofd.at(kb, np + D / 32)) + b_tile);
-        mma_f16(X[2 * np], a, bs[0], bs[1]);
-        mma_f16(X[2 * np + 1], a, bs[2], bs[3]);
+        uint32_t bk[4];
+        ldsm4t(bk, cols(kb, np) + L::k);
+        mma_f16(Q[2 * np], ap, bk[0], bk[1]);
+        mma_f16(Q[2 * np + 1], ap, bk[2], bk[3]);
+        mma_f16(K[2 * np], an, bk[0], bk[1]);
+        mma_f16(K[2 * np + 1], an, bk[2], bk[3]);
       }
     }
-  };
-  const float e0 = expf(G[i0] + Gl[i0]), e1 = expf(G[i0 + 8] + Gl[i0 + 8]);
-  const float l0 = expf((G[63] - G[i0]) + (Gl[63] - Gl[i0])), l1 = expf((G[63] - G[i0 + 8]) + (Gl[63] - Gl[i0 + 8]));
-  // scale e^G dO S^T
-  rows_by_state(L::o, L::s);
-  {
-    const float f0 = p.s.scale * e0 * oinv[i0] * sinv, f1 = p.s.scale * e1 * oinv[i0 + 8] * sinv;
+    const int col0 = cw * NH * 8 + 2 * t4;   // this thread's first channel
+    T *dq = static_cast<T *>(p.dq) + (row + i0) * ldc + h * D + col0;
+    T *dk = static_cast<T *>(p.dk) + (row + i0) * ldc + h * D + col0;
+    const bool on0 = i0 < len, on1 = i0 + 8 < len;
+    {   // dots with the key and the query
+      const float l0 = expf((G[63] - G[i0]) + (Gl[63] - Gl[i0])) * uinv * dsinv;
+      const float l1 = expf((G[63] - G[i0 + 8]) + (Gl[63] - Gl[i0 + 8])) * uinv * dsinv;
+      float2 z0 = make_float2(0, 0), z1 = z0, w0 = z0, w1 = z0, y0 = z0, y1 = z0;
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {
+        const uint32_t o = tile_off<D * 2>(i0, cw * NH + i) + 4 * t4;
+        const float2 k0 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::k + o));
+        const float2 k1 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::k + o + 8 * D * 2));
+        const float2 q0 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::q + o));
+        const float2 q1 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::q + o + 8 * D * 2));
+        z0 = fma2(row_lo(K[i]), k0, z0);
+        z1 = fma2(row_hi(K[i]), k1, z1);
+        w0 = fma2(row_lo(X[i]), k0, w0);
+        w1 = fma2(row_hi(X[i]), k1, w1);
+        y0 = fma2(row_lo(Q[i]), q0, y0);
+        y1 = fma2(row_hi(Q[i]), q1, y1);
+        set_lo(X[i], mul2(row_lo(X[i]), splat(l0)));
+        set_hi(X[i], mul2(row_hi(X[i]), splat(l1)));
+        if (on0) *reinterpret_cast<uint32_t *>(dq + 8 * i) = pack_io<T>(Q[i][0] * fq, Q[i][1] * fq);
+        if (on1) *reinterpret_cast<uint32_t *>(dq + 8 * ldc + 8 * i) = pack_io<T>(Q[i][2] * fq, Q[i][3] * fq);
+      }
+      float r[6] = {z0.x + z0.y, z1.x + z1.y, w0.x + w0.y, w1.x + w1.y, y0.x + y0.y, y1.x + y1.y};
+#pragma unroll
+      for (int i = 0; i < 6; ++i) {
+        r[i] += __shfl_xor_sync(0xffffffffu, r[i], 1);
+        r[i] += __shfl_xor_sync(0xffffffffu, r[i], 2);
+      }
+      if (t4 == 0) {
+        zk[cw * 64 + i0] = r[0] * (pinv * ktop);
+        zk[cw * 64 + i0 + 8] = r[1] * (pinv * ktop);
+        wk[cw * 64 + i0] = r[2] * (l0 * ktop);
+        wk[cw * 64 + i0 + 8] = r[3] * (l1 * ktop);
+        qdq[cw * 64 + i0] = r[4] * (fq * qtop);
+        qdq[cw * 64 + i0 + 8] = r[5] * (fq * qtop);
+      }
+    }
+    // K += N^T K + dP^T Q
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+      if (kb < m) continue;
+      uint32_t rp[4], rn[4];
+      const uint32_t at = s0 + tile_off<128>(16 * kb + (lane & 15), 2 * m + (lane >> 4));
+      ldsm4t(rp, at + L::dp);
+      ldsm4t(rn, at + L::n);
+      const uint32_t ap[4] = {rp[0], rp[2], rp[1], rp[3]}, an[4] = {rn[0], rn[2], rn[1], rn[3]};
+#pragma unroll
+      for (int np = 0; np < NH / 2; ++np) {
+        uint32_t bk[4], bq[4];
+        ldsm4t(bk, cols(kb, np) + L::k);
+        ldsm4t(bq, cols(kb, np) + L::q);
+        mma_f16(K[2 * np], an, bk[0], bk[1]);
+        mma_f16(K[2 * np + 1], an, bk[2], bk[3]);
+        mma_f16(K[2 * np], ap, bq[0], bq[1]);
+        mma_f16(K[2 * np + 1], ap, bq[2], bq[3]);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
-      Qa[i][0] = X[i][0] * f0; Qa[i][1] = X[i][1] * f0; Qa[i][2] = X[i][2] * f1; Qa[i][3] = X[i][3] * f1;
+      const float2 x0 = fma2(row_lo(K[i]), splat(pinv), row_lo(X[i])), x1 = fma2(row_hi(K[i]), splat(pinv), row_hi(X[i]));
+      if (on0) *reinterpret_cast<uint32_t *>(dk + 8 * i) = pack_io<T>(x0.x, x0.y);
+      if (on1) *reinterpret_cast<uint32_t *>(dk + 8 * ldc + 8 * i) = pack_io<T>(x1.x, x1.y);
     }
-  }
-  // -beta e^G du S^T
-  rows_by_state(L::r, L::s);
-  {
-    const float f0 = -beta[i0] * e0 * rinv * sinv, f1 = -beta[i0 + 8] * e1 * rinv * sinv;
+    __syncthreads();   // K, Q, dP, N have been used, the dots are written
+    fetch_keys(next);
+    if (warp == 0) {   // the gates' gradients: two tokens a lane, later tokens first
+      float in = lane < KS ? red[16 + lane] : 0.0f, w = 0.0f, gain[2];
 #pragma unroll
-    for (int i = 0; i < NH; ++i) {
-      Ka[i][0] = X[i][0] * f0; Ka[i][1] = X[i][1] * f0; Ka[i][2] = X[i][2] * f1; Ka[i][3] = X[i][3] * f1;
-    }
-  }
-  // e^{G_last - G} U dS^T, and its product with the key
-  rows_by_state(L::u, L::ds);
-  {
-    const float f0 = l0 * uinv * dsinv, f1 = l1 * uinv * dsinv;
-    float w0 = 0.0f, w1 = 0.0f;
+      for (int e = 0; e < 2; ++e) {
+        const int i = 2 * lane + e;
+        float x = -udu[i];
 #pragma unroll
-    for (int i = 0; i < NH; ++i) {
-      const int unit = half * NH + i;
-      const float2 k0 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::k + tile_off<D * 2>(i0, unit) + 4 * t4));
-      const float2 k1 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::k + tile_off<D * 2>(i0 + 8, unit) + 4 * t4));
-      w0 = fmaf(X[i][0], k0.x, fmaf(X[i][1], k0.y, w0));
-      w1 = fmaf(X[i][2], k1.x, fmaf(X[i][3], k1.y, w1));
-      Ka[i][0] = fmaf(X[i][0], f0, Ka[i][0]);
-      Ka[i][1] = fmaf(X[i][1], f0, Ka[i][1]);
-      Ka[i][2] = fmaf(X[i][2], f1, Ka[i][2]);
-      Ka[i][3] = fmaf(X[i][3], f1, Ka[i][3]);
-    }
+        for (int j = 0; j < CW; ++j) {
+          w += wk[j * 64 + i];
+          x += qdq[j * 64 + i] + zk[j * 64 + i];
+        }
+        gain[e] = x;
+      }
+      const float last = *reinterpret_cast<const float *>(sb + L::h + R::fac);
+      const float cc = head_sum<32>(fmaf(last * sinv * dsinv, in, w));
+      const float own = gain[0] + gain[1];
+      float sum = own;
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      w0 += __shfl_xor_sync(0xffffffffu, w0, o);
-      w1 += __shfl_xor_sync(0xffffffffu, w1, o);
-    }
-    if (t4 == 0) {
-      wk[half * 64 + i0] = w0 * f0 * ktop;
-      wk[half * 64 + i0 + 8] = w1 * f1 * ktop;
-    }
-  }
-  const float pinv = red[8];
-  T *dq = static_cast<T *>(p.dq) + row * ldc + h * D + half * (D / 2) + 2 * t4;
-  T *dk = static_cast<T *>(p.dk) + row * ldc + h * D + half * (D / 2) + 2 * t4;
-  // dP K
-  zero();
-  mat_by_rows(L::dp, false, L::k);
-  {
-    const float f = pinv * (ktop / qtop);
-    float w0 = 0.0f, w1 = 0.0f;
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_down_sync(0xffffffffu, sum, o);
+        if (lane + o < 32) sum += y;
+      }
+      const float after = cc + (sum - own);
 #pragma unroll
-    for (int i = 0; i < NH; ++i) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) Qa[i][e] = fmaf(X[i][e], f, Qa[i][e]);
-      const int unit = half * NH + i;
-      const float2 q0 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::q + tile_off<D * 2>(i0, unit) + 4 * t4));
-      const float2 q1 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::q + tile_off<D * 2>(i0 + 8, unit) + 4 * t4));
-      w0 = fmaf(Qa[i][0], q0.x, fmaf(Qa[i][1], q0.y, w0));
-      w1 = fmaf(Qa[i][2], q1.x, fmaf(Qa[i][3], q1.y, w1));
-      if (i0 < len) *reinterpret_cast<uint32_t *>(dq + i0 * ldc + 8 * i) = pack_io<T>(Qa[i][0], Qa[i][1]);
-      if (i0 + 8 < len) *reinterpret_cast<uint32_t *>(dq + (i0 + 8) * ldc + 8 * i) = pack_io<T>(Qa[i][2], Qa[i][3]);
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      w0 += __shfl_xor_sync(0xffffffffu, w0, o);
-      w1 += __shfl_xor_sync(0xffffffffu, w1, o);
-    }
-    if (t4 == 0) {
-      qdq[half * 64 + i0] = w0 * qtop;
-      qdq[half * 64 + i0 + 8] = w1 * qtop;
-    }
-  }
-  // dP^T Q + N K + N^T K
-  zero();
-  mat_by_rows(L::dp, true, L::q);
-  mat_by_rows(L::n, false, L::k);
-  mat_by_rows(L::n, true, L::k);
-#pragma unroll
-  for (int i = 0; i < NH; ++i) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) Ka[i][e] = fmaf(X[i][e], pinv, Ka[i][e]);
-    if (i0 < len) *reinterpret_cast<uint32_t *>(dk + i0 * ldc + 8 * i) = pack_io<T>(Ka[i][0], Ka[i][1]);
-    if (i0 + 8 < len) *reinterpret_cast<uint32_t *>(dk + (i0 + 8) * ldc + 8 * i) = pack_io<T>(Ka[i][2], Ka[i][3]);
-  }
-  __syncthreads();
-  if (warp == 0) {   // the gates' gradients: two tokens a lane, later tokens first
-    float in = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) in += red[16 + i];
-    float w = wk[2 * lane] + wk[2 * lane + 1] + wk[64 + 2 * lane] + wk[64 + 2 * lane + 1];
-    w = head_sum<32>(w);
-    const float cc = fmaf(last * sinv * dsinv, in, w);
-    const float x1 = qdq[2 * lane + 1] + qdq[64 + 2 * lane + 1] - vdu[2 * lane + 1];
-    const float x0 = qdq[2 * lane] + qdq[64 + 2 * lane] - vdu[2 * lane];
-    const float own = x0 + x1;
-    float sum = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float y = __shfl_down_sync(0xffffffffu, sum, o);
-      if (lane + o < 32) sum += y;
-    }
-    const float after = cc + (sum - own);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = 2 * lane + e;
-      if (i < len) {
-        const float a = fmaxf(sweep::widen(static_cast<const T *>(p.a)[(row + i) * p.s.ld_g + h]), -80.0f);
-        const float bb = fmaxf(sweep::widen(static_cast<const T *>(p.b)[(row + i) * p.s.ld_g + h]), -80.0f);
-        const float dl = after + x1 + (e == 0 ? x0 : 0.0f);
-        static_cast<T *>(p.da)[(row + i) * p.s.H + h] = sweep::narrow<T>(dl / (1.0f + expf(a)));
-        static_cast<T *>(p.db)[(row + i) * p.s.H + h] = sweep::narrow<T>(udu[i] / (1.0f + expf(bb)));
+      for (int e = 0; e < 2; ++e) {
+        const int i = 2 * lane + e;
+        if (i < len) {
+          const float a = fmaxf(sweep::widen(static_cast<const T *>(p.a)[(row + i) * p.s.ld_g + h]), -80.0f);
+          const float bb = fmaxf(sweep::widen(static_cast<const T *>(p.b)[(row + i) * p.s.ld_g + h]), -80.0f);
+          const float dl = after + gain[1] + (e == 0 ? gain[0] : 0.0f);
+          static_cast<T *>(p.da)[(row + i) * p.s.H + h] = sweep::narrow<T>(dl / (1.0f + expf(a)));
+          static_cast<T *>(p.db)[(row + i) * p.s.H + h] = sweep::narrow<T>(udu[i] / (1.0f + expf(bb)));
+        }
       }
     }
   }
+  sweep::cp_async_wait<0>();
 }
 
 template <typename T, int D>
 int run(const ChunkArgs &a, cudaStream_t st) {
+  using L = GradShape<D>;
   auto kern = delta_grad_kernel<T, D>;
-  const int rc = runtime_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GradSmem<D>::total));
+  int rc = runtime_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total));
   if (rc) return rc;
-  kern<<<static_cast<unsigned>(a.s.B) * a.s.H * a.w.nc, kThreads, GradSmem<D>::total, st>>>(a);
+  int per_sm = 0;
+  if ((rc = runtime_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, L::threads, L::total)))) return rc;
+  const long long chunks = static_cast<long long>(a.s.B) * a.s.H * a.w.nc, full = static_cast<long long>(sm_count()) * (per_sm > 0 ? per_sm : 1);
+  kern<<<static_cast<unsigned>(chunks < full ? chunks : full), L::threads, L::total, st>>>(a, static_cast<int>(chunks));
   return runtime_status(cudaGetLastError());
 }
 

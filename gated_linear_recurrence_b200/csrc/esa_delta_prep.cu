@@ -38,52 +38,51 @@ struct PrepSmem {
   using R = ChunkRecord<D>;
   static constexpr int m = R::th;                               // M [64][64] float32, until T's terms take its place
   static constexpr int t = (R::bytes + 127) / 128 * 128;        // T [64][LDT] float32
-  static constexpr int tmp = t + 64 * LDT * 4, vec = tmp + 32 * 36 * 4, red = vec + 3 * 64 * 4, total = red + 64;
+  static constexpr int tmp = t + 64 * LDT * 4, vec = tmp + 32 * 36 * 4, red = vec + 11 * 64 * 4, total = red + 64;
 };
 static_assert(ChunkRecord<64>::ph - ChunkRecord<64>::th == 64 * 64 * 4, "M takes the place of T's terms");
 
 // M's element (i, j): columns permuted by fours so that a column's rows fall into different banks.
 __device__ __forceinline__ int m_at(int i, int j) { return i * 64 + (j ^ ((i & 7) << 2)); }
 
+// Bits of the largest magnitude of a 16-byte unit of 16-bit elements, as a
+// float32 (exact): NaN and infinity compare above every finite value.
+template <typename T>
+__device__ __forceinline__ float unit_top(uint4 v) {
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+  const uint32_t top = max(m & 0xffffu, m >> 16);
+  return unpack_io<T>(top).x;
+}
+
 // Scale 64 rows to float16 with the threads of four warps; 1 / scale of each
-// row into `inv` (0 for a row of zeros; NaN marks a row that is not finite, which becomes zero).
+// row into `inv` (0 for a row of zeros; NaN marks a row that is not finite,
+// which becomes zero).
 template <typename T, int D>
 __device__ __forceinline__ void stage_rows(const T *src, long long ld, int n, int warp, unsigned char *tile, float *inv) {
   constexpr int LPR = D / 8, RPI = 32 / LPR;
   const int lane = threadIdx.x & 31;
-  const int sub = lane % LPR;
+  const int sub = lane % LPR, r0 = 16 * warp + lane / LPR;
+  src += r0 * ld + sub * 8;
   uint4 raw[16 / RPI];
 #pragma unroll
   for (int i = 0; i < 16 / RPI; ++i) {
-    const int r = 16 * warp + i * RPI + lane / LPR;
     raw[i] = make_uint4(0, 0, 0, 0);
-    if (r < n) raw[i] = *reinterpret_cast<const uint4 *>(src + r * ld + sub * 8);
+    if (r0 + i * RPI < n) raw[i] = *reinterpret_cast<const uint4 *>(src + i * RPI * ld);
   }
 #pragma unroll
   for (int i = 0; i < 16 / RPI; ++i) {
-    const int r = 16 * warp + i * RPI + lane / LPR;
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(&raw[i]);
-    float2 x[4];
-    float top = 0.0f, bad = 0.0f;
+    uint32_t *w = reinterpret_cast<uint32_t *>(&raw[i]);
+    uint32_t bits = __float_as_uint(unit_top<T>(raw[i]));   // not negative: orders as an integer, NaN on top
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[j] = unpack_io<T>(w[j]);
-      top = fmaxf(top, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
-      bad = fmaf(x[j].x, 0.0f, fmaf(x[j].y, 0.0f, bad));   // NaN when either is not finite
-    }
+    for (int o = LPR / 2; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+    const bool fine = bits < 0x7f800000u;
+    const Pow2 p = pow2_scale(__uint_as_float(fine ? bits : 0u));
+    const float s = fine ? p.s : 0.0f;
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) {
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      bad += __shfl_xor_sync(0xffffffffu, bad, o);
-    }
-    const bool fine = bad == 0.0f;
-    const Pow2 p = pow2_scale(fine ? top : 0.0f);
-    uint4 o;
-    uint32_t *ow = reinterpret_cast<uint32_t *>(&o);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) ow[j] = fine ? pack2(mul2(x[j], splat(p.s))) : 0u;
-    *reinterpret_cast<uint4 *>(tile + tile_off<D * 2>(r, sub)) = o;
-    if (sub == 0) inv[r] = fine ? (top > 0.0f ? p.inv : 0.0f) : __int_as_float(0x7fc00000);
+    for (int j = 0; j < 4; ++j) w[j] = pack2(mul2(unpack_io<T>(w[j]), splat(s)));
+    if (!fine) raw[i] = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4 *>(tile + tile_off<D * 2>(r0 + i * RPI, sub)) = raw[i];
+    if (sub == 0) inv[r0 + i * RPI] = fine ? (bits ? p.inv : 0.0f) : __int_as_float(0x7fc00000);
   }
 }
 
@@ -158,6 +157,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
   {
     const LaneOff<D * 2> off(lane, smem_u32(smem + R::k));
+    const LaneOffB<D * 2> ofb(lane, smem_u32(smem + R::k));
     const uint32_t ao = (warp < 4 ? 0 : R::q - R::k) + 16 * mw * D * 2;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
@@ -167,38 +167,60 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
       for (int np = 0; np < 4; ++np) {
         if (np > mw) continue;
         uint32_t bk[4];
-        ldsm4(bk, off.at(np, ks));   // tokens 0-7: [0],[2]; 8-15: [1],[3]
-        mma_f16(acc[2 * np], a, bk[0], bk[2]);
-        mma_f16(acc[2 * np + 1], a, bk[1], bk[3]);
+        ldsm4(bk, ofb.at(np, ks));
+        mma_f16(acc[2 * np], a, bk[0], bk[1]);
+        mma_f16(acc[2 * np + 1], a, bk[2], bk[3]);
       }
     }
   }
+  // times e^{Gi - Gj}.  Below the diagonal block that is e^{Gi - Gr} e^{Gr - Gj}
+  // with r the block's first row: two factors of at most 1, one exponential
+  // per row and one per column instead of one per element.
   float top = 0.0f;
   {
     const float *rinv = warp < 4 ? kinv : qinv;
-    const int i0 = 16 * mw + g;
-    float f[2], gi[2], gli[2];
+    const int r = 16 * mw, i0 = r + g;
+    const float gr = G[r], grl = Gl[r];
+    float *cf = vec + 192 + 64 * warp;   // this warp's column factors
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float r = rinv[i0 + 8 * e];
-      f[e] = r == r ? r : 0.0f;
+      const int j = lane + 32 * e;
+      const float kj = kinv[j];
+      if (j < r) cf[j] = expf((gr - G[j]) + (grl - Gl[j])) * (kj == kj ? kj : 0.0f);
+    }
+    float f[2], gi[2], gli[2], fe[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float ri = rinv[i0 + 8 * e];
+      f[e] = ri == ri ? ri : 0.0f;
       if (warp < 4) f[e] *= beta[i0 + 8 * e];
       gi[e] = G[i0 + 8 * e];
       gli[e] = Gl[i0 + 8 * e];
+      fe[e] = f[e] * expf((gi[e] - gr) + (gli[e] - grl));
     }
+    __syncwarp();
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
       if (nt > 2 * mw + 1) continue;
+      if (nt < 2 * mw) {
+        const float2 c2 = *reinterpret_cast<const float2 *>(cf + 8 * nt + 2 * t4);
+        set_lo(acc[nt], mul2(row_lo(acc[nt]), mul2(c2, splat(fe[0]))));
+        set_hi(acc[nt], mul2(row_hi(acc[nt]), mul2(c2, splat(fe[1]))));
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = i0 + (e >> 1) * 8, j = 8 * nt + 2 * t4 + (e & 1);
-        const float kj = kinv[j];
-        float x = 0.0f;
-        if (j < i || (j == i && warp >= 4))
-          x = expf((gi[e >> 1] - G[j]) + (gli[e >> 1] - Gl[j])) * (kj == kj ? kj : 0.0f) * f[e >> 1] * acc[nt][e];
-        acc[nt][e] = x;
-        top = fmaxf(top, fabsf(x));
-        if (warp < 4) M[m_at(i, j)] = x;
+        for (int e = 0; e < 4; ++e) {
+          const int i = i0 + (e >> 1) * 8, j = 8 * nt + 2 * t4 + (e & 1);
+          const float kj = kinv[j];
+          float x = 0.0f;
+          if (j < i || (j == i && warp >= 4))
+            x = expf((gi[e >> 1] - G[j]) + (gli[e >> 1] - Gl[j])) * (kj == kj ? kj : 0.0f) * f[e >> 1] * acc[nt][e];
+          acc[nt][e] = x;
+        }
+      }
+      top = max_tile(acc[nt], top);
+      if (warp < 4) {
+        *reinterpret_cast<float2 *>(M + m_at(i0, 8 * nt + 2 * t4)) = row_lo(acc[nt]);
+        *reinterpret_cast<float2 *>(M + m_at(i0 + 8, 8 * nt + 2 * t4)) = row_hi(acc[nt]);
       }
     }
   }

@@ -9,9 +9,9 @@
 // exchange between lanes.
 //
 // A float32 value x is kept as two float16 terms of x s, with s a power of two
-// that brings the largest |x| of its group to [2^12, 2^13): hi = fp16(x s),
+// that brings the largest |x| of its group to [2^5, 2^13): hi = fp16(x s),
 // lo = fp16(x s - hi).  The two carry 22 bits (an absolute error of at most
-// 2^-37 of the group's largest value for its small elements), and a product
+// 2^-30 of the group's largest value for its small elements), and a product
 // with an exact float16 operand is two mma with one accumulator.
 #pragma once
 
@@ -58,15 +58,6 @@ __device__ __forceinline__ uint32_t tile_off(int row, int c) {
   else return row * RB + ((c ^ ((row >> 2) & 1)) << 4);
 }
 
-// Address for ldmatrix.x4 of the 16 x 16 block at (row0, col0): matrices in
-// the order (rows 0-7, cols 0-7), (rows 8-15, cols 0-7), (rows 0-7, cols
-// 8-15), (rows 8-15, cols 8-15) -- the order of an A operand (plain), or of
-// an A operand's transpose when loaded with .trans and read as [0,2,1,3].
-template <int RB>
-__device__ __forceinline__ uint32_t block_addr(uint32_t tile, int row0, int col0, int lane) {
-  return tile + tile_off<RB>(row0 + (lane & 15), (col0 >> 3) + (lane >> 4));
-}
-
 __device__ __forceinline__ float2 unpack_h2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
 __device__ __forceinline__ uint32_t pack_h2(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
@@ -86,15 +77,16 @@ template <> __device__ __forceinline__ uint32_t pack_io<__nv_bfloat16>(float x, 
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Power of two that brings `top` (>= 0) to [2^12, 2^13), and its inverse;
-// 1 for zero, and bounded so that both are normal numbers.
+// Power of two, of an exponent divisible by 8, that brings `top` (>= 0) to
+// [2^5, 2^13), and its inverse; 1 for zero.  Steps of 2^8 let the groups of a
+// tile have the same scale almost always; float16 has the room.
 struct Pow2 {
   float s, inv;
 };
 __device__ __forceinline__ Pow2 pow2_scale(float top) {
-  int e = static_cast<int>(__float_as_uint(top) >> 23) - 12;      // biased exponent of top / 2^12
-  e = top > 0.0f ? max(1, min(e, 253)) : 127;
-  return {__uint_as_float(static_cast<uint32_t>(254 - e) << 23), __uint_as_float(static_cast<uint32_t>(e) << 23)};
+  int e = ((static_cast<int>(__float_as_uint(top) >> 23) - 132) >> 3) * 8;   // floor((exponent - 5) / 8) * 8
+  e = top > 0.0f ? max(-120, min(e, 120)) : 0;
+  return {__uint_as_float(static_cast<uint32_t>(127 - e) << 23), __uint_as_float(static_cast<uint32_t>(127 + e) << 23)};
 }
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -103,16 +95,17 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 
-// hi and lo terms of an already scaled pair.  hi - x is one mixed-precision
-// subtraction (exact), its sign goes into the second conversion.
+// hi and lo terms of an already scaled pair; x - hi is one mixed-precision
+// multiply-add (exact).
 __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
   hi = pack_h2(x.x, x.y);
   unsigned short h0, h1;
   float d0, d1;
   asm("mov.b32 {%0, %1}, %2;" : "=h"(h0), "=h"(h1) : "r"(hi));
-  asm("sub.rn.f32.f16 %0, %1, %2;" : "=f"(d0) : "h"(h0), "f"(x.x));
-  asm("sub.rn.f32.f16 %0, %1, %2;" : "=f"(d1) : "h"(h1), "f"(x.y));
-  lo = pack_h2(-d0, -d1);
+  const unsigned short minus_one = 0xBC00;
+  asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d0) : "h"(h0), "h"(minus_one), "f"(x.x));
+  asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d1) : "h"(h1), "h"(minus_one), "f"(x.y));
+  lo = pack_h2(d0, d1);
 }
 
 // An accumulator tile's two rows, as pairs.
@@ -150,7 +143,10 @@ __device__ __forceinline__ void single_a(const float (&c0)[4], const float (&c1)
 
 // A lane's offsets for ldmatrix.x4 of 16 x 16 blocks of a tile of RB-byte
 // rows: block (16 i, 16 j) is at off[j % 4] + 128 (j / 4) + 16 i RB, so a whole
-// chunk's fragment loads are a few registers and immediate offsets.
+// chunk's fragment loads are a few registers and immediate offsets.  The
+// matrices come in the order (rows 0-7, columns 0-7), (rows 8-15, 0-7), (rows
+// 0-7, 8-15), (rows 8-15, 8-15): that of an A operand, and with .trans and
+// read as [0, 2, 1, 3] that of its transpose.
 template <int RB>
 struct LaneOff {
   static constexpr int N = RB >= 128 ? 4 : RB / 32;
@@ -159,7 +155,23 @@ struct LaneOff {
 #pragma unroll
     for (int j = 0; j < N; ++j) o[j] = base + tile_off<RB>(lane & 15, 2 * j + (lane >> 4));
   }
-  __device__ __forceinline__ uint32_t at(int i, int j) const { return o[j % N] + 128 * (j / 4) + 16 * i * RB; }
+  __device__ __forceinline__ uint32_t at(int i, int j) const { return o[j % N] + 128 * (j / N) + 16 * i * RB; }
+};
+
+// The same for B operands stored [column n][k] and loaded without .trans: the
+// matrices come in the order (n 0-7: k 0-7, k 8-15), (n 8-15: k 0-7, k 8-15),
+// so that each mma's two registers are neighbours (the hardware wants an
+// aligned pair; in the order above every fragment cost two moves).  With
+// LaneOff and .trans the blocks of B stored [k][n] come in that order too.
+template <int RB>
+struct LaneOffB {
+  static constexpr int N = LaneOff<RB>::N;
+  uint32_t o[N];
+  __device__ __forceinline__ explicit LaneOffB(int lane, uint32_t base = 0) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = base + tile_off<RB>((lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1));
+  }
+  __device__ __forceinline__ uint32_t at(int i, int j) const { return o[j % N] + 128 * (j / N) + 16 * i * RB; }
 };
 
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool valid) {
@@ -179,6 +191,21 @@ __device__ __forceinline__ void copy_linear(uint32_t dst, const unsigned char *s
   for (int i = 0; i < U / THREADS; ++i) cp_async16_s(d + i * THREADS * 16, s + i * THREADS * 16);
   if constexpr (U % THREADS != 0)
     if (threadIdx.x < U % THREADS) cp_async16_s(d + U / THREADS * THREADS * 16, s + U / THREADS * THREADS * 16);
+}
+
+// Copy ROWS plain rows of RB bytes into a swizzled tile with all THREADS
+// threads; a thread's units lie a whole number of 8 rows apart, so its place
+// in the swizzle does not change.
+template <int RB, int ROWS, int THREADS>
+__device__ __forceinline__ void copy_rows(uint32_t dst, const void *src) {
+  constexpr int U = RB / 16, STEP = THREADS / U;
+  static_assert(THREADS % U == 0 && STEP % 8 == 0, "whole groups of 8 rows");
+  const int r = threadIdx.x / U;
+  const uint32_t d = dst + tile_off<RB>(r, threadIdx.x % U);
+  const unsigned char *s = static_cast<const unsigned char *>(src) + threadIdx.x * 16;
+#pragma unroll
+  for (int i = 0; i < (ROWS + STEP - 1) / STEP; ++i)
+    if (ROWS % STEP == 0 || r + i * STEP < ROWS) cp_async16_s(d + i * STEP * RB, s + i * THREADS * 16);
 }
 
 }  // namespace esa
