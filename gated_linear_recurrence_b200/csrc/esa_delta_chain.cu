@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     const uint32_t st = s0 + buf * L::stage;
     const LaneOff<D * 2> ofd(lane, st);        // tiles of keys and queries
     const LaneOffB<D * 2> ofb(lane, st);       // the same as [token][channel] B operands
-    const LaneOffB<128> of64(lane, st);        // T and P
+    const uint32_t tri0 = LaneOffB<32>(lane, st).o[0];   // blocks of T and P
     const unsigned char *sb = smem + buf * L::stage;
     const float *tok = reinterpret_cast<const float *>(sb + R::tok) + 2 * t4;
     const float4 fac = *reinterpret_cast<const float4 *>(sb + R::fac);
@@ -224,15 +224,21 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t hi[4], lo[4];
       split_a(X[2 * kb], X[2 * kb + 1], splat(pr.s), splat(pr.s), hi, lo);
+      uint32_t bh[4][4], bl[4];
 #pragma unroll
       for (int np = kb; np < 4; ++np) {
-        uint32_t bh[4], bl[4];
-        ldsm4(bh, of64.at(np, kb) + R::th);
-        ldsm4(bl, of64.at(np, kb) + R::tl);
-        mma_f16(U[2 * np], hi, bh[0], bh[1]);
-        mma_f16(U[2 * np + 1], hi, bh[2], bh[3]);
-        mma_f16(U[2 * np], lo, bh[0], bh[1]);
-        mma_f16(U[2 * np + 1], lo, bh[2], bh[3]);
+        ldsm4(bh[np], tri0 + tri(np, kb) + R::th);
+        mma_f16(U[2 * np], hi, bh[np][0], bh[np][1]);
+        mma_f16(U[2 * np + 1], hi, bh[np][2], bh[np][3]);
+      }
+#pragma unroll
+      for (int np = kb; np < 4; ++np) {
+        mma_f16(U[2 * np], lo, bh[np][0], bh[np][1]);
+        mma_f16(U[2 * np + 1], lo, bh[np][2], bh[np][3]);
+      }
+#pragma unroll
+      for (int np = kb; np < 4; ++np) {
+        ldsm4(bl, tri0 + tri(np, kb) + R::tl);
         mma_f16(U[2 * np], hi, bl[0], bl[1]);
         mma_f16(U[2 * np + 1], hi, bl[2], bl[3]);
       }
@@ -266,14 +272,21 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t hi[4], lo[4];
       split_a(X[2 * kb], X[2 * kb + 1], splat(xs), splat(xs), hi, lo);
+      // two blocks at a time: an accumulator's second product comes four mma
+      // (32 clocks) after its first, which takes 25
 #pragma unroll
-      for (int np = 0; np < D / 16; ++np) {
-        uint32_t bk[4];
-        ldsm4t(bk, ofd.at(kb, np) + R::k);
-        mma_f16(S[2 * np], hi, bk[0], bk[1]);
-        mma_f16(S[2 * np + 1], hi, bk[2], bk[3]);
-        mma_f16(S[2 * np], lo, bk[0], bk[1]);
-        mma_f16(S[2 * np + 1], lo, bk[2], bk[3]);
+      for (int np = 0; np < D / 16; np += 2) {
+        uint32_t b0[4], b1[4];
+        ldsm4t(b0, ofd.at(kb, np) + R::k);
+        ldsm4t(b1, ofd.at(kb, np + 1) + R::k);
+        mma_f16(S[2 * np], hi, b0[0], b0[1]);
+        mma_f16(S[2 * np + 1], hi, b0[2], b0[3]);
+        mma_f16(S[2 * np + 2], hi, b1[0], b1[1]);
+        mma_f16(S[2 * np + 3], hi, b1[2], b1[3]);
+        mma_f16(S[2 * np], lo, b0[0], b0[1]);
+        mma_f16(S[2 * np + 1], lo, b0[2], b0[3]);
+        mma_f16(S[2 * np + 2], lo, b1[0], b1[1]);
+        mma_f16(S[2 * np + 3], lo, b1[2], b1[3]);
       }
     }
     // Y = (scale e^G) S^T Q^T + scale U P^T; the first product joins the
@@ -295,7 +308,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
 #pragma unroll
       for (int np = kb; np < 4; ++np) {
         uint32_t bp[4];
-        ldsm4(bp, of64.at(np, kb) + R::ph);
+        ldsm4(bp, tri0 + tri(np, kb) + R::ph);
         mma_f16(Y[2 * np], uh[kb], bp[0], bp[1]);
         mma_f16(Y[2 * np + 1], uh[kb], bp[2], bp[3]);
         if constexpr (kTwo) {

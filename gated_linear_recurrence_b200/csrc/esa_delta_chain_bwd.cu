@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     const uint32_t st = s0 + buf * L::stage;
     const LaneOff<D * 2> ofd(lane, st);
     const LaneOffB<D * 2> ofb(lane, st);
-    const LaneOff<128> of64(lane, st);
+    const uint32_t tri0 = LaneOff<32>(lane, st).o[0];   // blocks of T and P
     const unsigned char *sb = smem + buf * L::stage;
     const float *tok = reinterpret_cast<const float *>(sb + R::tok) + 2 * t4;
     const float4 fac = *reinterpret_cast<const float4 *>(sb + R::fac);
@@ -126,13 +126,18 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
       *reinterpret_cast<uint32_t *>(o + 8 * D) = hi[1];
       *reinterpret_cast<uint32_t *>(o + 8 * D + 8) = hi[3];
 #pragma unroll
-      for (int np = 0; np < 4; ++np) {
-        uint32_t bk[4];
-        ldsm4(bk, ofb.at(np, ks) + R::k);
-        mma_f16(X[2 * np], hi, bk[0], bk[1]);
-        mma_f16(X[2 * np + 1], hi, bk[2], bk[3]);
-        mma_f16(X[2 * np], lo, bk[0], bk[1]);
-        mma_f16(X[2 * np + 1], lo, bk[2], bk[3]);
+      for (int np = 0; np < 4; np += 2) {   // an accumulator's second product four mma after its first
+        uint32_t b0[4], b1[4];
+        ldsm4(b0, ofb.at(np, ks) + R::k);
+        ldsm4(b1, ofb.at(np + 1, ks) + R::k);
+        mma_f16(X[2 * np], hi, b0[0], b0[1]);
+        mma_f16(X[2 * np + 1], hi, b0[2], b0[3]);
+        mma_f16(X[2 * np + 2], hi, b1[0], b1[1]);
+        mma_f16(X[2 * np + 3], hi, b1[2], b1[3]);
+        mma_f16(X[2 * np], lo, b0[0], b0[1]);
+        mma_f16(X[2 * np + 1], lo, b0[2], b0[3]);
+        mma_f16(X[2 * np + 2], lo, b1[0], b1[1]);
+        mma_f16(X[2 * np + 3], lo, b1[2], b1[3]);
       }
     }
     // dO^T as an A operand, scaled to float16
@@ -166,17 +171,22 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     }
     if (with) {
 #pragma unroll
-      for (int kb = 0; kb < 4; ++kb)
+      for (int kb = 0; kb < 4; ++kb) {
 #pragma unroll
         for (int np = 0; np <= kb; ++np) {
-          uint32_t bh[4], bl[4];
-          ldsm4t(bh, of64.at(kb, np) + R::ph);
-          ldsm4t(bl, of64.at(kb, np) + R::pl);
+          uint32_t bh[4];
+          ldsm4t(bh, tri0 + tri(kb, np) + R::ph);
           mma_f16(X[2 * np], od[kb], bh[0], bh[1]);
           mma_f16(X[2 * np + 1], od[kb], bh[2], bh[3]);
+        }
+#pragma unroll
+        for (int np = 0; np <= kb; ++np) {
+          uint32_t bl[4];
+          ldsm4t(bl, tri0 + tri(kb, np) + R::pl);
           mma_f16(X[2 * np], od[kb], bl[0], bl[1]);
           mma_f16(X[2 * np + 1], od[kb], bl[2], bl[3]);
         }
+      }
     }
     // du^T = dU^T T
     top = 0.0f;
@@ -192,15 +202,21 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t hi[4], lo[4];
       split_a(X[2 * kb], X[2 * kb + 1], splat(pr.s), splat(pr.s), hi, lo);
+      uint32_t bh[4][4], bl[4];
 #pragma unroll
       for (int np = 0; np <= kb; ++np) {
-        uint32_t bh[4], bl[4];
-        ldsm4t(bh, of64.at(kb, np) + R::th);
-        ldsm4t(bl, of64.at(kb, np) + R::tl);
-        mma_f16(U[2 * np], hi, bh[0], bh[1]);
-        mma_f16(U[2 * np + 1], hi, bh[2], bh[3]);
-        mma_f16(U[2 * np], lo, bh[0], bh[1]);
-        mma_f16(U[2 * np + 1], lo, bh[2], bh[3]);
+        ldsm4t(bh[np], tri0 + tri(kb, np) + R::th);
+        mma_f16(U[2 * np], hi, bh[np][0], bh[np][1]);
+        mma_f16(U[2 * np + 1], hi, bh[np][2], bh[np][3]);
+      }
+#pragma unroll
+      for (int np = 0; np <= kb; ++np) {
+        mma_f16(U[2 * np], lo, bh[np][0], bh[np][1]);
+        mma_f16(U[2 * np + 1], lo, bh[np][2], bh[np][3]);
+      }
+#pragma unroll
+      for (int np = 0; np <= kb; ++np) {
+        ldsm4t(bl, tri0 + tri(kb, np) + R::tl);
         mma_f16(U[2 * np], hi, bl[0], bl[1]);
         mma_f16(U[2 * np + 1], hi, bl[2], bl[3]);
       }
@@ -246,18 +262,28 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
       split2(mul2(unpack_h2(od[kb][2]), y1), qh[2], ql[2]);
       split2(mul2(unpack_h2(od[kb][3]), y1), qh[3], ql[3]);
 #pragma unroll
-      for (int np = 0; np < D / 16; ++np) {
-        uint32_t bk[4], bq[4];
-        ldsm4t(bk, ofd.at(kb, np) + R::k);
-        ldsm4t(bq, ofd.at(kb, np) + R::q);
-        mma_f16(S[2 * np], hi, bk[0], bk[1]);
-        mma_f16(S[2 * np + 1], hi, bk[2], bk[3]);
-        mma_f16(S[2 * np], lo, bk[0], bk[1]);
-        mma_f16(S[2 * np + 1], lo, bk[2], bk[3]);
-        mma_f16(S[2 * np], qh, bq[0], bq[1]);
-        mma_f16(S[2 * np + 1], qh, bq[2], bq[3]);
-        mma_f16(S[2 * np], ql, bq[0], bq[1]);
-        mma_f16(S[2 * np + 1], ql, bq[2], bq[3]);
+      for (int np = 0; np < D / 16; np += 2) {
+        uint32_t b0[4], b1[4];
+        ldsm4t(b0, ofd.at(kb, np) + R::k);
+        ldsm4t(b1, ofd.at(kb, np + 1) + R::k);
+        mma_f16(S[2 * np], hi, b0[0], b0[1]);
+        mma_f16(S[2 * np + 1], hi, b0[2], b0[3]);
+        mma_f16(S[2 * np + 2], hi, b1[0], b1[1]);
+        mma_f16(S[2 * np + 3], hi, b1[2], b1[3]);
+        mma_f16(S[2 * np], lo, b0[0], b0[1]);
+        mma_f16(S[2 * np + 1], lo, b0[2], b0[3]);
+        mma_f16(S[2 * np + 2], lo, b1[0], b1[1]);
+        mma_f16(S[2 * np + 3], lo, b1[2], b1[3]);
+        ldsm4t(b0, ofd.at(kb, np) + R::q);
+        ldsm4t(b1, ofd.at(kb, np + 1) + R::q);
+        mma_f16(S[2 * np], qh, b0[0], b0[1]);
+        mma_f16(S[2 * np + 1], qh, b0[2], b0[3]);
+        mma_f16(S[2 * np + 2], qh, b1[0], b1[1]);
+        mma_f16(S[2 * np + 3], qh, b1[2], b1[3]);
+        mma_f16(S[2 * np], ql, b0[0], b0[1]);
+        mma_f16(S[2 * np + 1], ql, b0[2], b0[3]);
+        mma_f16(S[2 * np + 2], ql, b1[0], b1[1]);
+        mma_f16(S[2 * np + 3], ql, b1[2], b1[3]);
       }
     }
     // dv = beta du, and du itself, through this warp's own columns of the dy tile

@@ -8,9 +8,9 @@
 // shared memory, so that a copy of it is linear:
 //   tok    [kTokRows][64] float32  per-token factors (rows below)
 //   fac    [4] float32             e^{G_last}, 1/scale of T, 1/scale of P, unused
-//   k, q   [64][D] float16         keys and queries, each row scaled by a power of two (exact)
-//   th, tl [64][64] float16        two terms of T = (1 + M)^-1, scaled by one power of two
-//   ph, pl [64][64] float16        two terms of P_ij = e^{Gi-Gj} q_i.k_j (j <= i), scaled likewise
+//   k, q   [64][D] float16         keys and queries, each tile scaled by a power of two (exact)
+//   th, tl 10 blocks 16 x 16       two float16 terms of T = (1 + M)^-1 (lower triangle), scaled likewise
+//   ph, pl 10 blocks 16 x 16       two float16 terms of P_ij = e^{Gi-Gj} q_i.k_j (j <= i), scaled likewise
 //   g      [2][64] float32         running sums of log alpha, two terms
 // and, kept for the backward or written by it,
 //   u16, r16   [64][D] float16     u and du (token rows), one power of two per 16 channels
@@ -34,12 +34,15 @@ enum { kTokBeta = 0, kTokX = 1, kTokL = 2, kTokY = 3, kTokK = 4, kTokQ = 5, kTok
 //   kTokX     beta e^G / key scale          (what the state's prediction K16 S is multiplied by)
 //   kTokL     e^{G_last - G} / key scale    (what u is multiplied by before it is added to the state)
 //   kTokY     scale e^G / query scale       (NaN where the query is not finite)
-//   kTokK, kTokQ  1 / key scale, 1 / query scale
+//   kTokK, kTokQ  1 / key scale, 1 / query scale (0 where the row is not finite)
+
+constexpr int kTriangle = 10 * 512;   // bytes of a triangle (kTriBytes of esa_mma.cuh)
 
 template <int D>
 struct ChunkRecord {
   static constexpr int tok = 0, fac = kTokRows * 64 * 4, k = fac + 128, q = k + 64 * D * 2, th = q + 64 * D * 2,
-                       tl = th + 8192, ph = tl + 8192, pl = ph + 8192, g = pl + 8192, bytes = g + 512;
+                       tl = th + kTriangle, ph = tl + kTriangle, pl = ph + kTriangle, g = pl + kTriangle,
+                       bytes = g + 512;
 };
 
 enum { kSliceU = 0, kSliceR = 8, kSliceS = 16, kSliceDs = 24 };   // rows of `slice`

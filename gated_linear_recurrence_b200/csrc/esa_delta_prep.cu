@@ -6,16 +6,26 @@
 //   (1 + M) U = beta (V - e^G K S),   M_ij = beta_i e^{Gi - Gj} k_i.k_j  (j < i),
 // where S is the state entering the chunk.  This kernel forms M from K K^T and
 // P_ij = e^{Gi - Gj} q_i.k_j (j <= i) from Q K^T on the tensor cores, and
-// T = (1 + M)^-1 in float32: four 16 x 16 diagonal blocks by substitution (one
-// column a thread), then the blocks below the diagonal, first of 16, then of
-// 32, as T21 = -T22 M21 T11.  G is kept in two float32 terms: its differences
-// are exponentiated, and a token that forgets everything (G falls by 80) must
-// not cost its successors their digits.
+// T = (1 + M)^-1 in blocks of 16: the diagonal blocks D_i by substitution in
+// float32 (one column a thread), the blocks below by
+//   T_ij = -D_i sum_{j <= l < i} M_il T_lj,
+// a block column a warp, on the tensor cores with two float16 terms per
+// operand (22 bits).  A warp works on the transposes, so that each block it
+// has formed is, as it lies in its registers, the next product's A operand:
+// a column takes no barrier.  (In float32 multiply-adds with barriers between
+// the block levels this kernel took 182 us instead of WALL at 4096 chunks of
+// D = 128.)
 //
-// Keys and queries are brought to float16 with a power of two of their own per
-// row (exact for bfloat16 and float16 rows up to elements 2^-26 of the row's
-// largest), so that bfloat16 tensors take the same products as float16 ones
-// and the split terms of T and P keep 22 bits.
+// G is kept in two float32 terms: its differences are exponentiated, and a
+// token that forgets everything (G falls by 80) must not cost its successors
+// their digits.  Below the diagonal blocks e^{Gi - Gj} is e^{Gi - Gr} e^{Gr - Gj}
+// with r the row block's first token: two factors of at most 1, one
+// exponential per row and one per column instead of one per element.
+//
+// Keys and queries are brought to float16 with one power of two per tile
+// (exact for bfloat16 and float16 elements down to 2^-19 of the tile's
+// largest, then off by at most 2^-30 of it), so that bfloat16 tensors take the
+// same products as float16 ones and the split terms keep 22 bits.
 //
 // The record (esa_delta_chunk.h) is put together in shared memory and leaves
 // in one bulk copy.
@@ -31,81 +41,61 @@ namespace esa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int LDT = 68;   // floats per row of T in shared memory
+constexpr int kDiag = 16 * 20;   // floats of a 16 x 16 block, rows of 20 (float4 rows, spread over the banks)
+constexpr unsigned kInf = 0x7f800000u;
+static_assert(kTriangle == kTriBytes, "one layout of a triangle");
 
 template <int D>
 struct PrepSmem {
   using R = ChunkRecord<D>;
-  static constexpr int m = R::th;                               // M [64][64] float32, until T's terms take its place
-  static constexpr int t = (R::bytes + 127) / 128 * 128;        // T [64][LDT] float32
-  static constexpr int tmp = t + 64 * LDT * 4, vec = tmp + 32 * 36 * 4, red = vec + 11 * 64 * 4, total = red + 64;
+  static constexpr int mh = R::th, ml = R::tl;                  // M's terms, until T's take their place
+  static constexpr int md = (R::bytes + 127) / 128 * 128;       // M's diagonal blocks, float32
+  static constexpr int dd = md + 4 * kDiag * 4;                 // their inverses D, float32
+  static constexpr int dh = dd + 4 * kDiag * 4, dl = dh + 2048; // and in two terms
+  static constexpr int vec = dl + 2048, red = vec + (2 + 8) * 64 * 4, total = red + 160;
 };
-static_assert(ChunkRecord<64>::ph - ChunkRecord<64>::th == 64 * 64 * 4, "M takes the place of T's terms");
-
-// M's element (i, j): columns permuted by fours so that a column's rows fall into different banks.
-__device__ __forceinline__ int m_at(int i, int j) { return i * 64 + (j ^ ((i & 7) << 2)); }
 
 // Bits of the largest magnitude of a 16-byte unit of 16-bit elements, as a
 // float32 (exact): NaN and infinity compare above every finite value.
 template <typename T>
-__device__ __forceinline__ float unit_top(uint4 v) {
+__device__ __forceinline__ uint32_t unit_top(uint4 v) {
   const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-  const uint32_t top = max(m & 0xffffu, m >> 16);
-  return unpack_io<T>(top).x;
-}
-
-// Scale 64 rows to float16 with the threads of four warps; 1 / scale of each
-// row into `inv` (0 for a row of zeros; NaN marks a row that is not finite,
-// which becomes zero).
-template <typename T, int D>
-__device__ __forceinline__ void stage_rows(const T *src, long long ld, int n, int warp, unsigned char *tile, float *inv) {
-  constexpr int LPR = D / 8, RPI = 32 / LPR;
-  const int lane = threadIdx.x & 31;
-  const int sub = lane % LPR, r0 = 16 * warp + lane / LPR;
-  src += r0 * ld + sub * 8;
-  uint4 raw[16 / RPI];
-#pragma unroll
-  for (int i = 0; i < 16 / RPI; ++i) {
-    raw[i] = make_uint4(0, 0, 0, 0);
-    if (r0 + i * RPI < n) raw[i] = *reinterpret_cast<const uint4 *>(src + i * RPI * ld);
-  }
-#pragma unroll
-  for (int i = 0; i < 16 / RPI; ++i) {
-    uint32_t *w = reinterpret_cast<uint32_t *>(&raw[i]);
-    uint32_t bits = __float_as_uint(unit_top<T>(raw[i]));   // not negative: orders as an integer, NaN on top
-#pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
-    const bool fine = bits < 0x7f800000u;
-    const Pow2 p = pow2_scale(__uint_as_float(fine ? bits : 0u));
-    const float s = fine ? p.s : 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = pack2(mul2(unpack_io<T>(w[j]), splat(s)));
-    if (!fine) raw[i] = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4 *>(tile + tile_off<D * 2>(r0 + i * RPI, sub)) = raw[i];
-    if (sub == 0) inv[r0 + i * RPI] = fine ? (bits ? p.inv : 0.0f) : __int_as_float(0x7fc00000);
-  }
+  return __float_as_uint(unpack_io<T>(max(m & 0xffffu, m >> 16)).x);
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
   using L = PrepSmem<D>;
   using R = ChunkRecord<D>;
+  constexpr int LPR = D / 8, RPI = 32 / LPR, NV = 16 / RPI;   // lanes of a row, rows of a load, loads of a warp's 16 rows
   extern __shared__ __align__(128) unsigned char smem[];
-  float *M = reinterpret_cast<float *>(smem + L::m), *Ti = reinterpret_cast<float *>(smem + L::t);
-  float *tmp = reinterpret_cast<float *>(smem + L::tmp), *red = reinterpret_cast<float *>(smem + L::red);
-  float *vec = reinterpret_cast<float *>(smem + L::vec);
-  float *kinv = vec, *qinv = vec + 64, *beta = vec + 128;
+  float *Md = reinterpret_cast<float *>(smem + L::md), *Dd = reinterpret_cast<float *>(smem + L::dd);
+  float *vec = reinterpret_cast<float *>(smem + L::vec), *red = reinterpret_cast<float *>(smem + L::red);
+  uint32_t *redu = reinterpret_cast<uint32_t *>(red);
+  float *beta = vec, *bad = vec + 64;   // bad: key (bit 0) and query (bit 1) rows that are not finite
   float *G = reinterpret_cast<float *>(smem + R::g), *Gl = G + 64;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  const int mw = warp & 3;
   const long long c = blockIdx.x;
   const int head = static_cast<int>(c / p.w.nc), n = static_cast<int>(c - static_cast<long long>(head) * p.w.nc);
   const int b = head / p.s.H, h = head - b * p.s.H;
   const int t0 = n * kChunk, len = min(kChunk, p.s.T - t0);
   const long long row = static_cast<long long>(b) * p.s.T + t0;
 
-  float la[2] = {0.0f, 0.0f};
-  if (warp == 0) {   // two tokens a lane
+  // K rows (warps 0-3) and Q rows (warps 4-7), 16 a warp
+  uint4 raw[NV];
+  const int sub = lane % LPR, r0 = 16 * mw + lane / LPR;
+  {
+    const T *src = static_cast<const T *>(warp < 4 ? p.k : p.q) + (row + r0) * p.s.ld_qk + h * D + sub * 8;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (r0 + i * RPI < len) raw[i] = *reinterpret_cast<const uint4 *>(src + i * RPI * p.s.ld_qk);
+    }
+  }
+  if (warp == 0) {   // gates and their running sum, two tokens a lane
     const T *ga = static_cast<const T *>(p.a), *gb = static_cast<const T *>(p.b);
+    float la[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = 2 * lane + e;
@@ -115,13 +105,8 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
         be = sweep::gate(sweep::widen(gb[(row + i) * p.s.ld_g + h]));
       }
       beta[i] = be;
+      bad[i] = 0.0f;
     }
-  }
-  if (warp < 4)
-    stage_rows<T, D>(static_cast<const T *>(p.k) + row * p.s.ld_qk + h * D, p.s.ld_qk, len, warp, smem + R::k, kinv);
-  else
-    stage_rows<T, D>(static_cast<const T *>(p.q) + row * p.s.ld_qk + h * D, p.s.ld_qk, len, warp - 4, smem + R::q, qinv);
-  if (warp == 0) {   // running sum, in two terms
     double x = static_cast<double>(la[0]) + la[1];
     const double own = x;
 #pragma unroll
@@ -134,22 +119,64 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
     *reinterpret_cast<float2 *>(G + 2 * lane) = make_float2(f0, f1);
     *reinterpret_cast<float2 *>(Gl + 2 * lane) = make_float2(static_cast<float>(first - f0), static_cast<float>(x - f1));
   }
+  {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) top = max(top, unit_top<T>(raw[i]));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) redu[warp] = top;
+  }
+  __syncthreads();
+  uint32_t topk = max(max(redu[0], redu[1]), max(redu[2], redu[3])), topq = max(max(redu[4], redu[5]), max(redu[6], redu[7]));
+  if (max(topk, topq) >= kInf) {   // rows that are not finite become zero and are marked
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      uint32_t bits = unit_top<T>(raw[i]);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+      if (bits >= kInf) {
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (sub == 0) atomicAdd(bad + r0 + i * RPI, warp < 4 ? 1.0f : 2.0f);
+      } else {
+        top = max(top, bits);
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    __syncthreads();
+    if (lane == 0) redu[warp] = top;
+    __syncthreads();
+    topk = max(max(redu[0], redu[1]), max(redu[2], redu[3]));
+    topq = max(max(redu[4], redu[5]), max(redu[6], redu[7]));
+  }
+  const Pow2 sk = pow2_scale(__uint_as_float(topk)), sq = pow2_scale(__uint_as_float(topq));
+  {
+    unsigned char *tile = smem + (warp < 4 ? R::k : R::q) + tile_off<D * 2>(r0, sub);
+    const float2 s = splat(warp < 4 ? sk.s : sq.s);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      uint32_t *w = reinterpret_cast<uint32_t *>(&raw[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = pack2(mul2(unpack_io<T>(w[j]), s));
+      if constexpr (RPI == 8) *reinterpret_cast<uint4 *>(tile + i * RPI * D * 2) = raw[i];
+      else *reinterpret_cast<uint4 *>(smem + (warp < 4 ? R::k : R::q) + tile_off<D * 2>(r0 + i * RPI, sub)) = raw[i];
+    }
+  }
   __syncthreads();
   if (tid < 64) {
-    const int i = tid;
+    const int i = tid, flag = static_cast<int>(bad[i]);
     const float into = expf(G[i] + Gl[i]), out = expf((G[63] - G[i]) + (Gl[63] - Gl[i]));
-    const float ki = kinv[i], qi = qinv[i], be = beta[i];
-    const float kf = ki == ki ? ki : 0.0f, qf = qi == qi ? qi : 0.0f;
+    const float nan = __int_as_float(0x7fc00000), be = beta[i];
+    const float kf = flag & 1 ? 0.0f : sk.inv, qf = flag & 2 ? 0.0f : sq.inv;
     float *tok = reinterpret_cast<float *>(smem + R::tok);
-    tok[kTokBeta * 64 + i] = ki == ki ? be : ki;
+    tok[kTokBeta * 64 + i] = flag & 1 ? nan : be;
     tok[kTokX * 64 + i] = be * into * kf;
     tok[kTokL * 64 + i] = out * kf;
-    tok[kTokY * 64 + i] = p.s.scale * into * qi;
+    tok[kTokY * 64 + i] = flag & 2 ? nan : p.s.scale * into * qf;
     tok[kTokK * 64 + i] = kf;
     tok[kTokQ * 64 + i] = qf;
   }
   // K K^T (warps 0-3) and Q K^T (warps 4-7): 16 rows a warp, tiles on and below the diagonal
-  const int mw = warp & 3;
   float acc[8][4];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -173,30 +200,24 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
       }
     }
   }
-  // times e^{Gi - Gj}.  Below the diagonal block that is e^{Gi - Gr} e^{Gr - Gj}
-  // with r the block's first row: two factors of at most 1, one exponential
-  // per row and one per column instead of one per element.
   float top = 0.0f;
   {
-    const float *rinv = warp < 4 ? kinv : qinv;
     const int r = 16 * mw, i0 = r + g;
     const float gr = G[r], grl = Gl[r];
-    float *cf = vec + 192 + 64 * warp;   // this warp's column factors
+    float *cf = vec + 128 + 64 * warp;   // this warp's column factors
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int j = lane + 32 * e;
-      const float kj = kinv[j];
-      if (j < r) cf[j] = expf((gr - G[j]) + (grl - Gl[j])) * (kj == kj ? kj : 0.0f);
+      if (j < r) cf[j] = expf((gr - G[j]) + (grl - Gl[j]));
     }
-    float f[2], gi[2], gli[2], fe[2];
+    const float f = sk.inv * (warp < 4 ? sk.inv : sq.inv);
+    float fr[2], gi[2], gli[2], fe[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const float ri = rinv[i0 + 8 * e];
-      f[e] = ri == ri ? ri : 0.0f;
-      if (warp < 4) f[e] *= beta[i0 + 8 * e];
+      fr[e] = warp < 4 ? f * beta[i0 + 8 * e] : f;
       gi[e] = G[i0 + 8 * e];
       gli[e] = Gl[i0 + 8 * e];
-      fe[e] = f[e] * expf((gi[e] - gr) + (gli[e] - grl));
+      fe[e] = fr[e] * expf((gi[e] - gr) + (gli[e] - grl));
     }
     __syncwarp();
 #pragma unroll
@@ -210,47 +231,52 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = i0 + (e >> 1) * 8, j = 8 * nt + 2 * t4 + (e & 1);
-          const float kj = kinv[j];
           float x = 0.0f;
           if (j < i || (j == i && warp >= 4))
-            x = expf((gi[e >> 1] - G[j]) + (gli[e >> 1] - Gl[j])) * (kj == kj ? kj : 0.0f) * f[e >> 1] * acc[nt][e];
+            x = expf((gi[e >> 1] - G[j]) + (gli[e >> 1] - Gl[j])) * fr[e >> 1] * acc[nt][e];
           acc[nt][e] = x;
+        }
+        if (warp < 4) {
+          float *o = Md + mw * kDiag + 8 * (nt & 1) + 2 * t4;
+          *reinterpret_cast<float2 *>(o + g * 20) = row_lo(acc[nt]);
+          *reinterpret_cast<float2 *>(o + (g + 8) * 20) = row_hi(acc[nt]);
         }
       }
       top = max_tile(acc[nt], top);
-      if (warp < 4) {
-        *reinterpret_cast<float2 *>(M + m_at(i0, 8 * nt + 2 * t4)) = row_lo(acc[nt]);
-        *reinterpret_cast<float2 *>(M + m_at(i0 + 8, 8 * nt + 2 * t4)) = row_hi(acc[nt]);
-      }
     }
   }
   top = warp_max(top);
-  if (lane == 0) red[warp] = top;
+  if (lane == 0) red[8 + warp] = top;
   __syncthreads();
-  const Pow2 sp = pow2_scale(fmaxf(fmaxf(red[4], red[5]), fmaxf(red[6], red[7])));
-  if (warp >= 4) {
+  const Pow2 sm = pow2_scale(fmaxf(fmaxf(red[8], red[9]), fmaxf(red[10], red[11])));
+  const Pow2 sp = pow2_scale(fmaxf(fmaxf(red[12], red[13]), fmaxf(red[14], red[15])));
+  {   // P with its diagonal blocks, M without
+    const float2 s = splat(warp < 4 ? sm.s : sp.s);
+    unsigned char *th = smem + (warp < 4 ? L::mh : R::ph), *tl = smem + (warp < 4 ? L::ml : R::pl);
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const int i = 16 * mw + g + (e >> 1) * 8;
-        uint32_t hi = 0, lo = 0;
-        if (nt <= 2 * mw + 1) split2(make_float2(acc[nt][e] * sp.s, acc[nt][e + 1] * sp.s), hi, lo);
-        const uint32_t o = tile_off<128>(i, nt) + 4 * t4;
-        *reinterpret_cast<uint32_t *>(smem + R::ph + o) = hi;
-        *reinterpret_cast<uint32_t *>(smem + R::pl + o) = lo;
-      }
+    for (int nt = 0; nt < 8; ++nt) {
+      if (nt > 2 * mw + 1 || (warp < 4 && nt >= 2 * mw)) continue;
+      const uint32_t o = tri(mw, nt >> 1) + tile_off<32>(g, nt & 1) + 4 * t4;   // rows g and g + 8: the same swizzle
+      uint32_t hi, lo;
+      split2(mul2(row_lo(acc[nt]), s), hi, lo);
+      *reinterpret_cast<uint32_t *>(th + o) = hi;
+      *reinterpret_cast<uint32_t *>(tl + o) = lo;
+      split2(mul2(row_hi(acc[nt]), s), hi, lo);
+      *reinterpret_cast<uint32_t *>(th + o + 256) = hi;
+      *reinterpret_cast<uint32_t *>(tl + o + 256) = lo;
+    }
   }
-  // T = (1 + M)^-1
-  if (tid < 64) {   // column `col` of the 16 x 16 block at r0
-    const int r0 = tid & 48, col = tid & 15;
-    float x[16];
+  if (warp < 2) {   // D_blk: column `col` a thread
+    const int blk = tid >> 4, col = tid & 15;
+    const float *Mb = Md + blk * kDiag;
+    float *Db = Dd + blk * kDiag;
+    float x[16], dt = 1.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int l = 0; l < i; l += 4) {
-        const float4 m = *reinterpret_cast<const float4 *>(M + m_at(r0 + i, r0 + l));
+        const float4 m = *reinterpret_cast<const float4 *>(Mb + i * 20 + l);
         s[0] = fmaf(m.x, x[l], s[0]);
         if (l + 1 < i) s[1] = fmaf(m.y, x[l + 1], s[1]);
         if (l + 2 < i) s[2] = fmaf(m.z, x[l + 2], s[2]);
@@ -258,77 +284,119 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
       }
       const float sum = (s[0] + s[1]) + (s[2] + s[3]);
       x[i] = i == col ? 1.0f : (i > col ? -sum : 0.0f);
-      Ti[(r0 + i) * LDT + r0 + col] = x[i];
+      dt = fmaxf(dt, fabsf(x[i]));
+      Db[i * 20 + col] = x[i];
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) dt = fmaxf(dt, __shfl_xor_sync(0xffffffffu, dt, o));
+    if (col == 0) red[16 + blk] = dt;
+    const Pow2 sd = pow2_scale(dt);
+    __half *dh = reinterpret_cast<__half *>(smem + L::dh + blk * 512), *dl = reinterpret_cast<__half *>(smem + L::dl + blk * 512);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t o = tile_off<32>(i, col >> 3) / 2 + (col & 7);
+      const float v = x[i] * sd.s;
+      const __half hi = __float2half_rn(v);
+      dh[o] = hi;
+      dl[o] = __float2half_rn(v - __half2float(hi));
     }
   }
   __syncthreads();
-  {   // blocks (1,0) and (3,2): 128 threads each, 2 columns of a row a thread
-    const int pr = tid >> 7, i = (tid & 127) >> 3, j = (tid & 7) * 2, r0 = 32 * pr;
-    float2 s = make_float2(0, 0);
+  // Block column j = warp of T, blocks (i, j) with i > j, as transposes
+  float Tt[3][2][4];
+  float tt = 0.0f;
+  if (warp < 3) {
+    const uint32_t trib = LaneOffB<32>(lane, smem_u32(smem)).o[0];
+    float Dj[2][4];
+    {
+      const float *o = Dd + warp * kDiag;
 #pragma unroll
-    for (int l = 0; l < 16; ++l)
-      s = fma2(splat(M[m_at(r0 + 16 + i, r0 + l)]), *reinterpret_cast<const float2 *>(Ti + (r0 + l) * LDT + r0 + j), s);
-    *reinterpret_cast<float2 *>(tmp + (16 * pr + i) * 36 + j) = s;
-    __syncthreads();
-    s = make_float2(0, 0);
-#pragma unroll
-    for (int l = 0; l < 16; ++l)
-      s = fma2(splat(-Ti[(r0 + 16 + i) * LDT + r0 + 16 + l]), *reinterpret_cast<const float2 *>(tmp + (16 * pr + l) * 36 + j), s);
-    *reinterpret_cast<float2 *>(Ti + (r0 + 16 + i) * LDT + r0 + j) = s;
-    *reinterpret_cast<float2 *>(Ti + (r0 + i) * LDT + r0 + 16 + j) = make_float2(0, 0);   // above the diagonal
-  }
-  __syncthreads();
-  {   // rows 32-63, columns 0-31: 4 columns of a row a thread
-    const int i = tid >> 3, j = (tid & 7) * 4;
-    float2 s0 = make_float2(0, 0), s1 = s0;
-#pragma unroll 16
-    for (int l = 0; l < 32; ++l) {
-      const float2 m = splat(M[m_at(32 + i, l)]);
-      const float4 x = *reinterpret_cast<const float4 *>(Ti + l * LDT + j);
-      s0 = fma2(m, make_float2(x.x, x.y), s0);
-      s1 = fma2(m, make_float2(x.z, x.w), s1);
+      for (int e = 0; e < 2; ++e) {
+        const int i = 8 * e + 2 * t4;   // row of D, column of the transpose
+        Dj[e][0] = o[i * 20 + g];
+        Dj[e][1] = o[(i + 1) * 20 + g];
+        Dj[e][2] = o[i * 20 + g + 8];
+        Dj[e][3] = o[(i + 1) * 20 + g + 8];
+      }
     }
-    *reinterpret_cast<float4 *>(tmp + i * 36 + j) = make_float4(s0.x, s0.y, s1.x, s1.y);
-    __syncthreads();
-    s0 = s1 = make_float2(0, 0);
-#pragma unroll 16
-    for (int l = 0; l < 32; ++l) {
-      const float2 m = splat(-Ti[(32 + i) * LDT + 32 + l]);
-      const float4 x = *reinterpret_cast<const float4 *>(tmp + l * 36 + j);
-      s0 = fma2(m, make_float2(x.x, x.y), s0);
-      s1 = fma2(m, make_float2(x.z, x.w), s1);
+    float run = red[16 + warp];   // largest entry of the column so far
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {   // i = warp + 1 + d
+      const int i = warp + 1 + d;
+      if (i > 3) continue;
+      float Z[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) Z[0][e] = Z[1][e] = 0.0f;
+      const Pow2 st = pow2_scale(run);
+#pragma unroll
+      for (int l = 0; l <= d; ++l) {   // block row warp + l
+        uint32_t hi[4], lo[4], bh[4], bl[4];
+        if (l == 0) split_a(Dj[0], Dj[1], splat(st.s), splat(st.s), hi, lo);
+        else split_a(Tt[l > 0 ? l - 1 : 0][0], Tt[l > 0 ? l - 1 : 0][1], splat(st.s), splat(st.s), hi, lo);
+        const uint32_t at = trib + (i * (i + 1) / 2 + warp + l) * 512;
+        ldsm4(bh, at + L::mh);
+        ldsm4(bl, at + L::ml);
+        mma_f16(Z[0], hi, bh[0], bh[1]);
+        mma_f16(Z[1], hi, bh[2], bh[3]);
+        mma_f16(Z[0], lo, bh[0], bh[1]);
+        mma_f16(Z[1], lo, bh[2], bh[3]);
+        mma_f16(Z[0], hi, bl[0], bl[1]);
+        mma_f16(Z[1], hi, bl[2], bl[3]);
+      }
+      const Pow2 sz = pow2_scale(warp_max(max_tile(Z[0], max_tile(Z[1], 0.0f))));
+      uint32_t hi[4], lo[4], bh[4], bl[4];
+      split_a(Z[0], Z[1], splat(sz.s), splat(sz.s), hi, lo);
+      ldsm4(bh, trib + L::dh + i * 512);
+      ldsm4(bl, trib + L::dl + i * 512);
+      float Y[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) Y[0][e] = Y[1][e] = 0.0f;
+      mma_f16(Y[0], hi, bh[0], bh[1]);
+      mma_f16(Y[1], hi, bh[2], bh[3]);
+      mma_f16(Y[0], lo, bh[0], bh[1]);
+      mma_f16(Y[1], lo, bh[2], bh[3]);
+      mma_f16(Y[0], hi, bl[0], bl[1]);
+      mma_f16(Y[1], hi, bl[2], bl[3]);
+      const float f = -(sz.inv * st.inv) * (sm.inv * pow2_scale(red[16 + i]).inv);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        scale_tile(Y[e], splat(f));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) Tt[d][e][k] = Y[e][k];
+      }
+      run = fmaxf(run, warp_max(max_tile(Y[0], max_tile(Y[1], 0.0f))));
     }
-    *reinterpret_cast<float4 *>(Ti + (32 + i) * LDT + j) = make_float4(s0.x, s0.y, s1.x, s1.y);
-    *reinterpret_cast<float4 *>(Ti + i * LDT + 32 + j) = make_float4(0, 0, 0, 0);
+    tt = run;
+    if (lane == 0) red[20 + warp] = tt;
   }
   __syncthreads();
-  const int ti = tid >> 2, tu = (tid & 3) * 2;   // a row's 16-byte units tu and tu + 1 (16 columns) a thread
-  float x[16];
-  top = 0.0f;
+  const Pow2 st = pow2_scale(fmaxf(fmaxf(red[20], red[21]), fmaxf(red[22], red[19])));
+  if (warp < 3) {
+    const uint32_t tria = LaneOff<32>(lane, smem_u32(smem)).o[0];
 #pragma unroll
-  for (int j = 0; j < 16; j += 4) {
-    const float4 v = *reinterpret_cast<const float4 *>(Ti + ti * LDT + 8 * tu + j);
-    x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
-    top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-  }
-  top = warp_max(top);
-  if (lane == 0) red[8 + warp] = top;
-  __syncthreads();
-  top = red[8];
-#pragma unroll
-  for (int w = 1; w < 8; ++w) top = fmaxf(top, red[8 + w]);
-  const Pow2 stt = pow2_scale(top);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
+    for (int d = 0; d < 3; ++d) {
+      const int i = warp + 1 + d;
+      if (i > 3) continue;
+      uint32_t hi[4], lo[4];
+      split_a(Tt[d][0], Tt[d][1], splat(st.s), splat(st.s), hi, lo);
+      const uint32_t at = tria + (i * (i + 1) / 2 + warp) * 512;
+      const uint32_t oh[4] = {hi[0], hi[2], hi[1], hi[3]}, ol[4] = {lo[0], lo[2], lo[1], lo[3]};
+      stsm4t(at + R::th, oh);
+      stsm4t(at + R::tl, ol);
+    }
+  } else if (warp >= 4) {   // diagonal blocks: half a row a lane
+    const int blk = warp - 4, i = lane >> 1, u = lane & 1;
+    const float *o = Dd + blk * kDiag + i * 20 + 8 * u;
     uint4 hi, lo;
     uint32_t *hw = reinterpret_cast<uint32_t *>(&hi), *lw = reinterpret_cast<uint32_t *>(&lo);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) split2(mul2(make_float2(x[8 * u + 2 * e], x[8 * u + 2 * e + 1]), splat(stt.s)), hw[e], lw[e]);
-    *reinterpret_cast<uint4 *>(smem + R::th + tile_off<128>(ti, tu + u)) = hi;   // M has been read
-    *reinterpret_cast<uint4 *>(smem + R::tl + tile_off<128>(ti, tu + u)) = lo;
+    for (int e = 0; e < 4; ++e) split2(mul2(*reinterpret_cast<const float2 *>(o + 2 * e), splat(st.s)), hw[e], lw[e]);
+    const uint32_t at = (blk * (blk + 1) / 2 + blk) * 512 + tile_off<32>(i, u);
+    *reinterpret_cast<uint4 *>(smem + R::th + at) = hi;
+    *reinterpret_cast<uint4 *>(smem + R::tl + at) = lo;
+  } else if (lane == 0) {
+    *reinterpret_cast<float4 *>(smem + R::fac) = make_float4(expf(G[63] + Gl[63]), st.inv, sp.inv, 0.0f);
   }
-  if (tid == 0)
-    *reinterpret_cast<float4 *>(smem + R::fac) = make_float4(expf(G[63] + Gl[63]), stt.inv, sp.inv, 0.0f);
   fence_proxy_async_smem();
   __syncthreads();
   if (tid == 0) {

@@ -89,10 +89,11 @@ __device__ __forceinline__ Pow2 pow2_scale(float top) {
   return {__uint_as_float(static_cast<uint32_t>(127 - e) << 23), __uint_as_float(static_cast<uint32_t>(127 + e) << 23)};
 }
 
+// Largest |x| of the warp (a NaN is passed over unless all are).
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
+  float y;
+  asm volatile("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // hi and lo terms of an already scaled pair; x - hi is one mixed-precision
@@ -173,6 +174,11 @@ struct LaneOffB {
   }
   __device__ __forceinline__ uint32_t at(int i, int j) const { return o[j % N] + 128 * (j / N) + 16 * i * RB; }
 };
+
+// Lower triangle of a 64 x 64 float16 matrix as ten 16 x 16 blocks of 512
+// bytes, rows of 32 bytes: byte offset of block (i, j), j <= i.
+constexpr int kTriBytes = 10 * 512;
+__host__ __device__ constexpr int tri(int i, int j) { return (i * (i + 1) / 2 + j) * 512; }
 
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
