@@ -26,6 +26,7 @@
 // the whole head in one SM, with the state converted through tensor memory
 // three times a chunk; with few heads (the usual case of a long prompt) that
 // leaves most SMs idle, where 16-row warps spread a head over eight.
+#include <cstdlib>
 #include <type_traits>
 
 #include "esa_delta_chunk.h"
@@ -390,7 +391,7 @@ int by_keep(const ChunkArgs &a, cudaStream_t st) {
 template <typename T, int D>
 int by_warps(const ChunkArgs &a, cudaStream_t st) {
   if constexpr (D == 128)
-    if (chain_splits(a.s.B * a.s.H)) return by_keep<T, D, 4>(a, st);
+    if (chain_plan(a.s.B * a.s.H, D) == kChainHalves) return by_keep<T, D, 4>(a, st);
   return by_keep<T, D, D / 16>(a, st);
 }
 
@@ -406,9 +407,18 @@ int by_d(const ChunkArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-bool chain_splits(int heads) { return 2ll * heads <= sm_count(); }
+// Four warps a slice while every slice's block has an SM to itself; else whole
+// heads, of which a block takes eight warps at D = 128 once four warps a block
+// would put more than one block on an SM (16 heads: 129 us a pass of 32 chunks
+// in halves against 205 whole; 128 heads: 263 against 215).
+ChainPlan chain_plan(int heads, int D) {
+  if (getenv("ESA_PLAN")) return static_cast<ChainPlan>(atoi(getenv("ESA_PLAN")));
+  if (D >= 64 && static_cast<long long>(heads) * (D / 16) <= sm_count()) return kChainSplit;
+  return D == 128 && 2ll * heads <= sm_count() ? kChainHalves : kChainWhole;
+}
 
 int launch_chunk_fwd(int dtype, const ChunkArgs &a, cudaStream_t st) {
+  if (chain_plan(a.s.B * a.s.H, a.s.D) == kChainSplit) return launch_split_fwd(dtype, a, st);
   return dtype == ESA_F16 ? by_d<__half>(a, st) : by_d<__nv_bfloat16>(a, st);
 }
 

@@ -346,7 +346,7 @@ int by_d(const ChunkArgs &a, cudaStream_t st) {
   switch (a.s.D) {
     case 32: return run<T, 32, 2>(a, st);
     case 64: return run<T, 64, 4>(a, st);
-    case 128: return chain_splits(a.s.B * a.s.H) ? run<T, 128, 4>(a, st) : run<T, 128, 8>(a, st);
+    case 128: return chain_plan(a.s.B * a.s.H, 128) == kChainHalves ? run<T, 128, 4>(a, st) : run<T, 128, 8>(a, st);
     default: return ESA_ERR_UNSUPPORTED;
   }
 }
@@ -354,6 +354,7 @@ int by_d(const ChunkArgs &a, cudaStream_t st) {
 }  // namespace
 
 int launch_chunk_bwd(int dtype, const ChunkArgs &a, cudaStream_t st) {
+  if (chain_plan(a.s.B * a.s.H, a.s.D) == kChainSplit) return launch_split_bwd(dtype, a, st);
   return dtype == ESA_F16 ? by_d<__half>(a, st) : by_d<__nv_bfloat16>(a, st);
 }
 

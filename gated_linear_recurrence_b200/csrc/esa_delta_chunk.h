@@ -69,10 +69,12 @@ int launch_chunk_fwd(int dtype, const ChunkArgs &a, cudaStream_t st);
 int launch_chunk_bwd(int dtype, const ChunkArgs &a, cudaStream_t st);    // dv, dS_init, du
 int launch_chunk_grad(int dtype, const ChunkArgs &a, cudaStream_t st);   // dq, dk, da, db
 
-// Whether the two chain kernels cut a head of 128 channels over two blocks of
-// four warps: while that gives no SM more than one block, every warp has an SM
-// quarter to itself (16 heads: 129 us a pass of 32 chunks against 205 with
-// eight warps in one SM; 128 heads: 263 against 215 the other way).
-bool chain_splits(int heads);
+// The chains with a slice of 16 value channels shared by four warps (D = 64, 128).
+int launch_split_fwd(int dtype, const ChunkArgs &a, cudaStream_t st);
+int launch_split_bwd(int dtype, const ChunkArgs &a, cudaStream_t st);
+
+// How the chains spread a head over the device.
+enum ChainPlan { kChainWhole, kChainHalves, kChainSplit };
+ChainPlan chain_plan(int heads, int D);
 
 }  // namespace esa
