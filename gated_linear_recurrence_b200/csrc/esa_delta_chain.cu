@@ -47,25 +47,41 @@ struct ChainSmem {
   static constexpr int total = 2 * stage;
 };
 
-// First token (or 64) from which each of the thread's two rows is not finite,
-// agreed over the row's four lanes; those entries become zero.
-__device__ __forceinline__ void cut_rows(float (&R)[8][4], int t4, int (&first)[2]) {
-  first[0] = first[1] = 64;
-#pragma unroll
-  for (int nt = 7; nt >= 0; --nt)
-#pragma unroll
-    for (int e = 3; e >= 0; --e)
-      if (!(fabsf(R[nt][e]) <= 3.4028235e38f)) first[e >> 1] = min(first[e >> 1], 8 * nt + 2 * t4 + (e & 1));
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    first[r] = min(first[r], __shfl_xor_sync(0xffffffffu, first[r], 1));
-    first[r] = min(first[r], __shfl_xor_sync(0xffffffffu, first[r], 2));
-  }
-#pragma unroll
-  for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (8 * nt + 2 * t4 + (e & 1) >= first[e >> 1]) R[nt][e] = 0.0f;
+// A warp's 16 value channels (columns `unit`, `unit` + 1 of the tile) hold an
+// entry that is not finite, or a key of the chunk does (from token `key` on).
+// Entries that are not finite become zero, so that they cannot reach earlier
+// tokens of the chunk through the zeros above the diagonals of T and P;
+// first[r] is the token from which this thread's channels g and g + 8 are to
+// be NaN.
+template <typename T, int RB>
+__device__ __noinline__ void cut_values(unsigned char *tile, int unit, int key, int *first) {
+  const int lane = threadIdx.x & 31, g = lane >> 2;
+  first[0] = first[1] = key;
+  for (int r = 63; r >= 0; --r)
+    for (int e = 0; e < 2; ++e) {
+      const T *v = reinterpret_cast<const T *>(tile + tile_off<RB>(r, unit + e)) + g;
+      if (!(fabsf(sweep::widen(*v)) <= 3.4028235e38f)) first[e] = min(first[e], r);
+    }
+  __syncwarp();
+  for (int r = lane; r < 64; r += 32)
+    for (int e = 0; e < 16; ++e) {
+      T *v = reinterpret_cast<T *>(tile + tile_off<RB>(r, unit + (e >> 3))) + (e & 7);
+      if (!(fabsf(sweep::widen(*v)) <= 3.4028235e38f)) *v = sweep::narrow<T>(0.0f);
+    }
+  __syncwarp();
+}
+
+// NaN into the staged output rows (32 bytes a token) of those channels.
+template <typename T, int RB>
+__device__ __noinline__ void poison_rows(unsigned char *tile, int unit, int first0, int first1) {
+  const int lane = threadIdx.x & 31, g = lane >> 2;
+  const T nan = sweep::narrow<T>(__int_as_float(0x7fc00000));
+  if ((lane & 3) == 0)
+    for (int r = 0; r < 64; ++r) {
+      if (r >= first0) reinterpret_cast<T *>(tile + tile_off<RB>(r, unit))[g] = nan;
+      if (r >= first1) reinterpret_cast<T *>(tile + tile_off<RB>(r, unit + 1))[g] = nan;
+    }
+  __syncwarp();
 }
 
 template <typename T, int D, int W, bool KEEP>
@@ -122,6 +138,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       for (int e = 0; e < 4; ++e) S[nt][e] = 0.0f;
   }
 
+  bool dead0 = false, dead1 = false;   // channels g and g + 8 are NaN from an earlier token on
   fetch(0, 0);
 #pragma unroll 1
   for (int n = 0; n < nc; ++n) {
@@ -141,6 +158,26 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     const float *tok = reinterpret_cast<const float *>(sb + R::tok) + 2 * t4;
     const float4 fac = *reinterpret_cast<const float4 *>(sb + R::fac);
     const long long c = c0 + n;
+    int first0 = 64, first1 = 64;
+    bool cut;
+    {
+      uint32_t top = fac.w < 64.0f ? 0x7f800000u : 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        top = max(top, unit_top<T>(*reinterpret_cast<const uint4 *>(sb + L::v + vrow + 16 * i * L::kRow)));
+      cut = __reduce_max_sync(0xffffffffu, top) >= 0x7f800000u;
+      if (cut) {
+        int first[2];
+        cut_values<T, L::kRow>(smem + buf * L::stage + L::v, 2 * warp, static_cast<int>(fac.w), first);
+        first0 = first[0];
+        first1 = first[1];
+      }
+      if (dead0) first0 = 0;
+      if (dead1) first1 = 0;
+      dead0 = first0 < 64;
+      dead1 = first1 < 64;
+      cut = __any_sync(0xffffffffu, dead0 || dead1);
+    }
 
     // X = S^T K^T and the output's S^T Q^T
     float X[8][4], Y[8][4];
@@ -154,17 +191,19 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     const float tops = warp_max(top);
     const Pow2 ps = pow2_scale(tops);
     const float xinv = ps.inv * sinv;
-    if (KEEP && lane == 0) p.w.slice[c * 32 + kSliceS + (dvw >> 4)] = tops > 0.0f ? xinv : 0.0f;
+    // what the backward keeps of the state has a scale of its own
+    const Pow2 pss = store_scale(tops * sinv);
+    const float sf = pss.s * xinv;
+    if (KEEP && lane == 0)
+      p.w.slice[c * 32 + kSliceS + (dvw >> 4)] = cut ? __int_as_float(0x7fc00000) : tops > 0.0f ? pss.inv : 0.0f;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint32_t hi[4], lo[4];
       split_a(S[2 * ks], S[2 * ks + 1], splat(ps.s), splat(ps.s), hi, lo);
       if constexpr (KEEP) {
-        __half *o = p.w.s16 + c * (D * D) + (dvw + g) * D + 16 * ks + 2 * t4;
-        *reinterpret_cast<uint32_t *>(o) = hi[0];
-        *reinterpret_cast<uint32_t *>(o + 8) = hi[2];
-        *reinterpret_cast<uint32_t *>(o + 8 * D) = hi[1];
-        *reinterpret_cast<uint32_t *>(o + 8 * D + 8) = hi[3];
+        uint32_t x[4] = {hi[0], hi[1], hi[2], hi[3]};
+        if (sf != 1.0f) scale_h2(x, sf);
+        store_block(p.w.s16 + c * (D * D) + dvw * D + 16 * ks, D, x, lane);
       }
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
@@ -184,7 +223,6 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       }
     }
     // R = beta V^T - (beta e^G) X, in place of X
-    float2 chk = make_float2(0.0f, 0.0f);
     top = 0.0f;
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
@@ -197,22 +235,10 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
         const float2 tx = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 8 * nt), splat(-xinv));
         const float2 r0 = fma2(tx, row_lo(X[nt]), mul2(be, unpack_io<T>(vv[half])));
         const float2 r1 = fma2(tx, row_hi(X[nt]), mul2(be, unpack_io<T>(vv[2 + half])));
-        chk = fma2(r0, splat(0.0f), fma2(r1, splat(0.0f), chk));
         set_lo(X[nt], r0);
         set_hi(X[nt], r1);
         top = max_tile(X[nt], top);
       }
-    }
-    // A value, key or state that is not finite poisons its channel from that
-    // token on; zero there keeps it from reaching earlier tokens of the chunk
-    // through the zeros above the diagonals of T and P.
-    int first[2] = {64, 64};
-    const bool cut = __any_sync(0xffffffffu, !(chk.x + chk.y == 0.0f));
-    if (cut) {
-      cut_rows(X, t4, first);
-      top = 0.0f;
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt) top = max_tile(X[nt], top);
     }
     const Pow2 pr = pow2_scale(warp_max(top));
     // U = R T^T: T_ij = 0 for j > i, in blocks of 16
@@ -299,7 +325,9 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       for (int nt = 0; nt < 8; ++nt)
         scale_tile(Y[nt], mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 8 * nt), splat(r)));
     }
-    if (KEEP && lane == 0) p.w.slice[c * 32 + kSliceU + (dvw >> 4)] = top > 0.0f ? uinv : 0.0f;
+    const Pow2 pus = store_scale(top * uf);
+    if (KEEP && lane == 0)
+      p.w.slice[c * 32 + kSliceU + (dvw >> 4)] = cut ? __int_as_float(0x7fc00000) : top > 0.0f ? pus.inv : 0.0f;
     uint32_t uh[4][4];
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
@@ -318,19 +346,6 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
         }
       }
     }
-    if (cut) {   // rows that are not finite from token `first` on
-      const float nan = __int_as_float(0x7fc00000);
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (8 * nt + 2 * t4 + (e & 1) >= first[e >> 1]) Y[nt][e] = nan;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (first[e >> 1] < 64) S[nt][e] = nan;
-    }
     // Transpose through this warp's own columns of the value tile (read above) and store rows of 32 bytes.
     const int len = min(kChunk, p.s.T - n * kChunk);
     const uint32_t vw = st + L::v + vofs;
@@ -344,6 +359,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       stsm4t(vw + 16 * np * L::kRow, o);
     }
     __syncwarp();
+    if (cut) poison_rows<T, L::kRow>(smem + buf * L::stage + L::v, 2 * warp, first0, first1);
     T *yr = y + (row0 + n * kChunk + (lane >> 1)) * ldy;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -353,7 +369,8 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       __syncwarp();
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
-        const uint32_t o[4] = {uh[kb][0], uh[kb][2], uh[kb][1], uh[kb][3]};
+        uint32_t o[4] = {uh[kb][0], uh[kb][2], uh[kb][1], uh[kb][3]};
+        if (pus.s * uinv != 1.0f) scale_h2(o, pus.s * uinv);
         stsm4t(vw + 16 * kb * L::kRow, o);
       }
       __syncwarp();
@@ -369,7 +386,9 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) So[(8 * nt + 2 * t4 + (e & 1)) * D + dvw + g + (e >> 1) * 8] = S[nt][e] * sinv;
+      for (int e = 0; e < 4; ++e) 
+        So[(8 * nt + 2 * t4 + (e & 1)) * D + dvw + g + (e >> 1) * 8] =
+            (e < 2 ? dead0 : dead1) ? __int_as_float(0x7fc00000) : S[nt][e] * sinv;
   }
 }
 

@@ -115,16 +115,16 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     const float tops = warp_max(top);
     const Pow2 ps = pow2_scale(tops);
     const float xinv = ps.inv * sinv;
-    if (lane == 0) p.w.slice[c * 32 + kSliceDs + (dvw >> 4)] = tops > 0.0f ? xinv : 0.0f;
+    const Pow2 pss = store_scale(tops * sinv);
+    const float sf = pss.s * xinv;
+    if (lane == 0) p.w.slice[c * 32 + kSliceDs + (dvw >> 4)] = tops > 0.0f ? pss.inv : 0.0f;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint32_t hi[4], lo[4];
       split_a(S[2 * ks], S[2 * ks + 1], splat(ps.s), splat(ps.s), hi, lo);
-      __half *o = p.w.ds16 + c * (D * D) + (dvw + g) * D + 16 * ks + 2 * t4;
-      *reinterpret_cast<uint32_t *>(o) = hi[0];
-      *reinterpret_cast<uint32_t *>(o + 8) = hi[2];
-      *reinterpret_cast<uint32_t *>(o + 8 * D) = hi[1];
-      *reinterpret_cast<uint32_t *>(o + 8 * D + 8) = hi[3];
+      uint32_t x[4] = {hi[0], hi[1], hi[2], hi[3]};
+      if (sf != 1.0f) scale_h2(x, sf);
+      store_block(p.w.ds16 + c * (D * D) + dvw * D + 16 * ks, D, x, lane);
 #pragma unroll
       for (int np = 0; np < 4; np += 2) {   // an accumulator's second product four mma after its first
         uint32_t b0[4], b1[4];
@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
         topo = fmaxf(topo, fmaxf(fabsf(x.x), fabsf(x.y)));
       }
     top = warp_max(top);
-    const Pow2 pu = pow2_scale(top), pl = pow2_scale(warp_max(fmaxf(topx, topo)));
+    const Pow2 pus = store_scale(top * rf), pl = pow2_scale(warp_max(fmaxf(topx, topo)));
+    const float us = pus.s * rf;
     const float asc = fminf(pl.s, tops > 0.0f ? ps.s * scur * 68719476736.0f : __int_as_float(0x7f800000));
     {
       const float2 sc = splat(fac.x * (asc * sinv));
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
       uint32_t r[4];
-      single_a(U[2 * np], U[2 * np + 1], splat(pu.s), splat(pu.s), r);
+      single_a(U[2 * np], U[2 * np + 1], splat(us), splat(us), r);
       const uint32_t o[4] = {r[0], r[2], r[1], r[3]};
       stsm4t(vw + 16 * np * L::kRow, o);
     }
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<uint4 *>(ur + 16 * i * D) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
-    if (lane == 0) p.w.slice[c * 32 + kSliceR + (dvw >> 4)] = top > 0.0f ? pu.inv * rf : 0.0f;
+    if (lane == 0) p.w.slice[c * 32 + kSliceR + (dvw >> 4)] = top > 0.0f ? pus.inv : 0.0f;
     __syncthreads();
   }
   if (p.S_out != nullptr) {

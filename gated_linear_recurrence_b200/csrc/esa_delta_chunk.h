@@ -7,7 +7,7 @@
 // kernel in the order and with the swizzle in which later kernels hold it in
 // shared memory, so that a copy of it is linear:
 //   tok    [kTokRows][64] float32  per-token factors (rows below)
-//   fac    [4] float32             e^{G_last}, 1/scale of T, 1/scale of P, unused
+//   fac    [4] float32             e^{G_last}, 1/scale of T, 1/scale of P, first token whose key is not finite (or 64)
 //   k, q   [64][D] float16         keys and queries, each tile scaled by a power of two (exact)
 //   th, tl 10 blocks 16 x 16       two float16 terms of T = (1 + M)^-1 (lower triangle), scaled likewise
 //   ph, pl 10 blocks 16 x 16       two float16 terms of P_ij = e^{Gi-Gj} q_i.k_j (j <= i), scaled likewise
@@ -16,7 +16,7 @@
 //   u16, r16   [64][D] float16     u and du (token rows), one power of two per 16 channels
 //   s16, ds16  [D][D] float16      state entering the chunk and gradient of the state leaving it
 //                                  (row: value channel), one power of two per 16 rows
-//   slice      [4][8] float32      inverses of those powers of two (0 for a group of zeros)
+//   slice      [4][8] float32      inverses of those powers of two (0 for a group of zeros, NaN for one that is not finite)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -30,7 +30,7 @@ namespace esa {
 
 constexpr int kChunk = 64;
 enum { kTokBeta = 0, kTokX = 1, kTokL = 2, kTokY = 3, kTokK = 4, kTokQ = 5, kTokRows = 6 };
-//   kTokBeta  beta (NaN where the key is not finite: the token poisons what follows it)
+//   kTokBeta  beta (0 where the key is not finite)
 //   kTokX     beta e^G / key scale          (what the state's prediction K16 S is multiplied by)
 //   kTokL     e^{G_last - G} / key scale    (what u is multiplied by before it is added to the state)
 //   kTokY     scale e^G / query scale       (NaN where the query is not finite)

@@ -63,6 +63,19 @@ __device__ __forceinline__ void scale_frag(uint32_t (&a)[4], float f) {
   }
 }
 
+// Two neighbouring accumulator tiles times f, rounded, as 8-byte stores: lanes
+// exchange as in store_block.  `o` is the thread's first element of a pair.
+template <typename T>
+__device__ __forceinline__ void store_pair(T *o, long long ld, int col, const float (&c0)[4], const float (&c1)[4], float f,
+                                           bool on0, bool on1, int lane) {
+  const bool odd = lane & 1;
+  const uint32_t a0 = pack_io<T>(c0[0] * f, c0[1] * f), a1 = pack_io<T>(c0[2] * f, c0[3] * f);
+  const uint32_t b0 = pack_io<T>(c1[0] * f, c1[1] * f), b1 = pack_io<T>(c1[2] * f, c1[3] * f);
+  const uint32_t x0 = __shfl_xor_sync(0xffffffffu, odd ? a0 : b0, 1), x1 = __shfl_xor_sync(0xffffffffu, odd ? a1 : b1, 1);
+  if (on0) *reinterpret_cast<uint2 *>(o + col) = odd ? make_uint2(x0, b0) : make_uint2(a0, x0);
+  if (on1) *reinterpret_cast<uint2 *>(o + 8 * ld + col) = odd ? make_uint2(x1, b1) : make_uint2(a1, x1);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(ChunkArgs p, int chunks) {
   using L = GradShape<D>;
@@ -85,13 +98,14 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
     h = head - b * p.s.H;
     t0 = (c - head * p.w.nc) * kChunk;
   };
+  int nb = 0, nh = 0, nt0 = 0;              // place of the chunk whose rows were fetched last
   auto fetch_rows = [&](int c, int buf) {   // U, du, dO and the header
     if (c < chunks) {
       const uint32_t st = s0 + L::buf + buf * L::stage;
       copy_rows<D * 2, 64, kThreads>(st + L::u, p.w.u16 + static_cast<long long>(c) * (64 * D));
       copy_rows<D * 2, 64, kThreads>(st + L::r, p.w.r16 + static_cast<long long>(c) * (64 * D));
-      int b, h, t0;
-      place(c, b, h, t0);
+      place(c, nb, nh, nt0);
+      const int b = nb, h = nh, t0 = nt0;
       constexpr int U = D / 8, STEP = kThreads / U;
       const int r = tid / U, u = tid % U, len = min(kChunk, p.s.T - t0);
       const T *dy = static_cast<const T *>(p.dy) + (static_cast<long long>(b) * p.s.T + t0) * ldc + h * D + u * 8;
@@ -132,8 +146,7 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
 #pragma unroll 1
   for (int c = blockIdx.x; c < chunks; c += gridDim.x, ++it) {
     const int buf = it & 1, next = c + gridDim.x;
-    int b, h, t0;
-    place(c, b, h, t0);
+    const int b = nb, h = nh, t0 = nt0;
     const int len = min(kChunk, p.s.T - t0);
     const long long row = static_cast<long long>(b) * p.s.T + t0;
     const uint32_t bo = L::buf + buf * L::stage;
@@ -143,6 +156,16 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
     sweep::cp_async_wait<2>();   // rows of this chunk
     __syncthreads();
     fetch_rows(next, buf ^ 1);
+    T la[2], lb[2];              // warp 0: the gates' logits, for the end
+    la[0] = la[1] = lb[0] = lb[1] = sweep::narrow<T>(0.0f);
+    if (warp == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (2 * lane + e < len) {
+          la[e] = static_cast<const T *>(p.a)[(row + 2 * lane + e) * p.s.ld_g + h];
+          lb[e] = static_cast<const T *>(p.b)[(row + 2 * lane + e) * p.s.ld_g + h];
+        }
+    }
     // dO, each row to float16 with its own power of two
     {
       constexpr int U = D / 8;
@@ -171,12 +194,13 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
     float part, uinv, rinv, sinv, dsinv;
     bool flat;
     {
-      const float v = (lane & 7) < KS ? reinterpret_cast<const float *>(sb + L::h + R::k + 512)[lane] : 0.0f;
+      float v = (lane & 7) < KS ? reinterpret_cast<const float *>(sb + L::h + R::k + 512)[lane] : 0.0f;
       float t = v;
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-      if (!(t > 0.0f)) t = 1.0f;
-      part = v > 0.0f ? v / t : 1.0f;
+      if (__any_sync(0xffffffffu, v != v)) t = v = __int_as_float(0x7fc00000);   // a channel of the chunk is not finite
+      else if (!(t > 0.0f)) t = 1.0f;
+      part = v > 0.0f && v != t ? v / t : 1.0f;
       flat = __all_sync(0xffffffffu, part == 1.0f);
       uinv = __shfl_sync(0xffffffffu, t, kSliceU);
       rinv = __shfl_sync(0xffffffffu, t, kSliceR);
@@ -376,7 +400,7 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
         mma_f16(K[2 * np + 1], an, bk[2], bk[3]);
       }
     }
-    const int col0 = cw * NH * 8 + 2 * t4;   // this thread's first channel
+    const int col0 = cw * NH * 8 + (lane & 1 ? 8 : 0) + 2 * (t4 & 2);   // this thread's first channel in a pair of tiles
     T *dq = static_cast<T *>(p.dq) + (row + i0) * ldc + h * D + col0;
     T *dk = static_cast<T *>(p.dk) + (row + i0) * ldc + h * D + col0;
     const bool on0 = i0 < len, on1 = i0 + 8 < len;
@@ -399,9 +423,9 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
         y1 = fma2(row_hi(Q[i]), q1, y1);
         set_lo(X[i], mul2(row_lo(X[i]), splat(l0)));
         set_hi(X[i], mul2(row_hi(X[i]), splat(l1)));
-        if (on0) *reinterpret_cast<uint32_t *>(dq + 8 * i) = pack_io<T>(Q[i][0] * fq, Q[i][1] * fq);
-        if (on1) *reinterpret_cast<uint32_t *>(dq + 8 * ldc + 8 * i) = pack_io<T>(Q[i][2] * fq, Q[i][3] * fq);
       }
+#pragma unroll
+      for (int i = 0; i < NH; i += 2) store_pair<T>(dq, ldc, 8 * i, Q[i], Q[i + 1], fq, on0, on1, lane);
       float r[6] = {z0.x + z0.y, z1.x + z1.y, w0.x + w0.y, w1.x + w1.y, y0.x + y0.y, y1.x + y1.y};
 #pragma unroll
       for (int i = 0; i < 6; ++i) {
@@ -439,10 +463,11 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
     }
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
-      const float2 x0 = fma2(row_lo(K[i]), splat(pinv), row_lo(X[i])), x1 = fma2(row_hi(K[i]), splat(pinv), row_hi(X[i]));
-      if (on0) *reinterpret_cast<uint32_t *>(dk + 8 * i) = pack_io<T>(x0.x, x0.y);
-      if (on1) *reinterpret_cast<uint32_t *>(dk + 8 * ldc + 8 * i) = pack_io<T>(x1.x, x1.y);
+      set_lo(K[i], fma2(row_lo(K[i]), splat(pinv), row_lo(X[i])));
+      set_hi(K[i], fma2(row_hi(K[i]), splat(pinv), row_hi(X[i])));
     }
+#pragma unroll
+    for (int i = 0; i < NH; i += 2) store_pair<T>(dk, ldc, 8 * i, K[i], K[i + 1], 1.0f, on0, on1, lane);
     __syncthreads();   // K, Q, dP, N have been used, the dots are written
     fetch_keys(next);
     if (warp == 0) {   // the gates' gradients: two tokens a lane, later tokens first
@@ -472,8 +497,8 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
       for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
         if (i < len) {
-          const float a = fmaxf(sweep::widen(static_cast<const T *>(p.a)[(row + i) * p.s.ld_g + h]), -80.0f);
-          const float bb = fmaxf(sweep::widen(static_cast<const T *>(p.b)[(row + i) * p.s.ld_g + h]), -80.0f);
+          const float a = fmaxf(sweep::widen(la[e]), -80.0f);
+          const float bb = fmaxf(sweep::widen(lb[e]), -80.0f);
           const float dl = after + gain[1] + (e == 0 ? gain[0] : 0.0f);
           static_cast<T *>(p.da)[(row + i) * p.s.H + h] = sweep::narrow<T>(dl / (1.0f + expf(a)));
           static_cast<T *>(p.db)[(row + i) * p.s.H + h] = sweep::narrow<T>(udu[i] / (1.0f + expf(bb)));

@@ -55,14 +55,6 @@ struct PrepSmem {
   static constexpr int vec = dl + 2048, red = vec + (2 + 8) * 64 * 4, total = red + 160;
 };
 
-// Bits of the largest magnitude of a 16-byte unit of 16-bit elements, as a
-// float32 (exact): NaN and infinity compare above every finite value.
-template <typename T>
-__device__ __forceinline__ uint32_t unit_top(uint4 v) {
-  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-  return __float_as_uint(unpack_io<T>(max(m & 0xffffu, m >> 16)).x);
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
   using L = PrepSmem<D>;
@@ -169,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
     const float nan = __int_as_float(0x7fc00000), be = beta[i];
     const float kf = flag & 1 ? 0.0f : sk.inv, qf = flag & 2 ? 0.0f : sq.inv;
     float *tok = reinterpret_cast<float *>(smem + R::tok);
-    tok[kTokBeta * 64 + i] = flag & 1 ? nan : be;
+    tok[kTokBeta * 64 + i] = flag & 1 ? 0.0f : be;
     tok[kTokX * 64 + i] = be * into * kf;
     tok[kTokL * 64 + i] = out * kf;
     tok[kTokY * 64 + i] = flag & 2 ? nan : p.s.scale * into * qf;
@@ -395,7 +387,10 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
     *reinterpret_cast<uint4 *>(smem + R::th + at) = hi;
     *reinterpret_cast<uint4 *>(smem + R::tl + at) = lo;
   } else if (lane == 0) {
-    *reinterpret_cast<float4 *>(smem + R::fac) = make_float4(expf(G[63] + Gl[63]), st.inv, sp.inv, 0.0f);
+    float first = 64.0f;
+    for (int i = 63; i >= 0; --i)
+      if (static_cast<int>(bad[i]) & 1) first = static_cast<float>(i);
+    *reinterpret_cast<float4 *>(smem + R::fac) = make_float4(expf(G[63] + Gl[63]), st.inv, sp.inv, first);
   }
   fence_proxy_async_smem();
   __syncthreads();

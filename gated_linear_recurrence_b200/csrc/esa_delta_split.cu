@@ -152,7 +152,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
     const float tops = top4(tops_);
     const Pow2 ps = pow2_scale(tops);
     const float xinv = ps.inv * sinv;
-    if (KEEP && threadIdx.x == 0) p.w.slice[c * 32 + kSliceS + slice] = tops > 0.0f ? xinv : 0.0f;
+    const Pow2 pss = store_scale(tops * sinv);
+    const float sf = pss.s * xinv;
+    if (KEEP && threadIdx.x == 0) p.w.slice[c * 32 + kSliceS + slice] = tops > 0.0f ? pss.inv : 0.0f;
     {
       float X[8][4], Y[8][4];
       zero_tiles(X);
@@ -162,11 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
         uint32_t hi[4], lo[4];
         split_a(S[2 * ks], S[2 * ks + 1], splat(ps.s), splat(ps.s), hi, lo);
         if constexpr (KEEP) {
-          __half *o = p.w.s16 + c * (D * D) + (dvw + g) * D + w * (D / 4) + 16 * ks + 2 * t4;
-          *reinterpret_cast<uint32_t *>(o) = hi[0];
-          *reinterpret_cast<uint32_t *>(o + 8) = hi[2];
-          *reinterpret_cast<uint32_t *>(o + 8 * D) = hi[1];
-          *reinterpret_cast<uint32_t *>(o + 8 * D + 8) = hi[3];
+          uint32_t x[4] = {hi[0], hi[1], hi[2], hi[3]};
+          if (sf != 1.0f) scale_h2(x, sf);
+          store_block(p.w.s16 + c * (D * D) + dvw * D + w * (D / 4) + 16 * ks, D, x, lane);
         }
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
@@ -225,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
     __syncthreads();
     // 2. U = R T^T for this warp's tokens: all of R up to them
     float topr = top4(tops_ + 4);
-    const bool cut = topr == __int_as_float(0x7f800000);
-    int first[2] = {64, 64};   // first token from which a row is not finite
+    const bool cut = topr == __int_as_float(0x7f800000) || fac.w < 64.0f;
+    int first[2] = {static_cast<int>(fac.w), static_cast<int>(fac.w)};   // first token from which a row is not finite
     if (cut) {
       topr = 0.0f;
 #pragma unroll 1
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
         get_tile(smem + L::mid + i * kTileF, r, lane);
 #pragma unroll
         for (int e = 3; e >= 0; --e)
-          if (!(fabsf(r[e]) <= 3.4028235e38f)) first[e >> 1] = 8 * i + 2 * t4 + (e & 1);
+          if (!(fabsf(r[e]) <= 3.4028235e38f)) first[e >> 1] = min(first[e >> 1], 8 * i + 2 * t4 + (e & 1));
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -382,11 +382,13 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
       if (r < len) *reinterpret_cast<uint4 *>(y + (row0 + n * kChunk + r) * ldy) = *reinterpret_cast<const uint4 *>(vr);
       if constexpr (KEEP) {
         __syncwarp();
-        const uint32_t u[4] = {own[0], own[2], own[1], own[3]};
+        const Pow2 pus = store_scale(topu);
+        uint32_t u[4] = {own[0], own[2], own[1], own[3]};
+        if (pus.s * uinv != 1.0f) scale_h2(u, pus.s * uinv);
         stsm4t(vw, u);
         __syncwarp();
         *reinterpret_cast<uint4 *>(p.w.u16 + (c * 64 + r) * D + dvw + 8 * (lane & 1)) = *reinterpret_cast<const uint4 *>(vr);
-        if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceU + slice] = topu > 0.0f ? uinv : 0.0f;
+        if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceU + slice] = cut ? __int_as_float(0x7fc00000) : topu > 0.0f ? pus.inv : 0.0f;
       }
     }
     __syncthreads();
@@ -461,7 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
     const float tops = top4(tops_);
     const Pow2 ps = pow2_scale(tops);
     const float xinv = ps.inv * sinv;
-    if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceDs + slice] = tops > 0.0f ? xinv : 0.0f;
+    const Pow2 pss = store_scale(tops * sinv);
+    const float sf = pss.s * xinv;
+    if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceDs + slice] = tops > 0.0f ? pss.inv : 0.0f;
     {
       float X[8][4];
       zero_tiles(X);
@@ -469,11 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
       for (int ks = 0; ks < KQ; ++ks) {
         uint32_t hi[4], lo[4];
         split_a(S[2 * ks], S[2 * ks + 1], splat(ps.s), splat(ps.s), hi, lo);
-        __half *o = p.w.ds16 + c * (D * D) + (dvw + g) * D + w * (D / 4) + 16 * ks + 2 * t4;
-        *reinterpret_cast<uint32_t *>(o) = hi[0];
-        *reinterpret_cast<uint32_t *>(o + 8) = hi[2];
-        *reinterpret_cast<uint32_t *>(o + 8 * D) = hi[1];
-        *reinterpret_cast<uint32_t *>(o + 8 * D + 8) = hi[3];
+        uint32_t x[4] = {hi[0], hi[1], hi[2], hi[3]};
+        if (sf != 1.0f) scale_h2(x, sf);
+        store_block(p.w.ds16 + c * (D * D) + dvw * D + w * (D / 4) + 16 * ks, D, x, lane);
 #pragma unroll
         for (int np = 0; np < 4; np += 2) {
           uint32_t b0[4], b1[4];
@@ -612,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
     __syncthreads();
     // 3. the quarter of dS^T, dv and du of this warp's tokens
     const float topu = top4(tops_ + 8);
-    const Pow2 pu = pow2_scale(topu), pl = pow2_scale(fmaxf(top4(tops_ + 12), topo));
+    const Pow2 pus = store_scale(topu), pl = pow2_scale(fmaxf(top4(tops_ + 12), topo));
     const float asc = fminf(pl.s, tops > 0.0f ? ps.s * scur * 68719476736.0f : __int_as_float(0x7f800000));
     {
       const float2 sc = splat(fac.x * (asc * sinv));
@@ -667,12 +669,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
       if (r < len) *reinterpret_cast<uint4 *>(dv + (row0 + n * kChunk + r) * ldc) = *reinterpret_cast<const uint4 *>(vr);
       __syncwarp();
       uint32_t x[4];
-      single_a(Uo[0], Uo[1], splat(pu.s), splat(pu.s), x);
+      single_a(Uo[0], Uo[1], splat(pus.s), splat(pus.s), x);
       const uint32_t u[4] = {x[0], x[2], x[1], x[3]};
       stsm4t(vw, u);
       __syncwarp();
       *reinterpret_cast<uint4 *>(p.w.r16 + (c * 64 + r) * D + dvw + 8 * (lane & 1)) = *reinterpret_cast<const uint4 *>(vr);
-      if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceR + slice] = topu > 0.0f ? pu.inv : 0.0f;
+      if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceR + slice] = topu > 0.0f ? pus.inv : 0.0f;
     }
     __syncthreads();
   }

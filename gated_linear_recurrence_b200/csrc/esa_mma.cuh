@@ -77,6 +77,14 @@ template <> __device__ __forceinline__ uint32_t pack_io<__nv_bfloat16>(float x, 
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// Bits of the largest magnitude of a 16-byte unit of 16-bit elements, as a
+// float32 (exact): NaN and infinity compare above every finite value.
+template <typename T>
+__device__ __forceinline__ uint32_t unit_top(uint4 v) {
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+  return __float_as_uint(unpack_io<T>(max(m & 0xffffu, m >> 16)).x);
+}
+
 // Power of two, of an exponent divisible by 8, that brings `top` (>= 0) to
 // [2^5, 2^13), and its inverse; 1 for zero.  Steps of 2^8 let the groups of a
 // tile have the same scale almost always; float16 has the room.
@@ -87,6 +95,35 @@ __device__ __forceinline__ Pow2 pow2_scale(float top) {
   int e = ((static_cast<int>(__float_as_uint(top) >> 23) - 132) >> 3) * 8;   // floor((exponent - 5) / 8) * 8
   e = top > 0.0f ? max(-120, min(e, 120)) : 0;
   return {__uint_as_float(static_cast<uint32_t>(127 - e) << 23), __uint_as_float(static_cast<uint32_t>(127 + e) << 23)};
+}
+
+// Scale of a group that another kernel reads as one float16 term: 2^8 for any
+// largest value in [2^-9, 2^7), so that the groups of a tile agree and need not
+// be brought together there; else that of pow2_scale.
+__device__ __forceinline__ Pow2 store_scale(float top) {
+  if (top >= 0.001953125f && top < 128.0f) return {256.0f, 0.00390625f};
+  return pow2_scale(top);
+}
+__device__ __forceinline__ void scale_h2(uint32_t (&r)[4], float f) {
+  const __half2 s = __float2half2_rn(f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&r[i]), s);
+    r[i] = *reinterpret_cast<const uint32_t *>(&x);
+  }
+}
+
+// Store a 16 x 16 float16 block held as an A operand, rows `ld` elements apart.
+// Neighbouring lanes exchange one register of each row's two, so that four
+// lanes write the 32 bytes of a row (a whole sector) with 8-byte stores.
+__device__ __forceinline__ void store_block(__half *p, int ld, const uint32_t (&a)[4], int lane) {
+  const bool odd = lane & 1;
+  const int g = lane >> 2, t4 = lane & 3;
+  const uint32_t x0 = __shfl_xor_sync(0xffffffffu, odd ? a[0] : a[2], 1);
+  const uint32_t x1 = __shfl_xor_sync(0xffffffffu, odd ? a[1] : a[3], 1);
+  __half *o = p + g * ld + (odd ? 8 : 0) + 2 * (t4 & 2);
+  *reinterpret_cast<uint2 *>(o) = odd ? make_uint2(x0, a[2]) : make_uint2(a[0], x0);
+  *reinterpret_cast<uint2 *>(o + 8 * ld) = odd ? make_uint2(x1, a[3]) : make_uint2(a[1], x1);
 }
 
 // Largest |x| of the warp (a NaN is passed over unless all are).

@@ -328,3 +328,39 @@ def test_refusals(cuda_device):
         wide = torch.zeros(1, 8, 2 * 64 + 4, dtype=torch.bfloat16, device="cuda")
         w = wide[..., :128].view(1, 8, 2, 64)
         esa_delta_fwd(w, w, v, a, b)
+
+
+@pytest.mark.parametrize("dt,D,H", [("bf16", 128, 2), ("f16", 64, 2), ("bf16", 32, 2), ("f32", 64, 2), ("bf16", 128, 40),
+                                    ("f16", 128, 80), ("bf16", 64, 80)])
+@pytest.mark.parametrize("what", ["v_nan", "v_inf", "k_nan", "q_nan", "S_nan"])
+def test_values_that_are_not_finite_stay_where_they_belong(cuda_device, dt, D, H, what):
+    """A value channel is poisoned from its token on, a key poisons its head from its token on, a query its token
+    alone; earlier tokens, other channels and other heads keep their results."""
+    T = 150
+    x, S0, _ = draw(dt, 1, T, H, D, seed=20)
+    bad = float("inf") if what == "v_inf" else float("nan")
+    if what[0] == "S":
+        S0[0, 1, 3, 5] = bad
+    else:
+        x[what[0]][0, 70, 1, 5] = bad
+    y, S, _ = esa_delta_fwd(*ins(x), S_init=S0)
+    ref = delta_reference(*(t[:, :, :3] for t in ins(x)), D ** -0.5, S0[:, :3])
+    got = {"y": y[:, :, :3].cpu(), "S": S[:, :3].cpu()}
+    for n in ("y", "S"):
+        fine = torch.isfinite(ref[n])
+        assert torch.equal(torch.isfinite(got[n]), fine), n
+        extra = 3 * 2.0 ** -11 if n == "y" and dt != "f32" else 0.0
+        assert_within(n, torch.where(fine, got[n], torch.zeros_like(got[n])), torch.where(fine, ref[n], 0.0),
+                      PER_TOKEN * T + extra, PER_TOKEN * T ** 0.5 + extra)
+
+
+@pytest.mark.parametrize("D,H", [(128, 18), (128, 19), (128, 37), (128, 38), (128, 75), (64, 37), (64, 38), (32, 150)])
+def test_every_spread_of_heads(cuda_device, D, H):
+    """The head counts at which the work is spread differently over the device; two heads of each are checked."""
+    T = 100
+    x, S0, dS = draw("bf16", 1, T, H, D, seed=H)
+    out = run(x, S0, dS, D ** -0.5)
+    pick = [0, H - 1]
+    cut = {n: (t[:, pick] if n in ("S", "dS0") else t[:, :, pick]) for n, t in out.items()}
+    xs = {n: t[:, :, pick] for n, t in x.items()}
+    check(xs, cut, delta_reference(*ins(xs), D ** -0.5, S0[:, pick], xs["dy"], dS[:, pick]), T, D, half_p=3 * 2.0 ** -11)
