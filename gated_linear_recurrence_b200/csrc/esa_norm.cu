@@ -13,13 +13,11 @@ namespace {
 
 int elem(int dtype) { return dtype == ESA_F32 ? 4 : 2; }
 
-// Elements per vector: 16 bytes of the I/O type, or two 16-bit elements, or
-// one, the first of which divides N and every row stride and suits every
-// pointer's alignment.
+// Elements per vector: 16, 8, 4 or 2 bytes of the I/O type, the first of which
+// divides N and every row stride and suits every pointer's alignment.
 int pick_vec(int dtype, int wdtype, int N, std::initializer_list<long long> lds, std::initializer_list<const void *> io,
              std::initializer_list<const void *> wt) {
-  for (const int vec : {16 / elem(dtype), 2, 1}) {
-    if (vec == 2 && dtype == ESA_F32) continue;
+  for (int vec = 16 / elem(dtype); vec > 1; vec >>= 1) {
     bool ok = N % vec == 0;
     for (long long ld : lds) ok = ok && ld % vec == 0;
     for (const void *p : io) ok = ok && (p == nullptr || aligned_to(p, vec * elem(dtype)));
@@ -31,18 +29,13 @@ int pick_vec(int dtype, int wdtype, int N, std::initializer_list<long long> lds,
 }
 
 // A row of `nvec` vectors: part of a warp with one vector a thread while it
-// fits, then a warp with up to four, then 256 to 1024 threads with two (more
-// only for rows wider than that).
-NormRow row_shape(int nvec) {
-  int tpr = 4;
+// fits, a warp with up to `most`, then as few threads as hold it with `most`.
+NormRow norm_row(int nvec, int most) {
+  int tpr = 4, nv = 1;
   while (tpr < 32 && tpr < nvec) tpr <<= 1;
-  if (nvec > 32 * 4) {
-    tpr = 256;
-    while (tpr < 1024 && tpr * 2 < nvec) tpr <<= 1;
-  }
-  int nv = 1;
+  while (tpr >= 32 && tpr * most < nvec) tpr <<= 1;
   while (nv * tpr < nvec) nv <<= 1;
-  return {tpr, nv};
+  return {tpr, tpr > 32 ? most : nv};
 }
 
 int check_norm(long long rows, int N, int dtype, int wdtype) {
@@ -58,17 +51,8 @@ int check_norm(long long rows, int N, int dtype, int wdtype) {
 
 bool bad_ld(long long ld, int N) { return ld < N || ld > INT_MAX; }
 
-// Blocks of the backward: at most four of 256 threads (one of 1024) per SM,
-// never more than there are rows to share out.  Depends on the shape only, so
-// the caller can size the workspace.
-int bwd_grid(long long rows, NormRow s, int sms) {
-  const int block = s.tpr > 256 ? s.tpr : 256, groups = s.tpr > 32 ? 1 : block / s.tpr;
-  const long long most = (rows + groups - 1) / groups;
-  const long long full = static_cast<long long>(sms) * (1024 / block);
-  return static_cast<int>(most < full ? most : full);
-}
-
-constexpr int kMaxBwdBlocks = 1024;
+// Partial rows of the column sums.
+int max_blocks(int N) { return N <= 1024 ? 2368 : 1184; }
 
 }  // namespace
 }  // namespace esa
@@ -79,7 +63,7 @@ extern "C" {
 
 size_t esa_norm_workspace_size(long long rows, int N, int dtype, int wdtype) {
   if (check_norm(rows, N, dtype, wdtype) != ESA_OK) return 0;
-  const long long blocks = rows < kMaxBwdBlocks ? (rows > 0 ? rows : 1) : kMaxBwdBlocks;
+  const long long most = max_blocks(N), blocks = rows < most ? (rows > 0 ? rows : 1) : most;
   return static_cast<size_t>(blocks) * 2 * N * sizeof(float);
 }
 
@@ -104,7 +88,7 @@ int esa_norm_fwd(const void *x, long long ld_x, const void *residual, long long 
   NormFwdArgs a{x, residual, weight, bias, y, h, reinterpret_cast<float2 *>(stats), rows, ld_x, ld_res, N, eps,
                 static_cast<float>(N)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const NormRow shape = row_shape(N / vec);
+  const NormRow shape = norm_row(N / vec, kNormFwdElems / vec);
   const bool wide = wdtype == ESA_F32;
   if (dtype == ESA_F32) return norm_fwd_f32(vec, shape, a, st);
   return dtype == ESA_F16 ? norm_fwd_f16(vec, shape, wide, a, st) : norm_fwd_bf16(vec, shape, wide, a, st);
@@ -135,15 +119,14 @@ int esa_norm_bwd(const void *dy, long long ld_dy, const void *h, long long ld_h,
     return dbias ? runtime_status(cudaMemsetAsync(dbias, 0, static_cast<size_t>(N) * ws, st)) : ESA_OK;
   }
   const int vec = pick_vec(dtype, wdtype, N, {ld_dy, ld_h, dh ? ld_dh : 0}, {dy, h, dh, dx}, {weight});
-  const NormRow shape = row_shape(N / vec);
-  int grid = bwd_grid(rows, shape, sm_count());
-  if (grid > kMaxBwdBlocks) grid = kMaxBwdBlocks;
+  const NormRow shape = norm_row(N / vec, kNormBwdElems / vec);
+  const int most = max_blocks(N);
   NormBwdArgs a{dy, h, weight, dh, dx, reinterpret_cast<const float2 *>(stats), dweight, dbias,
                 sums ? static_cast<float *>(workspace) : nullptr, rows, ld_dy, ld_h, ld_dh, N,
                 static_cast<float>(N)};
   const bool wide = wdtype == ESA_F32;
-  if (dtype == ESA_F32) return norm_bwd_f32(vec, shape, a, grid, st);
-  return dtype == ESA_F16 ? norm_bwd_f16(vec, shape, wide, a, grid, st) : norm_bwd_bf16(vec, shape, wide, a, grid, st);
+  if (dtype == ESA_F32) return norm_bwd_f32(vec, shape, a, most, st);
+  return dtype == ESA_F16 ? norm_bwd_f16(vec, shape, wide, a, most, st) : norm_bwd_bf16(vec, shape, wide, a, most, st);
 }
 
 }  // extern "C"

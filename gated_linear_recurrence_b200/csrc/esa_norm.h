@@ -6,7 +6,9 @@
 
 namespace esa {
 
-constexpr int kNormMaxN = 16384;   // the widest row: 1024 threads of 16 elements
+constexpr int kNormMaxN = 16384;    // the widest row: 1024 threads of 16 elements
+constexpr int kNormFwdElems = 32;   // most elements a thread, forward and backward
+constexpr int kNormBwdElems = 16;
 
 // Threads of a row and vectors of a thread.
 struct NormRow {
@@ -34,12 +36,12 @@ struct NormBwdArgs {
 };
 
 // wide: the weight, the bias and their gradients are float32 (else the I/O
-// type).  vec: elements per vector, one of 16 bytes' worth, 2 (16-bit types), 1.
+// type).  vec: elements per vector: 16, 8, 4 or 2 bytes' worth.
 int norm_fwd_f32(int vec, NormRow s, const NormFwdArgs &a, cudaStream_t st);
 int norm_fwd_f16(int vec, NormRow s, bool wide, const NormFwdArgs &a, cudaStream_t st);
 int norm_fwd_bf16(int vec, NormRow s, bool wide, const NormFwdArgs &a, cudaStream_t st);
-int norm_bwd_f32(int vec, NormRow s, const NormBwdArgs &a, int grid, cudaStream_t st);
-int norm_bwd_f16(int vec, NormRow s, bool wide, const NormBwdArgs &a, int grid, cudaStream_t st);
-int norm_bwd_bf16(int vec, NormRow s, bool wide, const NormBwdArgs &a, int grid, cudaStream_t st);
+int norm_bwd_f32(int vec, NormRow s, const NormBwdArgs &a, int most, cudaStream_t st);
+int norm_bwd_f16(int vec, NormRow s, bool wide, const NormBwdArgs &a, int most, cudaStream_t st);
+int norm_bwd_bf16(int vec, NormRow s, bool wide, const NormBwdArgs &a, int most, cudaStream_t st);
 
 }  // namespace esa

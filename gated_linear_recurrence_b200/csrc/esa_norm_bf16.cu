@@ -5,7 +5,7 @@ namespace esa {
 int norm_fwd_bf16(int vec, NormRow s, bool wide, const NormFwdArgs &a, cudaStream_t st) {
   return wide ? norm_fwd_typed<__nv_bfloat16, float>(vec, s, a, st) : norm_fwd_typed<__nv_bfloat16, __nv_bfloat16>(vec, s, a, st);
 }
-int norm_bwd_bf16(int vec, NormRow s, bool wide, const NormBwdArgs &a, int grid, cudaStream_t st) {
-  return wide ? norm_bwd_typed<__nv_bfloat16, float>(vec, s, a, grid, st) : norm_bwd_typed<__nv_bfloat16, __nv_bfloat16>(vec, s, a, grid, st);
+int norm_bwd_bf16(int vec, NormRow s, bool wide, const NormBwdArgs &a, int most, cudaStream_t st) {
+  return wide ? norm_bwd_typed<__nv_bfloat16, float>(vec, s, a, most, st) : norm_bwd_typed<__nv_bfloat16, __nv_bfloat16>(vec, s, a, most, st);
 }
 }  // namespace esa

@@ -5,7 +5,7 @@ namespace esa {
 int norm_fwd_f32(int vec, NormRow s, const NormFwdArgs &a, cudaStream_t st) {
   return norm_fwd_typed<float, float>(vec, s, a, st);
 }
-int norm_bwd_f32(int vec, NormRow s, const NormBwdArgs &a, int grid, cudaStream_t st) {
-  return norm_bwd_typed<float, float>(vec, s, a, grid, st);
+int norm_bwd_f32(int vec, NormRow s, const NormBwdArgs &a, int most, cudaStream_t st) {
+  return norm_bwd_typed<float, float>(vec, s, a, most, st);
 }
 }  // namespace esa
