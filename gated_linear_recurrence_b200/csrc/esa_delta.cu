@@ -19,11 +19,12 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 constexpr int kChunkMinT = 17;
 bool chunked(const DeltaShape &s, int dtype) { return dtype != ESA_F32 && s.T >= kChunkMinT; }
 
-// What the forward keeps for the backward (u), then the backward's scratch.
+// Token by token: what the forward keeps for the backward (u, the state at
+// each chunk), then the backward's scratch.
 struct DeltaLayout {
-  size_t u = 0, du = 0, dk = 0, dq = 0, gain = 0, end = 0, total = 0;
+  int nc = 0;
+  size_t u = 0, S_ck = 0, dS_ck = 0, du = 0, dk = 0, dq = 0, gain = 0, end = 0, total = 0;
 };
-
 // The chunk arrays, laid out from `base`; `*total` gets their size.
 ChunkArrays chunk_arrays(unsigned char *base, const DeltaShape &s, bool keep, size_t *total) {
   ChunkArrays w{};
@@ -51,16 +52,19 @@ ChunkArrays chunk_arrays(unsigned char *base, const DeltaShape &s, bool keep, si
 
 DeltaLayout delta_layout(const DeltaShape &s, bool keep) {
   DeltaLayout lo;
-  const size_t n = static_cast<size_t>(s.B) * s.T * s.H;
+  lo.nc = (s.T + 63) / 64;
+  const size_t n = static_cast<size_t>(s.B) * s.T * s.H, chunks = static_cast<size_t>(s.B) * s.H * lo.nc;
   size_t o = 0;
   if (keep) {
-    const size_t rows = up256(n * s.D * sizeof(float));
+    const size_t rows = up256(n * s.D * sizeof(float)), states = up256(chunks * s.D * s.D * sizeof(float));
     lo.u = o; o += rows;
+    lo.S_ck = o; o += states;
+    lo.dS_ck = o; o += states;
     lo.du = o; o += rows;
     lo.dk = o; o += rows;
     lo.dq = o; o += rows;
     lo.gain = o; o += up256(n * sizeof(float));
-    lo.end = o; o += up256(static_cast<size_t>(s.B) * s.H * (s.D / 16) * sizeof(float));
+    lo.end = o; o += up256(chunks * (s.D * s.D / 1024) * sizeof(float));
   }
   lo.total = o;
   return lo;
@@ -162,7 +166,12 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
   p.S_in = S_init;
   p.S_out = S_final;
   p.y = y;
-  p.u = keep ? reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + lo.u) : nullptr;
+  p.nc = lo.nc;
+  if (keep) {
+    unsigned char *base = static_cast<unsigned char *>(workspace);
+    p.u = reinterpret_cast<float *>(base + lo.u);
+    p.S_ck = reinterpret_cast<float *>(base + lo.S_ck);
+  }
   return launch_sweep(kSweepFwd, dtype, p, st);
 }
 
@@ -209,16 +218,17 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
   p.dk = reinterpret_cast<float *>(base + lo.dk);
   p.dq = reinterpret_cast<float *>(base + lo.dq);
   p.end = reinterpret_cast<float *>(base + lo.end);
+  p.S_ck = reinterpret_cast<float *>(base + lo.S_ck);
+  p.dS_ck = reinterpret_cast<float *>(base + lo.dS_ck);
+  p.nc = lo.nc;
   p.S_in = dS_final;
   p.S_out = dS_init;
   if ((rc = launch_sweep(kSweepDu, dtype, p, st))) return rc;
-  p.S_out = nullptr;
   if ((rc = launch_sweep(kSweepDk, dtype, p, st))) return rc;
-  p.S_in = S_init;
-  p.dS_final = dS_final;
   if ((rc = launch_sweep(kSweepDq, dtype, p, st))) return rc;
   FinishArgs f{};
   f.s = s;
+  f.nc = lo.nc;
   f.q = q; f.v = v; f.a = a; f.b = b;
   f.u = p.u; f.du = p.du; f.dkf = p.dk; f.dqf = p.dq; f.end = p.end;
   f.gain = reinterpret_cast<float *>(base + lo.gain);
@@ -244,7 +254,7 @@ int esa_delta_step(const void *q_t, const void *k_t, const void *v_t, const void
   p.S_in = S;
   p.S_out = S;
   p.y = y_t;
-  return launch_sweep(kSweepFwd, dtype, p, static_cast<cudaStream_t>(stream));
+  return launch_delta_step(dtype, p, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

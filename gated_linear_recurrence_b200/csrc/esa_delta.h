@@ -22,20 +22,24 @@ struct SweepArgs {
   const void *q, *k, *v, *dy, *a, *b;   // I/O type
   const float *S_in;                    // state (or its gradient) before the first token visited; NULL = zeros
   float *S_out;                         // after the last one; NULL = not written
-  const float *dS_final;                // forward row sweep: joined with the final state
   void *y;                              // forward sweep's output, I/O type
-  float *u, *du, *dk, *dq, *end;        // float32 scratch, [B,T,H,D] and [B,H,D/16]
+  float *u, *du, *dk, *dq;              // float32 scratch, [B,T,H,D]
+  float *S_ck, *dS_ck;                  // [B,H,nc,D,D] state entering, gradient leaving each chunk of 64 tokens
+  float *end;                           // [B,H,nc,D*D/1024] parts of their inner product at the chunk's end
+  int nc;
 };
 
 // Kinds of sweep.
 enum { kSweepFwd = 0, kSweepDu = 1, kSweepDk = 2, kSweepDq = 3 };
 
 int launch_sweep(int kind, int dtype, const SweepArgs &a, cudaStream_t st);
+int launch_delta_step(int dtype, const SweepArgs &a, cudaStream_t st);   // one token, S_in = S_out
 
 struct FinishArgs {
   DeltaShape s;
   const void *q, *v, *a, *b;
   const float *u, *du, *dkf, *dqf, *end;
+  int nc;
   float *gain;   // [B,H,T]
   void *dq, *dk, *dv, *da, *db;
 };

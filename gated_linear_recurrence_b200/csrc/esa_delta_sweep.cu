@@ -8,19 +8,20 @@
 namespace esa {
 namespace {
 
-// Warps per block (16 independent entries each): all of a head's when the
-// heads alone give every SM two blocks, else fewer, so that a small batch
-// still spreads over the device; one decode step of 8 heads at D = 64 is 32
-// blocks of one warp instead of 8 of four.
-int sweep_warps(int heads, int D) {
-  int W = D / sweep::COLS;
-  while (W > 1 && static_cast<long long>(heads) * (D / sweep::COLS / W) < 2 * sm_count()) W >>= 1;
+// Warps per block: all of a head's when whole heads (or chunks of them) give
+// every SM two blocks, else fewer, so that a small batch still spreads over
+// the device.
+int sweep_warps(long long units, int most) {
+  int W = most;
+  while (W > 1 && units * (most / W) < 2 * sm_count()) W >>= 1;
   return W;
 }
 
 template <typename T, int D, int KIND>
 int run(const SweepArgs &a, cudaStream_t st) {
-  const int heads = a.s.B * a.s.H, W = sweep_warps(heads, D);
+  const long long heads = static_cast<long long>(a.s.B) * a.s.H;
+  const long long units = KIND == kSweepFwd || KIND == kSweepDu ? heads : heads * a.nc;
+  const int W = sweep_warps(units, D / sweep::columns<D>());
   const sweep::Layout<T, D, KIND> lo(W);
   auto kern = sweep::delta_sweep_kernel<T, D, KIND>;
   if (lo.total > 48 * 1024) {
@@ -28,7 +29,7 @@ int run(const SweepArgs &a, cudaStream_t st) {
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lo.total)));
     if (rc) return rc;
   }
-  kern<<<static_cast<unsigned>(heads) * (D / lo.cols), W * 32, lo.total, st>>>(a);
+  kern<<<static_cast<unsigned>(units * (D / lo.cols)), W * 32, lo.total, st>>>(a);
   return runtime_status(cudaGetLastError());
 }
 
@@ -62,7 +63,8 @@ int finish(const FinishArgs &a, cudaStream_t st) {
     case 128: sweep::delta_finish_kernel<T, 128><<<grid, 256, 0, st>>>(a); break;
     default: return ESA_ERR_UNSUPPORTED;
   }
-  sweep::delta_da_kernel<T><<<a.s.B * a.s.H, 256, 0, st>>>(a, a.s.D / sweep::COLS);
+  const long long chunks = static_cast<long long>(a.s.B) * a.s.H * a.nc;
+  sweep::delta_da_kernel<T><<<static_cast<unsigned>((chunks + 7) / 8), 256, 0, st>>>(a, a.s.D * a.s.D / 1024);
   return runtime_status(cudaGetLastError());
 }
 

@@ -4,29 +4,32 @@
 //   u_t = beta_t (v_t - alpha_t S_{t-1}^T k_t),  S_t = alpha_t S_{t-1} + k_t u_t^T,
 //   y_t = scale S_t^T q_t,      S [D key channels][D value channels], float32.
 //
-// A sweep keeps a matrix M in registers and visits the tokens in order.  M has
-// a split axis (its D entries are shared by 8 lanes, which sum their parts of
-// each dot product by shuffles) and an independent axis (4 entries a thread,
-// 16 a warp, no communication).  The forward is split over the key channels:
-// every value channel is a recurrence of its own.  The gradients need both
-// orientations, so the backward is three more sweeps, each with two dot
-// products or one and one or two rank-one updates per token:
-//   kSweepFwd  forward,  M = S,  split = key:   u (kept for the backward), y, S_T
-//   kSweepDu   backward, M = dS, split = key:   du_t = dS_t^T k_t with dS_t += scale q_t dy_t^T first,
-//                                               then dS <- alpha_t (dS - beta_t k_t du_t^T);  dS_init
-//   kSweepDk   backward, M = dS^T, split = value: dk_t = dS_t u_t
-//   kSweepDq   forward,  M = S^T, split = value:  dk_t -= alpha_t beta_t S_{t-1} du_t, dq_t = scale S_t dy_t,
-//                                               and <S_T, dS_final>
-// All arithmetic is float32, as the state is; this is the path of float32
-// tensors, of short sequences (a decode step is a sweep of one token) and of
-// D = 32.  It is bound by float32 issue: 8 D^2 multiply-adds (packed in pairs)
-// a token forward, so at D = 128 about 1.4 ns a token and head with every SM
-// busy, and by the latency of one token (a dot product, three shuffles, a
-// broadcast) when there are few heads.  More warps per block share the
-// staged rows; fewer give more blocks: see sweep_warps().
+// A sweep keeps a matrix M in registers and visits the tokens in order.  D / 32
+// neighbouring lanes share one entry of M's independent axis, 32 entries of
+// the other, the split axis, each; a dot product over the split axis is 32
+// multiply-adds a lane and log2(D / 32) shuffles, and the update needs no
+// other thread.  The forward has M = S with its value channels independent:
+// each is a recurrence of its own.  The gradients need both orientations:
+//   kSweepFwd  forward,  M = S:    u (kept for the backward), y, S_T; the state entering each chunk of 64 tokens
+//   kSweepDu   backward, M = dS:   du_t = dS_t^T k_t with dS_t += scale q_t dy_t^T first, then
+//                                  dS <- alpha_t (dS - beta_t k_t du_t^T); dS_init; the gradient leaving each chunk
+//   kSweepDk   backward, M = dS^T: dk_t = dS_t u_t
+//   kSweepDq   forward,  M = S^T:  dk_t -= alpha_t beta_t S_{t-1} du_t, dq_t = scale S_t dy_t, <dS, S> at each chunk's end
+// The first two pass over the whole sequence; the last two start every chunk
+// from what those left and take all chunks at once.
 //
-// Rows are staged 16 tokens at a time: cp.async into a double buffer in the
-// tensors' own type, then widened once to float32 for all warps of the block.
+// All arithmetic is float32, as the state is; this is the path of float32
+// tensors and of short sequences (a decode step is a sweep of one token).
+// With few heads it is bound by the latency of a token (load k, dot, shuffles,
+// update), with many by the issue of some 200 instructions a token, warp and
+// 32 x 32 of the state.  Measured a token, few heads: TOK32 ns at D = 32, TOK64
+// at 64, TOK128 at 128.  (Columns shared by 8 lanes whatever D: 390, 450,
+// 600; a whole column a thread: 312, 448, 924, since one warp then issues all
+// of it.)  More warps per block share the staged rows; fewer give more blocks:
+// see sweep_warps().
+//
+// Rows are staged 16 or 32 tokens at a time: cp.async into a double buffer in
+// the tensors' own type, then widened once to float32 for the block's warps.
 #pragma once
 
 #include "esa_common.cuh"
@@ -35,10 +38,10 @@
 namespace esa {
 namespace sweep {
 
-constexpr int TC = 16;      // tokens staged at a time
-constexpr int SPLIT = 8;    // lanes that share the split axis
-constexpr int PER = 4;      // independent entries a thread
-constexpr int COLS = 16;    // independent entries a warp
+constexpr int CHUNK = 64;    // tokens between the states that are kept
+template <int D> constexpr int lanes() { return D / 32; }         // that share the split axis
+template <int D> constexpr int columns() { return 32 / lanes<D>(); }   // independent entries a warp
+template <int D> constexpr int tokens() { return D == 128 ? 16 : 32; }   // staged at a time
 
 __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(__half v) { return __half2float(v); }
@@ -90,17 +93,18 @@ template <typename T> struct Rows<T, kSweepDu> { static constexpr bool x0f = fal
 template <typename T> struct Rows<T, kSweepDk> { static constexpr bool x0f = true, x2 = true, y1 = true; };
 template <typename T> struct Rows<T, kSweepDq> { static constexpr bool x0f = true, x2 = true, y1 = false; };
 
-// Shared memory, in floats and bytes, for W warps.
+// Shared memory, byte offsets, for W warps.
 template <typename T, int D, int KIND>
 struct Layout {
   using R = Rows<T, KIND>;
   static constexpr bool kWide = sizeof(T) == 4;
+  static constexpr int TC = tokens<D>();
   int cols;
-  size_t x0, x1, x2, y0, y1, raw;    // raw buffer (one stage): byte offsets
-  size_t fx0, fx1, fy0, fy1, tok;    // widened rows and per-token scalars: byte offsets from the start
+  size_t x0, x1, x2, y0, y1, raw;    // raw buffer (one stage)
+  size_t fx0, fx1, fy0, fy1, tok;    // widened rows and per-token scalars, from the start
   size_t total;
   __host__ __device__ explicit Layout(int W) {
-    cols = COLS * W;
+    cols = columns<D>() * W;
     size_t o = 0;
     x0 = o; o += static_cast<size_t>(TC) * D * (R::x0f ? 4 : sizeof(T));
     x1 = o; o += static_cast<size_t>(TC) * D * sizeof(T);
@@ -113,74 +117,75 @@ struct Layout {
     fx1 = o; o += kWide ? 0 : static_cast<size_t>(TC) * D * 4;
     fy0 = o; o += kWide ? 0 : static_cast<size_t>(TC) * cols * 4;
     fy1 = o; o += kWide || !R::y1 ? 0 : static_cast<size_t>(TC) * cols * 4;
-    tok = o; o += 3 * TC * sizeof(float);
+    tok = o; o += 2 * TC * sizeof(float);
     total = o;
   }
 };
 
 template <typename T, int D, int KIND>
-__global__ void __launch_bounds__(D * 2) delta_sweep_kernel(SweepArgs p) {
+__global__ void __launch_bounds__(D * lanes<D>()) delta_sweep_kernel(SweepArgs p) {
   constexpr bool kReverse = KIND == kSweepDu || KIND == kSweepDk;
-  constexpr bool kCols = KIND == kSweepFwd || KIND == kSweepDu;   // split over the key channels
-  constexpr int RPT = D / SPLIT;                                  // split entries a thread
-  constexpr int M4 = RPT / 4;
+  constexpr bool kCols = KIND == kSweepFwd || KIND == kSweepDu;   // whole sequences, value channels independent
+  constexpr int TC = tokens<D>(), SP = lanes<D>();
   using R = Rows<T, KIND>;
   extern __shared__ __align__(16) unsigned char smem[];
   const int W = blockDim.x >> 5;
   const Layout<T, D, KIND> lo(W);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = lane & 7, cg = lane >> 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sl = threadIdx.x % SP, jj = threadIdx.x / SP;
   const int slices = D / lo.cols;
   const int slice = blockIdx.x % slices;
-  const int head = blockIdx.x / slices;                // b H + h
+  int head = blockIdx.x / slices, chunk = 0;           // head = b H + h
+  if (!kCols) {
+    chunk = head % p.nc;
+    head /= p.nc;
+  }
   const int b = head / p.s.H, h = head - b * p.s.H;
-  const int c_blk = slice * lo.cols;                   // first independent entry of the block
-  const int c_thr = c_blk + warp * COLS + cg * PER;    // and of this thread
-  const int T_ = p.s.T;
-  const long long tok0 = static_cast<long long>(b) * T_;
+  const int c_blk = slice * lo.cols, j = c_blk + jj;   // first independent entry of the block, this thread's
+  const int t_begin = kCols ? 0 : chunk * CHUNK, t_end = kCols ? p.s.T : min(p.s.T, t_begin + CHUNK);
+  const long long tok0 = static_cast<long long>(b) * p.s.T;
   const long long ldc = static_cast<long long>(p.s.H) * D;   // contiguous rows (dy, y, scratch)
+  const long long state0 = static_cast<long long>(head) * D * D;
 
-  // M in registers: entry (split i, independent j) at m[j][i / 2], pairs along the split axis;
-  // this lane's split entries are 32 g + 4 r + 0..3.
-  float2 m[PER][RPT / 2];
-  const float *Sin = p.S_in ? p.S_in + static_cast<long long>(head) * D * D : nullptr;
+  // This lane's split entries: 4 (SP i + sl) + 0..3 at m[2 i], m[2 i + 1]
+  float2 m[16];
+  if constexpr (kCols) {
+    const float *Sin = p.S_in ? p.S_in + state0 + 4 * sl * D + j : nullptr;
 #pragma unroll
-  for (int g = 0; g < M4; ++g) {
-    const int i0 = 32 * g + 4 * r;
-    if (Sin == nullptr) {
+    for (int i = 0; i < 16; ++i) {
+      const int r = 4 * SP * (i >> 1) + 2 * (i & 1);
+      m[i] = Sin ? make_float2(Sin[r * D], Sin[(r + 1) * D]) : make_float2(0.0f, 0.0f);
+    }
+  } else {
+    const float4 *Sin = reinterpret_cast<const float4 *>(
+        (KIND == kSweepDk ? p.dS_ck : p.S_ck) + (static_cast<long long>(head) * p.nc + chunk) * D * D + j * D) + sl;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) m[j][2 * g] = m[j][2 * g + 1] = make_float2(0.0f, 0.0f);
-    } else if (kCols) {
-      float4 row[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) row[e] = *reinterpret_cast<const float4 *>(Sin + (i0 + e) * D + c_thr);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m[0][2 * g + e] = make_float2(row[2 * e].x, row[2 * e + 1].x);
-        m[1][2 * g + e] = make_float2(row[2 * e].y, row[2 * e + 1].y);
-        m[2][2 * g + e] = make_float2(row[2 * e].z, row[2 * e + 1].z);
-        m[3][2 * g + e] = make_float2(row[2 * e].w, row[2 * e + 1].w);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const float4 x = *reinterpret_cast<const float4 *>(Sin + (c_thr + j) * D + i0);
-        m[j][2 * g] = make_float2(x.x, x.y);
-        m[j][2 * g + 1] = make_float2(x.z, x.w);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float4 x = Sin[SP * i];
+      m[2 * i] = make_float2(x.x, x.y);
+      m[2 * i + 1] = make_float2(x.z, x.w);
     }
   }
+  // M to [D][D] memory: the final state, and what enters (leaves) a chunk
+  auto keep = [&](float *base) {
+    float *o = base + 4 * sl * D + j;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 4 * SP * (i >> 1) + 2 * (i & 1);
+      o[r * D] = m[i].x;
+      o[(r + 1) * D] = m[i].y;
+    }
+  };
 
   const T *q = static_cast<const T *>(p.q) + h * D, *k = static_cast<const T *>(p.k) + h * D;
   const T *v = static_cast<const T *>(p.v), *dy = static_cast<const T *>(p.dy);
   const T *ga = static_cast<const T *>(p.a), *gb = static_cast<const T *>(p.b);
-  const int nch = (T_ + TC - 1) / TC;
+  const int nch = (t_end - t_begin + TC - 1) / TC;
 
   auto fetch = [&](int c, int buf) {
-    const int t0 = c * TC, n = min(TC, T_ - t0);
+    const int t0 = t_begin + c * TC, n = min(TC, t_end - t0);
     const long long row = tok0 + t0;
     unsigned char *s = smem + buf * lo.raw;
-    if constexpr (KIND == kSweepFwd || KIND == kSweepDu) {
+    if constexpr (kCols) {
       stage(reinterpret_cast<T *>(s + lo.x0), k + row * p.s.ld_qk, p.s.ld_qk, n, D);
       stage(reinterpret_cast<T *>(s + lo.x1), q + row * p.s.ld_qk, p.s.ld_qk, n, D);
       if constexpr (KIND == kSweepFwd)
@@ -201,21 +206,25 @@ __global__ void __launch_bounds__(D * 2) delta_sweep_kernel(SweepArgs p) {
   };
   float ga_next = 0.0f, gb_next = 0.0f;
   auto fetch_gates = [&](int c) {
-    const int t = c * TC + threadIdx.x;
-    if (threadIdx.x < TC && t < T_) {
+    const int t = t_begin + c * TC + threadIdx.x;
+    if (threadIdx.x < TC && t < t_end) {
       ga_next = widen(ga[(tok0 + t) * p.s.ld_g + h]);
       gb_next = widen(gb[(tok0 + t) * p.s.ld_g + h]);
     }
   };
 
-  float *tok = reinterpret_cast<float *>(smem + lo.tok);   // alpha, beta, dot, TC each
+  float *tok = reinterpret_cast<float *>(smem + lo.tok);   // alpha, beta, TC each
   if (nch > 0) {
     fetch(kReverse ? nch - 1 : 0, 0);
     fetch_gates(kReverse ? nch - 1 : 0);
   }
   for (int it = 0; it < nch; ++it) {
     const int c = kReverse ? nch - 1 - it : it, buf = it & 1;
-    const int t0 = c * TC, n = min(TC, T_ - t0);
+    const int t0 = t_begin + c * TC, n = min(TC, t_end - t0);
+    if constexpr (KIND == kSweepFwd)
+      if (p.S_ck != nullptr && t0 % CHUNK == 0) keep(p.S_ck + (static_cast<long long>(head) * p.nc + t0 / CHUNK) * D * D);
+    if constexpr (KIND == kSweepDu)
+      if (t0 + n == t_end || (t0 + n) % CHUNK == 0) keep(p.dS_ck + (static_cast<long long>(head) * p.nc + (t0 + n - 1) / CHUNK) * D * D);
     if (threadIdx.x < TC) {
       tok[threadIdx.x] = gate(ga_next);
       tok[TC + threadIdx.x] = gate(gb_next);
@@ -255,187 +264,119 @@ __global__ void __launch_bounds__(D * 2) delta_sweep_kernel(SweepArgs p) {
       __syncthreads();
     }
     if constexpr (R::x2) X2 = reinterpret_cast<const float *>(s + lo.x2);
-    // k.q (sweeps over columns) or u.dy (sweeps over rows) of each token
-    {
-      const float *d0 = KIND == kSweepDq ? X2 : X0;   // k, k, u, u
-      for (int t = warp; t < n; t += W) {
-        float x = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) x = fmaf(d0[t * D + 32 * i + lane], X1[t * D + 32 * i + lane], x);
-        x = head_sum<32>(x);
-        if (lane == 0) tok[2 * TC + t] = x;
-      }
-    }
-    __syncthreads();
 
-    for (int e = 0; e < n; ++e) {
-      const int t = kReverse ? n - 1 - e : e;
-      const float alpha = tok[t], beta = tok[TC + t], dot = tok[2 * TC + t];
-      const float4 *x0 = reinterpret_cast<const float4 *>(X0 + t * D) + r;
-      const float4 *x1 = reinterpret_cast<const float4 *>(X1 + t * D) + r;
-      float4 a0[M4], a1[M4];
+    const int step = kReverse ? -1 : 1;
+    int t = kReverse ? n - 1 : 0;
+    // the first operand of the coming token is loaded while this one is finished
+    float4 x[8];
+    float alpha, beta, in;
+    auto load = [&](const float *rows, int at) {
+      const float4 *r = reinterpret_cast<const float4 *>(rows + at * D) + sl;
 #pragma unroll
-      for (int g = 0; g < M4; ++g) {
-        a0[g] = x0[8 * g];
-        a1[g] = x1[8 * g];
-      }
-      const float4 in0 = *reinterpret_cast<const float4 *>(Y0 + t * lo.cols + warp * COLS + cg * PER);
-      const float i0[4] = {in0.x, in0.y, in0.z, in0.w};
-      const long long out = (tok0 + t0 + t) * ldc + h * D + c_thr;
-      // P_j = sum_i x0_i m_ij; Q_j = sum_i x1_i m_ij (forward kinds only)
-      float P[PER], Q[PER];
+      for (int i = 0; i < 8; ++i) x[i] = r[SP * i];
+      alpha = tok[at];
+      beta = tok[TC + at];
+      in = Y0[at * lo.cols + jj];
+    };
+    // sum over the lanes of an entry
+    auto total = [&](float2 a, float2 b, float2 c, float2 d) {
+      const float2 z = add2(add2(a, b), add2(c, d));
+      float f = z.x + z.y;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        float2 s0 = make_float2(0.0f, 0.0f), s1 = make_float2(0.0f, 0.0f);
+      for (int o = 1; o < SP; o <<= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+      return f;
+    };
+    load(KIND == kSweepDq ? X0 : KIND == kSweepDk ? X1 : KIND == kSweepDu ? X1 : X0, t);
+#pragma unroll 1
+    for (int e = 0; e < n; ++e, t += step) {
+      const long long out = (tok0 + t0 + t) * ldc + h * D + j;
+      const float2 al = splat(alpha);
+      const int next = e + 1 < n ? t + step : t;
+      float2 P[4];
 #pragma unroll
-        for (int g = 0; g < M4; ++g) {
-          s0 = fma2(make_float2(a0[g].x, a0[g].y), m[j][2 * g], s0);
-          s0 = fma2(make_float2(a0[g].z, a0[g].w), m[j][2 * g + 1], s0);
-          if constexpr (!kReverse) {
-            s1 = fma2(make_float2(a1[g].x, a1[g].y), m[j][2 * g], s1);
-            s1 = fma2(make_float2(a1[g].z, a1[g].w), m[j][2 * g + 1], s1);
-          }
+      for (int i = 0; i < 4; ++i) P[i] = make_float2(0.0f, 0.0f);
+      if constexpr (kReverse) {
+        // M += scale x1 in^T (dO, q or the other way round), then P = sum x0 M (k or u), then
+        // M <- alpha (M - beta k du^T).  x holds x1.
+        const float2 qs = splat(p.s.scale * in);
+        const float4 *x0 = reinterpret_cast<const float4 *>(X0 + t * D) + sl;
+        const float4 *x2 = reinterpret_cast<const float4 *>(KIND == kSweepDk ? X2 + t * D : X0 + t * D) + sl;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 a0 = x0[SP * i];
+          m[2 * i] = fma2(make_float2(x[i].x, x[i].y), qs, m[2 * i]);
+          m[2 * i + 1] = fma2(make_float2(x[i].z, x[i].w), qs, m[2 * i + 1]);
+          P[(2 * i) & 3] = fma2(make_float2(a0.x, a0.y), m[2 * i], P[(2 * i) & 3]);
+          P[(2 * i + 1) & 3] = fma2(make_float2(a0.z, a0.w), m[2 * i + 1], P[(2 * i + 1) & 3]);
         }
-        P[j] = s0.x + s0.y;
-        Q[j] = s1.x + s1.y;
-      }
-      // Sum over the 8 lanes of a column group by halving: a lane gives away
-      // the half of its values that its partner keeps.  After it lane r holds
-      // column r & 3 of P (r < 4) or of Q (r >= 4); the backward kinds have no
-      // Q and add the two halves instead, so both halves hold P.
-      float mine;
-      {
-        const bool hi = r & 4;
-        float x[4];
+        const float dp = total(P[0], P[1], P[2], P[3]);
+        const float ks = KIND == kSweepDk ? -beta * Y1[t * lo.cols + jj] : -beta * dp;
+        if (sl == 0) (KIND == kSweepDk ? p.dk : p.du)[out] = dp;
+        load(X1, next);
+        const float2 k2 = splat(ks);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (!kReverse) {
-            const float keep = hi ? Q[j] : P[j], give = hi ? P[j] : Q[j];
-            x[j] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
-          } else {
-            x[j] = P[j] + __shfl_xor_sync(0xffffffffu, P[j], 4);
-          }
-        }
-        const bool h2 = r & 2, h1 = r & 1;
-        const float k0 = h2 ? x[2] : x[0], k1 = h2 ? x[3] : x[1], g0 = h2 ? x[0] : x[2], g1 = h2 ? x[1] : x[3];
-        const float z0 = k0 + __shfl_xor_sync(0xffffffffu, g0, 2), z1 = k1 + __shfl_xor_sync(0xffffffffu, g1, 2);
-        mine = (h1 ? z1 : z0) + __shfl_xor_sync(0xffffffffu, h1 ? z0 : z1, 1);
-      }
-      const int jj = r & 3;                                           // the column (of this thread's 4) that `mine` is of
-      const float mi0 = jj < 2 ? (jj == 0 ? i0[0] : i0[1]) : (jj == 2 ? i0[2] : i0[3]);
-      if constexpr (KIND == kSweepFwd) {
-        // lanes 0-3: u; lanes 4-7: y = scale (alpha S^T q + (k.q) u)
-        float u = beta * fmaf(-alpha, mine, mi0);
-        const float u_other = __shfl_xor_sync(0xffffffffu, u, 4);
-        if (r >= 4)
-          static_cast<T *>(p.y)[out + jj] = narrow<T>(p.s.scale * fmaf(alpha, mine, dot * u_other));
-        else if (p.u != nullptr)
-          p.u[out + jj] = u;
-        float uu[PER];
-#pragma unroll
-        for (int j = 0; j < PER; ++j) uu[j] = __shfl_sync(0xffffffffu, u, (lane & 24) | j);
-        const float2 al = splat(alpha);
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const float2 us = splat(uu[j]);
-#pragma unroll
-          for (int g = 0; g < M4; ++g) {
-            m[j][2 * g] = fma2(make_float2(a0[g].x, a0[g].y), us, mul2(al, m[j][2 * g]));
-            m[j][2 * g + 1] = fma2(make_float2(a0[g].z, a0[g].w), us, mul2(al, m[j][2 * g + 1]));
-          }
-        }
-      } else if constexpr (KIND == kSweepDu) {
-        const float du = fmaf(p.s.scale * dot, mi0, mine);
-        if (r < 4) p.du[out + jj] = du;
-        float uu[PER];
-#pragma unroll
-        for (int j = 0; j < PER; ++j) uu[j] = __shfl_sync(0xffffffffu, du, (lane & 24) | j);
-        const float2 al = splat(alpha);
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const float2 ks = splat(-beta * uu[j]), qs = splat(p.s.scale * i0[j]);
-#pragma unroll
-          for (int g = 0; g < M4; ++g) {
-            m[j][2 * g] = mul2(al, fma2(make_float2(a0[g].x, a0[g].y), ks,
-                                        fma2(make_float2(a1[g].x, a1[g].y), qs, m[j][2 * g])));
-            m[j][2 * g + 1] = mul2(al, fma2(make_float2(a0[g].z, a0[g].w), ks,
-                                            fma2(make_float2(a1[g].z, a1[g].w), qs, m[j][2 * g + 1])));
-          }
-        }
-      } else if constexpr (KIND == kSweepDk) {
-        // x0 = u, x1 = dy, x2 = du; independent: q, k.  dk_i = sum_j dS_ij u_j + scale q_i (u.dy)
-        if (r < 4) p.dk[out + jj] = fmaf(p.s.scale * dot, mi0, mine);
-        const float4 in1 = *reinterpret_cast<const float4 *>(Y1 + t * lo.cols + warp * COLS + cg * PER);
-        const float i1[4] = {in1.x, in1.y, in1.z, in1.w};
-        const float4 *x2 = reinterpret_cast<const float4 *>(X2 + t * D) + r;
-        const float2 al = splat(alpha);
-#pragma unroll
-        for (int g = 0; g < M4; ++g) {
-          const float4 a2 = x2[8 * g];
-#pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            const float2 ks = splat(-beta * i1[j]), qs = splat(p.s.scale * i0[j]);
-            m[j][2 * g] = mul2(al, fma2(make_float2(a2.x, a2.y), ks,
-                                        fma2(make_float2(a1[g].x, a1[g].y), qs, m[j][2 * g])));
-            m[j][2 * g + 1] = mul2(al, fma2(make_float2(a2.z, a2.w), ks,
-                                            fma2(make_float2(a1[g].z, a1[g].w), qs, m[j][2 * g + 1])));
-          }
+        for (int i = 0; i < 8; ++i) {
+          const float4 a2 = x2[SP * i];
+          m[2 * i] = mul2(al, fma2(make_float2(a2.x, a2.y), k2, m[2 * i]));
+          m[2 * i + 1] = mul2(al, fma2(make_float2(a2.z, a2.w), k2, m[2 * i + 1]));
         }
       } else {
-        // x0 = du, x1 = dy, x2 = u; independent: k.  lanes 0-3: S_{t-1} du, lanes 4-7: S_{t-1} dy
-        if (r < 4)
-          p.dk[out + jj] = fmaf(-alpha * beta, mine, p.dk[out + jj]);
-        else
-          p.dq[out + jj] = p.s.scale * fmaf(alpha, mine, dot * mi0);
-        const float4 *x2 = reinterpret_cast<const float4 *>(X2 + t * D) + r;
-        const float2 al = splat(alpha);
+        // P = sum x0 M (k or du), M <- alpha M + x2 w^T, then sum x1 M (q or dy).  x holds x0.
+        float2 Q[4];
 #pragma unroll
-        for (int g = 0; g < M4; ++g) {
-          const float4 a2 = x2[8 * g];
+        for (int i = 0; i < 4; ++i) Q[i] = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            const float2 ks = splat(i0[j]);
-            m[j][2 * g] = fma2(make_float2(a2.x, a2.y), ks, mul2(al, m[j][2 * g]));
-            m[j][2 * g + 1] = fma2(make_float2(a2.z, a2.w), ks, mul2(al, m[j][2 * g + 1]));
-          }
+        for (int i = 0; i < 8; ++i) {
+          P[(2 * i) & 3] = fma2(make_float2(x[i].x, x[i].y), m[2 * i], P[(2 * i) & 3]);
+          P[(2 * i + 1) & 3] = fma2(make_float2(x[i].z, x[i].w), m[2 * i + 1], P[(2 * i + 1) & 3]);
+        }
+        const float4 *x1 = reinterpret_cast<const float4 *>(X1 + t * D) + sl;
+        const float4 *x2 = reinterpret_cast<const float4 *>(KIND == kSweepDq ? X2 + t * D : X0 + t * D) + sl;
+        const float dp = total(P[0], P[1], P[2], P[3]);
+        float w;
+        if constexpr (KIND == kSweepFwd) {
+          w = beta * fmaf(-alpha, dp, in);
+          if (p.u != nullptr && sl == 0) p.u[out] = w;
+        } else {
+          w = in;
+          if (sl == 0) p.dk[out] = fmaf(-alpha * beta, dp, p.dk[out]);
+        }
+        const float2 ws = splat(w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float4 a2;
+          if constexpr (KIND == kSweepDq) a2 = x2[SP * i];
+          else a2 = x[i];
+          const float4 a1 = x1[SP * i];
+          m[2 * i] = fma2(make_float2(a2.x, a2.y), ws, mul2(al, m[2 * i]));
+          m[2 * i + 1] = fma2(make_float2(a2.z, a2.w), ws, mul2(al, m[2 * i + 1]));
+          Q[(2 * i) & 3] = fma2(make_float2(a1.x, a1.y), m[2 * i], Q[(2 * i) & 3]);
+          Q[(2 * i + 1) & 3] = fma2(make_float2(a1.z, a1.w), m[2 * i + 1], Q[(2 * i + 1) & 3]);
+        }
+        load(X0, next);
+        const float dq = p.s.scale * total(Q[0], Q[1], Q[2], Q[3]);
+        if (sl == 0) {
+          if constexpr (KIND == kSweepFwd) static_cast<T *>(p.y)[out] = narrow<T>(dq);
+          else p.dq[out] = dq;
         }
       }
     }
     __syncthreads();   // the next turn overwrites the widened rows and the other raw buffer
   }
 
-  if constexpr (KIND == kSweepDq) {   // <S_T, dS_final> over this warp's 16 rows
-    if (p.end != nullptr) {
-      float x = 0.0f;
-      if (p.dS_final != nullptr) {
-        const float *d = p.dS_final + static_cast<long long>(head) * D * D;
+  if constexpr (KIND == kSweepDq) {   // <dS, S> at the chunk's end over this warp's rows
+    const float4 *g = reinterpret_cast<const float4 *>(p.dS_ck + (static_cast<long long>(head) * p.nc + chunk) * D * D + j * D) + sl;
+    float x = 0.0f;
 #pragma unroll
-        for (int g = 0; g < M4; ++g)
-#pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            const float4 f = *reinterpret_cast<const float4 *>(d + (c_thr + j) * D + 32 * g + 4 * r);
-            x = fmaf(f.x, m[j][2 * g].x, fmaf(f.y, m[j][2 * g].y, fmaf(f.z, m[j][2 * g + 1].x, fmaf(f.w, m[j][2 * g + 1].y, x))));
-          }
-      }
-      x = head_sum<32>(x);
-      if (lane == 0) p.end[static_cast<long long>(head) * (D / COLS) + slice * W + warp] = x;
+    for (int i = 0; i < 8; ++i) {
+      const float4 f = g[SP * i];
+      x = fmaf(f.x, m[2 * i].x, fmaf(f.y, m[2 * i].y, fmaf(f.z, m[2 * i + 1].x, fmaf(f.w, m[2 * i + 1].y, x))));
     }
+    x = head_sum<32>(x);
+    if (lane == 0) p.end[(static_cast<long long>(head) * p.nc + chunk) * (D / columns<D>()) + slice * W + warp] = x;
   }
   if constexpr (kCols) {
-    if (p.S_out != nullptr) {
-      float *So = p.S_out + static_cast<long long>(head) * D * D;
-#pragma unroll
-      for (int g = 0; g < M4; ++g) {
-        const int i0 = 32 * g + 4 * r;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          *reinterpret_cast<float4 *>(So + (i0 + 2 * e) * D + c_thr) =
-              make_float4(m[0][2 * g + e].x, m[1][2 * g + e].x, m[2][2 * g + e].x, m[3][2 * g + e].x);
-          *reinterpret_cast<float4 *>(So + (i0 + 2 * e + 1) * D + c_thr) =
-              make_float4(m[0][2 * g + e].y, m[1][2 * g + e].y, m[2][2 * g + e].y, m[3][2 * g + e].y);
-        }
-      }
-    }
+    if (p.S_out != nullptr) keep(p.S_out + state0);
   }
 }
 
@@ -473,40 +414,35 @@ __global__ void __launch_bounds__(256) delta_finish_kernel(FinishArgs p) {
   }
 }
 
-// da_t = (1 - alpha_t) (sum_{s >= t} gain_s + <S_T, dS_final>), one block per
-// head, from the last token back.  The running sum is float64: it passes over
-// the whole sequence without the decay that would forget its roundings.
+// da_t = (1 - alpha_t) (sum of gain_s over the chunk's later tokens + <dS, S> at
+// its end): one warp per chunk and head, two tokens a lane.  The sums start
+// anew in every chunk, so their roundings do not add up over the sequence.
 template <typename T>
 __global__ void __launch_bounds__(256) delta_da_kernel(FinishArgs p, int slices) {
-  __shared__ double part[8];
-  const int head = blockIdx.x, b = head / p.s.H, h = head - b * p.s.H, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long id = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (id >= static_cast<long long>(p.s.B) * p.s.H * p.nc) return;
+  const int head = static_cast<int>(id / p.nc), t0 = static_cast<int>(id - static_cast<long long>(head) * p.nc) * CHUNK;
+  const int b = head / p.s.H, h = head - b * p.s.H, lane = threadIdx.x & 31;
   const float *gain = p.gain + static_cast<long long>(head) * p.s.T;
-  double carry = 0.0;
-  for (int i = 0; i < slices; ++i) carry += p.end[static_cast<long long>(head) * slices + i];
-  for (int last = p.s.T; last > 0; last -= 256) {
-    const int t = last - 1 - static_cast<int>(threadIdx.x);
-    double x = t >= 0 ? static_cast<double>(gain[t]) : 0.0;
+  float end = 0.0f;
+  for (int i = 0; i < slices; ++i) end += p.end[id * slices + i];
+  const int t = t0 + 2 * lane;
+  const float x0 = t < p.s.T ? gain[t] : 0.0f, x1 = t + 1 < p.s.T ? gain[t + 1] : 0.0f;
+  float sum = x0 + x1;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) part[warp] = x;
-    __syncthreads();
-    double before = carry, all = carry;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i < warp) before += part[i];
-      all += part[i];
-    }
-    if (t >= 0) {
-      const long long bt = static_cast<long long>(b) * p.s.T + t;
-      const float a = fmaxf(widen(static_cast<const T *>(p.a)[bt * p.s.ld_g + h]), -80.0f);
-      static_cast<T *>(p.da)[bt * p.s.H + h] = narrow<T>(static_cast<float>(before + x) / (1.0f + expf(a)));
-    }
-    carry = all;
-    __syncthreads();
+  for (int o = 1; o < 32; o <<= 1) {
+    const float y = __shfl_down_sync(0xffffffffu, sum, o);
+    if (lane + o < 32) sum += y;
   }
+  const float after = __shfl_down_sync(0xffffffffu, sum, 1);
+  const float later = end + (lane < 31 ? after : 0.0f);
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (t + e < p.s.T) {
+      const long long bt = static_cast<long long>(b) * p.s.T + t + e;
+      const float a = fmaxf(widen(static_cast<const T *>(p.a)[bt * p.s.ld_g + h]), -80.0f);
+      static_cast<T *>(p.da)[bt * p.s.H + h] = narrow<T>((later + x1 + (e == 0 ? x0 : 0.0f)) / (1.0f + expf(a)));
+    }
 }
 
 }  // namespace sweep
