@@ -20,9 +20,23 @@ from __future__ import annotations
 import torch
 
 from . import esa as _esa
-from .esa import EsaError, _on, _ptr, _stream, load_library, row_stride
+from .esa import EsaError, _on, load_library, row_stride
 
 _DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+# The current stream's handle without building a Stream object (2 us of a decode step's call).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(device, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None and device.index is not None:
+        return _current_raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def esa_delta_workspace_size(B: int, T: int, H: int, D: int, dtype, keep: bool = True) -> int:
@@ -172,19 +186,23 @@ def esa_delta_bwd(q, k, v, a, b, dy, workspace, scale=None, S_init=None, dS_fina
 def _step_args(q_t, k_t, v_t, a_t, b_t, S, y_t, scale):
     if not isinstance(q_t, torch.Tensor) or not q_t.is_cuda or q_t.dim() != 3:
         raise TypeError("q_t must be a CUDA tensor [B, H, D] (the ESA library has no CPU path)")
-    if q_t.dtype not in _DTYPE_CODE or not q_t.is_contiguous():
+    shape, dtype, where = q_t.shape, q_t.dtype, q_t.get_device()
+    if dtype not in _DTYPE_CODE or not q_t.is_contiguous():
         raise ValueError("q_t must be contiguous with dtype float32, float16 or bfloat16")
-    B, H, D = (int(s) for s in q_t.shape)
-    for name, t, shape in (("k_t", k_t, (B, H, D)), ("v_t", v_t, (B, H, D)), ("a_t", a_t, (B, H)),
-                           ("b_t", b_t, (B, H))):
-        if tuple(t.shape) != shape or t.dtype != q_t.dtype or t.device != q_t.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {q_t.dtype} tensor of shape {shape} on {q_t.device}")
+    B, H, D = shape
+    gates = shape[:2]
+    for name, t, want in (("k_t", k_t, shape), ("v_t", v_t, shape), ("a_t", a_t, gates), ("b_t", b_t, gates)):
+        if t.shape != want or t.dtype is not dtype or t.get_device() != where or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(want)} on {q_t.device}")
     if S is None:
         raise ValueError("S (the recurrent state) is required")
-    _check_state("S", S, B, H, D, q_t.device)
-    y_t = _out("y_t", y_t, q_t.shape, q_t.dtype, q_t.device)
-    return y_t, (_ptr(q_t), _ptr(k_t), _ptr(v_t), _ptr(a_t), _ptr(b_t), _ptr(S), _ptr(y_t), B, H, D,
-                 _scale(scale, D), _DTYPE_CODE[q_t.dtype])
+    if not isinstance(S, torch.Tensor) or S.get_device() != where:
+        raise TypeError(f"S must be a CUDA tensor on {q_t.device}")
+    if S.shape != (B, H, D, D) or S.dtype is not torch.float32 or not S.is_contiguous():
+        raise ValueError(f"S must be a contiguous float32 tensor of shape {(B, H, D, D)}")
+    y_t = torch.empty_like(q_t) if y_t is None else _out("y_t", y_t, shape, dtype, q_t.device)
+    return y_t, (q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(), a_t.data_ptr(), b_t.data_ptr(), S.data_ptr(),
+                 y_t.data_ptr(), B, H, D, D ** -0.5 if scale is None else float(scale), _DTYPE_CODE[dtype])
 
 
 def esa_delta_step(q_t, k_t, v_t, a_t, b_t, S, y_t=None, scale=None, stream=None):

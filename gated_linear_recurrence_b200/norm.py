@@ -13,7 +13,8 @@ from __future__ import annotations
 
 import torch
 
-from .esa import EsaError, _on, _ptr, _stream, load_library
+from .delta import _ptr, _stream
+from .esa import EsaError, _on, load_library
 
 _DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
@@ -23,10 +24,10 @@ def _rows(name, t, like=None):
     contiguous and evenly spaced."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor (the ESA library has no CPU path)")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+    if like is not None and (t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must have shape {tuple(like.shape)}, dtype {like.dtype}, {like.device}")
     N = int(t.shape[-1])
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return N
     ld, expect = N, None
     if N > 1 and t.stride(-1) != 1:
@@ -49,7 +50,7 @@ def _check_x(x, name="x"):
         raise TypeError(f"{name} must be a CUDA tensor [..., N] (the ESA library has no CPU path)")
     if x.dtype not in _DTYPE_CODE:
         raise TypeError(f"unsupported dtype {x.dtype} (float32, float16 or bfloat16)")
-    N = int(x.shape[-1])
+    N = x.shape[-1]
     if N < 1:
         raise ValueError(f"{name} must have at least one channel")
     return x.numel() // N, N
@@ -58,17 +59,17 @@ def _check_x(x, name="x"):
 def _check_param(name, p, x, N):
     if p is None:
         return
-    if not isinstance(p, torch.Tensor) or p.device != x.device or tuple(p.shape) != (N,) or not p.is_contiguous():
+    if not isinstance(p, torch.Tensor) or p.get_device() != x.get_device() or p.shape != (N,) or not p.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {(N,)} on {x.device}")
     if p.dtype not in (x.dtype, torch.float32):
         raise TypeError(f"{name} must be {x.dtype} or float32")
 
 
 def _wdtype(x, *params):
-    given = {p.dtype for p in params if p is not None}
-    if len(given) > 1:
+    given = [p.dtype for p in params if p is not None]
+    if any(dt is not given[0] for dt in given):
         raise TypeError("weight and bias must share one dtype")
-    return given.pop() if given else x.dtype
+    return given[0] if given else x.dtype
 
 
 def _out(name, t, shape, dtype, device):
@@ -95,12 +96,13 @@ def esa_norm_fwd(x, weight=None, bias=None, eps=1e-5, residual=None, y=None, h=N
     _check_param("weight", weight, x, N)
     _check_param("bias", bias, x, N)
     wdt = _wdtype(x, weight, bias)
-    y = _out("y", y, x.shape, x.dtype, x.device)
+    y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else \
+        _out("y", y, x.shape, x.dtype, x.device)
     if residual is None:
         if h is not None:
             raise ValueError("h is an output of the residual addition: give residual too")
     else:
-        h = _out("h", h, x.shape, x.dtype, x.device)
+        h = torch.empty_like(y) if h is None else _out("h", h, x.shape, x.dtype, x.device)
     if stats is not None or want_stats:
         stats = _out("stats", stats, (rows, 2), torch.float32, x.device)
     with _on(x.device):
