@@ -35,7 +35,7 @@ from .delta import (  # noqa: F401
     esa_delta_step,
     esa_delta_workspace_size,
 )
-from .layer import ESA, esa_scan  # noqa: F401
+from .layer import ESA, GatedDelta, PreNorm, delta_rule, esa_scan, layer_norm  # noqa: F401
 from .norm import esa_norm_bwd, esa_norm_fwd  # noqa: F401
 
 __all__ = [
@@ -43,5 +43,5 @@ __all__ = [
     "esa_scan_bwd_map", "esa_scan_fwd", "esa_scan_map", "esa_step", "esa_strerror", "esa_version",
     "esa_workspace_init", "esa_workspace_size", "load_library", "new_workspace", "ESA", "esa_scan",
     "PreparedDeltaStep", "esa_delta_bwd", "esa_delta_fwd", "esa_delta_step", "esa_delta_workspace_size",
-    "esa_norm_bwd", "esa_norm_fwd",
+    "esa_norm_bwd", "esa_norm_fwd", "GatedDelta", "PreNorm", "delta_rule", "layer_norm",
 ]

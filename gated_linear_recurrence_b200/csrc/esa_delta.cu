@@ -236,13 +236,12 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
   return launch_delta_finish(dtype, f, st);
 }
 
-int esa_delta_step(const void *q_t, const void *k_t, const void *v_t, const void *a_t, const void *b_t, float *S,
-                   void *y_t, int B, int H, int D, float scale, int dtype, void *stream) {
-  int rc = check_shape(B, 1, H, D, dtype);
+int esa_delta_step(const void *q_t, const void *k_t, long long ld_qk, const void *v_t, long long ld_v,
+                   const void *a_t, const void *b_t, long long ld_g, float *S, void *y_t, int B, int H, int D,
+                   float scale, int dtype, void *stream) {
+  const DeltaShape s{B, 1, H, D, ld_qk, ld_v, ld_g, scale};
+  int rc = check_inputs(s, dtype, q_t, k_t, v_t, a_t, b_t);
   if (rc) return rc;
-  const long long C = static_cast<long long>(H) * D;
-  const DeltaShape s{B, 1, H, D, C, C, H, scale};
-  if ((rc = check_inputs(s, dtype, q_t, k_t, v_t, a_t, b_t))) return rc;
   if (B > 0 && (!S || !y_t)) return ESA_ERR_ARG;
   for (const void *p : {static_cast<const void *>(S), static_cast<const void *>(y_t)})
     if (p && !aligned_to(p, 16)) return ESA_ERR_ALIGN;

@@ -26,7 +26,6 @@
 // the whole head in one SM, with the state converted through tensor memory
 // three times a chunk; with few heads (the usual case of a long prompt) that
 // leaves most SMs idle, where 16-row warps spread a head over eight.
-#include <cstdlib>
 #include <type_traits>
 
 #include "esa_delta_chunk.h"
@@ -431,7 +430,6 @@ int by_d(const ChunkArgs &a, cudaStream_t st) {
 // would put more than one block on an SM (16 heads: 129 us a pass of 32 chunks
 // in halves against 205 whole; 128 heads: 263 against 215).
 ChainPlan chain_plan(int heads, int D) {
-  if (getenv("ESA_PLAN")) return static_cast<ChainPlan>(atoi(getenv("ESA_PLAN")));
   if (D >= 64 && static_cast<long long>(heads) * (D / 16) <= sm_count()) return kChainSplit;
   return D == 128 && 2ll * heads <= sm_count() ? kChainHalves : kChainWhole;
 }

@@ -19,11 +19,11 @@
 // from what those left and take all chunks at once.
 //
 // All arithmetic is float32, as the state is; this is the path of float32
-// tensors and of short sequences (a decode step is a sweep of one token).
+// tensors and of short sequences.
 // With few heads it is bound by the latency of a token (load k, dot, shuffles,
 // update), with many by the issue of some 200 instructions a token, warp and
-// 32 x 32 of the state.  Measured a token, few heads: TOK32 ns at D = 32, TOK64
-// at 64, TOK128 at 128.  (Columns shared by 8 lanes whatever D: 390, 450,
+// 32 x 32 of the state.  Measured a token, few heads: 174 ns at D = 32, 205
+// at 64, 302 at 128.  (Columns shared by 8 lanes whatever D: 390, 450,
 // 600; a whole column a thread: 312, 448, 924, since one warp then issues all
 // of it.)  More warps per block share the staged rows; fewer give more blocks:
 // see sweep_warps().

@@ -183,30 +183,49 @@ def esa_delta_bwd(q, k, v, a, b, dy, workspace, scale=None, S_init=None, dS_fina
     return dq, dk, dv, da, db, dS_init
 
 
+def _token_stride(name, t, H, width):
+    """Elements between consecutive batch entries of [B, H, width] or [B, H]."""
+    if t.is_contiguous():
+        return H * width
+    st = t.stride()
+    if (width > 1 and st[-1] != 1) or (H > 1 and st[1] != width) or (t.shape[0] > 1 and st[0] < H * width):
+        raise ValueError(f"{name} must have each token's elements contiguous and tokens that do not overlap")
+    return st[0] if t.shape[0] > 1 else H * width
+
+
 def _step_args(q_t, k_t, v_t, a_t, b_t, S, y_t, scale):
     if not isinstance(q_t, torch.Tensor) or not q_t.is_cuda or q_t.dim() != 3:
         raise TypeError("q_t must be a CUDA tensor [B, H, D] (the ESA library has no CPU path)")
     shape, dtype, where = q_t.shape, q_t.dtype, q_t.get_device()
-    if dtype not in _DTYPE_CODE or not q_t.is_contiguous():
-        raise ValueError("q_t must be contiguous with dtype float32, float16 or bfloat16")
+    if dtype not in _DTYPE_CODE:
+        raise TypeError(f"unsupported dtype {dtype} (float32, float16 or bfloat16)")
     B, H, D = shape
     gates = shape[:2]
     for name, t, want in (("k_t", k_t, shape), ("v_t", v_t, shape), ("a_t", a_t, gates), ("b_t", b_t, gates)):
-        if t.shape != want or t.dtype is not dtype or t.get_device() != where or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(want)} on {q_t.device}")
+        if not isinstance(t, torch.Tensor) or t.get_device() != where:
+            raise TypeError(f"{name} must be a CUDA tensor on {q_t.device}")
+        if t.shape != want or t.dtype is not dtype:
+            raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(want)}")
+    ld_qk, ld_v, ld_g = (_token_stride(n, t, H, w) for n, t, w in (("q_t", q_t, D), ("v_t", v_t, D), ("a_t", a_t, 1)))
+    if _token_stride("k_t", k_t, H, D) != ld_qk or _token_stride("b_t", b_t, H, 1) != ld_g:
+        raise ValueError("q_t and k_t must share one row stride, a_t and b_t another")
     if S is None:
         raise ValueError("S (the recurrent state) is required")
     if not isinstance(S, torch.Tensor) or S.get_device() != where:
         raise TypeError(f"S must be a CUDA tensor on {q_t.device}")
     if S.shape != (B, H, D, D) or S.dtype is not torch.float32 or not S.is_contiguous():
         raise ValueError(f"S must be a contiguous float32 tensor of shape {(B, H, D, D)}")
-    y_t = torch.empty_like(q_t) if y_t is None else _out("y_t", y_t, shape, dtype, q_t.device)
-    return y_t, (q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(), a_t.data_ptr(), b_t.data_ptr(), S.data_ptr(),
-                 y_t.data_ptr(), B, H, D, D ** -0.5 if scale is None else float(scale), _DTYPE_CODE[dtype])
+    y_t = torch.empty(shape, dtype=dtype, device=q_t.device) if y_t is None else \
+        _out("y_t", y_t, shape, dtype, q_t.device)
+    return y_t, (q_t.data_ptr(), k_t.data_ptr(), ld_qk, v_t.data_ptr(), ld_v, a_t.data_ptr(), b_t.data_ptr(), ld_g,
+                 S.data_ptr(), y_t.data_ptr(), B, H, D, D ** -0.5 if scale is None else float(scale),
+                 _DTYPE_CODE[dtype])
 
 
 def esa_delta_step(q_t, k_t, v_t, a_t, b_t, S, y_t=None, scale=None, stream=None):
-    """One token: ``S`` (float32 [B, H, D, D]) is updated in place.  Returns ``y_t``."""
+    """One token: ``S`` (float32 [B, H, D, D]) is updated in place.  Returns
+    ``y_t`` [B, H, D].  ``q_t, k_t, v_t`` [B, H, D] and ``a_t, b_t`` [B, H] may
+    be row-strided views, as in :func:`esa_delta_fwd`."""
     y_t, args = _step_args(q_t, k_t, v_t, a_t, b_t, S, y_t, scale)
     with _on(q_t.device):
         rc = load_library().esa_delta_step(*args, _stream(q_t.device, stream))

@@ -111,7 +111,7 @@ def load_library():
         lib.esa_delta_fwd.restype = I
         lib.esa_delta_bwd.argtypes = [P, P, L, P, L, P, P, L, P, P, P, P, P, P, P, P, I, I, I, I, F, P, I, P, S, P]
         lib.esa_delta_bwd.restype = I
-        lib.esa_delta_step.argtypes = [P, P, P, P, P, P, P, I, I, I, F, I, P]
+        lib.esa_delta_step.argtypes = [P, P, L, P, L, P, P, L, P, P, I, I, I, F, I, P]
         lib.esa_delta_step.restype = I
         lib.esa_norm_workspace_size.argtypes = [L, I, I, I]
         lib.esa_norm_workspace_size.restype = S

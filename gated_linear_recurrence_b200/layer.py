@@ -3,6 +3,11 @@
 * :func:`esa_scan` -- differentiable scan ``(a, v, q) -> (y, E_final)``: the
   forward is ``esa_scan_fwd``, the backward ``esa_scan_bwd`` (the forward's
   workspace, which holds the chunk checkpoints, is kept for it).
+* :func:`delta_rule`, :func:`layer_norm` -- the same for the gated delta rule
+  (``esa_delta_fwd`` / ``esa_delta_bwd``) and the layer norm with the residual
+  addition before it (``esa_norm_fwd`` / ``esa_norm_bwd``).
+* :class:`GatedDelta` -- the matrix-state counterpart of :class:`ESA`, and
+  :class:`PreNorm`, the residual block around either of them.
 * :class:`ESA` -- the sequence-mixing layer of "Entangled State Attention
   v2.1", section 1 ("ESA layer": ``ESA(embd, head, ...)`` mapping
   ``[B, T, embd]`` to ``[B, T, embd]``), computed as on the
@@ -29,10 +34,13 @@ is no CPU path.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
+from . import delta as _delta
 from . import esa as _esa
+from . import norm as _norm
 
-__all__ = ["ESA", "esa_scan"]
+__all__ = ["ESA", "GatedDelta", "PreNorm", "delta_rule", "esa_scan", "layer_norm"]
 
 _MODES = {"direct": _esa.DIRECT, "controlled": _esa.CONTROLLED}
 
@@ -294,3 +302,206 @@ class ESA(torch.nn.Module):
         """``(out_t, state)`` for one token ``x_t`` [B, embd]; ``state`` is
         updated in place and returned."""
         return self.step(x_t, state), state
+
+
+def _wants_grad(*ts):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
+
+
+class _DeltaRuleFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, a, b, S_init, scale, keep, want_S):
+        S0 = None if S_init is None else S_init.detach().contiguous()
+        y, S, ws = _delta.esa_delta_fwd(q, k, v, a, b, scale=scale, S_init=S0, keep=keep, want_S_final=want_S)
+        ctx.set_materialize_grads(False)
+        ctx.scale = scale
+        if keep:
+            ctx.save_for_backward(q, k, v, a, b, S0, ws)
+        return y, S
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dS):
+        q, k, v, a, b, S0, ws = ctx.saved_tensors
+        dy = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if dy is None else dy.contiguous()
+        dS = None if dS is None else dS.contiguous()
+        *grads, dS0 = _delta.esa_delta_bwd(q, k, v, a, b, dy, ws, scale=ctx.scale, S_init=S0, dS_final=dS,
+                                           want_dS_init=ctx.needs_input_grad[5])
+        return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), dS0, None, None, None)
+
+
+def delta_rule(q, k, v, a, b, scale=None, S_init=None, want_S_final=True):
+    """Differentiable gated delta rule (see :func:`~.delta.esa_delta_fwd`):
+    ``q, k, v`` [B, T, H, D] and the logits ``a, b`` [B, T, H], D of 32, 64 or
+    128.  Returns ``(y, S_final)``, ``S_final`` float32 [B, H, D, D] (None with
+    ``want_S_final=False``).  ``S_init`` (float32 [B, H, D, D]) may require
+    grad.  Column blocks of one projection output are read in place; any other
+    layout is copied.  Without a gradient to come nothing is kept for it."""
+    if q.dim() == 4 and q.numel() and (_esa.row_stride(q) is None or _esa.row_stride(q) != _esa.row_stride(k)):
+        q, k = q.contiguous(), k.contiguous()
+    if v.dim() == 4 and v.numel() and _esa.row_stride(v) is None:
+        v = v.contiguous()
+    if a.dim() == 3 and a.numel() and (_delta._gate_stride(a) is None or _delta._gate_stride(a) != _delta._gate_stride(b)):
+        a, b = a.contiguous(), b.contiguous()
+    return _DeltaRuleFn.apply(q, k, v, a, b, S_init, scale, _wants_grad(q, k, v, a, b, S_init), want_S_final)
+
+
+class _LayerNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps, keep):
+        y, h, stats = _norm.esa_norm_fwd(x, weight, bias, eps=eps, residual=residual, want_stats=keep)
+        ctx.set_materialize_grads(False)
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        if keep:
+            ctx.save_for_backward(h, weight, stats)
+        return y if residual is None else (y, h)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight, stats = ctx.saved_tensors
+        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        dy = torch.zeros(h.shape, dtype=h.dtype, device=h.device) if dy is None else _even_rows(dy)
+        dh = None if dh is None else _even_rows(dh)
+        dx, dw, db = _norm.esa_norm_bwd(dy, h, weight, stats, dh=dh, want_dweight=need_w, want_dbias=need_b,
+                                        wdtype=ctx.bias_dtype)
+        return dx if need_x else None, dw, db, dx if need_r else None, None, None
+
+
+def _even_rows(t):
+    try:
+        _norm._rows("x", t)
+        return t
+    except ValueError:
+        return t.contiguous()
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None):
+    """Differentiable layer norm over the last axis (see
+    :func:`~.norm.esa_norm_fwd`).  Returns ``y``; with a ``residual`` of ``x``'s
+    shape ``(y, h)``, the norm of ``h = x + residual`` and ``h`` itself, the
+    residual stream's next value."""
+    x, residual = _even_rows(x), (None if residual is None else _even_rows(residual))
+    return _LayerNormFn.apply(x, weight, bias, residual, eps, _wants_grad(x, weight, bias, residual))
+
+
+class GatedDelta(torch.nn.Module):
+    """Gated delta rule mixer: ``[B, T, embd] -> [B, T, embd]``, the matrix-state
+    counterpart of :class:`ESA` with the same interface.
+
+    Args:
+        embd: embedding width C.
+        head: number of heads H; the head dimension ``embd // head`` must be
+            32, 64 or 128.
+        bias: bias terms in the projections.
+        eps: of the norm of queries and keys.
+
+    Queries, keys (``W_QK``), values (``W_V``) and each head's two gate logits
+    (``W_G``: forget, write) are projections of the input.  Queries and keys
+    pass a layer norm over the head dimension, scaled to unit length
+    (D^(-1/2) n): with the write strength below 1 the state's update is then a
+    contraction.  ``W_O`` projects the recurrence's output.
+
+    ``forward(x, state=None, return_state=False)``, ``step(x_t, state)``,
+    ``init_state``, ``prefill`` and ``decode_step`` are :class:`ESA`'s, with the
+    state float32 [B, H, D, D].
+    """
+
+    def __init__(self, embd: int, head: int, bias: bool = False, eps: float = 1e-5, device=None, dtype=None):
+        super().__init__()
+        if embd % head != 0:
+            raise ValueError("embd must be a multiple of head")
+        if embd // head not in (32, 64, 128):
+            raise ValueError("head dimension embd // head must be one of 32, 64, 128")
+        self.embd, self.head, self.head_dim, self.eps = embd, head, embd // head, eps
+        kw = {"device": device, "dtype": dtype}
+        self.W_QK = torch.nn.Linear(embd, 2 * embd, bias=bias, **kw)
+        self.W_V = torch.nn.Linear(embd, embd, bias=bias, **kw)
+        self.W_G = torch.nn.Linear(embd, 2 * head, bias=bias, **kw)
+        self.W_O = torch.nn.Linear(embd, embd, bias=bias, **kw)
+        # unit length of the normalised queries and keys
+        self.register_buffer("unit", torch.full((self.head_dim,), self.head_dim ** -0.5, **kw), persistent=False)
+
+    def _inputs(self, x):
+        """q, k, v, a, b of the tokens ``x`` [..., embd]: q, k and a, b are
+        column blocks, read in place."""
+        lead, H, D = x.shape[:-1], self.head, self.head_dim
+        qk = layer_norm(self.W_QK(x).reshape(*lead, 2, H, D), self.unit, eps=self.eps)
+        a, b = self.W_G(x).reshape(*lead, 2, H).unbind(-2)
+        return (*qk.unbind(-3), self.W_V(x).reshape(*lead, H, D), a, b)
+
+    def forward(self, x, state=None, return_state=False):
+        B, T, C = x.shape
+        if C != self.embd:
+            raise ValueError(f"expected last dimension {self.embd}, got {C}")
+        y, S = delta_rule(*self._inputs(x), scale=1.0, S_init=state, want_S_final=return_state)
+        out = self.W_O(y.reshape(B, T, C))
+        return (out, S) if return_state else out
+
+    @torch.no_grad()
+    def step(self, x_t, state):
+        B, C = x_t.shape
+        if C != self.embd:
+            raise ValueError(f"expected last dimension {self.embd}, got {C}")
+        return self.W_O(_delta.esa_delta_step(*self._inputs(x_t), state, scale=1.0).reshape(B, C))
+
+    def init_state(self, batch: int, device=None):
+        """A zero state ``[batch, head, head_dim, head_dim]`` (float32)."""
+        return torch.zeros(batch, self.head, self.head_dim, self.head_dim, dtype=torch.float32,
+                           device=device if device is not None else self.W_V.weight.device)
+
+    @torch.no_grad()
+    def prefill(self, x, state=None):
+        """``(out, state)`` after the whole prompt ``x`` [B, T, embd]."""
+        return self.forward(x, state=state, return_state=True)
+
+    @torch.no_grad()
+    def decode_step(self, x_t, state):
+        """``(out_t, state)`` for one token ``x_t`` [B, embd]; ``state`` is
+        updated in place and returned."""
+        return self.step(x_t, state), state
+
+
+class PreNorm(torch.nn.Module):
+    """Residual block ``h = x + residual``, ``y = mixer(LayerNorm(h))`` around
+    an :class:`ESA` or :class:`GatedDelta` mixer.
+
+    ``forward(x, residual=None, state=None, return_state=False)`` returns
+    ``(y, h)`` (and the state): ``y`` is not yet added to ``h``, the next
+    block's norm does that in its one pass over both, as ``x`` and ``residual``
+    (``for block in blocks: x, residual = block(x, residual)``; the stream's
+    end is ``x + residual``).  ``step(x_t, residual_t, state)`` is the same for
+    one token, with ``state`` updated in place.
+
+    The norm's weight and bias have ``norm_dtype`` (the mixer's by default; float32
+    weights go with 16-bit inputs).
+    """
+
+    def __init__(self, mixer, eps: float = 1e-5, norm_dtype=None):
+        super().__init__()
+        w = mixer.W_O.weight
+        kw = {"device": w.device, "dtype": norm_dtype or w.dtype}
+        self.mixer, self.eps = mixer, eps
+        self.weight = torch.nn.Parameter(torch.ones(mixer.embd, **kw))
+        self.bias = torch.nn.Parameter(torch.zeros(mixer.embd, **kw))
+
+    def _norm(self, x, residual):
+        if residual is None:
+            return layer_norm(x, self.weight, self.bias, self.eps), x
+        return layer_norm(x, self.weight, self.bias, self.eps, residual)
+
+    def forward(self, x, residual=None, state=None, return_state=False):
+        n, h = self._norm(x, residual)
+        if return_state:
+            y, S = self.mixer(n, state=state, return_state=True)
+            return y, h, S
+        return self.mixer(n, state=state), h
+
+    @torch.no_grad()
+    def step(self, x_t, residual_t, state):
+        n, h = self._norm(x_t, residual_t)
+        return self.mixer.step(n, state), h
+
+    def init_state(self, batch: int, device=None):
+        """The mixer's zero state."""
+        return self.mixer.init_state(batch, device=device)

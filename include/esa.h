@@ -391,10 +391,13 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
                   void *da, void *db, float *dS_init, int B, int T, int H, int D, float scale, const float *S_init,
                   int dtype, void *workspace, size_t workspace_bytes, void *stream);
 
-/* One token: q_t, k_t, v_t, y_t [B,H,D] and a_t, b_t [B,H] contiguous; S
- * [B,H,D,D] float32 is read and overwritten.  Needs no workspace. */
-int esa_delta_step(const void *q_t, const void *k_t, const void *v_t, const void *a_t, const void *b_t, float *S,
-                   void *y_t, int B, int H, int D, float scale, int dtype, void *stream);
+/* One token: q_t, k_t, v_t [B,H,D] with rows ld_qk and ld_v elements apart,
+ * a_t, b_t [B,H] ld_g apart (strides and alignment as above), y_t [B,H,D]
+ * contiguous; S [B,H,D,D] float32 is read and overwritten.  Needs no
+ * workspace. */
+int esa_delta_step(const void *q_t, const void *k_t, long long ld_qk, const void *v_t, long long ld_v,
+                   const void *a_t, const void *b_t, long long ld_g, float *S, void *y_t, int B, int H, int D,
+                   float scale, int dtype, void *stream);
 
 /*
  * ---- Layer norm -------------------------------------------------------------

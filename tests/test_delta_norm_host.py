@@ -61,7 +61,8 @@ def test_delta_backward_and_step_errors(lib):
     assert bwd(wsb=lib.esa_delta_workspace_size(2, 8, 2, 64, 1, 1) - 1) == esa.ESA_ERR_WORKSPACE
 
     def step(S=0x6000, y=0x7000, D=64, dtype=1, q=0x1000):
-        return lib.esa_delta_step(P(q), P(0x2000), P(0x3000), P(0x4000), P(0x5000), P(S), P(y), 2, 2, D, 0.1, dtype, None)
+        return lib.esa_delta_step(P(q), P(0x2000), 2 * D, P(0x3000), 2 * D, P(0x4000), P(0x5000), 2, P(S), P(y), 2, 2, D, 0.1,
+                                  dtype, None)
 
     assert step(S=0) == esa.ESA_ERR_ARG
     assert step(y=0) == esa.ESA_ERR_ARG
