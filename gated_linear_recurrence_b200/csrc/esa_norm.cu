@@ -13,29 +13,20 @@ namespace {
 
 int elem(int dtype) { return dtype == ESA_F32 ? 4 : 2; }
 
-// Elements per vector: 16, 8, 4 or 2 bytes of the I/O type, the first of which
-// divides N and every row stride and suits every pointer's alignment.
+// Elements per vector: 16 or 8 bytes of the I/O type if that divides N and every
+// row stride and suits every pointer's alignment, else one element.
 int pick_vec(int dtype, int wdtype, int N, std::initializer_list<long long> lds, std::initializer_list<const void *> io,
              std::initializer_list<const void *> wt) {
-  for (int vec = 16 / elem(dtype); vec > 1; vec >>= 1) {
+  for (int bytes = 16; bytes >= 8; bytes >>= 1) {
+    const int vec = bytes / elem(dtype);
     bool ok = N % vec == 0;
     for (long long ld : lds) ok = ok && ld % vec == 0;
-    for (const void *p : io) ok = ok && (p == nullptr || aligned_to(p, vec * elem(dtype)));
+    for (const void *p : io) ok = ok && (p == nullptr || aligned_to(p, bytes));
     const int wbytes = vec * elem(wdtype) > 16 ? 16 : vec * elem(wdtype);
     for (const void *p : wt) ok = ok && (p == nullptr || aligned_to(p, wbytes));
     if (ok) return vec;
   }
   return 1;
-}
-
-// A row of `nvec` vectors: part of a warp with one vector a thread while it
-// fits, a warp with up to `most`, then as few threads as hold it with `most`.
-NormRow norm_row(int nvec, int most) {
-  int tpr = 4, nv = 1;
-  while (tpr < 32 && tpr < nvec) tpr <<= 1;
-  while (tpr >= 32 && tpr * most < nvec) tpr <<= 1;
-  while (nv * tpr < nvec) nv <<= 1;
-  return {tpr, tpr > 32 ? most : nv};
 }
 
 int check_norm(long long rows, int N, int dtype, int wdtype) {
@@ -88,10 +79,9 @@ int esa_norm_fwd(const void *x, long long ld_x, const void *residual, long long 
   NormFwdArgs a{x, residual, weight, bias, y, h, reinterpret_cast<float2 *>(stats), rows, ld_x, ld_res, N, eps,
                 static_cast<float>(N)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const NormRow shape = norm_row(N / vec, kNormFwdElems / vec);
   const bool wide = wdtype == ESA_F32;
-  if (dtype == ESA_F32) return norm_fwd_f32(vec, shape, a, st);
-  return dtype == ESA_F16 ? norm_fwd_f16(vec, shape, wide, a, st) : norm_fwd_bf16(vec, shape, wide, a, st);
+  if (dtype == ESA_F32) return norm_fwd_f32(vec, a, st);
+  return dtype == ESA_F16 ? norm_fwd_f16(vec, wide, a, st) : norm_fwd_bf16(vec, wide, a, st);
 }
 
 int esa_norm_bwd(const void *dy, long long ld_dy, const void *h, long long ld_h, const void *weight,
@@ -119,14 +109,13 @@ int esa_norm_bwd(const void *dy, long long ld_dy, const void *h, long long ld_h,
     return dbias ? runtime_status(cudaMemsetAsync(dbias, 0, static_cast<size_t>(N) * ws, st)) : ESA_OK;
   }
   const int vec = pick_vec(dtype, wdtype, N, {ld_dy, ld_h, dh ? ld_dh : 0}, {dy, h, dh, dx}, {weight});
-  const NormRow shape = norm_row(N / vec, kNormBwdElems / vec);
   const int most = max_blocks(N);
   NormBwdArgs a{dy, h, weight, dh, dx, reinterpret_cast<const float2 *>(stats), dweight, dbias,
                 sums ? static_cast<float *>(workspace) : nullptr, rows, ld_dy, ld_h, ld_dh, N,
                 static_cast<float>(N)};
   const bool wide = wdtype == ESA_F32;
-  if (dtype == ESA_F32) return norm_bwd_f32(vec, shape, a, most, st);
-  return dtype == ESA_F16 ? norm_bwd_f16(vec, shape, wide, a, most, st) : norm_bwd_bf16(vec, shape, wide, a, most, st);
+  if (dtype == ESA_F32) return norm_bwd_f32(vec, a, most, st);
+  return dtype == ESA_F16 ? norm_bwd_f16(vec, wide, a, most, st) : norm_bwd_bf16(vec, wide, a, most, st);
 }
 
 }  // extern "C"

@@ -223,10 +223,9 @@ __global__ void __launch_bounds__(norm_block<TPR>()) norm_fwd_kernel(NormFwdArgs
 }
 
 // A thread's vectors of the rows under way, in shared memory that no other
-// thread touches: [stage][h, dy, dh][NV][thread].  Vectors of less than 8
-// bytes are loaded into registers instead, one row at a time: a copy
-// instruction for every 2 or 4 bytes costs more than it hides (4099 x 5001
-// float32: 142 us staged, SCAL in registers).
+// thread touches: [stage][h, dy, dh][NV][thread].  Single elements are loaded
+// into registers instead, one row at a time: a copy instruction for each costs
+// more than it hides (4099 x 5001 float32: 142 us staged, 90 in registers).
 template <typename V>
 constexpr bool norm_staged() { return sizeof(V) >= 8; }
 template <typename V, int NV, int BLOCK>
@@ -235,10 +234,10 @@ constexpr int norm_stage_bytes() { return norm_staged<V>() ? 3 * NV * BLOCK * st
 template <typename V, int NV, int BLOCK>
 constexpr int norm_stages() { return 2 * norm_stage_bytes<V, NV, BLOCK>() <= 200 * 1024 ? 2 : 1; }
 
-template <typename V>
-__device__ __forceinline__ void copy_async(V *dst, const V *src) {
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src) {
   const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  if constexpr (sizeof(V) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
   else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
 }
 
@@ -277,9 +276,9 @@ __global__ void __launch_bounds__(norm_block<TPR>()) norm_bwd_kernel(NormBwdArgs
           }
         } else if (col < p.N) {
           V *s = stage + (k * 3 * NV + i) * BLOCK;
-          copy_async(s, reinterpret_cast<const V *>(h + row * p.ld_h + col));
-          copy_async(s + NV * BLOCK, reinterpret_cast<const V *>(dy + row * p.ld_dy + col));
-          if (dh) copy_async(s + 2 * NV * BLOCK, reinterpret_cast<const V *>(dh + row * p.ld_dh + col));
+          copy_async<sizeof(V)>(s, h + row * p.ld_h + col);
+          copy_async<sizeof(V)>(s + NV * BLOCK, dy + row * p.ld_dy + col);
+          if (dh) copy_async<sizeof(V)>(s + 2 * NV * BLOCK, dh + row * p.ld_dh + col);
         }
       }
       stats[k] = p.stats[row];
@@ -498,28 +497,6 @@ int by_shape(NormRow s, const F &f) {
     case 1024: return by_nv<VEC, 1024>(s.nv, f);
     default: return ESA_ERR_UNSUPPORTED;
   }
-}
-
-template <typename T, typename WT>
-int norm_fwd_typed(int vec, NormRow s, const NormFwdArgs &a, cudaStream_t st) {
-  if (vec == 16 / static_cast<int>(sizeof(T))) return by_shape<16 / sizeof(T)>(s, RunFwd<T, WT, 16 / sizeof(T)>{a, st});
-  if (vec == 8 / static_cast<int>(sizeof(T))) return by_shape<8 / sizeof(T)>(s, RunFwd<T, WT, 8 / sizeof(T)>{a, st});
-  if constexpr (sizeof(T) == 2)
-    if (vec == 2) return by_shape<2>(s, RunFwd<T, WT, 2>{a, st});
-  return by_shape<1>(s, RunFwd<T, WT, 1>{a, st});
-}
-
-template <typename T, typename WT>
-int norm_bwd_typed(int vec, NormRow s, const NormBwdArgs &a, int most, cudaStream_t st) {
-  int rc, grid = 0;
-  if (vec == 16 / static_cast<int>(sizeof(T))) rc = by_shape<16 / sizeof(T)>(s, RunBwd<T, WT, 16 / sizeof(T)>{a, most, &grid, st});
-  else if (vec == 8 / static_cast<int>(sizeof(T))) rc = by_shape<8 / sizeof(T)>(s, RunBwd<T, WT, 8 / sizeof(T)>{a, most, &grid, st});
-  else if (sizeof(T) == 2 && vec == 2) rc = by_shape<2>(s, RunBwd<T, WT, 2>{a, most, &grid, st});
-  else rc = by_shape<1>(s, RunBwd<T, WT, 1>{a, most, &grid, st});
-  if (rc || a.part == nullptr) return rc;
-  norm_fold_kernel<WT><<<(2 * a.N + 31) / 32, 1024, 0, st>>>(a.part, grid, a.N, static_cast<WT *>(a.dweight),
-                                                             static_cast<WT *>(a.dbias));
-  return runtime_status(cudaGetLastError());
 }
 
 }  // namespace

@@ -15,6 +15,16 @@ struct NormRow {
   int tpr, nv;
 };
 
+// A row of `nvec` vectors: part of a warp with one vector a thread while it
+// fits, a warp with up to `most`, then as few threads as hold it with `most`.
+inline NormRow norm_row(int nvec, int most) {
+  int tpr = 4, nv = 1;
+  while (tpr < 32 && tpr < nvec) tpr <<= 1;
+  while (tpr >= 32 && tpr * most < nvec) tpr <<= 1;
+  while (nv * tpr < nvec) nv <<= 1;
+  return {tpr, tpr > 32 ? most : nv};
+}
+
 struct NormFwdArgs {
   const void *x, *res, *w, *c;
   void *y, *h;
@@ -36,12 +46,12 @@ struct NormBwdArgs {
 };
 
 // wide: the weight, the bias and their gradients are float32 (else the I/O
-// type).  vec: elements per vector: 16, 8, 4 or 2 bytes' worth.
-int norm_fwd_f32(int vec, NormRow s, const NormFwdArgs &a, cudaStream_t st);
-int norm_fwd_f16(int vec, NormRow s, bool wide, const NormFwdArgs &a, cudaStream_t st);
-int norm_fwd_bf16(int vec, NormRow s, bool wide, const NormFwdArgs &a, cudaStream_t st);
-int norm_bwd_f32(int vec, NormRow s, const NormBwdArgs &a, int most, cudaStream_t st);
-int norm_bwd_f16(int vec, NormRow s, bool wide, const NormBwdArgs &a, int most, cudaStream_t st);
-int norm_bwd_bf16(int vec, NormRow s, bool wide, const NormBwdArgs &a, int most, cudaStream_t st);
+// type).  vec: elements per vector: 16 or 8 bytes' worth, or 1.
+int norm_fwd_f32(int vec, const NormFwdArgs &a, cudaStream_t st);
+int norm_fwd_f16(int vec, bool wide, const NormFwdArgs &a, cudaStream_t st);
+int norm_fwd_bf16(int vec, bool wide, const NormFwdArgs &a, cudaStream_t st);
+int norm_bwd_f32(int vec, const NormBwdArgs &a, int most, cudaStream_t st);
+int norm_bwd_f16(int vec, bool wide, const NormBwdArgs &a, int most, cudaStream_t st);
+int norm_bwd_bf16(int vec, bool wide, const NormBwdArgs &a, int most, cudaStream_t st);
 
 }  // namespace esa

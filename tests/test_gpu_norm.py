@@ -114,6 +114,54 @@ def test_strided_rows_and_in_place(cuda_device):
     assert torch.equal(d, g0[0])
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+@pytest.mark.parametrize("rows,N", [(1, 1), (2, 3), (19, 5), (9, 131), (37, 300), (13, 511), (5, 1001), (700, 1501),
+                                    (3, 4095), (4, 5001), (3, 8191), (2, 12345), (2, 16383)])
+@pytest.mark.parametrize("alike", [False, True])
+def test_any_alignment_and_nothing_written_outside(cuda_device, dt, rows, N, alike):
+    """Every tensor at its own distance from a 16-byte boundary, or all at the same, inside a buffer whose other
+    elements stay as they were and, as they are not a number, show if they are used."""
+    x, res, w, c, dy, dh = draw(dt, dt, rows, N, seed=N)
+    room = 64
+
+    def at(t, shift):
+        buf = torch.full((2 * room + t.numel(),), float("nan"), dtype=t.dtype, device="cuda")
+        view = buf[room // 2 + (1 if alike else shift):][:t.numel()].view(t.shape)
+        view.copy_(t)
+        return buf, view
+
+    outside = lambda buf, view: buf.isnan().sum() - view.isnan().sum() == 2 * room   # noqa: E731
+    plain = esa_norm_fwd(x, w, c, residual=res)
+    grads = esa_norm_bwd(dy, plain[1], w, plain[2], dh=dh)
+    bufs = {n: at(t, s) for n, t, s in (("x", x, 1), ("res", res, 3), ("w", w, 1), ("c", c, 2), ("dy", dy, 5), ("dh", dh, 2),
+                                        ("y", torch.zeros_like(x), 7), ("h", torch.zeros_like(x), 6),
+                                        ("dx", torch.zeros_like(x), 1), ("dw", torch.zeros_like(w), 3),
+                                        ("dc", torch.zeros_like(w), 5))}
+    v = {n: t for n, (_, t) in bufs.items()}
+    y, h, st = esa_norm_fwd(v["x"], v["w"], v["c"], residual=v["res"], y=v["y"], h=v["h"])
+    dx, dw, dc = esa_norm_bwd(v["dy"], h, v["w"], st, dh=v["dh"], dx=v["dx"], dweight=v["dw"], dbias=v["dc"])
+    assert torch.equal(h, plain[1])
+    ref = norm_reference(x, w, c, 1e-5, res, dy, dh)
+    tol = 100 * E * (1 + float(ref["y"].abs().max()))
+    assert_within("y", y, ref["y"], tol, tol)
+    assert_within("dx", dx, ref["dx"], tol, tol)
+    for a, b in zip((dw, dc), grads[1:]):   # two orders of one sum, each a float32 chain, then a rounding each
+        size = (dy.float().abs() * (1 + ref["y"].abs().max())).sum(0)
+        step = torch.finfo(a.dtype).eps
+        assert bool(((a.float() - b.float()).abs() <= step * b.float().abs() + 200 * E * size).all())
+    for buf, view in bufs.values():
+        assert outside(buf, view)
+    # rows apart from one another, which lets each row start elsewhere
+    ld = N + (8 if alike else 3)
+    wide = [torch.full((rows, ld), float("nan"), dtype=x.dtype, device="cuda")[:, :N] for _ in range(4)]
+    for u, t in zip(wide, (x, res, dy, dh)):
+        u.copy_(t)
+    y, h, st = esa_norm_fwd(wide[0], w, c, residual=wide[1])
+    assert torch.equal(h, plain[1])
+    assert_within("y", y, ref["y"], tol, tol)
+    assert_within("dx", esa_norm_bwd(wide[2], h, w, st, dh=wide[3])[0], ref["dx"], tol, tol)
+
+
 def test_no_rows(cuda_device):
     x = torch.empty(0, 32, device="cuda")
     y, h, s = esa_norm_fwd(x, torch.ones(32, device="cuda"), None)
