@@ -12,7 +12,12 @@
 // so it keeps their weights in registers and adds up their gradients there.
 // Rows are staged ahead in shared memory, each thread's units its own.
 //
-// MEASURED_RAGGED
+// Measured: 4099 x 5001 float32 51 us forward (3.2 TB/s), 60 backward (4.1);
+// 3000 x 8001 float16 46 and 76; 200000 x 129 float16 74 and 95.  Element by
+// element (the kernels of esa_norm.cuh with VEC = 1): 60 and 90, 115 and 224,
+// 71 and 96.  With whole rows copied through shared memory, elements dealt to
+// threads there: 68 and 115, bound by some 70 instructions an element.  The
+// forward without staging, a block a row, weights read anew: 61, 88, 108.
 #pragma once
 
 #include <climits>
