@@ -15,9 +15,18 @@ namespace {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Sequences of 16-bit types of at least this many tokens go through the
-// chunked kernels, shorter ones and float32 token by token.
-constexpr int kChunkMinT = 17;
-bool chunked(const DeltaShape &s, int dtype) { return dtype != ESA_F32 && s.T >= kChunkMinT; }
+// chunked kernels, shorter ones and float32 token by token.  A chunk costs the
+// same however few its tokens, a sweep goes by the token, and the gradients
+// have four sweeps.  Forward alone (us, chunked / token by token): 8 heads
+// 9.5 / 7.1 at T = 32 and D = 32, 10.2 / 8.8 at D = 64, 11.6 / 13.9 at D = 128;
+// 512 heads of D = 64 22 / 16 at T = 24, 22 / 20 at 32, 23 / 30 at 48.  With
+// the backward: 8 heads of D = 64 21 / 21 at T = 4, 21 / 25 at 8; 512 heads of
+// D = 64 54 / 47 at T = 8, 55 / 69 at 16; of D = 128 132 / 127 at T = 4, 133 /
+// 178 at 8.
+constexpr int kChunkMinT = 32, kChunkMinKeptT = 8;
+bool chunked(const DeltaShape &s, int dtype, bool keep) {
+  return dtype != ESA_F32 && s.T >= (keep ? kChunkMinKeptT : kChunkMinT);
+}
 
 // Token by token: what the forward keeps for the backward (u, the state at
 // each chunk), then the backward's scratch.
@@ -123,7 +132,7 @@ size_t esa_delta_workspace_size(int B, int T, int H, int D, int dtype, int keep)
   if (check_shape(B, T, H, D, dtype) != ESA_OK || (keep != 0 && keep != 1)) return 0;
   const DeltaShape s{B, T, H, D, 0, 0, 0, 1.0f};
   size_t total = 0;
-  if (chunked(s, dtype)) {
+  if (chunked(s, dtype, keep != 0)) {
     chunk_arrays(nullptr, s, keep != 0, &total);
     return total + 256;
   }
@@ -146,7 +155,7 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (B == 0) return ESA_OK;
   if (T == 0) return copy_state(S_final, S_init, s, st);
-  if (chunked(s, dtype)) {
+  if (chunked(s, dtype, keep != 0)) {
     ChunkArgs c{};
     size_t total;
     c.s = s;
@@ -196,7 +205,7 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
   if (B == 0) return ESA_OK;
   if (T == 0) return copy_state(dS_init, dS_final, s, st);
   unsigned char *base = static_cast<unsigned char *>(workspace);
-  if (chunked(s, dtype)) {
+  if (chunked(s, dtype, true)) {
     ChunkArgs c{};
     size_t total;
     c.s = s;

@@ -90,6 +90,18 @@ def test_inference_call_and_many_heads(cuda_device, D, T):
     check(x, {"y": y[pick, :, :4], "S": full["S"][pick, :4]}, ref, T, D, gradients=False, half_p=3 * 2.0 ** -11)
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("T", [7, 8, 31, 32])
+def test_short_sequences(cuda_device, dt, D, T):
+    """Around the lengths from which chunks are used, with and without a backward to come."""
+    x, S0, dS = draw(dt, 2, T, 3, D, seed=T + D)
+    ref = delta_reference(*ins(x), D ** -0.5, S0, x["dy"], dS)
+    check(x, run(x, S0, dS, None), ref, T, D, half_p=3 * 2.0 ** -11)
+    y, S, _ = esa_delta_fwd(*ins(x), S_init=S0, keep=False)
+    check(x, {"y": y, "S": S}, ref, T, D, gradients=False, half_p=3 * 2.0 ** -11)
+
+
 @pytest.mark.parametrize("D", [32, 64, 128])
 def test_steps_equal_the_sequence(cuda_device, D):
     T = 21
