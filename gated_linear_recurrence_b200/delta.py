@@ -44,11 +44,11 @@ def esa_delta_workspace_size(B: int, T: int, H: int, D: int, dtype, keep: bool =
     return int(load_library().esa_delta_workspace_size(B, T, H, D, code, int(bool(keep))))
 
 
-def _new_workspace(B, T, H, D, dtype, keep, device):
-    n = esa_delta_workspace_size(B, T, H, D, dtype, keep)
+def _new_workspace(B, T, H, D, q, keep):
+    n = load_library().esa_delta_workspace_size(B, T, H, D, _DTYPE_CODE[q.dtype], 1 if keep else 0)
     if n == 0:
         raise ValueError(f"unsupported shape for the delta rule: B={B}, T={T}, H={H}, D={D} (D is 32, 64 or 128)")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return q.new_empty(n, dtype=torch.uint8)
 
 
 def _check_workspace(workspace, device):
@@ -81,13 +81,16 @@ def _inputs(q, k, v, a, b):
         raise ValueError("sequence tensors must be [B, T, H, D]")
     if q.dtype not in _DTYPE_CODE:
         raise TypeError(f"unsupported dtype {q.dtype} (float32, float16 or bfloat16)")
-    for name, t, shape in (("k", k, q.shape), ("v", v, q.shape), ("a", a, q.shape[:3]), ("b", b, q.shape[:3])):
+    shape, dtype, where = q.shape, q.dtype, q.get_device()
+    gates, dense = shape[:3], q.is_contiguous()
+    for name, t, want in (("k", k, shape), ("v", v, shape), ("a", a, gates), ("b", b, gates)):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor (the ESA library has no CPU path)")
-        if t.shape != shape or t.dtype != q.dtype or t.device != q.device:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, dtype {q.dtype}, {q.device}")
-    B, T, H, D = (int(s) for s in q.shape)
-    if B == 0 or T == 0:
+        if t.shape != want or t.dtype is not dtype or t.get_device() != where:
+            raise ValueError(f"{name} must have shape {tuple(want)}, dtype {dtype}, {q.device}")
+        dense = dense and t.is_contiguous()
+    B, T, H, D = shape
+    if dense or B == 0 or T == 0:
         return B, T, H, D, H * D, H * D, H
     ld_q, ld_k, ld_v, ld_a, ld_b = row_stride(q), row_stride(k), row_stride(v), _gate_stride(a), _gate_stride(b)
     for name, ld in (("q", ld_q), ("k", ld_k), ("v", ld_v)):
@@ -110,8 +113,6 @@ def _check_state(name, t, B, H, D, device):
 
 
 def _out(name, t, shape, dtype, device):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device \
             or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
@@ -133,13 +134,14 @@ def esa_delta_fwd(q, k, v, a, b, scale=None, S_init=None, y=None, S_final=None, 
     inference call passes False and needs next to no workspace.
     """
     B, T, H, D, ld_qk, ld_v, ld_g = _inputs(q, k, v, a, b)
-    y = _out("y", y, q.shape, q.dtype, q.device)
-    if S_final is None and want_S_final:
-        S_final = torch.empty((B, H, D, D), dtype=torch.float32, device=q.device)
-    _check_state("S_final", S_final, B, H, D, q.device)
+    y = q.new_empty(q.shape) if y is None else _out("y", y, q.shape, q.dtype, q.device)
+    if S_final is not None:
+        _check_state("S_final", S_final, B, H, D, q.device)
+    elif want_S_final:
+        S_final = q.new_empty((B, H, D, D), dtype=torch.float32)
     _check_state("S_init", S_init, B, H, D, q.device)
     if workspace is None:
-        workspace = _new_workspace(B, T, H, D, q.dtype, keep, q.device)
+        workspace = _new_workspace(B, T, H, D, q, keep)
     nbytes = _check_workspace(workspace, q.device)
     with _on(q.device):
         rc = load_library().esa_delta_fwd(
@@ -160,14 +162,12 @@ def esa_delta_bwd(q, k, v, a, b, dy, workspace, scale=None, S_init=None, dS_fina
     if not isinstance(dy, torch.Tensor) or not dy.is_cuda:
         raise TypeError("dy must be a CUDA tensor (the ESA library has no CPU path)")
     dy = _out("dy", dy, q.shape, q.dtype, q.device)
-    dq = _out("dq", dq, q.shape, q.dtype, q.device)
-    dk = _out("dk", dk, q.shape, q.dtype, q.device)
-    dv = _out("dv", dv, q.shape, q.dtype, q.device)
-    da = _out("da", da, a.shape, q.dtype, q.device)
-    db = _out("db", db, a.shape, q.dtype, q.device)
-    if dS_init is None and want_dS_init:
-        dS_init = torch.empty((B, H, D, D), dtype=torch.float32, device=q.device)
-    _check_state("dS_init", dS_init, B, H, D, q.device)
+    dq, dk, dv, da, db = (like.new_empty(like.shape) if t is None else _out(name, t, like.shape, q.dtype, q.device)
+                          for name, t, like in (("dq", dq, q), ("dk", dk, q), ("dv", dv, q), ("da", da, a), ("db", db, a)))
+    if dS_init is not None:
+        _check_state("dS_init", dS_init, B, H, D, q.device)
+    elif want_dS_init:
+        dS_init = q.new_empty((B, H, D, D), dtype=torch.float32)
     _check_state("dS_final", dS_final, B, H, D, q.device)
     _check_state("S_init", S_init, B, H, D, q.device)
     if workspace is None:

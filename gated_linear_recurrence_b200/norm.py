@@ -73,8 +73,6 @@ def _wdtype(x, *params):
 
 
 def _out(name, t, shape, dtype, device):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device \
             or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
@@ -103,8 +101,10 @@ def esa_norm_fwd(x, weight=None, bias=None, eps=1e-5, residual=None, y=None, h=N
             raise ValueError("h is an output of the residual addition: give residual too")
     else:
         h = torch.empty_like(y) if h is None else _out("h", h, x.shape, x.dtype, x.device)
-    if stats is not None or want_stats:
-        stats = _out("stats", stats, (rows, 2), torch.float32, x.device)
+    if stats is not None:
+        _out("stats", stats, (rows, 2), torch.float32, x.device)
+    elif want_stats:
+        stats = x.new_empty((rows, 2), dtype=torch.float32)
     with _on(x.device):
         rc = load_library().esa_norm_fwd(_ptr(x), ld_x, _ptr(residual), ld_r, _ptr(weight), _ptr(bias), _ptr(y),
                                          _ptr(h), _ptr(stats), rows, N, float(eps), _DTYPE_CODE[x.dtype],
@@ -130,18 +130,22 @@ def esa_norm_bwd(dy, h, weight, stats, dh=None, dx=None, dweight=None, dbias=Non
     wdt = weight.dtype if weight is not None else (wdtype or h.dtype)
     if wdt not in (h.dtype, torch.float32):
         raise TypeError(f"wdtype must be {h.dtype} or float32")
-    if not isinstance(stats, torch.Tensor) or tuple(stats.shape) != (rows, 2) or stats.dtype != torch.float32 \
-            or stats.device != h.device or not stats.is_contiguous():
+    if not isinstance(stats, torch.Tensor) or stats.shape != (rows, 2) or stats.dtype is not torch.float32 \
+            or stats.get_device() != h.get_device() or not stats.is_contiguous():
         raise ValueError(f"stats must be the forward's contiguous float32 tensor of shape {(rows, 2)}")
-    dx = _out("dx", dx, h.shape, h.dtype, h.device)
-    if dweight is not None or want_dweight:
-        dweight = _out("dweight", dweight, (N,), wdt, h.device)
-    if dbias is not None or want_dbias:
-        dbias = _out("dbias", dbias, (N,), wdt, h.device)
+    dx = h.new_empty(h.shape) if dx is None else _out("dx", dx, h.shape, h.dtype, h.device)
+    if dweight is not None:
+        _out("dweight", dweight, (N,), wdt, h.device)
+    elif want_dweight:
+        dweight = h.new_empty((N,), dtype=wdt)
+    if dbias is not None:
+        _out("dbias", dbias, (N,), wdt, h.device)
+    elif want_dbias:
+        dbias = h.new_empty((N,), dtype=wdt)
     lib = load_library()
     codes = (_DTYPE_CODE[h.dtype], _DTYPE_CODE[wdt])
     if workspace is None and (dweight is not None or dbias is not None):
-        workspace = torch.empty(int(lib.esa_norm_workspace_size(rows, N, *codes)), dtype=torch.uint8, device=h.device)
+        workspace = h.new_empty(lib.esa_norm_workspace_size(rows, N, *codes), dtype=torch.uint8)
     nbytes = 0
     if workspace is not None:
         if not workspace.is_cuda or workspace.device != h.device or not workspace.is_contiguous():
