@@ -130,8 +130,9 @@ def esa_delta_fwd(q, k, v, a, b, scale=None, S_init=None, y=None, S_final=None, 
     ``q, k, v`` [B, T, H, D] and the logits ``a, b`` [B, T, H] may be
     row-strided views (column blocks of one projection output; q and k share
     a row stride, a and b another).  ``scale`` defaults to D ** -0.5.
-    ``keep`` leaves in the workspace what :func:`esa_delta_bwd` reads; an
-    inference call passes False and needs next to no workspace.
+    ``keep`` leaves in the workspace what :func:`esa_delta_bwd` reads (9 times
+    ``q``'s bytes with 16-bit tensors); an inference call passes False (3.4
+    times at D = 128, 4.8 at D = 64).
     """
     B, T, H, D, ld_qk, ld_v, ld_g = _inputs(q, k, v, a, b)
     y = q.new_empty(q.shape) if y is None else _out("y", y, q.shape, q.dtype, q.device)

@@ -330,6 +330,19 @@ class _DeltaRuleFn(torch.autograd.Function):
         return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), dS0, None, None, None)
 
 
+def _in_place(t):
+    """Whether the library reads these rows as they lie: evenly spaced, each on 16 bytes."""
+    if t.dim() != 4 or not t.numel():
+        return True   # for the call to refuse, or nothing to read
+    ld = _esa.row_stride(t)
+    return ld is not None and ld * t.element_size() % 16 == 0 and t.data_ptr() % 16 == 0
+
+
+def _dense(t):
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def delta_rule(q, k, v, a, b, scale=None, S_init=None, want_S_final=True):
     """Differentiable gated delta rule (see :func:`~.delta.esa_delta_fwd`):
     ``q, k, v`` [B, T, H, D] and the logits ``a, b`` [B, T, H], D of 32, 64 or
@@ -337,10 +350,10 @@ def delta_rule(q, k, v, a, b, scale=None, S_init=None, want_S_final=True):
     ``want_S_final=False``).  ``S_init`` (float32 [B, H, D, D]) may require
     grad.  Column blocks of one projection output are read in place; any other
     layout is copied.  Without a gradient to come nothing is kept for it."""
-    if q.dim() == 4 and q.numel() and (_esa.row_stride(q) is None or _esa.row_stride(q) != _esa.row_stride(k)):
-        q, k = q.contiguous(), k.contiguous()
-    if v.dim() == 4 and v.numel() and _esa.row_stride(v) is None:
-        v = v.contiguous()
+    if not _in_place(q) or not _in_place(k) or q.stride() != k.stride():
+        q, k = _dense(q), _dense(k)
+    if not _in_place(v):
+        v = _dense(v)
     if a.dim() == 3 and a.numel() and (_delta._gate_stride(a) is None or _delta._gate_stride(a) != _delta._gate_stride(b)):
         a, b = a.contiguous(), b.contiguous()
     return _DeltaRuleFn.apply(q, k, v, a, b, S_init, scale, _wants_grad(q, k, v, a, b, S_init), want_S_final)

@@ -215,6 +215,43 @@ def test_delta_rule_gradients_and_views(cuda_device, dtype, T):
     assert float(d3.abs().max()) == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_delta_rule_copies_rows_off_16_bytes(cuda_device, dtype):
+    torch.manual_seed(7)
+    B, T, H, D = 2, 40, 2, 32
+    P = torch.randn(B, T, 3 * H * D + 1, device="cuda", dtype=dtype) / 6       # an odd row stride
+    q, k, v = (P[..., i * H * D:(i + 1) * H * D].unflatten(-1, (H, D)) for i in range(3))
+    flat = torch.randn(B * T * H * D + 1, device="cuda", dtype=dtype)
+    g = torch.randn(B, T, H, device="cuda", dtype=dtype)
+    want = delta_rule(q.contiguous(), k.contiguous(), v.contiguous(), g, g)
+    assert all(torch.equal(x, y) for x, y in zip(delta_rule(q, k, v, g, g), want))
+    off = flat[1:].view(B, T, H, D)                                             # contiguous, one element off
+    want = delta_rule(q.contiguous(), k.contiguous(), off.clone(), g, g)
+    assert all(torch.equal(x, y) for x, y in zip(delta_rule(q, k, off, g, g), want))
+
+
+@pytest.mark.parametrize("dtype,D,H", [(torch.float32, 32, 2), (torch.bfloat16, 64, 2), (torch.bfloat16, 128, 40)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_gradient_that_is_not_finite_shows(cuda_device, dtype, D, H, value):
+    """It reaches its head's gradients of all earlier tokens, no other head, and none behind its chunk of 64."""
+    torch.manual_seed(12)
+    B, T = 2, 200
+    r = lambda *s: torch.randn(*s, device="cuda").to(dtype)   # noqa: E731
+    x = [r(B, T, H, D) / 8, r(B, T, H, D) / 16, r(B, T, H, D), r(B, T, H) + 3, r(B, T, H)]
+    x = [t.requires_grad_(True) for t in x]
+    y, _ = delta_rule(*x)
+    dy = r(B, T, H, D)
+    dy[1, 70, 1, 5] = value
+    grads = torch.autograd.grad(y, x, dy)
+    for name, g in zip("qkvab", grads):
+        bad = ~g.float().isfinite().reshape(B, T, H, -1).all(-1)
+        if name != "q":
+            assert bool(bad[1, :71, 1].all()), name
+        else:
+            assert bool(bad[1, 70, 1]), name
+        assert not bad[1, 128:].any() and not bad[0].any() and not bad[1, :, 0].any(), name
+
+
 def test_against_differences(cuda_device):
     """The gradients along a random direction against central differences of the float32 forward.
 

@@ -171,6 +171,15 @@ def test_split_sequence(cuda_device, T, D):
     assert_within("S", S2, S.double().cpu(), 2 * PER_TOKEN * T, 2 * PER_TOKEN * T ** 0.5)
 
 
+@pytest.mark.parametrize("dt,D,H,T", [("f32", 32, 2, 40), ("bf16", 128, 2, 150), ("bf16", 128, 40, 150), ("f16", 64, 90, 70),
+                                      ("bf16", 64, 3, 5)])
+def test_final_state_over_the_initial_one(cuda_device, dt, D, H, T):
+    x, S0, _ = draw(dt, 2, T, H, D, seed=17)
+    y, S, _ = esa_delta_fwd(*ins(x), S_init=S0)
+    y2, S2, _ = esa_delta_fwd(*ins(x), S_init=S0, S_final=S0)
+    assert S2 is S0 and torch.equal(S, S0) and torch.equal(y, y2)
+
+
 def test_strided_rows_and_outputs_given(cuda_device):
     B, T, H, D = 2, 77, 2, 64
     C = H * D
