@@ -12,12 +12,13 @@
 // so it keeps their weights in registers and adds up their gradients there.
 // Rows are staged ahead in shared memory, each thread's units its own.
 //
-// Measured: 4099 x 5001 float32 51 us forward (3.2 TB/s), 60 backward (4.1);
-// 3000 x 8001 float16 46 and 76; 200000 x 129 float16 74 and 95.  Element by
+// Measured: 4099 x 5001 float32 50 us forward (3.3 TB/s), 55 backward (4.5);
+// 3000 x 8001 float16 46 and 75; 200000 x 129 float16 75 and 97.  Element by
 // element (the kernels of esa_norm.cuh with VEC = 1): 60 and 90, 115 and 224,
 // 71 and 96.  With whole rows copied through shared memory, elements dealt to
 // threads there: 68 and 115, bound by some 70 instructions an element.  The
 // forward without staging, a block a row, weights read anew: 61, 88, 108.
+// Half the elements a thread: 56 and 68, 49 and 71.
 #pragma once
 
 #include <climits>
@@ -31,8 +32,8 @@ namespace {
 // Unit of VEC elements at element `at` of a tensor of `end` elements, column
 // `col` of its row, into a thread's own place in shared memory.
 template <typename V, typename T, int VEC>
-__device__ __forceinline__ void unit_fetch(V *s, const T *base, long long at, long long end, int col, int N) {
-  if (at >= 0 && at + VEC <= end) {
+__device__ __forceinline__ void unit_fetch(V *s, const T *base, long long at, bool inside, int col, int N) {
+  if (inside || (col >= 0 && col + VEC <= N)) {
     copy_async<16>(s, base + at);
   } else {
 #pragma unroll
@@ -57,6 +58,38 @@ __device__ __forceinline__ void unit_store(T *dst, const V &v, int col, int N) {
   }
 }
 
+// Sums over the threads of a row; of more than a warp each warp adds the
+// warps' sums for itself (with 16 warps and more, cheaper than every thread
+// adding all of them).
+template <int TPR>
+__device__ __forceinline__ float ragged_sum(float a, float (*red)[32], int &slot) {
+  a = row_sum<(TPR < 32 ? TPR : 32)>(a, red, slot);
+  if constexpr (TPR > 32) {
+    float *r = red[slot];
+    slot ^= 1;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) r[threadIdx.x >> 5] = a;
+    __syncthreads();
+    a = row_sum<TPR / 32>(r[lane & (TPR / 32 - 1)], red, slot);
+  }
+  return a;
+}
+template <int TPR>
+__device__ __forceinline__ void ragged_sum2(float &a, float &b, float2 (*red)[32], int &slot) {
+  row_sum2<(TPR < 32 ? TPR : 32)>(a, b, red, slot);
+  if constexpr (TPR > 32) {
+    float2 *r = red[slot];
+    slot ^= 1;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) r[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    const float2 v = r[lane & (TPR / 32 - 1)];
+    a = v.x;
+    b = v.y;
+    row_sum2<TPR / 32>(a, b, red, slot);
+  }
+}
+
 template <typename T, typename WT, int VEC, int NV, int TPR>
 __global__ void __launch_bounds__(norm_block<TPR>()) norm_fwd_ragged_kernel(NormFwdArgs p, int stages) {
   constexpr int BLOCK = norm_block<TPR>(), GROUPS = BLOCK / TPR;
@@ -68,7 +101,6 @@ __global__ void __launch_bounds__(norm_block<TPR>()) norm_fwd_ragged_kernel(Norm
   const T *x = static_cast<const T *>(p.x), *res = static_cast<const T *>(p.res);
   T *y = static_cast<T *>(p.y), *h = static_cast<T *>(p.h);
   const long long stride = static_cast<long long>(gridDim.x) * GROUPS;
-  const long long end_x = (p.rows - 1) * p.ld_x + p.N, end_r = (p.rows - 1) * p.ld_res + p.N;
   long long row = static_cast<long long>(blockIdx.x) * GROUPS + group;
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x + row * p.ld_x) & 15) / static_cast<int>(sizeof(T));
   auto col_of = [&](int i) { return (i * TPR + lane) * VEC - off; };
@@ -86,13 +118,14 @@ __global__ void __launch_bounds__(norm_block<TPR>()) norm_fwd_ragged_kernel(Norm
     }
   auto fetch = [&](long long r, int k) {
     if (r < p.rows) {
+      const bool inside = r > 0 && r < p.rows - 1;   // units that reach into other rows stay in the tensor
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int col = col_of(i);
         V *s = stage + (k * ins * NV + i) * BLOCK;
         if (used(col)) {
-          unit_fetch<V, T, VEC>(s, x, r * p.ld_x + col, end_x, col, p.N);
-          if (res) unit_fetch<V, T, VEC>(s + NV * BLOCK, res, r * p.ld_res + col, end_r, col, p.N);
+          unit_fetch<V, T, VEC>(s, x, r * p.ld_x + col, inside, col, p.N);
+          if (res) unit_fetch<V, T, VEC>(s + NV * BLOCK, res, r * p.ld_res + col, inside, col, p.N);
         }
       }
     }
@@ -130,7 +163,7 @@ __global__ void __launch_bounds__(norm_block<TPR>()) norm_fwd_ragged_kernel(Norm
     }
     fetch(row + stages * stride, k);
     k = k + 1 == stages ? 0 : k + 1;
-    const float mean = row_sum<TPR>(s, red, slot) / p.n;
+    const float mean = ragged_sum<TPR>(s, red, slot) / p.n;
     s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -146,7 +179,7 @@ __global__ void __launch_bounds__(norm_block<TPR>()) norm_fwd_ragged_kernel(Norm
           if (col + j >= 0 && col + j < p.N) s = fmaf(f[i][j], f[i][j], s);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<TPR>(s, red, slot) / p.n + p.eps);
+    const float rstd = 1.0f / sqrtf(ragged_sum<TPR>(s, red, slot) / p.n + p.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int col = col_of(i);
@@ -173,8 +206,6 @@ __global__ void __launch_bounds__(norm_block<TPR>()) norm_bwd_ragged_kernel(Norm
   const T *h = static_cast<const T *>(p.h), *dy = static_cast<const T *>(p.dy), *dh = static_cast<const T *>(p.dh);
   T *dx = static_cast<T *>(p.dx);
   const long long stride = static_cast<long long>(gridDim.x) * GROUPS;
-  const long long end_h = (p.rows - 1) * p.ld_h + p.N, end_y = (p.rows - 1) * p.ld_dy + p.N,
-                  end_d = (p.rows - 1) * p.ld_dh + p.N;
   long long row = static_cast<long long>(blockIdx.x) * GROUPS + group;
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(h + row * p.ld_h) & 15) / static_cast<int>(sizeof(T));
   auto col_of = [&](int i) { return (i * TPR + lane) * VEC - off; };
@@ -190,14 +221,15 @@ __global__ void __launch_bounds__(norm_block<TPR>()) norm_bwd_ragged_kernel(Norm
     }
   auto fetch = [&](long long r, int k) {
     if (r < p.rows) {
+      const bool inside = r > 0 && r < p.rows - 1;   // units that reach into other rows stay in the tensor
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int col = col_of(i);
         V *s = stage + (k * ins * NV + i) * BLOCK;
         if (used(col)) {
-          unit_fetch<V, T, VEC>(s, h, r * p.ld_h + col, end_h, col, p.N);
-          unit_fetch<V, T, VEC>(s + NV * BLOCK, dy, r * p.ld_dy + col, end_y, col, p.N);
-          if (dh) unit_fetch<V, T, VEC>(s + 2 * NV * BLOCK, dh, r * p.ld_dh + col, end_d, col, p.N);
+          unit_fetch<V, T, VEC>(s, h, r * p.ld_h + col, inside, col, p.N);
+          unit_fetch<V, T, VEC>(s + NV * BLOCK, dy, r * p.ld_dy + col, inside, col, p.N);
+          if (dh) unit_fetch<V, T, VEC>(s + 2 * NV * BLOCK, dh, r * p.ld_dh + col, inside, col, p.N);
         }
       }
     }
@@ -236,7 +268,7 @@ __global__ void __launch_bounds__(norm_block<TPR>()) norm_bwd_ragged_kernel(Norm
         }
       }
     }
-    row_sum2<TPR>(s1, s2, red, slot);
+    ragged_sum2<TPR>(s1, s2, red, slot);
     s1 /= p.n;
     s2 /= p.n;
 #pragma unroll

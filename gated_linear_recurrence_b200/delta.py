@@ -31,6 +31,11 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _like(t):
+    """A contiguous tensor of t's shape and type (empty_like is the cheapest call that makes one)."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _stream(device, stream):
     if stream is not None:
         return stream.cuda_stream
@@ -135,7 +140,7 @@ def esa_delta_fwd(q, k, v, a, b, scale=None, S_init=None, y=None, S_final=None, 
     times at D = 128, 4.8 at D = 64).
     """
     B, T, H, D, ld_qk, ld_v, ld_g = _inputs(q, k, v, a, b)
-    y = q.new_empty(q.shape) if y is None else _out("y", y, q.shape, q.dtype, q.device)
+    y = _like(q) if y is None else _out("y", y, q.shape, q.dtype, q.device)
     if S_final is not None:
         _check_state("S_final", S_final, B, H, D, q.device)
     elif want_S_final:
@@ -163,7 +168,7 @@ def esa_delta_bwd(q, k, v, a, b, dy, workspace, scale=None, S_init=None, dS_fina
     if not isinstance(dy, torch.Tensor) or not dy.is_cuda:
         raise TypeError("dy must be a CUDA tensor (the ESA library has no CPU path)")
     dy = _out("dy", dy, q.shape, q.dtype, q.device)
-    dq, dk, dv, da, db = (like.new_empty(like.shape) if t is None else _out(name, t, like.shape, q.dtype, q.device)
+    dq, dk, dv, da, db = (_like(like) if t is None else _out(name, t, like.shape, q.dtype, q.device)
                           for name, t, like in (("dq", dq, q), ("dk", dk, q), ("dv", dv, q), ("da", da, a), ("db", db, a)))
     if dS_init is not None:
         _check_state("dS_init", dS_init, B, H, D, q.device)
@@ -201,23 +206,26 @@ def _step_args(q_t, k_t, v_t, a_t, b_t, S, y_t, scale):
     if dtype not in _DTYPE_CODE:
         raise TypeError(f"unsupported dtype {dtype} (float32, float16 or bfloat16)")
     B, H, D = shape
-    gates = shape[:2]
+    gates, dense = shape[:2], q_t.is_contiguous()
     for name, t, want in (("k_t", k_t, shape), ("v_t", v_t, shape), ("a_t", a_t, gates), ("b_t", b_t, gates)):
         if not isinstance(t, torch.Tensor) or t.get_device() != where:
             raise TypeError(f"{name} must be a CUDA tensor on {q_t.device}")
         if t.shape != want or t.dtype is not dtype:
             raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(want)}")
-    ld_qk, ld_v, ld_g = (_token_stride(n, t, H, w) for n, t, w in (("q_t", q_t, D), ("v_t", v_t, D), ("a_t", a_t, 1)))
-    if _token_stride("k_t", k_t, H, D) != ld_qk or _token_stride("b_t", b_t, H, 1) != ld_g:
-        raise ValueError("q_t and k_t must share one row stride, a_t and b_t another")
+        dense = dense and t.is_contiguous()
+    ld_qk = ld_v = H * D
+    ld_g = H
+    if not dense:
+        ld_qk, ld_v, ld_g = (_token_stride(n, t, H, w) for n, t, w in (("q_t", q_t, D), ("v_t", v_t, D), ("a_t", a_t, 1)))
+        if _token_stride("k_t", k_t, H, D) != ld_qk or _token_stride("b_t", b_t, H, 1) != ld_g:
+            raise ValueError("q_t and k_t must share one row stride, a_t and b_t another")
     if S is None:
         raise ValueError("S (the recurrent state) is required")
     if not isinstance(S, torch.Tensor) or S.get_device() != where:
         raise TypeError(f"S must be a CUDA tensor on {q_t.device}")
     if S.shape != (B, H, D, D) or S.dtype is not torch.float32 or not S.is_contiguous():
         raise ValueError(f"S must be a contiguous float32 tensor of shape {(B, H, D, D)}")
-    y_t = torch.empty(shape, dtype=dtype, device=q_t.device) if y_t is None else \
-        _out("y_t", y_t, shape, dtype, q_t.device)
+    y_t = _like(q_t) if y_t is None else _out("y_t", y_t, shape, dtype, q_t.device)
     return y_t, (q_t.data_ptr(), k_t.data_ptr(), ld_qk, v_t.data_ptr(), ld_v, a_t.data_ptr(), b_t.data_ptr(), ld_g,
                  S.data_ptr(), y_t.data_ptr(), B, H, D, D ** -0.5 if scale is None else float(scale),
                  _DTYPE_CODE[dtype])

@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import torch
 
-from .delta import _ptr, _stream
+from .delta import _like, _ptr, _stream
 from .esa import EsaError, _on, load_library
 
 _DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
@@ -57,19 +57,11 @@ def _check_x(x, name="x"):
 
 
 def _check_param(name, p, x, N):
-    if p is None:
-        return
     if not isinstance(p, torch.Tensor) or p.get_device() != x.get_device() or p.shape != (N,) or not p.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {(N,)} on {x.device}")
-    if p.dtype not in (x.dtype, torch.float32):
+    if p.dtype is not torch.float32 and p.dtype is not x.dtype:
         raise TypeError(f"{name} must be {x.dtype} or float32")
-
-
-def _wdtype(x, *params):
-    given = [p.dtype for p in params if p is not None]
-    if any(dt is not given[0] for dt in given):
-        raise TypeError("weight and bias must share one dtype")
-    return given[0] if given else x.dtype
+    return p.dtype
 
 
 def _out(name, t, shape, dtype, device):
@@ -91,16 +83,17 @@ def esa_norm_fwd(x, weight=None, bias=None, eps=1e-5, residual=None, y=None, h=N
     rows, N = _check_x(x)
     ld_x = _rows("x", x)
     ld_r = N if residual is None else _rows("residual", residual, x)
-    _check_param("weight", weight, x, N)
-    _check_param("bias", bias, x, N)
-    wdt = _wdtype(x, weight, bias)
-    y = torch.empty_like(x, memory_format=torch.contiguous_format) if y is None else \
-        _out("y", y, x.shape, x.dtype, x.device)
+    wdt = None if weight is None else _check_param("weight", weight, x, N)
+    if bias is not None:
+        if _check_param("bias", bias, x, N) is not (wdt or bias.dtype):
+            raise TypeError("weight and bias must share one dtype")
+        wdt = bias.dtype
+    y = _like(x) if y is None else _out("y", y, x.shape, x.dtype, x.device)
     if residual is None:
         if h is not None:
             raise ValueError("h is an output of the residual addition: give residual too")
     else:
-        h = torch.empty_like(y) if h is None else _out("h", h, x.shape, x.dtype, x.device)
+        h = _like(y) if h is None else _out("h", h, x.shape, x.dtype, x.device)
     if stats is not None:
         _out("stats", stats, (rows, 2), torch.float32, x.device)
     elif want_stats:
@@ -108,7 +101,7 @@ def esa_norm_fwd(x, weight=None, bias=None, eps=1e-5, residual=None, y=None, h=N
     with _on(x.device):
         rc = load_library().esa_norm_fwd(_ptr(x), ld_x, _ptr(residual), ld_r, _ptr(weight), _ptr(bias), _ptr(y),
                                          _ptr(h), _ptr(stats), rows, N, float(eps), _DTYPE_CODE[x.dtype],
-                                         _DTYPE_CODE[wdt], _stream(x.device, stream))
+                                         _DTYPE_CODE[wdt or x.dtype], _stream(x.device, stream))
     if rc != 0:
         raise EsaError("esa_norm_fwd", rc)
     return y, (x if residual is None else h), stats
@@ -126,14 +119,13 @@ def esa_norm_bwd(dy, h, weight, stats, dh=None, dx=None, dweight=None, dbias=Non
     rows, N = _check_x(h, "h")
     ld_h, ld_dy = _rows("h", h), _rows("dy", dy, h)
     ld_dh = N if dh is None else _rows("dh", dh, h)
-    _check_param("weight", weight, h, N)
-    wdt = weight.dtype if weight is not None else (wdtype or h.dtype)
-    if wdt not in (h.dtype, torch.float32):
+    wdt = _check_param("weight", weight, h, N) if weight is not None else (wdtype or h.dtype)
+    if wdt is not torch.float32 and wdt is not h.dtype:
         raise TypeError(f"wdtype must be {h.dtype} or float32")
     if not isinstance(stats, torch.Tensor) or stats.shape != (rows, 2) or stats.dtype is not torch.float32 \
             or stats.get_device() != h.get_device() or not stats.is_contiguous():
         raise ValueError(f"stats must be the forward's contiguous float32 tensor of shape {(rows, 2)}")
-    dx = h.new_empty(h.shape) if dx is None else _out("dx", dx, h.shape, h.dtype, h.device)
+    dx = _like(h) if dx is None else _out("dx", dx, h.shape, h.dtype, h.device)
     if dweight is not None:
         _out("dweight", dweight, (N,), wdt, h.device)
     elif want_dweight:
