@@ -116,9 +116,10 @@ __global__ void __launch_bounds__(norm_block<TPR>()) norm_fwd_ragged_kernel(Norm
       w[i][j] = on && p.w ? to_f(load_readonly(static_cast<const WT *>(p.w) + col)) : 1.0f;
       c[i][j] = on && p.c ? to_f(load_readonly(static_cast<const WT *>(p.c) + col)) : 0.0f;
     }
+  const int edge = (VEC + p.N - 1) / p.N;   // rows, at least N apart, that hold a unit
   auto fetch = [&](long long r, int k) {
     if (r < p.rows) {
-      const bool inside = r > 0 && r < p.rows - 1;   // units that reach into other rows stay in the tensor
+      const bool inside = r >= edge && r < p.rows - edge;   // units that reach into other rows stay in the tensor
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int col = col_of(i);
@@ -219,9 +220,10 @@ __global__ void __launch_bounds__(norm_block<TPR>()) norm_bwd_ragged_kernel(Norm
       w[i][j] = col >= 0 && col < p.N && p.w ? to_f(load_readonly(static_cast<const WT *>(p.w) + col)) : 1.0f;
       aw[i][j] = ac[i][j] = 0.0f;
     }
+  const int edge = (VEC + p.N - 1) / p.N;   // rows, at least N apart, that hold a unit
   auto fetch = [&](long long r, int k) {
     if (r < p.rows) {
-      const bool inside = r > 0 && r < p.rows - 1;   // units that reach into other rows stay in the tensor
+      const bool inside = r >= edge && r < p.rows - edge;   // units that reach into other rows stay in the tensor
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int col = col_of(i);
