@@ -28,11 +28,25 @@ bool chunked(const DeltaShape &s, int dtype, bool keep) {
   return dtype != ESA_F32 && s.T >= (keep ? kChunkMinKeptT : kChunkMinT);
 }
 
+// Long float32 sequences of few heads: the states between chunks first, then
+// the sweeps of all chunks at once.  Forward (us, states first / one sweep): 8
+// heads at T = 128 27 / 24 (D = 32), 34 / 27 (64), 48 / 39 (128); at T = 333
+// 34 / 59, 45 / 69, 73 / 98; at T = 4096 144 / 707, 248 / 833, 565 / 1183, and
+// with the backward 389 / 1422, 684 / 1948, 1744 / 3327.  64 heads at T = 1024
+// 80 / 178, 197 / 214, 758 / 416; 32 heads of D = 128 410 / 321: one sweep
+// keeps the device busy there.
+constexpr int kCutMinT = 192, kCutMostHeads = 64, kCutMostState = 1 << 18;   // floats of all heads' states
+bool cut_sweeps(const DeltaShape &s, int dtype) {
+  const long long heads = static_cast<long long>(s.B) * s.H;
+  return dtype == ESA_F32 && s.T >= kCutMinT && heads <= kCutMostHeads && heads * s.D * s.D <= kCutMostState;
+}
+
 // Token by token: what the forward keeps for the backward (u, the state at
 // each chunk), then the backward's scratch.
 struct DeltaLayout {
   int nc = 0;
-  size_t u = 0, S_ck = 0, dS_ck = 0, du = 0, dk = 0, dq = 0, gain = 0, end = 0, total = 0;
+  bool cut = false;
+  size_t u = 0, S_ck = 0, dS_ck = 0, du = 0, dk = 0, dq = 0, gain = 0, end = 0, wt = 0, u0 = 0, fac = 0, total = 0;
 };
 // The chunk arrays, laid out from `base`; `*total` gets their size.
 ChunkArrays chunk_arrays(unsigned char *base, const DeltaShape &s, bool keep, size_t *total) {
@@ -59,15 +73,23 @@ ChunkArrays chunk_arrays(unsigned char *base, const DeltaShape &s, bool keep, si
   return w;
 }
 
-DeltaLayout delta_layout(const DeltaShape &s, bool keep) {
+DeltaLayout delta_layout(const DeltaShape &s, int dtype, bool keep) {
   DeltaLayout lo;
   lo.nc = (s.T + 63) / 64;
+  lo.cut = cut_sweeps(s, dtype);
   const size_t n = static_cast<size_t>(s.B) * s.T * s.H, chunks = static_cast<size_t>(s.B) * s.H * lo.nc;
   size_t o = 0;
-  if (keep) {
-    const size_t rows = up256(n * s.D * sizeof(float)), states = up256(chunks * s.D * s.D * sizeof(float));
-    lo.u = o; o += rows;
+  const size_t rows = up256(n * s.D * sizeof(float)), states = up256(chunks * s.D * s.D * sizeof(float));
+  if (keep || lo.cut) {
     lo.S_ck = o; o += states;
+  }
+  if (lo.cut) {
+    lo.wt = o; o += up256(chunks * 64 * s.D * sizeof(float));
+    lo.u0 = o; o += up256(chunks * 64 * s.D * sizeof(float));
+    lo.fac = o; o += up256(chunks * 3 * 64 * sizeof(float));
+  }
+  if (keep) {
+    lo.u = o; o += rows;
     lo.dS_ck = o; o += states;
     lo.du = o; o += rows;
     lo.dk = o; o += rows;
@@ -77,6 +99,13 @@ DeltaLayout delta_layout(const DeltaShape &s, bool keep) {
   }
   lo.total = o;
   return lo;
+}
+
+void between(SweepArgs *p, const DeltaLayout &lo, unsigned char *base) {
+  p->cut = true;
+  p->wt = reinterpret_cast<float *>(base + lo.wt);
+  p->u0 = reinterpret_cast<float *>(base + lo.u0);
+  p->fac = reinterpret_cast<float *>(base + lo.fac);
 }
 
 int elem(int dtype) { return dtype == ESA_F32 ? 4 : 2; }
@@ -136,7 +165,7 @@ size_t esa_delta_workspace_size(int B, int T, int H, int D, int dtype, int keep)
     chunk_arrays(nullptr, s, keep != 0, &total);
     return total + 256;
   }
-  return delta_layout(s, keep != 0).total + 256;
+  return delta_layout(s, dtype, keep != 0).total + 256;
 }
 
 int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, long long ld_v, const void *a,
@@ -168,7 +197,8 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
     if ((rc = launch_chunk_prep(dtype, c, st))) return rc;
     return launch_chunk_fwd(dtype, c, st);
   }
-  const DeltaLayout lo = delta_layout(s, keep != 0);
+  const DeltaLayout lo = delta_layout(s, dtype, keep != 0);
+  unsigned char *base = static_cast<unsigned char *>(workspace);
   SweepArgs p{};
   p.s = s;
   p.q = q; p.k = k; p.v = v; p.a = a; p.b = b;
@@ -176,10 +206,11 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
   p.S_out = S_final;
   p.y = y;
   p.nc = lo.nc;
-  if (keep) {
-    unsigned char *base = static_cast<unsigned char *>(workspace);
-    p.u = reinterpret_cast<float *>(base + lo.u);
-    p.S_ck = reinterpret_cast<float *>(base + lo.S_ck);
+  if (keep) p.u = reinterpret_cast<float *>(base + lo.u);
+  if (keep || lo.cut) p.S_ck = reinterpret_cast<float *>(base + lo.S_ck);
+  if (lo.cut) {
+    between(&p, lo, base);
+    if ((rc = launch_delta_states(false, p, st))) return rc;
   }
   return launch_sweep(kSweepFwd, dtype, p, st);
 }
@@ -218,7 +249,7 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
     if ((rc = launch_chunk_bwd(dtype, c, st))) return rc;
     return launch_chunk_grad(dtype, c, st);
   }
-  const DeltaLayout lo = delta_layout(s, true);
+  const DeltaLayout lo = delta_layout(s, dtype, true);
   SweepArgs p{};
   p.s = s;
   p.q = q; p.k = k; p.v = v; p.dy = dy; p.a = a; p.b = b;
@@ -232,6 +263,10 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
   p.nc = lo.nc;
   p.S_in = dS_final;
   p.S_out = dS_init;
+  if (lo.cut) {
+    between(&p, lo, base);
+    if ((rc = launch_delta_states(true, p, st))) return rc;
+  }
   if ((rc = launch_sweep(kSweepDu, dtype, p, st))) return rc;
   if ((rc = launch_sweep(kSweepDk, dtype, p, st))) return rc;
   if ((rc = launch_sweep(kSweepDq, dtype, p, st))) return rc;

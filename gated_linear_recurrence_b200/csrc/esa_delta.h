@@ -27,12 +27,16 @@ struct SweepArgs {
   float *S_ck, *dS_ck;                  // [B,H,nc,D,D] state entering, gradient leaving each chunk of 64 tokens
   float *end;                           // [B,H,nc,D*D/1024] parts of their inner product at the chunk's end
   int nc;
+  bool cut;                             // forward and Du sweeps start every chunk from S_ck, dS_ck, which are given
+  float *wt, *u0, *fac;                 // [B,H,nc,64,D] W, U0 (then Z0) and [B,H,nc,3,64] factors of esa_delta_wy.cu
 };
 
 // Kinds of sweep.
 enum { kSweepFwd = 0, kSweepDu = 1, kSweepDk = 2, kSweepDq = 3 };
 
 int launch_sweep(int kind, int dtype, const SweepArgs &a, cudaStream_t st);
+// The states between chunks, float32: S_ck from S_in, also wt, fac; backward dS_ck from S_in = dS_final. And S_out.
+int launch_delta_states(bool bwd, const SweepArgs &a, cudaStream_t st);
 int launch_delta_step(int dtype, const SweepArgs &a, cudaStream_t st);   // one token, S_in = S_out
 
 struct FinishArgs {

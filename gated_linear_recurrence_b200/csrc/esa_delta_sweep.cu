@@ -20,7 +20,7 @@ int sweep_warps(long long units, int most) {
 template <typename T, int D, int KIND>
 int run(const SweepArgs &a, cudaStream_t st) {
   const long long heads = static_cast<long long>(a.s.B) * a.s.H;
-  const long long units = KIND == kSweepFwd || KIND == kSweepDu ? heads : heads * a.nc;
+  const long long units = (KIND == kSweepFwd || KIND == kSweepDu) && !a.cut ? heads : heads * a.nc;
   const int W = sweep_warps(units, D / sweep::columns<D>());
   const sweep::Layout<T, D, KIND> lo(W);
   auto kern = sweep::delta_sweep_kernel<T, D, KIND>;

@@ -15,8 +15,8 @@
 //                                  dS <- alpha_t (dS - beta_t k_t du_t^T); dS_init; the gradient leaving each chunk
 //   kSweepDk   backward, M = dS^T: dk_t = dS_t u_t
 //   kSweepDq   forward,  M = S^T:  dk_t -= alpha_t beta_t S_{t-1} du_t, dq_t = scale S_t dy_t, <dS, S> at each chunk's end
-// The first two pass over the whole sequence; the last two start every chunk
-// from what those left and take all chunks at once.
+// The first two pass over the whole sequence, or start every chunk from the
+// states of esa_delta_wy.cu and take all chunks at once; the last two always do.
 //
 // All arithmetic is float32, as the state is; this is the path of float32
 // tensors and of short sequences.
@@ -135,13 +135,14 @@ __global__ void __launch_bounds__(D * lanes<D>()) delta_sweep_kernel(SweepArgs p
   const int slices = D / lo.cols;
   const int slice = blockIdx.x % slices;
   int head = blockIdx.x / slices, chunk = 0;           // head = b H + h
-  if (!kCols) {
+  const bool cut = !kCols || p.cut;                    // a chunk a block, else the sequence
+  if (cut) {
     chunk = head % p.nc;
     head /= p.nc;
   }
   const int b = head / p.s.H, h = head - b * p.s.H;
   const int c_blk = slice * lo.cols, j = c_blk + jj;   // first independent entry of the block, this thread's
-  const int t_begin = kCols ? 0 : chunk * CHUNK, t_end = kCols ? p.s.T : min(p.s.T, t_begin + CHUNK);
+  const int t_begin = cut ? chunk * CHUNK : 0, t_end = cut ? min(p.s.T, t_begin + CHUNK) : p.s.T;
   const long long tok0 = static_cast<long long>(b) * p.s.T;
   const long long ldc = static_cast<long long>(p.s.H) * D;   // contiguous rows (dy, y, scratch)
   const long long state0 = static_cast<long long>(head) * D * D;
@@ -150,6 +151,8 @@ __global__ void __launch_bounds__(D * lanes<D>()) delta_sweep_kernel(SweepArgs p
   float2 m[16];
   if constexpr (kCols) {
     const float *Sin = p.S_in ? p.S_in + state0 + 4 * sl * D + j : nullptr;
+    if (cut)
+      Sin = (KIND == kSweepDu ? p.dS_ck : p.S_ck) + (static_cast<long long>(head) * p.nc + chunk) * D * D + 4 * sl * D + j;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int r = 4 * SP * (i >> 1) + 2 * (i & 1);
@@ -222,9 +225,9 @@ __global__ void __launch_bounds__(D * lanes<D>()) delta_sweep_kernel(SweepArgs p
     const int c = kReverse ? nch - 1 - it : it, buf = it & 1;
     const int t0 = t_begin + c * TC, n = min(TC, t_end - t0);
     if constexpr (KIND == kSweepFwd)
-      if (p.S_ck != nullptr && t0 % CHUNK == 0) keep(p.S_ck + (static_cast<long long>(head) * p.nc + t0 / CHUNK) * D * D);
+      if (p.S_ck != nullptr && !cut && t0 % CHUNK == 0) keep(p.S_ck + (static_cast<long long>(head) * p.nc + t0 / CHUNK) * D * D);
     if constexpr (KIND == kSweepDu)
-      if (t0 + n == t_end || (t0 + n) % CHUNK == 0) keep(p.dS_ck + (static_cast<long long>(head) * p.nc + (t0 + n - 1) / CHUNK) * D * D);
+      if (!cut && (t0 + n == t_end || (t0 + n) % CHUNK == 0)) keep(p.dS_ck + (static_cast<long long>(head) * p.nc + (t0 + n - 1) / CHUNK) * D * D);
     if (threadIdx.x < TC) {
       tok[threadIdx.x] = gate(ga_next);
       tok[TC + threadIdx.x] = gate(gb_next);
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(D * lanes<D>()) delta_sweep_kernel(SweepArgs p
     if (lane == 0) p.end[(static_cast<long long>(head) * p.nc + chunk) * (D / columns<D>()) + slice * W + warp] = x;
   }
   if constexpr (kCols) {
-    if (p.S_out != nullptr) keep(p.S_out + state0);
+    if (p.S_out != nullptr && !cut) keep(p.S_out + state0);
   }
 }
 

@@ -103,6 +103,71 @@ def test_short_sequences(cuda_device, dt, D, T):
 
 
 @pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("B,T,H,state", [(1, 191, 2, True), (1, 192, 2, True), (2, 333, 3, False), (1, 1100, 1, True)])
+def test_long_float32_sequences(cuda_device, D, B, T, H, state):
+    """Around the length from which the states between chunks come first; strided inputs, without what the backward
+    needs, and a final state over the initial one as well."""
+    x, S0, dS = draw("f32", B, T, H, D, seed=T, state=state)
+    ref = delta_reference(*ins(x), D ** -0.5, S0, x["dy"], dS)
+    check(x, run(x, S0, dS, None), ref, T, D)
+    P = torch.zeros(B, T, 3 * H * D + 4, device="cuda")
+    for i, n in enumerate("qkv"):
+        P[..., i * H * D:(i + 1) * H * D] = x[n].flatten(2)
+    q, k, v = (P[..., i * H * D:(i + 1) * H * D].unflatten(-1, (H, D)) for i in range(3))
+    over = None if S0 is None else S0.clone()
+    y, S, _ = esa_delta_fwd(q, k, v, x["a"], x["b"], S_init=over, S_final=over, keep=False)
+    check(x, {"y": y, "S": S}, ref, T, D, gradients=False)
+
+
+@pytest.mark.parametrize("which", ["forget", "reset_inside"])
+def test_long_float32_gates(cuda_device, which):
+    x, S0, dS = draw("f32", 1, 260, 2, 64, seed=21)
+    if which == "forget":
+        x["a"].fill_(-100.0)
+    else:
+        x["a"].fill_(8.0)
+        x["a"][:, 77] = -90.0
+        x["a"][:, 200:202] = float("-inf")
+    ref = delta_reference(*ins(x), 0.125, S0, x["dy"], dS)
+    check(x, run(x, S0, dS, None), ref, 260, 64)
+
+
+@pytest.mark.parametrize("D,H", [(32, 64), (32, 65), (64, 64), (64, 65), (128, 16), (128, 17)])
+def test_long_float32_every_spread_of_heads(cuda_device, D, H):
+    x, S0, dS = draw("f32", 1, 200, H, D, seed=H)
+    out = run(x, S0, dS, None)
+    for h in (0, H - 1):
+        one = {n: t[:, :, h:h + 1] for n, t in x.items()}
+        ref = delta_reference(*ins(one), D ** -0.5, S0[:, h:h + 1], one["dy"], dS[:, h:h + 1])
+        check(one, {n: t[:, h:h + 1] if n in ("S", "dS0") else t[:, :, h:h + 1] for n, t in out.items()}, ref, 200, D)
+
+
+@pytest.mark.parametrize("what", ["v", "k", "q", "S"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_long_float32_values_that_are_not_finite(cuda_device, what, value):
+    """From their token on, in their value channel (v, S), their head (k) or their token (q) only."""
+    D, T = 32, 300
+    x, S0, _ = draw("f32", 2, T, 2, D, seed=23)
+    clean, _, _ = esa_delta_fwd(*ins(x), S_init=S0)
+    if what == "S":
+        S0[1, 1, 3, 5] = value
+    else:
+        x[what][1, 100, 1, 5] = value
+    y, S, _ = esa_delta_fwd(*ins(x), S_init=S0)
+    same = torch.ones_like(y, dtype=torch.bool)
+    if what == "q":
+        same[1, 100, 1] = False
+    elif what == "k":
+        same[1, 100:, 1] = False
+    else:
+        same[1, 100 if what == "v" else 0:, 1, 5] = False
+    assert torch.equal(y[same], clean[same])
+    assert not torch.isfinite(y[~same]).all()
+    if what == "k":
+        assert not torch.isfinite(S[1, 1]).any()
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
 def test_steps_equal_the_sequence(cuda_device, D):
     T = 21
     x, S0, _ = draw("f32", 3, T, 2, D, seed=2)
