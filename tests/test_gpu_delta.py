@@ -348,9 +348,9 @@ def test_same_results_every_time_and_two_streams(cuda_device, dt, D):
             assert torch.equal(a[n], first[n]) and torch.equal(b[n], second[n]), n
 
 
-@pytest.mark.parametrize("D", [64, 128])
-def test_graph_of_forward_and_backward(cuda_device, D):
-    x, S0, dS = draw("bf16", 1, 129, 2, D, seed=16)
+@pytest.mark.parametrize("dt,T,D", [("bf16", 129, 64), ("bf16", 129, 128), ("f32", 70, 64), ("f32", 260, 32), ("f32", 260, 128)])
+def test_graph_of_forward_and_backward(cuda_device, dt, T, D):
+    x, S0, dS = draw(dt, 1, T, 2, D, seed=16)
     want = run(x, S0, dS, 0.2)
     st = torch.cuda.Stream()
     g = torch.cuda.CUDAGraph()
@@ -367,10 +367,12 @@ def test_graph_of_forward_and_backward(cuda_device, D):
         assert torch.equal(out[n], want[n]), n
 
 
-def test_nothing_written_outside(cuda_device):
+@pytest.mark.parametrize("dt,T,H,D", [("f16", 67, 2, 128), ("f32", 67, 2, 64), ("f32", 200, 2, 128), ("f32", 257, 3, 32),
+                                      ("bf16", 67, 40, 64), ("bf16", 9, 3, 32), ("f16", 5, 2, 64)])
+def test_nothing_written_outside(cuda_device, dt, T, H, D):
     """Canary rows around every output stay as they were."""
-    B, T, H, D = 1, 67, 2, 128
-    x, S0, dS = draw("f16", B, T, H, D, seed=17)
+    B = 1
+    x, S0, dS = draw(dt, B, T, H, D, seed=17)
 
     def guarded(shape, dtype):
         n = 1
@@ -379,11 +381,11 @@ def test_nothing_written_outside(cuda_device):
         flat = torch.full((n + 512,), 3.0, dtype=dtype, device="cuda")
         return flat, flat[256:256 + n].view(shape)
 
-    h, f = torch.float16, torch.float32
+    h, f = DT[dt], torch.float32
     bufs = {n: guarded(s, t) for n, s, t in (("y", (B, T, H, D), h), ("S", (B, H, D, D), f), ("dq", (B, T, H, D), h),
                                              ("dk", (B, T, H, D), h), ("dv", (B, T, H, D), h), ("da", (B, T, H), h),
                                              ("db", (B, T, H), h), ("dS0", (B, H, D, D), f))}
-    need = esa_delta_workspace_size(B, T, H, D, torch.float16)
+    need = esa_delta_workspace_size(B, T, H, D, DT[dt])
     wflat = torch.full((need + 512,), 171, dtype=torch.uint8, device="cuda")
     ws = wflat[256:256 + need]
     out = {n: t[1] for n, t in bufs.items()}
