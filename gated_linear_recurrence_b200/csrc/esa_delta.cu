@@ -46,7 +46,7 @@ bool cut_sweeps(const DeltaShape &s, int dtype) {
 struct DeltaLayout {
   int nc = 0;
   bool cut = false;
-  size_t u = 0, S_ck = 0, dS_ck = 0, du = 0, dk = 0, dq = 0, gain = 0, end = 0, wt = 0, u0 = 0, fac = 0, total = 0;
+  size_t u = 0, S_ck = 0, dS_ck = 0, du = 0, dk = 0, dq = 0, gain = 0, end = 0, dk2 = 0, wt = 0, u0 = 0, fac = 0, total = 0;
 };
 // The chunk arrays, laid out from `base`; `*total` gets their size.
 ChunkArrays chunk_arrays(unsigned char *base, const DeltaShape &s, bool keep, size_t *total) {
@@ -93,6 +93,7 @@ DeltaLayout delta_layout(const DeltaShape &s, int dtype, bool keep) {
     lo.dS_ck = o; o += states;
     lo.du = o; o += rows;
     lo.dk = o; o += rows;
+    lo.dk2 = o; o += rows;
     lo.dq = o; o += rows;
     lo.gain = o; o += up256(n * sizeof(float));
     lo.end = o; o += up256(chunks * (s.D * s.D / 1024) * sizeof(float));
@@ -256,6 +257,7 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
   p.u = reinterpret_cast<float *>(base + lo.u);
   p.du = reinterpret_cast<float *>(base + lo.du);
   p.dk = reinterpret_cast<float *>(base + lo.dk);
+  p.dk2 = reinterpret_cast<float *>(base + lo.dk2);
   p.dq = reinterpret_cast<float *>(base + lo.dq);
   p.end = reinterpret_cast<float *>(base + lo.end);
   p.S_ck = reinterpret_cast<float *>(base + lo.S_ck);
@@ -269,12 +271,11 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
   }
   if ((rc = launch_sweep(kSweepDu, dtype, p, st))) return rc;
   if ((rc = launch_sweep(kSweepDk, dtype, p, st))) return rc;
-  if ((rc = launch_sweep(kSweepDq, dtype, p, st))) return rc;
   FinishArgs f{};
   f.s = s;
   f.nc = lo.nc;
   f.q = q; f.v = v; f.a = a; f.b = b;
-  f.u = p.u; f.du = p.du; f.dkf = p.dk; f.dqf = p.dq; f.end = p.end;
+  f.u = p.u; f.du = p.du; f.dkf = p.dk; f.dk2 = p.dk2; f.dqf = p.dq; f.end = p.end;
   f.gain = reinterpret_cast<float *>(base + lo.gain);
   f.dq = dq; f.dk = dk; f.dv = dv; f.da = da; f.db = db;
   return launch_delta_finish(dtype, f, st);

@@ -23,7 +23,7 @@ struct SweepArgs {
   const float *S_in;                    // state (or its gradient) before the first token visited; NULL = zeros
   float *S_out;                         // after the last one; NULL = not written
   void *y;                              // forward sweep's output, I/O type
-  float *u, *du, *dk, *dq;              // float32 scratch, [B,T,H,D]
+  float *u, *du, *dk, *dk2, *dq;        // float32 scratch, [B,T,H,D]; dk2: what the last sweep adds to dk
   float *S_ck, *dS_ck;                  // [B,H,nc,D,D] state entering, gradient leaving each chunk of 64 tokens
   float *end;                           // [B,H,nc,D*D/1024] parts of their inner product at the chunk's end
   int nc;
@@ -34,7 +34,7 @@ struct SweepArgs {
 // Kinds of sweep.
 enum { kSweepFwd = 0, kSweepDu = 1, kSweepDk = 2, kSweepDq = 3 };
 
-int launch_sweep(int kind, int dtype, const SweepArgs &a, cudaStream_t st);
+int launch_sweep(int kind, int dtype, const SweepArgs &a, cudaStream_t st);   // kSweepDk: that and kSweepDq
 // The states between chunks, float32: S_ck from S_in, also wt, fac; backward dS_ck from S_in = dS_final. And S_out.
 int launch_delta_states(bool bwd, const SweepArgs &a, cudaStream_t st);
 int launch_delta_step(int dtype, const SweepArgs &a, cudaStream_t st);   // one token, S_in = S_out
@@ -42,7 +42,7 @@ int launch_delta_step(int dtype, const SweepArgs &a, cudaStream_t st);   // one 
 struct FinishArgs {
   DeltaShape s;
   const void *q, *v, *a, *b;
-  const float *u, *du, *dkf, *dqf, *end;
+  const float *u, *du, *dkf, *dk2, *dqf, *end;
   int nc;
   float *gain;   // [B,H,T]
   void *dq, *dk, *dv, *da, *db;

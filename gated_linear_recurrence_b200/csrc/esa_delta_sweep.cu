@@ -20,7 +20,7 @@ int sweep_warps(long long units, int most) {
 template <typename T, int D, int KIND>
 int run(const SweepArgs &a, cudaStream_t st) {
   const long long heads = static_cast<long long>(a.s.B) * a.s.H;
-  const long long units = (KIND == kSweepFwd || KIND == kSweepDu) && !a.cut ? heads : heads * a.nc;
+  const long long units = a.cut ? heads * a.nc : heads;
   const int W = sweep_warps(units, D / sweep::columns<D>());
   const sweep::Layout<T, D, KIND> lo(W);
   auto kern = sweep::delta_sweep_kernel<T, D, KIND>;
@@ -34,12 +34,27 @@ int run(const SweepArgs &a, cudaStream_t st) {
 }
 
 template <typename T, int D>
+int run_keys(const SweepArgs &a, cudaStream_t st) {
+  const long long units = static_cast<long long>(a.s.B) * a.s.H * a.nc;
+  const int W = sweep_warps(units, D / sweep::columns<D>());
+  const sweep::Layout<T, D, kSweepDk> lo(W);
+  const size_t other = sweep::Layout<T, D, kSweepDq>(W).total, bytes = lo.total > other ? lo.total : other;
+  auto kern = sweep::delta_keys_kernel<T, D>;
+  if (bytes > 48 * 1024) {
+    const int rc =
+        runtime_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)));
+    if (rc) return rc;
+  }
+  kern<<<dim3(static_cast<unsigned>(units * (D / lo.cols)), 2), W * 32, bytes, st>>>(a);
+  return runtime_status(cudaGetLastError());
+}
+
+template <typename T, int D>
 int by_kind(int kind, const SweepArgs &a, cudaStream_t st) {
   switch (kind) {
     case kSweepFwd: return run<T, D, kSweepFwd>(a, st);
     case kSweepDu: return run<T, D, kSweepDu>(a, st);
-    case kSweepDk: return run<T, D, kSweepDk>(a, st);
-    default: return run<T, D, kSweepDq>(a, st);
+    default: return run_keys<T, D>(a, st);
   }
 }
 

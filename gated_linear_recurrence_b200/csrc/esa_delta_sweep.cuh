@@ -14,7 +14,7 @@
 //   kSweepDu   backward, M = dS:   du_t = dS_t^T k_t with dS_t += scale q_t dy_t^T first, then
 //                                  dS <- alpha_t (dS - beta_t k_t du_t^T); dS_init; the gradient leaving each chunk
 //   kSweepDk   backward, M = dS^T: dk_t = dS_t u_t
-//   kSweepDq   forward,  M = S^T:  dk_t -= alpha_t beta_t S_{t-1} du_t, dq_t = scale S_t dy_t, <dS, S> at each chunk's end
+//   kSweepDq   forward,  M = S^T:  dk_t's other part -alpha_t beta_t S_{t-1} du_t, dq_t = scale S_t dy_t, <dS, S> at each chunk's end
 // The first two pass over the whole sequence, or start every chunk from the
 // states of esa_delta_wy.cu and take all chunks at once; the last two always do.
 //
@@ -123,7 +123,7 @@ struct Layout {
 };
 
 template <typename T, int D, int KIND>
-__global__ void __launch_bounds__(D * lanes<D>()) delta_sweep_kernel(SweepArgs p) {
+__device__ __forceinline__ void sweep_body(const SweepArgs &p) {
   constexpr bool kReverse = KIND == kSweepDu || KIND == kSweepDk;
   constexpr bool kCols = KIND == kSweepFwd || KIND == kSweepDu;   // whole sequences, value channels independent
   constexpr int TC = tokens<D>(), SP = lanes<D>();
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(D * lanes<D>()) delta_sweep_kernel(SweepArgs p
           if (p.u != nullptr && sl == 0) p.u[out] = w;
         } else {
           w = in;
-          if (sl == 0) p.dk[out] = fmaf(-alpha * beta, dp, p.dk[out]);
+          if (sl == 0) p.dk2[out] = -alpha * beta * dp;
         }
         const float2 ws = splat(w);
 #pragma unroll
@@ -383,6 +383,21 @@ __global__ void __launch_bounds__(D * lanes<D>()) delta_sweep_kernel(SweepArgs p
   }
 }
 
+template <typename T, int D, int KIND>
+__global__ void __launch_bounds__(D * lanes<D>()) delta_sweep_kernel(SweepArgs p) {
+  sweep_body<T, D, KIND>(p);
+}
+
+// The two sweeps over key channels, which do not need one another, in one
+// launch: with few chunks both fit on the device (48 chunks of D = 32: 15 us,
+// one behind the other 14 + 16), with many they share it evenly (4096 chunks:
+// 195 and 99 + 180).
+template <typename T, int D>
+__global__ void __launch_bounds__(D * lanes<D>()) delta_keys_kernel(SweepArgs p) {
+  if (blockIdx.y == 0) sweep_body<T, D, kSweepDk>(p);
+  else sweep_body<T, D, kSweepDq>(p);
+}
+
 // One warp per token and head: round dq, dk, dv; db = (u.du)(1 - beta);
 // gain = q.dq - beta v.du, the summand of dlog alpha.
 template <typename T, int D>
@@ -402,7 +417,7 @@ __global__ void __launch_bounds__(256) delta_finish_kernel(FinishArgs p) {
     const int c = 32 * i + lane;
     const float du = p.du[o + c], dq = p.dqf[o + c];
     static_cast<T *>(p.dq)[o + c] = narrow<T>(dq);
-    static_cast<T *>(p.dk)[o + c] = narrow<T>(p.dkf[o + c]);
+    static_cast<T *>(p.dk)[o + c] = narrow<T>(p.dkf[o + c] + p.dk2[o + c]);
     static_cast<T *>(p.dv)[o + c] = narrow<T>(beta * du);
     g = fmaf(widen(q[c]), dq, fmaf(-beta * du, widen(v[c]), g));
     ub = fmaf(p.u[o + c], du, ub);
