@@ -338,18 +338,22 @@ NormRow ragged_row(int N) {
   return norm_row((N + 2 * (VEC - 1)) / VEC, kRaggedElems / VEC);
 }
 
+// `tile`: bytes of a stage; `resident`: blocks an SM holds, kept for the next
+// call (the same on every device the library runs on).
 template <typename K, typename A>
-int ragged_launch(K kern, const A &a, int block, int groups, int step, int tile, int least, int most, int *grid,
-                  cudaStream_t st) {
-  int rc, per = 0;
-  const int stages = 2 * tile <= kRaggedMost ? 2 : 1;
-  const int smem = stages * tile > least ? stages * tile : least;
+int ragged_launch(K kern, const A &a, int block, int groups, int step, int tile, int most, int *grid,
+                  std::atomic<int> *resident, cudaStream_t st) {
+  int rc, per = resident->load(std::memory_order_relaxed);
+  const int stages = 2 * tile <= kRaggedMost ? 2 : 1, smem = stages * tile;
   if (smem > 40 * 1024 &&   // 48 KB with the static part
       (rc = runtime_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRaggedMost))))
     return rc;
-  if ((rc = runtime_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, block, smem)))) return rc;
+  if (per == 0) {
+    if ((rc = runtime_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, block, smem)))) return rc;
+    resident->store(per = per > 0 ? per : 1, std::memory_order_relaxed);
+  }
   const long long need = (a.rows + groups - 1) / groups;
-  long long full = static_cast<long long>(sm_count()) * (per > 0 ? per : 1);
+  long long full = static_cast<long long>(sm_count()) * per;
   if (full > most) full = most;
   full -= full % step;   // a thread's rows are a multiple of VEC apart
   *grid = static_cast<int>(need < full ? need : full);
@@ -365,9 +369,10 @@ struct RaggedFwd {
   template <int NV, int TPR>
   int run() const {
     constexpr int BLOCK = norm_block<TPR>(), GROUPS = BLOCK / TPR;
+    static std::atomic<int> resident[2]{};
     int grid;
     return ragged_launch(norm_fwd_ragged_kernel<T, WT, VEC, NV, TPR>, a, BLOCK, GROUPS, GROUPS >= VEC ? 1 : VEC,
-                         (a.res ? 2 : 1) * NV * BLOCK * 16, 0, INT_MAX, &grid, st);
+                         (a.res ? 2 : 1) * NV * BLOCK * 16, INT_MAX, &grid, &resident[a.res != nullptr], st);
   }
 };
 template <typename T, typename WT>
@@ -379,8 +384,10 @@ struct RaggedBwd {
   template <int NV, int TPR>
   int run() const {
     constexpr int BLOCK = norm_block<TPR>(), GROUPS = BLOCK / TPR;
+    static std::atomic<int> resident[2]{};
+    // the sums of a block's groups, GROUPS N floats, fit in a stage: N <= TPR NV VEC, and it has two tensors at least
     return ragged_launch(norm_bwd_ragged_kernel<T, WT, VEC, NV, TPR>, a, BLOCK, GROUPS, GROUPS >= VEC ? 1 : VEC,
-                         (a.dh ? 3 : 2) * NV * BLOCK * 16, GROUPS > 1 ? GROUPS * a.N * 4 : 0, most, grid, st);
+                         (a.dh ? 3 : 2) * NV * BLOCK * 16, most, grid, &resident[a.dh != nullptr], st);
   }
 };
 
