@@ -31,8 +31,8 @@ bool chunked(const DeltaShape &s, int dtype, bool keep) {
 // Long float32 sequences of few heads: the states between chunks first, then
 // the sweeps of all chunks at once.  Forward (us, states first / one sweep): 8
 // heads at T = 128 27 / 24 (D = 32), 34 / 27 (64), 48 / 39 (128); at T = 333
-// 34 / 59, 45 / 69, 73 / 98; at T = 4096 144 / 707, 248 / 833, 565 / 1183, and
-// with the backward 389 / 1422, 684 / 1948, 1744 / 3327.  64 heads at T = 1024
+// 35 / 59, 43 / 69, 69 / 98; at T = 4096 143 / 707, 226 / 833, 508 / 1183, and
+// with the backward 361 / 1422, 605 / 1948, 1565 / 3327.  64 heads at T = 1024
 // 80 / 178, 197 / 214, 758 / 416; 32 heads of D = 128 410 / 321: one sweep
 // keeps the device busy there.
 constexpr int kCutMinT = 192, kCutMostHeads = 64, kCutMostState = 1 << 18;   // floats of all heads' states

@@ -16,9 +16,9 @@
 // are not finite included.
 //
 // The chain of states is bound by its latency, two products, their sums over
-// lanes and three barriers a chunk: forward 1.8 us a chunk at D = 32, 2.9 at
-// 64, 5.0 at 128 (backward 2.7, 4.0, 6.2), against 64 tokens of a sweep, 11,
-// 13 and 18.5 us.
+// lanes and three barriers a chunk, and by shared memory: forward 1.8 us a
+// chunk at D = 32, 2.5 at 64, 4.0 at 128 (backward 2.3, 3.4, 5.2), against 64
+// tokens of a sweep, 11, 13 and 18.5 us.
 #include "esa_delta_sweep.cuh"
 
 #include "esa.h"
@@ -265,11 +265,16 @@ __global__ void __launch_bounds__(kThreads) delta_wz_kernel(SweepArgs p) {
 template <int D, bool BWD>
 struct StateSmem {   // in floats
   static constexpr int pitch = BWD && D == 128 ? D : D + 4, mat = C * pitch, sp = kCols + 4;
+  static constexpr int yp = D == 32 ? 20 : D == 64 ? 24 : 16;   // rows of Y and dO: no bank conflicts between `SPL` rows
   static constexpr int first = 0, second = mat, third = 2 * mat;        // factor of the state; K (W); Q
   static constexpr int add = (BWD ? 3 : 2) * mat, dout = add + C * kCols;  // U0 (Z0) slice, dO slice
-  static constexpr int fac = dout + (BWD ? C * kCols : 0), stage = fac + 3 * C;
-  static constexpr int S = 2 * stage, Y = S + D * sp, total = Y + C * sp;
+  static constexpr int fac = dout + (BWD ? C * yp : 0), stage = fac + 3 * C;
+  static constexpr int S = 2 * stage, Y = S + D * sp, total = Y + C * yp;
 };
+
+// Float4 `cg` of row d of the state: rows 4, 8 and 12 apart, which the four
+// quarters of a product read together, lie in different banks.
+__device__ __forceinline__ int state_at(int d, int cg) { return d * (kCols + 4) + 4 * (cg ^ ((d >> 3 & 1) << 1)); }
 
 // The state (its gradient) from chunk to chunk: a block carries 16 value channels of a head.
 template <int D, bool BWD>
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) delta_state_kernel(SweepArgs p) {
       rows_in(s + L::add, kCols, p.u0 + a.chunk * (C * D) + c0, D, C, kCols);
       if constexpr (BWD) {
         rows_in(s + L::third, L::pitch, q + a.row * p.s.ld_qk + a.h * D, p.s.ld_qk, a.len, D);
-        rows_in(s + L::dout, kCols, dy + a.row * ldc + a.h * D + c0, ldc, a.len, kCols);
+        rows_in(s + L::dout, L::yp, dy + a.row * ldc + a.h * D + c0, ldc, a.len, kCols);
       }
       if (tid < 3 * C / 4) copy_or_zero(s + L::fac + 4 * tid, p.fac + a.chunk * 3 * C + 4 * tid, true);
     }
@@ -302,12 +307,12 @@ __global__ void __launch_bounds__(kThreads) delta_state_kernel(SweepArgs p) {
     const int d = i / (kCols / 4), c = i % (kCols / 4) * 4;
     float4 x = make_float4(0, 0, 0, 0);
     if (p.S_in) x = *reinterpret_cast<const float4 *>(p.S_in + state0 + d * D + c0 + c);
-    *reinterpret_cast<float4 *>(S + d * L::sp + c) = x;
+    *reinterpret_cast<float4 *>(S + state_at(d, c / 4)) = x;
   }
   auto keep = [&](float *base) {   // the state of this moment
     for (int i = tid; i < D * (kCols / 4); i += kThreads) {
       const int d = i / (kCols / 4), c = i % (kCols / 4) * 4;
-      *reinterpret_cast<float4 *>(base + d * D + c0 + c) = *reinterpret_cast<const float4 *>(S + d * L::sp + c);
+      *reinterpret_cast<float4 *>(base + d * D + c0 + c) = *reinterpret_cast<const float4 *>(S + state_at(d, c / 4));
     }
   };
   for (int it = 0; it < p.nc; ++it) {
@@ -329,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) delta_state_kernel(SweepArgs p) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           x[r] = *reinterpret_cast<const float4 *>(s + L::first + (rg + 16 * r) * L::pitch + d);
-          y[r] = *reinterpret_cast<const float4 *>(S + (d + r) * L::sp + 4 * cg);
+          y[r] = *reinterpret_cast<const float4 *>(S + state_at(d + r, cg));
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) delta_state_kernel(SweepArgs p) {
         o = make_float4(-fmaf(f, mine[0], u.x), -fmaf(f, mine[1], u.y), -fmaf(f, mine[2], u.z), -fmaf(f, mine[3], u.w));
       else
         o = make_float4(f * (u.x - mine[0]), f * (u.y - mine[1]), f * (u.z - mine[2]), f * (u.w - mine[3]));
-      *reinterpret_cast<float4 *>(Y + row * L::sp + 4 * cg) = o;
+      *reinterpret_cast<float4 *>(Y + row * L::yp + 4 * cg) = o;
     }
     __syncthreads();
     {   // S <- e^{G_last} S + K^T Y, backward - W^T Y + Q^T (scale e^G dO)
@@ -381,9 +386,9 @@ __global__ void __launch_bounds__(kThreads) delta_state_kernel(SweepArgs p) {
       };
 #pragma unroll 4
       for (int i = ss; i < C; i += SPL) {
-        rank(s + L::second, i, *reinterpret_cast<const float4 *>(Y + i * L::sp + 4 * cg));
+        rank(s + L::second, i, *reinterpret_cast<const float4 *>(Y + i * L::yp + 4 * cg));
         if constexpr (BWD) {
-          const float4 o = *reinterpret_cast<const float4 *>(s + L::dout + i * kCols + 4 * cg);
+          const float4 o = *reinterpret_cast<const float4 *>(s + L::dout + i * L::yp + 4 * cg);
           const float f = fac[C + i];
           rank(s + L::third, i, make_float4(f * o.x, f * o.y, f * o.z, f * o.w));
         }
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(kThreads) delta_state_kernel(SweepArgs p) {
         const float g = fac[2 * C];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float4 *o = reinterpret_cast<float4 *>(S + (4 * dg + r) * L::sp + 4 * cg);
+          float4 *o = reinterpret_cast<float4 *>(S + state_at(4 * dg + r, cg));
           const float4 x = *o;
           *o = make_float4(fmaf(g, x.x, acc[r][0]), fmaf(g, x.y, acc[r][1]), fmaf(g, x.z, acc[r][2]), fmaf(g, x.w, acc[r][3]));
         }
