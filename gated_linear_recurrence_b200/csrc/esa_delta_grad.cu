@@ -187,11 +187,11 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = pack2(mul2(unpack_io<T>(w[j]), splat(ps.s)));
         *reinterpret_cast<uint4 *>(at) = raw;
-        if (e % U == 0) oinv[rr] = ps.inv;
+        if (e % U == 0) oinv[rr] = top > 0.0f ? ps.inv : 0.0f;
       }
     }
     // slice scales: the largest of each kind, and what each slice has of it (1 almost always)
-    float part, uinv, rinv, sinv, dsinv;
+    float part, uinv, rinv, sinv, dsinv, sunit;   // sunit: sinv, or 0 for a state of zeros
     bool flat;
     {
       float v = (lane & 7) < KS ? reinterpret_cast<const float *>(sb + L::h + R::k + 512)[lane] : 0.0f;
@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
       if (__any_sync(0xffffffffu, v != v)) t = v = __int_as_float(0x7fc00000);   // a channel of the chunk is not finite
-      else if (!(t > 0.0f)) t = 1.0f;
+      sunit = __shfl_sync(0xffffffffu, t, kSliceS);
+      if (t == 0.0f) t = 1.0f;
       part = v > 0.0f && v != t ? v / t : 1.0f;
       flat = __all_sync(0xffffffffu, part == 1.0f);
       uinv = __shfl_sync(0xffffffffu, t, kSliceU);
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
     __syncthreads();
 
     const float be0 = tok[kTokBeta * 64 + i0], be1 = tok[kTokBeta * 64 + i0 + 8];
+    float uq, uk, fpk, fpq, fnk;   // units of dQ's and dK's sums; of dP in dQ, dP^T in dK, N in dK
     {   // dP and N: 16-column blocks NPA cw ..
       float P[2 * NPA][4], N[2 * NPA][4];
 #pragma unroll
@@ -251,14 +253,13 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
           }
         }
       }
-      // in the factors under which both enter dK: dP qtop, N ktop
-      float top = 0.0f;
+      float topp = 0.0f, topn = 0.0f;
       const float ru = rinv * uinv;
       float fp[2], fn[2], gi[2], gli[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        fp[e] = p.s.scale * oinv[i0 + 8 * e] * uinv * qtop;
-        fn[e] = -(e ? be1 : be0) * ru * ktop;
+        fp[e] = p.s.scale * oinv[i0 + 8 * e] * uinv;
+        fn[e] = -(e ? be1 : be0) * ru;
         gi[e] = G[i0 + 8 * e];
         gli[e] = Gl[i0 + 8 * e];
       }
@@ -275,21 +276,37 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
           P[nt][e] = j <= i ? P[nt][e] * (d * fp[e >> 1]) : 0.0f;
           N[nt][e] = j < i ? N[nt][e] * (d * fn[e >> 1]) : 0.0f;
         }
-        top = max_tile(P[nt], max_tile(N[nt], top));
+        topp = max_tile(P[nt], topp);
+        topn = max_tile(N[nt], topn);
       }
-      top = warp_max(top);
-      if (lane == 0) red[warp] = top;
+      topp = warp_max(topp);
+      topn = warp_max(topn);
+      if (lane == 0) {
+        red[warp] = topp;
+        red[32 + warp] = topn;
+      }
       __syncthreads();
-      top = red[lane & (kThreads / 32 - 1)];
-      const Pow2 pp = pow2_scale(warp_max(top));
-      if (tid == 0) red[32] = pp.inv;
+      topp = warp_max(red[lane & (kThreads / 32 - 1)]);
+      topn = warp_max(red[32 + (lane & (kThreads / 32 - 1))]);
+      const Pow2 pp = pow2_scale(topp), pn = pow2_scale(topn);
+      // Units of the sums of dQ and dK: the largest of their addends' (0 for addends of zeros), dP K, N K and dP^T Q
+      // here; those of the states' share, sums below 2^33 of the products of factors, need 2^-77 of theirs (see
+      // kLeastShare).  Fragments of a smaller unit are brought to it as they are read.
+      const float omax = warp_max(fmaxf(oinv[lane], oinv[32 + lane]));
+      const float bmax = warp_max(fmaxf(tok[kTokBeta * 64 + lane], tok[kTokBeta * 64 + 32 + lane]));
+      const float pk = topp > 0.0f ? pp.inv * ktop : 0.0f, pq = topp > 0.0f ? pp.inv * qtop : 0.0f, nk = topn > 0.0f ? pn.inv * ktop : 0.0f;
+      uq = fmaxf(fmaxf(pk, kLeastUnit), fabsf(p.s.scale) * omax * sunit * (1024.0f * kLeastShare));
+      uk = fmaxf(fmaxf(fmaxf(nk, pq), kLeastUnit), rinv * bmax * sunit * (1024.0f * kLeastShare));
+      fpk = pk / uq;
+      fpq = pq / uk;
+      fnk = nk / uk;
 #pragma unroll
       for (int nt = 0; nt < 2 * NPA; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const uint32_t o = tile_off<128>(i0 + (e >> 1) * 8, 2 * NPA * cw + nt) + 4 * t4;
           *reinterpret_cast<uint32_t *>(smem + L::dp + o) = pack_h2(P[nt][e] * pp.s, P[nt][e + 1] * pp.s);
-          *reinterpret_cast<uint32_t *>(smem + L::n + o) = pack_h2(N[nt][e] * pp.s, N[nt][e + 1] * pp.s);
+          *reinterpret_cast<uint32_t *>(smem + L::n + o) = pack_h2(N[nt][e] * pn.s, N[nt][e + 1] * pn.s);
         }
     }
     sweep::cp_async_wait<2>();   // S and dS
@@ -369,12 +386,11 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
       }
       __syncthreads();
     }
-    const float pinv = red[32], ps = 1.0f / pinv;
-    const float fq = pinv * (ktop / qtop);
     {   // the sums so far, in the units of what joins them
       const float e0 = expf(G[i0] + Gl[i0]), e1 = expf(G[i0 + 8] + Gl[i0 + 8]);
-      const float fs = p.s.scale * sinv * (1.0f / fq), fk = -rinv * sinv * ps;
-      const float q0 = fs * e0 * oinv[i0], q1 = fs * e1 * oinv[i0 + 8], k0 = fk * be0 * e0, k1 = fk * be1 * e1;
+      const float fs = p.s.scale * sinv, fk = -rinv * sinv, iq = 1.0f / uq, ik = 1.0f / uk;
+      const float q0 = fs * oinv[i0] * iq * e0, q1 = fs * oinv[i0 + 8] * iq * e1;
+      const float k0 = fk * be0 * ik * e0, k1 = fk * be1 * ik * e1;
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
         set_lo(Q[i], mul2(row_lo(Q[i]), splat(q0)));
@@ -390,6 +406,8 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
       uint32_t ap[4], an[4];
       ldsm4(ap, of64.at(0, kb) + L::dp + 16 * m * 128);
       ldsm4(an, of64.at(0, kb) + L::n + 16 * m * 128);
+      if (fpk != 1.0f) scale_frag(ap, fpk);
+      if (fnk != 1.0f) scale_frag(an, fnk);
 #pragma unroll
       for (int np = 0; np < NH / 2; ++np) {
         uint32_t bk[4];
@@ -425,7 +443,7 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
         set_hi(X[i], mul2(row_hi(X[i]), splat(l1)));
       }
 #pragma unroll
-      for (int i = 0; i < NH; i += 2) store_pair<T>(dq, ldc, 8 * i, Q[i], Q[i + 1], fq, on0, on1, lane);
+      for (int i = 0; i < NH; i += 2) store_pair<T>(dq, ldc, 8 * i, Q[i], Q[i + 1], uq, on0, on1, lane);
       float r[6] = {z0.x + z0.y, z1.x + z1.y, w0.x + w0.y, w1.x + w1.y, y0.x + y0.y, y1.x + y1.y};
 #pragma unroll
       for (int i = 0; i < 6; ++i) {
@@ -433,12 +451,12 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
         r[i] += __shfl_xor_sync(0xffffffffu, r[i], 2);
       }
       if (t4 == 0) {
-        zk[cw * 64 + i0] = r[0] * (pinv * ktop);
-        zk[cw * 64 + i0 + 8] = r[1] * (pinv * ktop);
+        zk[cw * 64 + i0] = r[0] * (uk * ktop);
+        zk[cw * 64 + i0 + 8] = r[1] * (uk * ktop);
         wk[cw * 64 + i0] = r[2] * (l0 * ktop);
         wk[cw * 64 + i0 + 8] = r[3] * (l1 * ktop);
-        qdq[cw * 64 + i0] = r[4] * (fq * qtop);
-        qdq[cw * 64 + i0 + 8] = r[5] * (fq * qtop);
+        qdq[cw * 64 + i0] = r[4] * (uq * qtop);
+        qdq[cw * 64 + i0 + 8] = r[5] * (uq * qtop);
       }
     }
     // K += N^T K + dP^T Q
@@ -449,7 +467,9 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
       const uint32_t at = s0 + tile_off<128>(16 * kb + (lane & 15), 2 * m + (lane >> 4));
       ldsm4t(rp, at + L::dp);
       ldsm4t(rn, at + L::n);
-      const uint32_t ap[4] = {rp[0], rp[2], rp[1], rp[3]}, an[4] = {rn[0], rn[2], rn[1], rn[3]};
+      uint32_t ap[4] = {rp[0], rp[2], rp[1], rp[3]}, an[4] = {rn[0], rn[2], rn[1], rn[3]};
+      if (fpq != 1.0f) scale_frag(ap, fpq);
+      if (fnk != 1.0f) scale_frag(an, fnk);
 #pragma unroll
       for (int np = 0; np < NH / 2; ++np) {
         uint32_t bk[4], bq[4];
@@ -463,8 +483,8 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
     }
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
-      set_lo(K[i], fma2(row_lo(K[i]), splat(pinv), row_lo(X[i])));
-      set_hi(K[i], fma2(row_hi(K[i]), splat(pinv), row_hi(X[i])));
+      set_lo(K[i], fma2(row_lo(K[i]), splat(uk), row_lo(X[i])));
+      set_hi(K[i], fma2(row_hi(K[i]), splat(uk), row_hi(X[i])));
     }
 #pragma unroll
     for (int i = 0; i < NH; i += 2) store_pair<T>(dk, ldc, 8 * i, K[i], K[i + 1], 1.0f, on0, on1, lane);

@@ -104,6 +104,16 @@ __device__ __forceinline__ Pow2 store_scale(float top) {
   if (top >= 0.001953125f && top < 128.0f) return {256.0f, 0.00390625f};
   return pow2_scale(top);
 }
+
+// A sum whose addends have different units (powers of two) is formed in one of
+// them, which must not be so much smaller than another that this one overflows:
+// where all write gates of a chunk are closed (beta = e^-80), the products of
+// its own values are 2^-115 of those with the state.  So a unit is at least
+// 2^-87 of that of sums below 2^33, and at least 2^-120; what the smaller
+// addends then lose is below 2^-80 of the larger.
+constexpr float kLeastShare = 6.462348535570529e-27f;   // 2^-87
+constexpr float kLeastUnit = 7.52316384526264e-37f;     // 2^-120
+
 __device__ __forceinline__ void scale_h2(uint32_t (&r)[4], float f) {
   const __half2 s = __float2half2_rn(f);
 #pragma unroll
