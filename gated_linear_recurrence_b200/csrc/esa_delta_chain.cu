@@ -155,19 +155,19 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     const uint32_t tri0 = LaneOffB<32>(lane, st).o[0];   // blocks of T and P
     const unsigned char *sb = smem + buf * L::stage;
     const float *tok = reinterpret_cast<const float *>(sb + R::tok) + 2 * t4;
-    const float4 fac = *reinterpret_cast<const float4 *>(sb + R::fac);
+    const Fac fac = load_fac(sb + R::fac);
     const long long c = c0 + n;
     int first0 = 64, first1 = 64;
     bool cut;
     {
-      uint32_t top = fac.w < 64.0f ? 0x7f800000u : 0u;
+      uint32_t top = fac.first < 64.0f ? 0x7f800000u : 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         top = max(top, unit_top<T>(*reinterpret_cast<const uint4 *>(sb + L::v + vrow + 16 * i * L::kRow)));
       cut = __reduce_max_sync(0xffffffffu, top) >= 0x7f800000u;
       if (cut) {
         int first[2];
-        cut_values<T, L::kRow>(smem + buf * L::stage + L::v, 2 * warp, static_cast<int>(fac.w), first);
+        cut_values<T, L::kRow>(smem + buf * L::stage + L::v, 2 * warp, static_cast<int>(fac.first), first);
         first0 = first[0];
         first1 = first[1];
       }
@@ -189,10 +189,10 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     for (int nt = 0; nt < NT; ++nt) top = max_tile(S[nt], top);
     const float tops = warp_max(top);
     const Pow2 ps = pow2_scale(tops);
-    const float xinv = ps.inv * sinv;
+    const float xinv = tops > 0.0f ? ps.inv * sinv : 0.0f;
     // what the backward keeps of the state has a scale of its own
     const Pow2 pss = store_scale(tops * sinv);
-    const float sf = pss.s * xinv;
+    const float sf = pss.s * (ps.inv * sinv);
     if (KEEP && lane == 0)
       p.w.slice[c * 32 + kSliceS + (dvw >> 4)] = cut ? __int_as_float(0x7fc00000) : tops > 0.0f ? pss.inv : 0.0f;
 #pragma unroll
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       for (int half = 0; half < 2; ++half) {
         const int nt = 2 * np + half;
         const float2 be = *reinterpret_cast<const float2 *>(tok + kTokBeta * 64 + 8 * nt);
-        const float2 tx = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 8 * nt), splat(-xinv));
+        const float2 tx = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 8 * nt), splat(-(xinv * fac.k)));
         const float2 r0 = fma2(tx, row_lo(X[nt]), mul2(be, unpack_io<T>(vv[half])));
         const float2 r1 = fma2(tx, row_hi(X[nt]), mul2(be, unpack_io<T>(vv[2 + half])));
         set_lo(X[nt], r0);
@@ -269,12 +269,13 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
         mma_f16(U[2 * np + 1], hi, bl[2], bl[3]);
       }
     }
-    // U is uf times the sums; U e^{G_last - G} / key scale into X
-    const float uf = pr.inv * fac.y;
+    // U itself, and U e^{G_last - G} into X
+    const float uf = pr.inv * fac.t;
     top = 0.0f;
     float topl = 0.0f;
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
+      scale_tile(U[nt], splat(uf));
       const float2 tl = *reinterpret_cast<const float2 *>(tok + kTokL * 64 + 8 * nt);
       top = max_tile(U[nt], top);
       set_lo(X[nt], mul2(row_lo(U[nt]), tl));
@@ -282,18 +283,17 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       topl = max_tile(X[nt], topl);
     }
     top = warp_max(top);
-    const Pow2 pu = pow2_scale(top), pl = pow2_scale(warp_max(topl));
-    // S^T <- e^{G_last} S^T + X K in the scale that suits X, unless that would
-    // lift the state by more than 2^36 over its own
-    const float asc = fminf(pl.s * (1.0f / uf), tops > 0.0f ? ps.s * scur * 68719476736.0f : __int_as_float(0x7f800000));
+    const Pow2 pu = pow2_scale(top);
+    // S^T <- e^{G_last} S^T + X K in the scale that suits X
+    const float asc = update_scale(warp_max(topl) * fac.k, tops, ps.s * scur, fac.last);
     {
-      const float2 sc = splat(fac.x * (asc * sinv));
+      const float2 sc = splat(fac.last * asc * sinv);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) scale_tile(S[nt], sc);
       scur = asc;
       sinv = 1.0f / asc;
     }
-    const float xs = asc * uf;
+    const float xs = asc * fac.k;
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t hi[4], lo[4];
@@ -315,24 +315,26 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
         mma_f16(S[2 * np + 3], lo, b1[2], b1[3]);
       }
     }
-    // Y = (scale e^G) S^T Q^T + scale U P^T; the first product joins the
-    // second's sum, its tokens' factors over the second's
-    const float uinv = pu.inv * uf, yf = p.s.scale * fac.z * uinv;
+    // Y = scale (e^G S^T Q^T + U P^T); the first product joins the second's
+    // sum, in its unit zu (see kLeastShare)
+    const float xq = xinv * fac.q;
+    const float uinv = fmaxf(pu.inv, fmaxf(xq * kLeastShare, kLeastUnit) * fac.ps), us = 1.0f / uinv;
+    const float zu = fac.p * uinv, yf = p.s.scale * zu;
     {
-      const float r = yf != 0.0f ? xinv / yf : 0.0f;
+      const float r = xq * (1.0f / zu);
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt)
         scale_tile(Y[nt], mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 8 * nt), splat(r)));
     }
-    const Pow2 pus = store_scale(top * uf);
+    const Pow2 pus = store_scale(top);
     if (KEEP && lane == 0)
       p.w.slice[c * 32 + kSliceU + (dvw >> 4)] = cut ? __int_as_float(0x7fc00000) : top > 0.0f ? pus.inv : 0.0f;
     uint32_t uh[4][4];
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t ul[4];
-      if constexpr (kTwo) split_a(U[2 * kb], U[2 * kb + 1], splat(pu.s), splat(pu.s), uh[kb], ul);
-      else single_a(U[2 * kb], U[2 * kb + 1], splat(pu.s), splat(pu.s), uh[kb]);
+      if constexpr (kTwo) split_a(U[2 * kb], U[2 * kb + 1], splat(us), splat(us), uh[kb], ul);
+      else single_a(U[2 * kb], U[2 * kb + 1], splat(us), splat(us), uh[kb]);
 #pragma unroll
       for (int np = kb; np < 4; ++np) {
         uint32_t bp[4];
@@ -368,8 +370,8 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       __syncwarp();
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
-        uint32_t o[4] = {uh[kb][0], uh[kb][2], uh[kb][1], uh[kb][3]};
-        if (pus.s * uinv != 1.0f) scale_h2(o, pus.s * uinv);
+        if (pus.s != us) single_a(U[2 * kb], U[2 * kb + 1], splat(pus.s), splat(pus.s), uh[kb]);
+        const uint32_t o[4] = {uh[kb][0], uh[kb][2], uh[kb][1], uh[kb][3]};
         stsm4t(vw + 16 * kb * L::kRow, o);
       }
       __syncwarp();

@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     const uint32_t tri0 = LaneOff<32>(lane, st).o[0];   // blocks of T and P
     const unsigned char *sb = smem + buf * L::stage;
     const float *tok = reinterpret_cast<const float *>(sb + R::tok) + 2 * t4;
-    const float4 fac = *reinterpret_cast<const float4 *>(sb + R::fac);
+    const Fac fac = load_fac(sb + R::fac);
     const long long c = c0 + n;
 
     // X = dS^T K^T
@@ -114,9 +114,9 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     for (int nt = 0; nt < NT; ++nt) top = max_tile(S[nt], top);
     const float tops = warp_max(top);
     const Pow2 ps = pow2_scale(tops);
-    const float xinv = ps.inv * sinv;
+    const float xinv = tops > 0.0f ? ps.inv * sinv : 0.0f;
     const Pow2 pss = store_scale(tops * sinv);
-    const float sf = pss.s * xinv;
+    const float sf = pss.s * (ps.inv * sinv);
     if (lane == 0) p.w.slice[c * 32 + kSliceDs + (dvw >> 4)] = tops > 0.0f ? pss.inv : 0.0f;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
@@ -154,17 +154,17 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
         top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
       }
     }
-    const Pow2 pd = pow2_scale(warp_max(top));
+    // dU^T = zf (X r + dO^T P) (see kLeastShare); without an output gradient's share (scale 0) P is left out
+    const float zp = p.s.scale * fac.p;
+    const bool with = zp != 0.0f;
+    const Pow2 pd = least_unit(pow2_scale(warp_max(top)), xinv * fac.k, zp);
+    const float zf = with ? zp * pd.inv : 1.0f, yd = p.s.scale * pd.inv;
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
       for (int e = 0; e < 4; ++e) od[kb][e] = pack2(mul2(unpack_io<T>(od[kb][e]), splat(pd.s)));
-    // dU^T = zf (X r + dO^T P); without an output gradient's share (scale 0) P is left out
-    const float zf0 = p.s.scale * fac.z * pd.inv;
-    const bool with = zf0 != 0.0f;
-    const float zf = with ? zf0 : 1.0f;
     {
-      const float2 r = splat(xinv / zf);
+      const float2 r = splat(xinv * fac.k / zf);
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt)
         scale_tile(X[nt], mul2(*reinterpret_cast<const float2 *>(tok + kTokL * 64 + 8 * nt), r));
@@ -221,13 +221,14 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
         mma_f16(U[2 * np + 1], hi, bl[2], bl[3]);
       }
     }
-    // du is rf times the sums.  -beta e^G du / key scale into X; the largest of that and of scale e^G dO / query scale
-    const float rf = pr.inv * zf * fac.y;
+    // du itself, -beta e^G du into X; the largest of that and of scale e^G dO
+    const float rf = pr.inv * zf * fac.t;
     top = 0.0f;
     float topx = 0.0f, topo = 0.0f;
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
-      const float2 tx = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 8 * nt), splat(-rf));
+      scale_tile(U[nt], splat(rf));
+      const float2 tx = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 8 * nt), splat(-1.0f));
       top = max_tile(U[nt], top);
       set_lo(X[nt], mul2(row_lo(U[nt]), tx));
       set_hi(X[nt], mul2(row_hi(U[nt]), tx));
@@ -237,15 +238,15 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 x = mul2(unpack_h2(od[kb][e]), mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8 * (e >> 1)), splat(pd.inv)));
+        const float2 x = mul2(unpack_h2(od[kb][e]), mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8 * (e >> 1)), splat(yd)));
         topo = fmaxf(topo, fmaxf(fabsf(x.x), fabsf(x.y)));
       }
     top = warp_max(top);
-    const Pow2 pus = store_scale(top * rf), pl = pow2_scale(warp_max(fmaxf(topx, topo)));
-    const float us = pus.s * rf;
-    const float asc = fminf(pl.s, tops > 0.0f ? ps.s * scur * 68719476736.0f : __int_as_float(0x7f800000));
+    const Pow2 pus = store_scale(top);
+    const float asc = update_scale(warp_max(fmaxf(topx * fac.k, topo * fac.q)), tops, ps.s * scur, fac.last);
+    const float xs = asc * fac.k, os = yd * (asc * fac.q);
     {
-      const float2 sc = splat(fac.x * (asc * sinv));
+      const float2 sc = splat(fac.last * asc * sinv);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) scale_tile(S[nt], sc);
       scur = asc;
@@ -254,8 +255,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t hi[4], lo[4], qh[4], ql[4];
-      split_a(X[2 * kb], X[2 * kb + 1], splat(asc), splat(asc), hi, lo);
-      const float os = pd.inv * asc;
+      split_a(X[2 * kb], X[2 * kb + 1], splat(xs), splat(xs), hi, lo);
       const float2 y0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb), splat(os));
       const float2 y1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8), splat(os));
       split2(mul2(unpack_h2(od[kb][0]), y0), qh[0], ql[0]);
@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     __syncwarp();
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
-      const float2 b0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokBeta * 64 + 16 * np), splat(rf));
-      const float2 b1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokBeta * 64 + 16 * np + 8), splat(rf));
+      const float2 b0 = *reinterpret_cast<const float2 *>(tok + kTokBeta * 64 + 16 * np);
+      const float2 b1 = *reinterpret_cast<const float2 *>(tok + kTokBeta * 64 + 16 * np + 8);
       const float2 a = mul2(row_lo(U[2 * np]), b0), bb = mul2(row_lo(U[2 * np + 1]), b1);
       const float2 cc = mul2(row_hi(U[2 * np]), b0), d = mul2(row_hi(U[2 * np + 1]), b1);
       const uint32_t o[4] = {pack_io<T>(a.x, a.y), pack_io<T>(bb.x, bb.y), pack_io<T>(cc.x, cc.y), pack_io<T>(d.x, d.y)};
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
       uint32_t r[4];
-      single_a(U[2 * np], U[2 * np + 1], splat(us), splat(us), r);
+      single_a(U[2 * np], U[2 * np + 1], splat(pus.s), splat(pus.s), r);
       const uint32_t o[4] = {r[0], r[2], r[1], r[3]};
       stsm4t(vw + 16 * np * L::kRow, o);
     }

@@ -7,7 +7,7 @@
 // kernel in the order and with the swizzle in which later kernels hold it in
 // shared memory, so that a copy of it is linear:
 //   tok    [kTokRows][64] float32  per-token factors (rows below)
-//   fac    [4] float32             e^{G_last}, 1/scale of T, 1/scale of P, first token whose key is not finite (or 64)
+//   fac    [8] float32             rows of `Fac` below
 //   k, q   [64][D] float16         keys and queries, each tile scaled by a power of two (exact)
 //   th, tl 10 blocks 16 x 16       two float16 terms of T = (1 + M)^-1 (lower triangle), scaled likewise
 //   ph, pl 10 blocks 16 x 16       two float16 terms of P_ij = e^{Gi-Gj} q_i.k_j (j <= i), scaled likewise
@@ -31,10 +31,22 @@ namespace esa {
 constexpr int kChunk = 64;
 enum { kTokBeta = 0, kTokX = 1, kTokL = 2, kTokY = 3, kTokK = 4, kTokQ = 5, kTokRows = 6 };
 //   kTokBeta  beta (0 where the key is not finite)
-//   kTokX     beta e^G / key scale          (what the state's prediction K16 S is multiplied by)
-//   kTokL     e^{G_last - G} / key scale    (what u is multiplied by before it is added to the state)
-//   kTokY     scale e^G / query scale       (NaN where the query is not finite)
+//   kTokX     beta e^G          (what the state's prediction K S is multiplied by; 0 where the key is not finite)
+//   kTokL     e^{G_last - G}    (what u is multiplied by before it is added to the state; the same)
+//   kTokY     e^G               (what the state's output Q S is multiplied by; NaN where the query is not finite)
 //   kTokK, kTokQ  1 / key scale, 1 / query scale (0 where the row is not finite)
+// The keys' and queries' scales are not multiplied into the factors: a product
+// of three scales can leave float32's range where the value itself does not.
+
+// The factors of a chunk: e^{G_last}, 1/scale of T, 1/scale of P, first token
+// whose key is not finite (or 64), 1/scale of the keys, of the queries, scale of P.
+struct Fac {
+  float last, t, p, first, k, q, ps, unused;
+};
+__device__ __forceinline__ Fac load_fac(const void *at) {
+  const float4 a = static_cast<const float4 *>(at)[0], b = static_cast<const float4 *>(at)[1];
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
 
 constexpr int kTriangle = 10 * 512;   // bytes of a triangle (kTriBytes of esa_mma.cuh)
 

@@ -159,14 +159,13 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
     const int i = tid, flag = static_cast<int>(bad[i]);
     const float into = expf(G[i] + Gl[i]), out = expf((G[63] - G[i]) + (Gl[63] - Gl[i]));
     const float nan = __int_as_float(0x7fc00000), be = beta[i];
-    const float kf = flag & 1 ? 0.0f : sk.inv, qf = flag & 2 ? 0.0f : sq.inv;
     float *tok = reinterpret_cast<float *>(smem + R::tok);
     tok[kTokBeta * 64 + i] = flag & 1 ? 0.0f : be;
-    tok[kTokX * 64 + i] = be * into * kf;
-    tok[kTokL * 64 + i] = out * kf;
-    tok[kTokY * 64 + i] = flag & 2 ? nan : p.s.scale * into * qf;
-    tok[kTokK * 64 + i] = kf;
-    tok[kTokQ * 64 + i] = qf;
+    tok[kTokX * 64 + i] = flag & 1 ? 0.0f : be * into;
+    tok[kTokL * 64 + i] = flag & 1 ? 0.0f : out;
+    tok[kTokY * 64 + i] = flag & 2 ? nan : into;
+    tok[kTokK * 64 + i] = flag & 1 ? 0.0f : sk.inv;
+    tok[kTokQ * 64 + i] = flag & 2 ? 0.0f : sq.inv;
   }
   // K K^T (warps 0-3) and Q K^T (warps 4-7): 16 rows a warp, tiles on and below the diagonal
   float acc[8][4];
@@ -390,7 +389,9 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
     float first = 64.0f;
     for (int i = 63; i >= 0; --i)
       if (static_cast<int>(bad[i]) & 1) first = static_cast<float>(i);
-    *reinterpret_cast<float4 *>(smem + R::fac) = make_float4(expf(G[63] + Gl[63]), st.inv, sp.inv, first);
+    float4 *fac = reinterpret_cast<float4 *>(smem + R::fac);
+    fac[0] = make_float4(expf(G[63] + Gl[63]), st.inv, sp.inv, first);
+    fac[1] = make_float4(sk.inv, sq.inv, sp.s, 0.0f);
   }
   fence_proxy_async_smem();
   __syncthreads();

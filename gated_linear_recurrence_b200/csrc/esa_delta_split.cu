@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
     const LaneOffB<D * 2> ofb(lane, st);
     const uint32_t tri0 = LaneOffB<32>(lane, st).o[0];
     const float *tok = reinterpret_cast<const float *>(sb + R::tok) + 2 * t4;
-    const float4 fac = *reinterpret_cast<const float4 *>(sb + R::fac);
+    const Fac fac = load_fac(sb + R::fac);
     const long long c = c0 + n;
     // The quarter's block columns: D = 128 has two a warp, D = 64 one.
     auto colb = [&](int np, int j) -> uint32_t {   // [token][channel] B blocks
@@ -151,9 +151,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
     float Xo[2][4], Yo[2][4];   // this warp's tokens
     const float tops = top4(tops_);
     const Pow2 ps = pow2_scale(tops);
-    const float xinv = ps.inv * sinv;
+    const float xinv = tops > 0.0f ? ps.inv * sinv : 0.0f;
     const Pow2 pss = store_scale(tops * sinv);
-    const float sf = pss.s * xinv;
+    const float sf = pss.s * (ps.inv * sinv);
     if (KEEP && threadIdx.x == 0) p.w.slice[c * 32 + kSliceS + slice] = tops > 0.0f ? pss.inv : 0.0f;
     {
       float X[8][4], Y[8][4];
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float2 be = *reinterpret_cast<const float2 *>(tok + kTokBeta * 64 + 16 * w + 8 * i);
-        const float2 tx = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * w + 8 * i), splat(-xinv));
+        const float2 tx = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * w + 8 * i), splat(-(xinv * fac.k)));
         set_lo(Xo[i], fma2(tx, row_lo(Xo[i]), mul2(be, unpack_io<T>(vv[i]))));
         set_hi(Xo[i], fma2(tx, row_hi(Xo[i]), mul2(be, unpack_io<T>(vv[2 + i]))));
         chk = fma2(row_lo(Xo[i]), splat(0.0f), fma2(row_hi(Xo[i]), splat(0.0f), chk));
@@ -225,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
     __syncthreads();
     // 2. U = R T^T for this warp's tokens: all of R up to them
     float topr = top4(tops_ + 4);
-    const bool cut = topr == __int_as_float(0x7f800000) || fac.w < 64.0f;
-    int first[2] = {static_cast<int>(fac.w), static_cast<int>(fac.w)};   // first token from which a row is not finite
+    const bool cut = topr == __int_as_float(0x7f800000) || fac.first < 64.0f;
+    int first[2] = {static_cast<int>(fac.first), static_cast<int>(fac.first)};   // first token from which a row is not finite
     if (cut) {
       topr = 0.0f;
 #pragma unroll 1
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
           mma_f16(A[2][i], hi, bl[2 * i], bl[2 * i + 1]);
         }
       }
-      const float uf = pr.inv * fac.y;
+      const float uf = pr.inv * fac.t;
       float top = 0.0f, topl = 0.0f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -307,18 +307,20 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
     __syncthreads();
     // 3. the state's quarter, and the outputs of this warp's tokens
     const float topu = top4(tops_ + 8);
-    const Pow2 pu = pow2_scale(topu), pl = pow2_scale(top4(tops_ + 12));
-    const float asc = fminf(pl.s, tops > 0.0f ? ps.s * scur * 68719476736.0f : __int_as_float(0x7f800000));
+    const Pow2 pu = pow2_scale(topu);
+    const float asc = update_scale(top4(tops_ + 12) * fac.k, tops, ps.s * scur, fac.last);
     {
-      const float2 sc = splat(fac.x * (asc * sinv));
+      const float2 sc = splat(fac.last * asc * sinv);
 #pragma unroll
       for (int i = 0; i < NQ; ++i) scale_tile(S[i], sc);
       scur = asc;
       sinv = 1.0f / asc;
     }
-    const float uinv = pu.inv, yf = p.s.scale * fac.z * uinv;
+    const float xq = xinv * fac.q, xs = asc * fac.k;
+    const float uinv = fmaxf(pu.inv, fmaxf(xq * kLeastShare, kLeastUnit) * fac.ps), us = 1.0f / uinv;
+    const float zu = fac.p * uinv, yf = p.s.scale * zu;
     {
-      const float r = yf != 0.0f ? xinv / yf : 0.0f;
+      const float r = xq * (1.0f / zu);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         scale_tile(Yo[i], mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * w + 8 * i), splat(r)));
@@ -330,8 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
       get_tile(smem + L::fin + (2 * kb) * kTileF, u0, lane);
       get_tile(smem + L::fin + (2 * kb + 1) * kTileF, u1, lane);
       uint32_t hi[4], lo[4];
-      const float2 l0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * kb), splat(asc));
-      const float2 l1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * kb + 8), splat(asc));
+      const float2 l0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * kb), splat(xs));
+      const float2 l1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * kb + 8), splat(xs));
       split_a(u0, u1, l0, l1, hi, lo);
 #pragma unroll
       for (int j = 0; j < NQ / 2; ++j) {
@@ -344,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
       }
       if (kb <= w) {
         uint32_t uh[4], ul[4], bp[4];
-        if constexpr (kTwo) split_a(u0, u1, splat(pu.s), splat(pu.s), uh, ul);
-        else single_a(u0, u1, splat(pu.s), splat(pu.s), uh);
+        if constexpr (kTwo) split_a(u0, u1, splat(us), splat(us), uh, ul);
+        else single_a(u0, u1, splat(us), splat(us), uh);
         ldsm4(bp, tri0 + (w * (w + 1) / 2 + kb) * 512 + R::ph);
         mma_f16(Yo[0], uh, bp[0], bp[1]);
         mma_f16(Yo[1], uh, bp[2], bp[3]);
@@ -383,8 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
       if constexpr (KEEP) {
         __syncwarp();
         const Pow2 pus = store_scale(topu);
-        uint32_t u[4] = {own[0], own[2], own[1], own[3]};
-        if (pus.s * uinv != 1.0f) scale_h2(u, pus.s * uinv);
+        if (pus.s != us) single_a(Uo[0], Uo[1], splat(pus.s), splat(pus.s), own);
+        const uint32_t u[4] = {own[0], own[2], own[1], own[3]};
         stsm4t(vw, u);
         __syncwarp();
         *reinterpret_cast<uint4 *>(p.w.u16 + (c * 64 + r) * D + dvw + 8 * (lane & 1)) = *reinterpret_cast<const uint4 *>(vr);
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
     const LaneOffB<D * 2> ofb(lane, st);
     const uint32_t tri0 = LaneOff<32>(lane, st).o[0];
     const float *tok = reinterpret_cast<const float *>(sb + R::tok) + 2 * t4;
-    const float4 fac = *reinterpret_cast<const float4 *>(sb + R::fac);
+    const Fac fac = load_fac(sb + R::fac);
     const long long c = c0 + n;
     auto colb = [&](int np, int j) -> uint32_t {
       if constexpr (D == 128) return ((w & 1) ? ofb.at(np, 2 + j) : ofb.at(np, j)) + (w >> 1) * 128u;
@@ -462,9 +464,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
     // 1. partial dS^T K^T; dO^T as an A operand (every warp needs all of it)
     const float tops = top4(tops_);
     const Pow2 ps = pow2_scale(tops);
-    const float xinv = ps.inv * sinv;
+    const float xinv = tops > 0.0f ? ps.inv * sinv : 0.0f;
     const Pow2 pss = store_scale(tops * sinv);
-    const float sf = pss.s * xinv;
+    const float sf = pss.s * (ps.inv * sinv);
     if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceDs + slice] = tops > 0.0f ? pss.inv : 0.0f;
     {
       float X[8][4];
@@ -507,7 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
         topd = fmaxf(fmaxf(topd, fabsf(x.x)), fabsf(x.y));
       }
     }
-    const Pow2 pd = pow2_scale(warp_max(topd));
+    // the unit of the output gradient's share of dU^T (see kLeastShare); without a share (scale 0) P is left out
+    const float zp = p.s.scale * fac.p;
+    const bool with = zp != 0.0f;
+    const Pow2 pd = least_unit(pow2_scale(warp_max(topd)), xinv * fac.k, zp);
+    const float zf = with ? zp * pd.inv : 1.0f, yd = p.s.scale * pd.inv;
     float topo = 0.0f;
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)
@@ -515,13 +521,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
       for (int e = 0; e < 4; ++e) {
         const float2 x = mul2(unpack_io<T>(od[kb][e]), splat(pd.s));
         od[kb][e] = pack2(x);
-        const float2 z = mul2(x, mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8 * (e >> 1)), splat(pd.inv)));
+        const float2 z = mul2(x, mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8 * (e >> 1)), splat(yd)));
         topo = fmaxf(fmaxf(topo, fabsf(z.x)), fabsf(z.y));
       }
     topo = warp_max(topo);
-    const float zf0 = p.s.scale * fac.z * pd.inv;
-    const bool with = zf0 != 0.0f;
-    const float zf = with ? zf0 : 1.0f;
     __syncthreads();
     // dU^T = zf (X r + dO^T P) for this warp's tokens, 16 w ..
     {
@@ -533,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
         for (int i = 0; i < 2; ++i) add_tile(smem + L::part + (j * 8 + 2 * w + i) * kTileF, X[i], lane);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        scale_tile(X[i], mul2(*reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * w + 8 * i), splat(xinv / zf)));
+        scale_tile(X[i], mul2(*reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * w + 8 * i), splat(xinv * fac.k / zf)));
       if (with) {
         float Z[2][4];
         zero_tiles(Z);
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
     __syncthreads();
     // 2. du^T = dU^T T for this warp's tokens: all of dU from them on
     const Pow2 pr = pow2_scale(top4(tops_ + 4));
-    const float rf = pr.inv * zf * fac.y;
+    const float rf = pr.inv * zf * fac.t;
     float Uo[2][4];
     {
       float A[3][2][4];
@@ -614,24 +617,24 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
     __syncthreads();
     // 3. the quarter of dS^T, dv and du of this warp's tokens
     const float topu = top4(tops_ + 8);
-    const Pow2 pus = store_scale(topu), pl = pow2_scale(fmaxf(top4(tops_ + 12), topo));
-    const float asc = fminf(pl.s, tops > 0.0f ? ps.s * scur * 68719476736.0f : __int_as_float(0x7f800000));
+    const Pow2 pus = store_scale(topu);
+    const float asc = update_scale(fmaxf(top4(tops_ + 12) * fac.k, topo * fac.q), tops, ps.s * scur, fac.last);
     {
-      const float2 sc = splat(fac.x * (asc * sinv));
+      const float2 sc = splat(fac.last * asc * sinv);
 #pragma unroll
       for (int i = 0; i < NQ; ++i) scale_tile(S[i], sc);
       scur = asc;
       sinv = 1.0f / asc;
     }
-    const float os = pd.inv * asc;
+    const float os = yd * (asc * fac.q), xs = asc * fac.k;
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       float u0[4], u1[4];
       get_tile(smem + L::fin + (2 * kb) * kTileF, u0, lane);
       get_tile(smem + L::fin + (2 * kb + 1) * kTileF, u1, lane);
       uint32_t hi[4], lo[4], qh[4], ql[4];
-      const float2 x0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * kb), splat(-asc));
-      const float2 x1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * kb + 8), splat(-asc));
+      const float2 x0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * kb), splat(-xs));
+      const float2 x1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * kb + 8), splat(-xs));
       split_a(u0, u1, x0, x1, hi, lo);
       const float2 y0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb), splat(os));
       const float2 y1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8), splat(os));

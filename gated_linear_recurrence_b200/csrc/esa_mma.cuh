@@ -87,7 +87,8 @@ __device__ __forceinline__ uint32_t unit_top(uint4 v) {
 
 // Power of two, of an exponent divisible by 8, that brings `top` (>= 0) to
 // [2^5, 2^13), and its inverse; 1 for zero.  Steps of 2^8 let the groups of a
-// tile have the same scale almost always; float16 has the room.
+// tile have the same scale almost always; float16 has the room.  A product of
+// two of them may have no reciprocal in float32: none is formed.
 struct Pow2 {
   float s, inv;
 };
@@ -110,9 +111,29 @@ __device__ __forceinline__ Pow2 store_scale(float top) {
 // where all write gates of a chunk are closed (beta = e^-80), the products of
 // its own values are 2^-115 of those with the state.  So a unit is at least
 // 2^-87 of that of sums below 2^33, and at least 2^-120; what the smaller
-// addends then lose is below 2^-80 of the larger.
+// addends then lose is below 2^-80 of the larger.  (The unit of a state of
+// zeros is zero here.)
 constexpr float kLeastShare = 6.462348535570529e-27f;   // 2^-87
 constexpr float kLeastUnit = 7.52316384526264e-37f;     // 2^-120
+
+// Scale of the state after a chunk: the one that suits its update, whose
+// largest value is `upd` (2^126 below 2^-113, so that updates of 2^-120 keep 22
+// bits), unless that would lift the state, of largest value `top` and scale
+// `own` and decaying by `decay`, by more than 2^36 over its own.
+__device__ __forceinline__ float update_scale(float upd, float top, float own, float decay) {
+  const float s = upd > 0.0f && upd < 9.62964972193618e-35f ? 8.507059173023462e37f : pow2_scale(upd).s;
+  return top > 0.0f ? fminf(s, own * 68719476736.0f * (1.0f / decay)) : s;
+}
+
+// The scale of an output gradient, `own`, such that its product's unit
+// |share| inv is no smaller than kLeastShare allows beside a product of unit
+// `other`; a power of two.  `share` may be zero (own is returned).
+__device__ __forceinline__ Pow2 least_unit(Pow2 own, float other, float share) {
+  const float least = fminf(fmaxf(other * kLeastShare, kLeastUnit) / fabsf(share), 2.5961484292674138e33f);   // 2^111
+  if (!(share != 0.0f && least > own.inv)) return own;
+  const uint32_t up = (__float_as_uint(least) & 0x7f800000u) + 0x00800000u;   // the next power of two
+  return {__uint_as_float(0x7f000000u - up), __uint_as_float(up)};
+}
 
 __device__ __forceinline__ void scale_h2(uint32_t (&r)[4], float f) {
   const __half2 s = __float2half2_rn(f);

@@ -37,3 +37,28 @@ def test_queries_and_keys_of_different_size(cuda_device, dt, which, factor, D, H
         x["dy"] = (x["dy"].float() / factor).to(x["dy"].dtype)
     xs, got, ref = two_heads(x, S0, dS, run(x, S0, dS, D ** -0.5))
     check(xs, got, ref, T, D, half_p=HALF_P)
+
+
+@pytest.mark.parametrize("D,H", SPREADS)
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("where", ["start", "middle", "end", "all"])
+def test_closed_write_gates(cuda_device, where, state, D, H):
+    """Chunks in which nothing is written (padding, b = -inf: beta = e^-80), from a state of zeros and from another:
+    what the chunk writes is 2^-115 of what it reads."""
+    x, S0, dS = draw("bf16", 1, T, H, D, seed=3, state=state)
+    x["b"][:, {"start": slice(0, 64), "middle": slice(64, 128), "end": slice(128, T), "all": slice(0, T)}[where]] = float("-inf")
+    xs, got, ref = two_heads(x, S0, dS, run(x, S0, dS, D ** -0.5))
+    if where == "all":
+        # the reference's clamp passes no gradient; the kernel's is u.du with |u| <= e^-80 (|v| + |S k|) < 1e-33, |du| < 1e2
+        assert float(got["db"].abs().max()) < 1e-31
+        got["db"] = None
+    check(xs, got, ref, T, D, half_p=HALF_P)
+
+
+@pytest.mark.parametrize("D,H", SPREADS)
+@pytest.mark.parametrize("which", ["v", "dy"])
+def test_tiny_values(cuda_device, which, D, H):
+    x, _, _ = draw("bf16", 1, T, H, D, seed=4, state=False)
+    x[which] = (x[which].float() * 1e-30).to(x[which].dtype)
+    xs, got, ref = two_heads(x, None, None, run(x, None, None, D ** -0.5))
+    check(xs, got, ref, T, D, half_p=HALF_P)
