@@ -120,10 +120,10 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     sweep::cp_async_commit();
   };
 
-  // S^T times a power of two, 1 / sinv: each chunk leaves it in the scale in
-  // which it added to it.
+  // S^T, each row times a power of two, 1 / sinv: each chunk leaves it in the
+  // scale in which it added to it.
   float S[NT][4];
-  float scur = 1.0f, sinv = 1.0f;
+  float2 sinv = splat(1.0f);
   if (p.S_in != nullptr) {
     const float *Si = p.S_in + static_cast<long long>(head) * D * D;
 #pragma unroll
@@ -184,24 +184,28 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) X[i][e] = Y[i][e] = 0.0f;
-    float top = 0.0f;
+    float2 top = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) top = max_tile(S[nt], top);
-    const float tops = warp_max(top);
-    const Pow2 ps = pow2_scale(tops);
-    const float xinv = tops > 0.0f ? ps.inv * sinv : 0.0f;
-    // what the backward keeps of the state has a scale of its own
-    const Pow2 pss = store_scale(tops * sinv);
-    const float sf = pss.s * (ps.inv * sinv);
-    if (KEEP && lane == 0)
-      p.w.slice[c * 32 + kSliceS + (dvw >> 4)] = cut ? __int_as_float(0x7fc00000) : tops > 0.0f ? pss.inv : 0.0f;
+    for (int nt = 0; nt < NT; ++nt) top = max_rows(S[nt], top);
+    const float2 tops = quad_max(top);
+    const RowPow2 ps = pow2_scale(tops);
+    const float2 sunit = mul2(ps.inv, sinv), xinv = unit_or_zero(tops, sunit);
+    // what the backward keeps of the state has one scale for the 16 channels
+    float2 sf;
+    if constexpr (KEEP) {
+      const float all = warp_max(fmaxf(tops.x * sinv.x, tops.y * sinv.y));
+      const Pow2 pss = store_scale(all);
+      sf = mul2(splat(pss.s), sunit);
+      if (lane == 0)
+        p.w.slice[c * 32 + kSliceS + (dvw >> 4)] = cut ? __int_as_float(0x7fc00000) : slice_unit(all, pss);
+    }
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint32_t hi[4], lo[4];
-      split_a(S[2 * ks], S[2 * ks + 1], splat(ps.s), splat(ps.s), hi, lo);
+      split_rows(S[2 * ks], S[2 * ks + 1], ps.s, hi, lo);
       if constexpr (KEEP) {
         uint32_t x[4] = {hi[0], hi[1], hi[2], hi[3]};
-        if (sf != 1.0f) scale_h2(x, sf);
+        if (sf.x != 1.0f || sf.y != 1.0f) scale_h2(x, sf);
         store_block(p.w.s16 + c * (D * D) + dvw * D + 16 * ks, D, x, lane);
       }
 #pragma unroll
@@ -222,7 +226,8 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       }
     }
     // R = beta V^T - (beta e^G) X, in place of X
-    top = 0.0f;
+    top = make_float2(0.0f, 0.0f);
+    const float2 xk = mul2(xinv, splat(-fac.k));
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
       uint32_t vv[4];
@@ -231,15 +236,15 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       for (int half = 0; half < 2; ++half) {
         const int nt = 2 * np + half;
         const float2 be = *reinterpret_cast<const float2 *>(tok + kTokBeta * 64 + 8 * nt);
-        const float2 tx = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 8 * nt), splat(-(xinv * fac.k)));
-        const float2 r0 = fma2(tx, row_lo(X[nt]), mul2(be, unpack_io<T>(vv[half])));
-        const float2 r1 = fma2(tx, row_hi(X[nt]), mul2(be, unpack_io<T>(vv[2 + half])));
+        const float2 tx = *reinterpret_cast<const float2 *>(tok + kTokX * 64 + 8 * nt);
+        const float2 r0 = fma2(mul2(tx, splat(xk.x)), row_lo(X[nt]), mul2(be, unpack_io<T>(vv[half])));
+        const float2 r1 = fma2(mul2(tx, splat(xk.y)), row_hi(X[nt]), mul2(be, unpack_io<T>(vv[2 + half])));
         set_lo(X[nt], r0);
         set_hi(X[nt], r1);
-        top = max_tile(X[nt], top);
+        top = max_rows(X[nt], top);
       }
     }
-    const Pow2 pr = pow2_scale(warp_max(top));
+    const RowPow2 pr = pow2_scale(quad_max(top));
     // U = R T^T: T_ij = 0 for j > i, in blocks of 16
     float U[8][4];
 #pragma unroll
@@ -249,7 +254,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t hi[4], lo[4];
-      split_a(X[2 * kb], X[2 * kb + 1], splat(pr.s), splat(pr.s), hi, lo);
+      split_rows(X[2 * kb], X[2 * kb + 1], pr.s, hi, lo);
       uint32_t bh[4][4], bl[4];
 #pragma unroll
       for (int np = kb; np < 4; ++np) {
@@ -270,34 +275,33 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       }
     }
     // U itself, and U e^{G_last - G} into X
-    const float uf = pr.inv * fac.t;
-    top = 0.0f;
-    float topl = 0.0f;
+    const float2 uf = mul2(pr.inv, splat(fac.t));
+    top = make_float2(0.0f, 0.0f);
+    float2 topl = top;
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
-      scale_tile(U[nt], splat(uf));
+      scale_rows(U[nt], uf);
       const float2 tl = *reinterpret_cast<const float2 *>(tok + kTokL * 64 + 8 * nt);
-      top = max_tile(U[nt], top);
+      top = max_rows(U[nt], top);
       set_lo(X[nt], mul2(row_lo(U[nt]), tl));
       set_hi(X[nt], mul2(row_hi(U[nt]), tl));
-      topl = max_tile(X[nt], topl);
+      topl = max_rows(X[nt], topl);
     }
-    top = warp_max(top);
-    const Pow2 pu = pow2_scale(top);
+    top = quad_max(top);
+    const RowPow2 pu = pow2_scale(top);
     // S^T <- e^{G_last} S^T + X K in the scale that suits X
-    const float asc = update_scale(warp_max(topl) * fac.k, tops, ps.s * scur, fac.last);
+    const float2 asc = update_scale(mul2(quad_max(topl), splat(fac.k)), tops, sunit, fac.last);
     {
-      const float2 sc = splat(fac.last * asc * sinv);
+      const float2 sc = mul2(mul2(asc, splat(fac.last)), sinv);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) scale_tile(S[nt], sc);
-      scur = asc;
-      sinv = 1.0f / asc;
+      for (int nt = 0; nt < NT; ++nt) scale_rows(S[nt], sc);
+      sinv = make_float2(pow2_inverse(asc.x), pow2_inverse(asc.y));
     }
-    const float xs = asc * fac.k;
+    const float2 xs = mul2(asc, splat(fac.k));
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t hi[4], lo[4];
-      split_a(X[2 * kb], X[2 * kb + 1], splat(xs), splat(xs), hi, lo);
+      split_rows(X[2 * kb], X[2 * kb + 1], xs, hi, lo);
       // two blocks at a time: an accumulator's second product comes four mma
       // (32 clocks) after its first, which takes 25
 #pragma unroll
@@ -317,24 +321,27 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     }
     // Y = scale (e^G S^T Q^T + U P^T); the first product joins the second's
     // sum, in its unit zu (see kLeastShare)
-    const float xq = xinv * fac.q;
-    const float uinv = fmaxf(pu.inv, fmaxf(xq * kLeastShare, kLeastUnit) * fac.ps), us = 1.0f / uinv;
-    const float zu = fac.p * uinv, yf = p.s.scale * zu;
-    {
-      const float r = xq * (1.0f / zu);
+    const OutputUnit ou0 = output_unit(xinv.x * fac.q, pu.inv.x, fac.p, fac.ps), ou1 = output_unit(xinv.y * fac.q, pu.inv.y, fac.p, fac.ps);
+    const float2 us = make_float2(ou0.us, ou1.us), yf = mul2(make_float2(ou0.unit, ou1.unit), splat(p.s.scale));
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-        scale_tile(Y[nt], mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 8 * nt), splat(r)));
+    for (int nt = 0; nt < 8; ++nt) {
+      const float2 ty = *reinterpret_cast<const float2 *>(tok + kTokY * 64 + 8 * nt);
+      set_lo(Y[nt], mul2(row_lo(Y[nt]), mul2(ty, splat(ou0.r))));
+      set_hi(Y[nt], mul2(row_hi(Y[nt]), mul2(ty, splat(ou1.r))));
     }
-    const Pow2 pus = store_scale(top);
-    if (KEEP && lane == 0)
-      p.w.slice[c * 32 + kSliceU + (dvw >> 4)] = cut ? __int_as_float(0x7fc00000) : top > 0.0f ? pus.inv : 0.0f;
+    Pow2 pus;
+    if constexpr (KEEP) {
+      const float all = warp_max(fmaxf(top.x, top.y));
+      pus = store_scale(all);
+      if (lane == 0)
+        p.w.slice[c * 32 + kSliceU + (dvw >> 4)] = cut ? __int_as_float(0x7fc00000) : slice_unit(all, pus);
+    }
     uint32_t uh[4][4];
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t ul[4];
-      if constexpr (kTwo) split_a(U[2 * kb], U[2 * kb + 1], splat(us), splat(us), uh[kb], ul);
-      else single_a(U[2 * kb], U[2 * kb + 1], splat(us), splat(us), uh[kb]);
+      if constexpr (kTwo) split_rows(U[2 * kb], U[2 * kb + 1], us, uh[kb], ul);
+      else single_rows(U[2 * kb], U[2 * kb + 1], us, uh[kb]);
 #pragma unroll
       for (int np = kb; np < 4; ++np) {
         uint32_t bp[4];
@@ -354,8 +361,8 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     __syncwarp();
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
-      const float2 a = mul2(row_lo(Y[2 * np]), splat(yf)), bb = mul2(row_lo(Y[2 * np + 1]), splat(yf));
-      const float2 cc = mul2(row_hi(Y[2 * np]), splat(yf)), d = mul2(row_hi(Y[2 * np + 1]), splat(yf));
+      const float2 a = mul2(row_lo(Y[2 * np]), splat(yf.x)), bb = mul2(row_lo(Y[2 * np + 1]), splat(yf.x));
+      const float2 cc = mul2(row_hi(Y[2 * np]), splat(yf.y)), d = mul2(row_hi(Y[2 * np + 1]), splat(yf.y));
       const uint32_t o[4] = {pack_io<T>(a.x, a.y), pack_io<T>(bb.x, bb.y), pack_io<T>(cc.x, cc.y), pack_io<T>(d.x, d.y)};
       stsm4t(vw + 16 * np * L::kRow, o);
     }
@@ -370,7 +377,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
       __syncwarp();
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
-        if (pus.s != us) single_a(U[2 * kb], U[2 * kb + 1], splat(pus.s), splat(pus.s), uh[kb]);
+        if (pus.s != us.x || pus.s != us.y) single_rows(U[2 * kb], U[2 * kb + 1], splat(pus.s), uh[kb]);
         const uint32_t o[4] = {uh[kb][0], uh[kb][2], uh[kb][1], uh[kb][3]};
         stsm4t(vw + 16 * kb * L::kRow, o);
       }
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
 #pragma unroll
       for (int e = 0; e < 4; ++e) 
         So[(8 * nt + 2 * t4 + (e & 1)) * D + dvw + g + (e >> 1) * 8] =
-            (e < 2 ? dead0 : dead1) ? __int_as_float(0x7fc00000) : S[nt][e] * sinv;
+            (e < 2 ? dead0 : dead1) ? __int_as_float(0x7fc00000) : S[nt][e] * (e < 2 ? sinv.x : sinv.y);
   }
 }
 

@@ -68,8 +68,8 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     sweep::cp_async_commit();
   };
 
-  float S[NT][4];   // dS^T times scur
-  float scur = 1.0f, sinv = 1.0f;
+  float S[NT][4];   // dS^T, each row over its sinv
+  float2 sinv = splat(1.0f);
   if (p.S_in != nullptr) {
     const float *Si = p.S_in + static_cast<long long>(head) * D * D;
 #pragma unroll
@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
       for (int e = 0; e < 4; ++e) S[nt][e] = 0.0f;
   }
 
+  const float iscale = 1.0f / fabsf(p.s.scale);
   fetch(nc - 1, 0);
 #pragma unroll 1
   for (int it = 0; it < nc; ++it) {
@@ -109,21 +110,22 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) X[i][e] = 0.0f;
-    float top = 0.0f;
+    float2 top = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) top = max_tile(S[nt], top);
-    const float tops = warp_max(top);
-    const Pow2 ps = pow2_scale(tops);
-    const float xinv = tops > 0.0f ? ps.inv * sinv : 0.0f;
-    const Pow2 pss = store_scale(tops * sinv);
-    const float sf = pss.s * (ps.inv * sinv);
-    if (lane == 0) p.w.slice[c * 32 + kSliceDs + (dvw >> 4)] = tops > 0.0f ? pss.inv : 0.0f;
+    for (int nt = 0; nt < NT; ++nt) top = max_rows(S[nt], top);
+    const float2 tops = quad_max(top);
+    const RowPow2 ps = pow2_scale(tops);
+    const float2 sunit = mul2(ps.inv, sinv), xinv = unit_or_zero(tops, sunit);
+    const float alls = warp_max(fmaxf(tops.x * sinv.x, tops.y * sinv.y));
+    const Pow2 pss = store_scale(alls);
+    const float2 sf = mul2(splat(pss.s), sunit);
+    if (lane == 0) p.w.slice[c * 32 + kSliceDs + (dvw >> 4)] = slice_unit(alls, pss);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       uint32_t hi[4], lo[4];
-      split_a(S[2 * ks], S[2 * ks + 1], splat(ps.s), splat(ps.s), hi, lo);
+      split_rows(S[2 * ks], S[2 * ks + 1], ps.s, hi, lo);
       uint32_t x[4] = {hi[0], hi[1], hi[2], hi[3]};
-      if (sf != 1.0f) scale_h2(x, sf);
+      if (sf.x != 1.0f || sf.y != 1.0f) scale_h2(x, sf);
       store_block(p.w.ds16 + c * (D * D) + dvw * D + 16 * ks, D, x, lane);
 #pragma unroll
       for (int np = 0; np < 4; np += 2) {   // an accumulator's second product four mma after its first
@@ -141,8 +143,8 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
       }
     }
     // dO^T as an A operand, scaled to float16
-    uint32_t od[4][4];
-    top = 0.0f;
+    uint32_t od[4][4];   // registers 0 and 2 of a block are row g
+    top = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t r[4];
@@ -151,23 +153,29 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 x = unpack_io<T>(od[kb][e]);
-        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+        float &t = e & 1 ? top.y : top.x;
+        t = fmaxf(t, fmaxf(fabsf(x.x), fabsf(x.y)));
       }
     }
     // dU^T = zf (X r + dO^T P) (see kLeastShare); without an output gradient's share (scale 0) P is left out
     const float zp = p.s.scale * fac.p;
     const bool with = zp != 0.0f;
-    const Pow2 pd = least_unit(pow2_scale(warp_max(top)), xinv * fac.k, zp);
-    const float zf = with ? zp * pd.inv : 1.0f, yd = p.s.scale * pd.inv;
+    const float2 xk = mul2(xinv, splat(fac.k));
+    RowPow2 pd = pow2_scale(quad_max(top));
+    if (with) pd = least_unit(pd, xk, iscale * fac.ps);
+    const float2 zf = with ? mul2(pd.inv, splat(zp)) : splat(1.0f), yd = mul2(pd.inv, splat(p.s.scale));
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) od[kb][e] = pack2(mul2(unpack_io<T>(od[kb][e]), splat(pd.s)));
+      for (int e = 0; e < 4; ++e) od[kb][e] = pack2(mul2(unpack_io<T>(od[kb][e]), splat(e & 1 ? pd.s.y : pd.s.x)));
     {
-      const float2 r = splat(xinv * fac.k / zf);
+      const float2 r = make_float2(xk.x / zf.x, xk.y / zf.y);
 #pragma unroll
-      for (int nt = 0; nt < 8; ++nt)
-        scale_tile(X[nt], mul2(*reinterpret_cast<const float2 *>(tok + kTokL * 64 + 8 * nt), r));
+      for (int nt = 0; nt < 8; ++nt) {
+        const float2 tl = *reinterpret_cast<const float2 *>(tok + kTokL * 64 + 8 * nt);
+        set_lo(X[nt], mul2(row_lo(X[nt]), mul2(tl, splat(r.x))));
+        set_hi(X[nt], mul2(row_hi(X[nt]), mul2(tl, splat(r.y))));
+      }
     }
     if (with) {
 #pragma unroll
@@ -189,10 +197,10 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
       }
     }
     // du^T = dU^T T
-    top = 0.0f;
+    top = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) top = max_tile(X[nt], top);
-    const Pow2 pr = pow2_scale(warp_max(top));
+    for (int nt = 0; nt < 8; ++nt) top = max_rows(X[nt], top);
+    const RowPow2 pr = pow2_scale(quad_max(top));
     float U[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -201,7 +209,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t hi[4], lo[4];
-      split_a(X[2 * kb], X[2 * kb + 1], splat(pr.s), splat(pr.s), hi, lo);
+      split_rows(X[2 * kb], X[2 * kb + 1], pr.s, hi, lo);
       uint32_t bh[4][4], bl[4];
 #pragma unroll
       for (int np = 0; np <= kb; ++np) {
@@ -222,46 +230,47 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
       }
     }
     // du itself, -beta e^G du into X; the largest of that and of scale e^G dO
-    const float rf = pr.inv * zf * fac.t;
-    top = 0.0f;
-    float topx = 0.0f, topo = 0.0f;
+    const float2 rf = mul2(mul2(pr.inv, zf), splat(fac.t));
+    top = make_float2(0.0f, 0.0f);
+    float2 topx = top, topo = top;
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
-      scale_tile(U[nt], splat(rf));
+      scale_rows(U[nt], rf);
       const float2 tx = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 8 * nt), splat(-1.0f));
-      top = max_tile(U[nt], top);
+      top = max_rows(U[nt], top);
       set_lo(X[nt], mul2(row_lo(U[nt]), tx));
       set_hi(X[nt], mul2(row_hi(U[nt]), tx));
-      topx = max_tile(X[nt], topx);
+      topx = max_rows(X[nt], topx);
     }
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 x = mul2(unpack_h2(od[kb][e]), mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8 * (e >> 1)), splat(yd)));
-        topo = fmaxf(topo, fmaxf(fabsf(x.x), fabsf(x.y)));
+        const float2 x = mul2(unpack_h2(od[kb][e]), mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8 * (e >> 1)), splat(e & 1 ? yd.y : yd.x)));
+        float &t = e & 1 ? topo.y : topo.x;
+        t = fmaxf(t, fmaxf(fabsf(x.x), fabsf(x.y)));
       }
-    top = warp_max(top);
-    const Pow2 pus = store_scale(top);
-    const float asc = update_scale(warp_max(fmaxf(topx * fac.k, topo * fac.q)), tops, ps.s * scur, fac.last);
-    const float xs = asc * fac.k, os = yd * (asc * fac.q);
+    const float allu = warp_max(fmaxf(top.x, top.y));
+    const Pow2 pus = store_scale(allu);
+    const float2 upd = make_float2(fmaxf(topx.x * fac.k, topo.x * fac.q), fmaxf(topx.y * fac.k, topo.y * fac.q));
+    const float2 asc = update_scale(quad_max(upd), tops, sunit, fac.last);
+    const float2 xs = mul2(asc, splat(fac.k)), os = mul2(yd, mul2(asc, splat(fac.q)));
     {
-      const float2 sc = splat(fac.last * asc * sinv);
+      const float2 sc = mul2(mul2(asc, splat(fac.last)), sinv);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) scale_tile(S[nt], sc);
-      scur = asc;
-      sinv = 1.0f / asc;
+      for (int nt = 0; nt < NT; ++nt) scale_rows(S[nt], sc);
+      sinv = make_float2(pow2_inverse(asc.x), pow2_inverse(asc.y));
     }
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t hi[4], lo[4], qh[4], ql[4];
-      split_a(X[2 * kb], X[2 * kb + 1], splat(xs), splat(xs), hi, lo);
-      const float2 y0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb), splat(os));
-      const float2 y1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8), splat(os));
-      split2(mul2(unpack_h2(od[kb][0]), y0), qh[0], ql[0]);
-      split2(mul2(unpack_h2(od[kb][1]), y0), qh[1], ql[1]);
-      split2(mul2(unpack_h2(od[kb][2]), y1), qh[2], ql[2]);
-      split2(mul2(unpack_h2(od[kb][3]), y1), qh[3], ql[3]);
+      split_rows(X[2 * kb], X[2 * kb + 1], xs, hi, lo);
+      const float2 y0 = *reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb);
+      const float2 y1 = *reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8);
+      split2(mul2(unpack_h2(od[kb][0]), mul2(y0, splat(os.x))), qh[0], ql[0]);
+      split2(mul2(unpack_h2(od[kb][1]), mul2(y0, splat(os.y))), qh[1], ql[1]);
+      split2(mul2(unpack_h2(od[kb][2]), mul2(y1, splat(os.x))), qh[2], ql[2]);
+      split2(mul2(unpack_h2(od[kb][3]), mul2(y1, splat(os.y))), qh[3], ql[3]);
 #pragma unroll
       for (int np = 0; np < D / 16; np += 2) {
         uint32_t b0[4], b1[4];
@@ -311,7 +320,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
       uint32_t r[4];
-      single_a(U[2 * np], U[2 * np + 1], splat(pus.s), splat(pus.s), r);
+      single_rows(U[2 * np], U[2 * np + 1], splat(pus.s), r);
       const uint32_t o[4] = {r[0], r[2], r[1], r[3]};
       stsm4t(vw + 16 * np * L::kRow, o);
     }
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<uint4 *>(ur + 16 * i * D) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
-    if (lane == 0) p.w.slice[c * 32 + kSliceR + (dvw >> 4)] = top > 0.0f ? pus.inv : 0.0f;
+    if (lane == 0) p.w.slice[c * 32 + kSliceR + (dvw >> 4)] = slice_unit(allu, pus);
     __syncthreads();
   }
   if (p.S_out != nullptr) {
@@ -328,7 +337,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) So[(8 * nt + 2 * t4 + (e & 1)) * D + dvw + g + (e >> 1) * 8] = S[nt][e] * sinv;
+      for (int e = 0; e < 4; ++e) So[(8 * nt + 2 * t4 + (e & 1)) * D + dvw + g + (e >> 1) * 8] = S[nt][e] * (e < 2 ? sinv.x : sinv.y);
   }
 }
 

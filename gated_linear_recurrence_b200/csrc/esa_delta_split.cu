@@ -40,8 +40,8 @@ struct SplitSmem {
   static constexpr int party = part + 32 * kTileF;              // the output's (forward)
   static constexpr int mid = party + (BWD ? 0 : 32 * kTileF);   // R (dU) of all tokens, then U (du) in `fin`
   static constexpr int fin = mid + 8 * kTileF;
-  static constexpr int top = fin + 8 * kTileF;                  // [4][4] maxima
-  static constexpr int total = top + 64 + 16;
+  static constexpr int top = fin + 8 * kTileF;                  // [4][row][warp] maxima
+  static constexpr int total = top + 4 * 4 * 16 * 4;
 };
 
 __device__ __forceinline__ void put_tile(unsigned char *p, const float (&c)[4], int lane) {
@@ -56,7 +56,18 @@ __device__ __forceinline__ void add_tile(const unsigned char *p, float (&c)[4], 
   set_lo(c, add2(row_lo(c), make_float2(v.x, v.y)));
   set_hi(c, add2(row_hi(c), make_float2(v.z, v.w)));
 }
-__device__ __forceinline__ float top4(const float *t) { return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])); }
+// The largest of each row (value channel): each warp's, from its threads', and that of the four warps.
+__device__ __forceinline__ void put_top(float *t, int w, float2 x, int lane) {
+  x = quad_max(x);
+  if ((lane & 3) == 0) {
+    t[lane + w] = x.x;
+    t[32 + lane + w] = x.y;
+  }
+}
+__device__ __forceinline__ float2 get_top(const float *t, int g) {
+  const float4 a = reinterpret_cast<const float4 *>(t)[g], b = reinterpret_cast<const float4 *>(t)[8 + g];
+  return make_float2(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
+}
 template <int N>
 __device__ __forceinline__ void zero_tiles(float (&c)[N][4]) {
 #pragma unroll
@@ -74,11 +85,11 @@ __device__ __forceinline__ void load_state(float (&S)[D / 32][4], const float *s
     for (int e = 0; e < 4; ++e) S[nt][e] = s ? s[(dk0 + 8 * nt + 2 * t4 + (e & 1)) * D + row0 + g + (e >> 1) * 8] : 0.0f;
 }
 template <int D>
-__device__ __forceinline__ void store_state(const float (&S)[D / 32][4], float f, float *s, int row0, int dk0, int g, int t4) {
+__device__ __forceinline__ void store_state(const float (&S)[D / 32][4], float2 f, float *s, int row0, int dk0, int g, int t4) {
 #pragma unroll
   for (int nt = 0; nt < D / 32; ++nt)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[(dk0 + 8 * nt + 2 * t4 + (e & 1)) * D + row0 + g + (e >> 1) * 8] = S[nt][e] * f;
+    for (int e = 0; e < 4; ++e) s[(dk0 + 8 * nt + 2 * t4 + (e & 1)) * D + row0 + g + (e >> 1) * 8] = S[nt][e] * (e < 2 ? f.x : f.y);
 }
 
 template <typename T, int D, bool KEEP>
@@ -109,18 +120,17 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
   };
 
   float S[NQ][4];
-  float scur = 1.0f, sinv = 1.0f;
+  float2 sinv = splat(1.0f);
   load_state<D>(S, p.S_in ? p.S_in + static_cast<long long>(head) * D * D : nullptr, dvw, w * (D / 4), g, t4);
   fetch(0, 0);
 #pragma unroll 1
   for (int n = 0; n < nc; ++n) {
     const int buf = n & 1;
     {
-      float top = 0.0f;
+      float2 top = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) top = max_tile(S[i], top);
-      top = warp_max(top);
-      if (lane == 0) tops_[w] = top;
+      for (int i = 0; i < NQ; ++i) top = max_rows(S[i], top);
+      put_top(tops_, w, top, lane);
     }
     if (n + 1 < nc) {
       fetch(n + 1, buf ^ 1);
@@ -149,12 +159,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
 
     // 1. partial X = S^T K^T and S^T Q^T
     float Xo[2][4], Yo[2][4];   // this warp's tokens
-    const float tops = top4(tops_);
-    const Pow2 ps = pow2_scale(tops);
-    const float xinv = tops > 0.0f ? ps.inv * sinv : 0.0f;
-    const Pow2 pss = store_scale(tops * sinv);
-    const float sf = pss.s * (ps.inv * sinv);
-    if (KEEP && threadIdx.x == 0) p.w.slice[c * 32 + kSliceS + slice] = tops > 0.0f ? pss.inv : 0.0f;
+    const float2 tops = get_top(tops_, g);
+    const RowPow2 ps = pow2_scale(tops);
+    const float2 sunit = mul2(ps.inv, sinv), xinv = unit_or_zero(tops, sunit);
+    float2 sf;
+    if constexpr (KEEP) {
+      const float all = warp_max(fmaxf(tops.x * sinv.x, tops.y * sinv.y));
+      const Pow2 pss = store_scale(all);
+      sf = mul2(splat(pss.s), sunit);
+      if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceS + slice] = slice_unit(all, pss);
+    }
     {
       float X[8][4], Y[8][4];
       zero_tiles(X);
@@ -162,10 +176,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
 #pragma unroll
       for (int ks = 0; ks < KQ; ++ks) {
         uint32_t hi[4], lo[4];
-        split_a(S[2 * ks], S[2 * ks + 1], splat(ps.s), splat(ps.s), hi, lo);
+        split_rows(S[2 * ks], S[2 * ks + 1], ps.s, hi, lo);
         if constexpr (KEEP) {
           uint32_t x[4] = {hi[0], hi[1], hi[2], hi[3]};
-          if (sf != 1.0f) scale_h2(x, sf);
+          if (sf.x != 1.0f || sf.y != 1.0f) scale_h2(x, sf);
           store_block(p.w.s16 + c * (D * D) + dvw * D + w * (D / 4) + 16 * ks, D, x, lane);
         }
 #pragma unroll
@@ -205,30 +219,31 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
         }
       uint32_t vv[4];
       ldsm4t(vv, st + L::rows + tile_off<32>(16 * w + (lane & 15), lane >> 4));
-      float top = 0.0f;
-      float2 chk = make_float2(0.0f, 0.0f);
+      const float2 xk = mul2(xinv, splat(-fac.k));
+      float2 top = make_float2(0.0f, 0.0f), chk0 = top, chk1 = top;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float2 be = *reinterpret_cast<const float2 *>(tok + kTokBeta * 64 + 16 * w + 8 * i);
-        const float2 tx = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * w + 8 * i), splat(-(xinv * fac.k)));
-        set_lo(Xo[i], fma2(tx, row_lo(Xo[i]), mul2(be, unpack_io<T>(vv[i]))));
-        set_hi(Xo[i], fma2(tx, row_hi(Xo[i]), mul2(be, unpack_io<T>(vv[2 + i]))));
-        chk = fma2(row_lo(Xo[i]), splat(0.0f), fma2(row_hi(Xo[i]), splat(0.0f), chk));
-        top = max_tile(Xo[i], top);
+        const float2 tx = *reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * w + 8 * i);
+        set_lo(Xo[i], fma2(mul2(tx, splat(xk.x)), row_lo(Xo[i]), mul2(be, unpack_io<T>(vv[i]))));
+        set_hi(Xo[i], fma2(mul2(tx, splat(xk.y)), row_hi(Xo[i]), mul2(be, unpack_io<T>(vv[2 + i]))));
+        chk0 = fma2(row_lo(Xo[i]), splat(0.0f), chk0);
+        chk1 = fma2(row_hi(Xo[i]), splat(0.0f), chk1);
+        top = max_rows(Xo[i], top);
         put_tile(smem + L::mid + (2 * w + i) * kTileF, Xo[i], lane);
       }
-      top = warp_max(top);
-      // an entry that is not finite is announced as an infinite maximum
-      if (__any_sync(0xffffffffu, !(chk.x + chk.y == 0.0f))) top = __int_as_float(0x7f800000);
-      if (lane == 0) tops_[4 + w] = top;
+      // an entry that is not finite is announced as its row's infinite maximum
+      if (!(chk0.x + chk0.y == 0.0f)) top.x = __int_as_float(0x7f800000);
+      if (!(chk1.x + chk1.y == 0.0f)) top.y = __int_as_float(0x7f800000);
+      put_top(tops_ + 64, w, top, lane);
     }
     __syncthreads();
     // 2. U = R T^T for this warp's tokens: all of R up to them
-    float topr = top4(tops_ + 4);
-    const bool cut = topr == __int_as_float(0x7f800000) || fac.first < 64.0f;
+    float2 topr = get_top(tops_ + 64, g);
+    const bool cut = __any_sync(0xffffffffu, fmaxf(topr.x, topr.y) == __int_as_float(0x7f800000)) || fac.first < 64.0f;
     int first[2] = {static_cast<int>(fac.first), static_cast<int>(fac.first)};   // first token from which a row is not finite
     if (cut) {
-      topr = 0.0f;
+      topr = make_float2(0.0f, 0.0f);
 #pragma unroll 1
       for (int i = 7; i >= 0; --i) {
         float r[4];
@@ -248,11 +263,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
         get_tile(smem + L::mid + i * kTileF, r, lane);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (8 * i + 2 * t4 + (e & 1) < first[e >> 1]) topr = fmaxf(topr, fabsf(r[e]));
+          if (8 * i + 2 * t4 + (e & 1) >= first[e >> 1]) r[e] = 0.0f;
+        topr = max_rows(r, topr);
       }
-      topr = warp_max(topr);
+      topr = quad_max(topr);
     }
-    const Pow2 pr = pow2_scale(topr);
+    const RowPow2 pr = pow2_scale(topr);
     float Uo[2][4];
     {
       float A[3][2][4];   // the three products of the two terms, summed apart: shorter chains
@@ -272,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
           }
         }
         uint32_t hi[4], lo[4], bh[4], bl[4];
-        split_a(r0, r1, splat(pr.s), splat(pr.s), hi, lo);
+        split_rows(r0, r1, pr.s, hi, lo);
         const uint32_t at = tri0 + (w * (w + 1) / 2 + kb) * 512;
         ldsm4(bh, at + R::th);
         ldsm4(bl, at + R::tl);
@@ -283,47 +299,42 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
           mma_f16(A[2][i], hi, bl[2 * i], bl[2 * i + 1]);
         }
       }
-      const float uf = pr.inv * fac.t;
-      float top = 0.0f, topl = 0.0f;
+      const float2 uf = mul2(pr.inv, splat(fac.t));
+      float2 top = make_float2(0.0f, 0.0f), topl = top;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float2 tl = *reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * w + 8 * i);
-        set_lo(Uo[i], mul2(add2(row_lo(A[0][i]), add2(row_lo(A[1][i]), row_lo(A[2][i]))), splat(uf)));
-        set_hi(Uo[i], mul2(add2(row_hi(A[0][i]), add2(row_hi(A[1][i]), row_hi(A[2][i]))), splat(uf)));
-        top = max_tile(Uo[i], top);
+        set_lo(Uo[i], mul2(add2(row_lo(A[0][i]), add2(row_lo(A[1][i]), row_lo(A[2][i]))), splat(uf.x)));
+        set_hi(Uo[i], mul2(add2(row_hi(A[0][i]), add2(row_hi(A[1][i]), row_hi(A[2][i]))), splat(uf.y)));
+        top = max_rows(Uo[i], top);
         float x[4];
         set_lo(x, mul2(row_lo(Uo[i]), tl));
         set_hi(x, mul2(row_hi(Uo[i]), tl));
-        topl = max_tile(x, topl);
+        topl = max_rows(x, topl);
         put_tile(smem + L::fin + (2 * w + i) * kTileF, Uo[i], lane);
       }
-      top = warp_max(top);
-      topl = warp_max(topl);
-      if (lane == 0) {
-        tops_[8 + w] = top;
-        tops_[12 + w] = topl;
-      }
+      put_top(tops_ + 128, w, top, lane);
+      put_top(tops_ + 192, w, topl, lane);
     }
     __syncthreads();
     // 3. the state's quarter, and the outputs of this warp's tokens
-    const float topu = top4(tops_ + 8);
-    const Pow2 pu = pow2_scale(topu);
-    const float asc = update_scale(top4(tops_ + 12) * fac.k, tops, ps.s * scur, fac.last);
+    const float2 topu = get_top(tops_ + 128, g);
+    const RowPow2 pu = pow2_scale(topu);
+    const float2 asc = update_scale(mul2(get_top(tops_ + 192, g), splat(fac.k)), tops, sunit, fac.last);
     {
-      const float2 sc = splat(fac.last * asc * sinv);
+      const float2 sc = mul2(mul2(asc, splat(fac.last)), sinv);
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) scale_tile(S[i], sc);
-      scur = asc;
-      sinv = 1.0f / asc;
+      for (int i = 0; i < NQ; ++i) scale_rows(S[i], sc);
+      sinv = make_float2(pow2_inverse(asc.x), pow2_inverse(asc.y));
     }
-    const float xq = xinv * fac.q, xs = asc * fac.k;
-    const float uinv = fmaxf(pu.inv, fmaxf(xq * kLeastShare, kLeastUnit) * fac.ps), us = 1.0f / uinv;
-    const float zu = fac.p * uinv, yf = p.s.scale * zu;
-    {
-      const float r = xq * (1.0f / zu);
+    const float2 xs = mul2(asc, splat(fac.k));
+    const OutputUnit ou0 = output_unit(xinv.x * fac.q, pu.inv.x, fac.p, fac.ps), ou1 = output_unit(xinv.y * fac.q, pu.inv.y, fac.p, fac.ps);
+    const float2 us = make_float2(ou0.us, ou1.us), yf = mul2(make_float2(ou0.unit, ou1.unit), splat(p.s.scale));
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        scale_tile(Yo[i], mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * w + 8 * i), splat(r)));
+    for (int i = 0; i < 2; ++i) {
+      const float2 ty = *reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * w + 8 * i);
+      set_lo(Yo[i], mul2(row_lo(Yo[i]), mul2(ty, splat(ou0.r))));
+      set_hi(Yo[i], mul2(row_hi(Yo[i]), mul2(ty, splat(ou1.r))));
     }
     uint32_t own[4];
 #pragma unroll
@@ -332,9 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
       get_tile(smem + L::fin + (2 * kb) * kTileF, u0, lane);
       get_tile(smem + L::fin + (2 * kb + 1) * kTileF, u1, lane);
       uint32_t hi[4], lo[4];
-      const float2 l0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * kb), splat(xs));
-      const float2 l1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * kb + 8), splat(xs));
-      split_a(u0, u1, l0, l1, hi, lo);
+      const float2 l0 = *reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * kb);
+      const float2 l1 = *reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * kb + 8);
+      split_grid(u0, u1, l0, l1, xs, hi, lo);
 #pragma unroll
       for (int j = 0; j < NQ / 2; ++j) {
         uint32_t bk[4];
@@ -346,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
       }
       if (kb <= w) {
         uint32_t uh[4], ul[4], bp[4];
-        if constexpr (kTwo) split_a(u0, u1, splat(us), splat(us), uh, ul);
-        else single_a(u0, u1, splat(us), splat(us), uh);
+        if constexpr (kTwo) split_rows(u0, u1, us, uh, ul);
+        else single_rows(u0, u1, us, uh);
         ldsm4(bp, tri0 + (w * (w + 1) / 2 + kb) * 512 + R::ph);
         mma_f16(Yo[0], uh, bp[0], bp[1]);
         mma_f16(Yo[1], uh, bp[2], bp[3]);
@@ -376,21 +387,22 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
     const uint32_t vw = st + L::rows + tile_off<32>(16 * w + (lane & 15), lane >> 4);
     const unsigned char *vr = sb + L::rows + tile_off<32>(r, lane & 1);
     {   // this warp's 16 rows of the value tile were read before the second barrier
-      const float2 a = mul2(row_lo(Yo[0]), splat(yf)), bb = mul2(row_lo(Yo[1]), splat(yf));
-      const float2 cc = mul2(row_hi(Yo[0]), splat(yf)), d = mul2(row_hi(Yo[1]), splat(yf));
+      const float2 a = mul2(row_lo(Yo[0]), splat(yf.x)), bb = mul2(row_lo(Yo[1]), splat(yf.x));
+      const float2 cc = mul2(row_hi(Yo[0]), splat(yf.y)), d = mul2(row_hi(Yo[1]), splat(yf.y));
       const uint32_t o[4] = {pack_io<T>(a.x, a.y), pack_io<T>(bb.x, bb.y), pack_io<T>(cc.x, cc.y), pack_io<T>(d.x, d.y)};
       stsm4t(vw, o);
       __syncwarp();
       if (r < len) *reinterpret_cast<uint4 *>(y + (row0 + n * kChunk + r) * ldy) = *reinterpret_cast<const uint4 *>(vr);
       if constexpr (KEEP) {
         __syncwarp();
-        const Pow2 pus = store_scale(topu);
-        if (pus.s != us) single_a(Uo[0], Uo[1], splat(pus.s), splat(pus.s), own);
+        const float all = warp_max(fmaxf(topu.x, topu.y));
+        const Pow2 pus = store_scale(all);
+        if (pus.s != us.x || pus.s != us.y) single_rows(Uo[0], Uo[1], splat(pus.s), own);
         const uint32_t u[4] = {own[0], own[2], own[1], own[3]};
         stsm4t(vw, u);
         __syncwarp();
         *reinterpret_cast<uint4 *>(p.w.u16 + (c * 64 + r) * D + dvw + 8 * (lane & 1)) = *reinterpret_cast<const uint4 *>(vr);
-        if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceU + slice] = cut ? __int_as_float(0x7fc00000) : topu > 0.0f ? pus.inv : 0.0f;
+        if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceU + slice] = cut ? __int_as_float(0x7fc00000) : slice_unit(all, pus);
       }
     }
     __syncthreads();
@@ -424,18 +436,18 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
   };
 
   float S[NQ][4];
-  float scur = 1.0f, sinv = 1.0f;
+  float2 sinv = splat(1.0f);
   load_state<D>(S, p.S_in ? p.S_in + static_cast<long long>(head) * D * D : nullptr, dvw, w * (D / 4), g, t4);
+  const float iscale = 1.0f / fabsf(p.s.scale);
   fetch(nc - 1, 0);
 #pragma unroll 1
   for (int it = 0; it < nc; ++it) {
     const int n = nc - 1 - it, buf = it & 1;
     {
-      float top = 0.0f;
+      float2 top = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) top = max_tile(S[i], top);
-      top = warp_max(top);
-      if (lane == 0) tops_[w] = top;
+      for (int i = 0; i < NQ; ++i) top = max_rows(S[i], top);
+      put_top(tops_, w, top, lane);
     }
     if (n > 0) {
       fetch(n - 1, buf ^ 1);
@@ -462,21 +474,22 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
     };
 
     // 1. partial dS^T K^T; dO^T as an A operand (every warp needs all of it)
-    const float tops = top4(tops_);
-    const Pow2 ps = pow2_scale(tops);
-    const float xinv = tops > 0.0f ? ps.inv * sinv : 0.0f;
-    const Pow2 pss = store_scale(tops * sinv);
-    const float sf = pss.s * (ps.inv * sinv);
-    if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceDs + slice] = tops > 0.0f ? pss.inv : 0.0f;
+    const float2 tops = get_top(tops_, g);
+    const RowPow2 ps = pow2_scale(tops);
+    const float2 sunit = mul2(ps.inv, sinv), xinv = unit_or_zero(tops, sunit);
+    const float alls = warp_max(fmaxf(tops.x * sinv.x, tops.y * sinv.y));
+    const Pow2 pss = store_scale(alls);
+    const float2 sf = mul2(splat(pss.s), sunit);
+    if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceDs + slice] = slice_unit(alls, pss);
     {
       float X[8][4];
       zero_tiles(X);
 #pragma unroll
       for (int ks = 0; ks < KQ; ++ks) {
         uint32_t hi[4], lo[4];
-        split_a(S[2 * ks], S[2 * ks + 1], splat(ps.s), splat(ps.s), hi, lo);
+        split_rows(S[2 * ks], S[2 * ks + 1], ps.s, hi, lo);
         uint32_t x[4] = {hi[0], hi[1], hi[2], hi[3]};
-        if (sf != 1.0f) scale_h2(x, sf);
+        if (sf.x != 1.0f || sf.y != 1.0f) scale_h2(x, sf);
         store_block(p.w.ds16 + c * (D * D) + dvw * D + w * (D / 4) + 16 * ks, D, x, lane);
 #pragma unroll
         for (int np = 0; np < 4; np += 2) {
@@ -496,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
 #pragma unroll
       for (int i = 0; i < 8; ++i) put_tile(smem + L::part + (w * 8 + i) * kTileF, X[i], lane);
     }
-    uint32_t od[4][4];
-    float topd = 0.0f;
+    uint32_t od[4][4];   // registers 0 and 2 of a block are row g
+    float2 topd = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       uint32_t r[4];
@@ -506,25 +519,29 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 x = unpack_io<T>(od[kb][e]);
-        topd = fmaxf(fmaxf(topd, fabsf(x.x)), fabsf(x.y));
+        float &t = e & 1 ? topd.y : topd.x;
+        t = fmaxf(fmaxf(t, fabsf(x.x)), fabsf(x.y));
       }
     }
     // the unit of the output gradient's share of dU^T (see kLeastShare); without a share (scale 0) P is left out
     const float zp = p.s.scale * fac.p;
     const bool with = zp != 0.0f;
-    const Pow2 pd = least_unit(pow2_scale(warp_max(topd)), xinv * fac.k, zp);
-    const float zf = with ? zp * pd.inv : 1.0f, yd = p.s.scale * pd.inv;
-    float topo = 0.0f;
+    const float2 xk = mul2(xinv, splat(fac.k));
+    RowPow2 pd = pow2_scale(quad_max(topd));
+    if (with) pd = least_unit(pd, xk, iscale * fac.ps);
+    const float2 zf = with ? mul2(pd.inv, splat(zp)) : splat(1.0f), yd = mul2(pd.inv, splat(p.s.scale));
+    float2 topo = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 x = mul2(unpack_io<T>(od[kb][e]), splat(pd.s));
+        const float2 x = mul2(unpack_io<T>(od[kb][e]), splat(e & 1 ? pd.s.y : pd.s.x));
         od[kb][e] = pack2(x);
-        const float2 z = mul2(x, mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8 * (e >> 1)), splat(yd)));
-        topo = fmaxf(fmaxf(topo, fabsf(z.x)), fabsf(z.y));
+        const float2 z = mul2(x, mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8 * (e >> 1)), splat(e & 1 ? yd.y : yd.x)));
+        float &t = e & 1 ? topo.y : topo.x;
+        t = fmaxf(fmaxf(t, fabsf(z.x)), fabsf(z.y));
       }
-    topo = warp_max(topo);
+    topo = quad_max(topo);
     __syncthreads();
     // dU^T = zf (X r + dO^T P) for this warp's tokens, 16 w ..
     {
@@ -535,8 +552,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
 #pragma unroll
         for (int i = 0; i < 2; ++i) add_tile(smem + L::part + (j * 8 + 2 * w + i) * kTileF, X[i], lane);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        scale_tile(X[i], mul2(*reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * w + 8 * i), splat(xinv * fac.k / zf)));
+      for (int i = 0; i < 2; ++i) {
+        const float2 tl = *reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * w + 8 * i);
+        set_lo(X[i], mul2(row_lo(X[i]), mul2(tl, splat(xk.x / zf.x))));
+        set_hi(X[i], mul2(row_hi(X[i]), mul2(tl, splat(xk.y / zf.y))));
+      }
       if (with) {
         float Z[2][4];
         zero_tiles(Z);
@@ -558,19 +578,18 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
           set_hi(X[i], add2(row_hi(X[i]), row_hi(Z[i])));
         }
       }
-      float top = 0.0f;
+      float2 top = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        top = max_tile(X[i], top);
+        top = max_rows(X[i], top);
         put_tile(smem + L::mid + (2 * w + i) * kTileF, X[i], lane);
       }
-      top = warp_max(top);
-      if (lane == 0) tops_[4 + w] = top;
+      put_top(tops_ + 64, w, top, lane);
     }
     __syncthreads();
     // 2. du^T = dU^T T for this warp's tokens: all of dU from them on
-    const Pow2 pr = pow2_scale(top4(tops_ + 4));
-    const float rf = pr.inv * zf * fac.t;
+    const RowPow2 pr = pow2_scale(get_top(tops_ + 64, g));
+    const float2 rf = mul2(mul2(pr.inv, zf), splat(fac.t));
     float Uo[2][4];
     {
       float A[3][2][4];
@@ -583,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
         get_tile(smem + L::mid + (2 * kb) * kTileF, r0, lane);
         get_tile(smem + L::mid + (2 * kb + 1) * kTileF, r1, lane);
         uint32_t hi[4], lo[4], bh[4], bl[4];
-        split_a(r0, r1, splat(pr.s), splat(pr.s), hi, lo);
+        split_rows(r0, r1, pr.s, hi, lo);
         const uint32_t at = tri0 + kb * (kb + 1) / 2 * 512 + w * 512;
         ldsm4t(bh, at + R::th);
         ldsm4t(bl, at + R::tl);
@@ -594,54 +613,51 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
           mma_f16(A[2][i], hi, bl[2 * i], bl[2 * i + 1]);
         }
       }
-      float top = 0.0f, topx = 0.0f;
+      float2 top = make_float2(0.0f, 0.0f), topx = top;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float2 tx = *reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * w + 8 * i);
-        set_lo(Uo[i], mul2(add2(row_lo(A[0][i]), add2(row_lo(A[1][i]), row_lo(A[2][i]))), splat(rf)));
-        set_hi(Uo[i], mul2(add2(row_hi(A[0][i]), add2(row_hi(A[1][i]), row_hi(A[2][i]))), splat(rf)));
-        top = max_tile(Uo[i], top);
+        set_lo(Uo[i], mul2(add2(row_lo(A[0][i]), add2(row_lo(A[1][i]), row_lo(A[2][i]))), splat(rf.x)));
+        set_hi(Uo[i], mul2(add2(row_hi(A[0][i]), add2(row_hi(A[1][i]), row_hi(A[2][i]))), splat(rf.y)));
+        top = max_rows(Uo[i], top);
         float x[4];
         set_lo(x, mul2(row_lo(Uo[i]), tx));
         set_hi(x, mul2(row_hi(Uo[i]), tx));
-        topx = max_tile(x, topx);
+        topx = max_rows(x, topx);
         put_tile(smem + L::fin + (2 * w + i) * kTileF, Uo[i], lane);
       }
-      top = warp_max(top);
-      topx = warp_max(topx);
-      if (lane == 0) {
-        tops_[8 + w] = top;
-        tops_[12 + w] = topx;
-      }
+      put_top(tops_ + 128, w, top, lane);
+      put_top(tops_ + 192, w, topx, lane);
     }
     __syncthreads();
     // 3. the quarter of dS^T, dv and du of this warp's tokens
-    const float topu = top4(tops_ + 8);
-    const Pow2 pus = store_scale(topu);
-    const float asc = update_scale(fmaxf(top4(tops_ + 12) * fac.k, topo * fac.q), tops, ps.s * scur, fac.last);
+    const float2 topu = get_top(tops_ + 128, g), topx = get_top(tops_ + 192, g);
+    const float allu = warp_max(fmaxf(topu.x, topu.y));
+    const Pow2 pus = store_scale(allu);
+    const float2 upd = make_float2(fmaxf(topx.x * fac.k, topo.x * fac.q), fmaxf(topx.y * fac.k, topo.y * fac.q));
+    const float2 asc = update_scale(upd, tops, sunit, fac.last);
     {
-      const float2 sc = splat(fac.last * asc * sinv);
+      const float2 sc = mul2(mul2(asc, splat(fac.last)), sinv);
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) scale_tile(S[i], sc);
-      scur = asc;
-      sinv = 1.0f / asc;
+      for (int i = 0; i < NQ; ++i) scale_rows(S[i], sc);
+      sinv = make_float2(pow2_inverse(asc.x), pow2_inverse(asc.y));
     }
-    const float os = yd * (asc * fac.q), xs = asc * fac.k;
+    const float2 os = mul2(yd, mul2(asc, splat(fac.q))), xs = mul2(asc, splat(-fac.k));
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       float u0[4], u1[4];
       get_tile(smem + L::fin + (2 * kb) * kTileF, u0, lane);
       get_tile(smem + L::fin + (2 * kb + 1) * kTileF, u1, lane);
       uint32_t hi[4], lo[4], qh[4], ql[4];
-      const float2 x0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * kb), splat(-xs));
-      const float2 x1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * kb + 8), splat(-xs));
-      split_a(u0, u1, x0, x1, hi, lo);
-      const float2 y0 = mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb), splat(os));
-      const float2 y1 = mul2(*reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8), splat(os));
-      split2(mul2(unpack_h2(od[kb][0]), y0), qh[0], ql[0]);
-      split2(mul2(unpack_h2(od[kb][1]), y0), qh[1], ql[1]);
-      split2(mul2(unpack_h2(od[kb][2]), y1), qh[2], ql[2]);
-      split2(mul2(unpack_h2(od[kb][3]), y1), qh[3], ql[3]);
+      const float2 x0 = *reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * kb);
+      const float2 x1 = *reinterpret_cast<const float2 *>(tok + kTokX * 64 + 16 * kb + 8);
+      split_grid(u0, u1, x0, x1, xs, hi, lo);
+      const float2 y0 = *reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb);
+      const float2 y1 = *reinterpret_cast<const float2 *>(tok + kTokY * 64 + 16 * kb + 8);
+      split2(mul2(unpack_h2(od[kb][0]), mul2(y0, splat(os.x))), qh[0], ql[0]);
+      split2(mul2(unpack_h2(od[kb][1]), mul2(y0, splat(os.y))), qh[1], ql[1]);
+      split2(mul2(unpack_h2(od[kb][2]), mul2(y1, splat(os.x))), qh[2], ql[2]);
+      split2(mul2(unpack_h2(od[kb][3]), mul2(y1, splat(os.y))), qh[3], ql[3]);
 #pragma unroll
       for (int j = 0; j < NQ / 2; ++j) {
         uint32_t bk[4], bq[4];
@@ -672,12 +688,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
       if (r < len) *reinterpret_cast<uint4 *>(dv + (row0 + n * kChunk + r) * ldc) = *reinterpret_cast<const uint4 *>(vr);
       __syncwarp();
       uint32_t x[4];
-      single_a(Uo[0], Uo[1], splat(pus.s), splat(pus.s), x);
+      single_rows(Uo[0], Uo[1], splat(pus.s), x);
       const uint32_t u[4] = {x[0], x[2], x[1], x[3]};
       stsm4t(vw, u);
       __syncwarp();
       *reinterpret_cast<uint4 *>(p.w.r16 + (c * 64 + r) * D + dvw + 8 * (lane & 1)) = *reinterpret_cast<const uint4 *>(vr);
-      if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceR + slice] = topu > 0.0f ? pus.inv : 0.0f;
+      if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceR + slice] = slice_unit(allu, pus);
     }
     __syncthreads();
   }

@@ -9,9 +9,9 @@
 // exchange between lanes.
 //
 // A float32 value x is kept as two float16 terms of x s, with s a power of two
-// that brings the largest |x| of its group to [2^5, 2^13): hi = fp16(x s),
+// that brings the largest |x| of its row to [2^5, 2^13): hi = fp16(x s),
 // lo = fp16(x s - hi).  The two carry 22 bits (an absolute error of at most
-// 2^-30 of the group's largest value for its small elements), and a product
+// 2^-30 of the row's largest value for its small elements), and a product
 // with an exact float16 operand is two mma with one accumulator.
 #pragma once
 
@@ -98,12 +98,21 @@ __device__ __forceinline__ Pow2 pow2_scale(float top) {
   return {__uint_as_float(static_cast<uint32_t>(127 - e) << 23), __uint_as_float(static_cast<uint32_t>(127 + e) << 23)};
 }
 
+// 1 / x of a normal power of two.
+__device__ __forceinline__ float pow2_inverse(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
+
 // Scale of a group that another kernel reads as one float16 term: 2^8 for any
 // largest value in [2^-9, 2^7), so that the groups of a tile agree and need not
 // be brought together there; else that of pow2_scale.
 __device__ __forceinline__ Pow2 store_scale(float top) {
   if (top >= 0.001953125f && top < 128.0f) return {256.0f, 0.00390625f};
   return pow2_scale(top);
+}
+
+// What is kept of that scale beside the group: its inverse, 0 for a group of
+// zeros, NaN for one that is not finite.
+__device__ __forceinline__ float slice_unit(float top, Pow2 s) {
+  return top <= 3.4028235e38f ? (top > 0.0f ? s.inv : 0.0f) : __int_as_float(0x7fc00000);
 }
 
 // A sum whose addends have different units (powers of two) is formed in one of
@@ -118,28 +127,76 @@ constexpr float kLeastUnit = 7.52316384526264e-37f;     // 2^-120
 
 // Scale of the state after a chunk: the one that suits its update, whose
 // largest value is `upd` (2^126 below 2^-113, so that updates of 2^-120 keep 22
-// bits), unless that would lift the state, of largest value `top` and scale
-// `own` and decaying by `decay`, by more than 2^36 over its own.
-__device__ __forceinline__ float update_scale(float upd, float top, float own, float decay) {
-  const float s = upd > 0.0f && upd < 9.62964972193618e-35f ? 8.507059173023462e37f : pow2_scale(upd).s;
-  return top > 0.0f ? fminf(s, own * 68719476736.0f * (1.0f / decay)) : s;
+// bits), unless that would lift the state, of largest value `top` and unit
+// `unit` and decaying by `decay`, by more than 2^36 over its own scale.
+__device__ __forceinline__ float update_scale(float upd, float top, float unit, float decay) {
+  const int s = upd > 0.0f && upd < 9.62964972193618e-35f ? 253 : static_cast<int>(__float_as_uint(pow2_scale(upd).s) >> 23);
+  const int most = 127 + 36 + 127 + 127 - static_cast<int>(__float_as_uint(unit) >> 23) - static_cast<int>(__float_as_uint(decay) >> 23);
+  return __uint_as_float(static_cast<uint32_t>(top > 0.0f ? min(s, most) : s) << 23);
+}
+__device__ __forceinline__ float2 update_scale(float2 upd, float2 top, float2 unit, float decay) {
+  return make_float2(update_scale(upd.x, top.x, unit.x, decay), update_scale(upd.y, top.y, unit.y, decay));
 }
 
-// The scale of an output gradient, `own`, such that its product's unit
-// |share| inv is no smaller than kLeastShare allows beside a product of unit
-// `other`; a power of two.  `share` may be zero (own is returned).
-__device__ __forceinline__ Pow2 least_unit(Pow2 own, float other, float share) {
-  const float least = fminf(fmaxf(other * kLeastShare, kLeastUnit) / fabsf(share), 2.5961484292674138e33f);   // 2^111
-  if (!(share != 0.0f && least > own.inv)) return own;
-  const uint32_t up = (__float_as_uint(least) & 0x7f800000u) + 0x00800000u;   // the next power of two
-  return {__uint_as_float(0x7f000000u - up), __uint_as_float(up)};
+// The scale of an output gradient, `own`, such that the unit of its product, its
+// inverse times a factor of inverse `ishare`, is no smaller than kLeastShare
+// allows beside a product of unit `other`; a power of two.
+__device__ __forceinline__ Pow2 least_unit(Pow2 own, float other, float ishare) {
+  const float least = fminf(fmaxf(other * kLeastShare, kLeastUnit) * ishare, 2.5961484292674138e33f);   // 2^111
+  if (!(least > own.inv)) return own;
+  const float inv = __uint_as_float((__float_as_uint(least) & 0x7f800000u) + 0x00800000u);   // the next power of two
+  return {pow2_inverse(inv), inv};
 }
 
-__device__ __forceinline__ void scale_h2(uint32_t (&r)[4], float f) {
-  const __half2 s = __float2half2_rn(f);
+// Y = scale (e^G S^T Q^T + U P^T), formed as unit scale (r e^G (S^T Q^T) + (us U) P^T):
+// `xq` is the unit of S^T Q^T, `uinv` that of U by its own size, `p` that of P
+// (`ps` its inverse).
+struct OutputUnit {
+  float us, unit, r;
+};
+__device__ __forceinline__ OutputUnit output_unit(float xq, float uinv, float p, float ps) {
+  uinv = fmaxf(uinv, fmaxf(xq * kLeastShare, kLeastUnit) * ps);
+  const float unit = p * uinv;
+  return {pow2_inverse(uinv), unit, xq * pow2_inverse(unit)};
+}
+
+// ---- factors of the two rows (g and g + 8) that a thread has of a tile --------
+// The chains' rows are value channels, which do not mix: each has scales of its
+// own, or a large (or infinite) channel would take its neighbours' digits.
+struct RowPow2 {
+  float2 s, inv;
+};
+__device__ __forceinline__ RowPow2 pow2_scale(float2 top) {
+  const Pow2 a = pow2_scale(top.x), b = pow2_scale(top.y);
+  return {make_float2(a.s, b.s), make_float2(a.inv, b.inv)};
+}
+__device__ __forceinline__ RowPow2 least_unit(RowPow2 own, float2 other, float ishare) {
+  const Pow2 a = least_unit(Pow2{own.s.x, own.inv.x}, other.x, ishare), b = least_unit(Pow2{own.s.y, own.inv.y}, other.y, ishare);
+  return {make_float2(a.s, b.s), make_float2(a.inv, b.inv)};
+}
+// A state's unit, zero for a state of zeros (see kLeastShare).
+__device__ __forceinline__ float2 unit_or_zero(float2 top, float2 unit) {
+  return make_float2(top.x > 0.0f ? unit.x : 0.0f, top.y > 0.0f ? unit.y : 0.0f);
+}
+// The largest of a row from the largest of each of the four threads that share it (a NaN is passed over).
+__device__ __forceinline__ float2 quad_max(float2 t) {
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    t.x = fmaxf(t.x, __shfl_xor_sync(0xffffffffu, t.x, o));
+    t.y = fmaxf(t.y, __shfl_xor_sync(0xffffffffu, t.y, o));
+  }
+  return t;
+}
+__device__ __forceinline__ float2 max_rows(const float (&c)[4], float2 t) {
+  return make_float2(fmaxf(fmaxf(t.x, fabsf(c[0])), fabsf(c[1])), fmaxf(fmaxf(t.y, fabsf(c[2])), fabsf(c[3])));
+}
+
+// An A operand's rows times f (registers 0 and 2 hold row g).
+__device__ __forceinline__ void scale_h2(uint32_t (&r)[4], float2 f) {
+  const __half2 s[2] = {__float2half2_rn(f.x), __float2half2_rn(f.y)};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&r[i]), s);
+    const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&r[i]), s[i & 1]);
     r[i] = *reinterpret_cast<const uint32_t *>(&x);
   }
 }
@@ -191,9 +248,14 @@ __device__ __forceinline__ float max_tile(const float (&c)[4], float top) {
   return fmaxf(fmaxf(top, fabsf(c[2])), fabsf(c[3]));
 }
 
+__device__ __forceinline__ void scale_rows(float (&c)[4], float2 s) {
+  set_lo(c, mul2(row_lo(c), splat(s.x)));
+  set_hi(c, mul2(row_hi(c), splat(s.y)));
+}
+
 // A operand (hi and lo terms, or hi alone) of columns 16 k .. 16 k + 15 from
 // the accumulators of tiles 2 k and 2 k + 1, whose columns are multiplied by
-// s0 and s1 first.
+// s0 and s1 first, or whose rows are by s, or both.
 __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], float2 s0, float2 s1,
                                         uint32_t (&hi)[4], uint32_t (&lo)[4]) {
   split2(mul2(row_lo(c0), s0), hi[0], lo[0]);
@@ -202,12 +264,25 @@ __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[
   split2(mul2(row_hi(c1), s1), hi[3], lo[3]);
 }
 __device__ __forceinline__ uint32_t pack2(float2 x) { return pack_h2(x.x, x.y); }
-__device__ __forceinline__ void single_a(const float (&c0)[4], const float (&c1)[4], float2 s0, float2 s1,
-                                         uint32_t (&hi)[4]) {
-  hi[0] = pack2(mul2(row_lo(c0), s0));
-  hi[1] = pack2(mul2(row_hi(c0), s0));
-  hi[2] = pack2(mul2(row_lo(c1), s1));
-  hi[3] = pack2(mul2(row_hi(c1), s1));
+__device__ __forceinline__ void split_rows(const float (&c0)[4], const float (&c1)[4], float2 s, uint32_t (&hi)[4],
+                                           uint32_t (&lo)[4]) {
+  split2(mul2(row_lo(c0), splat(s.x)), hi[0], lo[0]);
+  split2(mul2(row_hi(c0), splat(s.y)), hi[1], lo[1]);
+  split2(mul2(row_lo(c1), splat(s.x)), hi[2], lo[2]);
+  split2(mul2(row_hi(c1), splat(s.y)), hi[3], lo[3]);
+}
+__device__ __forceinline__ void split_grid(const float (&c0)[4], const float (&c1)[4], float2 s0, float2 s1, float2 s,
+                                           uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  split2(mul2(row_lo(c0), mul2(s0, splat(s.x))), hi[0], lo[0]);
+  split2(mul2(row_hi(c0), mul2(s0, splat(s.y))), hi[1], lo[1]);
+  split2(mul2(row_lo(c1), mul2(s1, splat(s.x))), hi[2], lo[2]);
+  split2(mul2(row_hi(c1), mul2(s1, splat(s.y))), hi[3], lo[3]);
+}
+__device__ __forceinline__ void single_rows(const float (&c0)[4], const float (&c1)[4], float2 s, uint32_t (&hi)[4]) {
+  hi[0] = pack2(mul2(row_lo(c0), splat(s.x)));
+  hi[1] = pack2(mul2(row_hi(c0), splat(s.y)));
+  hi[2] = pack2(mul2(row_lo(c1), splat(s.x)));
+  hi[3] = pack2(mul2(row_hi(c1), splat(s.y)));
 }
 
 // A lane's offsets for ldmatrix.x4 of 16 x 16 blocks of a tile of RB-byte

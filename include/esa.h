@@ -392,8 +392,11 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
  *     du = dS^T k,  dv = beta du,  dk = dS u - alpha beta S_{t-1} du,
  *     dq = scale S_t dy,  db = (du.u)(1 - beta),
  *     da = (<dS, S_t> - beta v.du)(1 - alpha),  dS <- alpha (dS - beta k du^T).
- * An entry of dy or dS_final that is not finite makes the gradients of its
- * head NaN for all earlier tokens, and for later ones of its chunk of 64.
+ * Value channels do not mix in dv and dS_init, whatever their sizes; dq, dk, da
+ * and db are sums over them.  An entry of dy or dS_final that is not finite
+ * makes dv and dS_init of its value channel NaN, and dk, da, db of its head (dy:
+ * dq of its token as well), for all earlier tokens, and may for later ones of
+ * its chunk of 64; one of v, k or S_init that of its chunk and later ones.
  */
 int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, long long ld_v, const void *a,
                   const void *b, long long ld_g, const void *dy, const float *dS_final, void *dq, void *dk, void *dv,

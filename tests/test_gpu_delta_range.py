@@ -6,7 +6,7 @@ outputs three float16 roundings of intermediates.
 import pytest
 import torch
 
-from tests._delta_reference import delta_reference
+from tests._delta_reference import PER_TOKEN, assert_within, delta_reference
 from tests.test_gpu_delta import check, draw, ins, run
 
 pytestmark = pytest.mark.gpu
@@ -62,3 +62,51 @@ def test_tiny_values(cuda_device, which, D, H):
     x[which] = (x[which].float() * 1e-30).to(x[which].dtype)
     xs, got, ref = two_heads(x, None, None, run(x, None, None, D ** -0.5))
     check(xs, got, ref, T, D, half_p=HALF_P)
+
+
+@pytest.mark.parametrize("D,H", SPREADS)
+@pytest.mark.parametrize("dt,which", [("bf16", "v"), ("bf16", "dy"), ("f16", "v"), ("f16", "dy"), ("bf16", "S")])
+def test_value_channels_do_not_mix(cuda_device, dt, which, D, H):
+    """One value channel 10^9 (float16: 10^7) times its neighbours: each channel is held to its own largest value."""
+    x, S0, dS = draw(dt, 1, T, H, D, seed=5)
+    factor = 1e7 if dt == "f16" else 1e9
+    if which == "S":
+        S0[..., 5] *= factor
+        dS[..., 5] *= factor
+    else:
+        S0 = dS = None
+        x[which] = (x[which].float() * 1e-3).to(x[which].dtype)
+        x[which][..., 5] *= factor
+    xs, got, ref = two_heads(x, S0, dS, run(x, S0, dS, D ** -0.5))
+    a, n = PER_TOKEN * T, PER_TOKEN * T ** 0.5
+    for name, k in (("y", 1), ("S", 1), ("dv", 2)) + ((("dS0", 2),) if which == "S" else ()):
+        extra = HALF_P if got[name].dtype != torch.float32 else 0.0
+        for c in (0, 4, 5, 6, 15, 16, D - 1):
+            assert_within(f"{name}[..., {c}]", got[name][..., c], ref[name][..., c], k * a + extra, k * n + extra)
+
+
+@pytest.mark.parametrize("D,H", SPREADS)
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_states_that_are_not_finite(cuda_device, value, D, H):
+    """An entry of S_init reaches y and S_final of its value channel alone, one of dS_final dv of its channel alone; the
+    gradients that sum over the channels are lost in its head alone."""
+    x, S0, dS = draw("bf16", 1, T, H, D, seed=6)
+    clean = run(x, S0, dS, D ** -0.5)
+    own = torch.zeros(1, 1, H, D, dtype=torch.bool, device="cuda")
+    own[0, 0, 1, 5] = True
+    S1, dS1 = S0.clone(), dS.clone()
+    S1[0, 1, 3, 5] = value
+    dS1[0, 1, 3, 5] = value
+    bad = run(x, S1, dS, D ** -0.5)
+    y_own, S_own = own.expand_as(clean["y"]), own.transpose(1, 2).expand_as(clean["S"])
+    assert torch.equal(bad["y"][~y_own], clean["y"][~y_own]) and not torch.isfinite(bad["y"][y_own]).any()
+    assert torch.equal(bad["S"][~S_own], clean["S"][~S_own]) and not torch.isfinite(bad["S"][S_own]).any()
+    for n in ("dq", "dk", "da"):
+        assert not torch.isfinite(bad[n][0, :64, 1]).any(), n
+        assert torch.equal(bad[n][:, :, 0], clean[n][:, :, 0]), n
+    bad = run(x, S0, dS1, D ** -0.5)
+    assert torch.equal(bad["dv"][~y_own], clean["dv"][~y_own]) and not torch.isfinite(bad["dv"][y_own]).any()
+    assert torch.equal(bad["dS0"][~S_own], clean["dS0"][~S_own]) and not torch.isfinite(bad["dS0"][S_own]).any()
+    for n in ("dk", "da", "db"):
+        assert not torch.isfinite(bad[n][0, :192, 1]).any(), n
+        assert torch.equal(bad[n][:, :, 0], clean[n][:, :, 0]), n
