@@ -8,13 +8,19 @@
 //   dQ = scale e^G dO S^T + dP K,
 //   dK = e^{G_last - G} U dS^T - beta e^G du S^T + dP^T Q + N K + N^T K,
 //   db = (du.u)(1 - beta),
-//   da_i = (1 - alpha_i)(c + sum_{s >= i} (q_s.dq_s - beta_s v_s.du_s)),
-//   c = <dS, S leaving> = e^{G_last} <dS, S> + sum_j k_j.(e^{G_last - G_j} u_j dS^T).
-// The triangular system gives beta_i v_i = u_i + sum_j M_ij u_j + beta_i e^{Gi} S^T k_i,
-// so beta_i v_i.du_i = u_i.du_i - k_i.(N K - beta e^G du S^T)_i comes from terms
-// that are at hand and v is not read.  <dS, S> is the diagonal of dS S^T, 16
-// rows at a time, on the tensor cores too.  Sums of the gate's gradient start
-// anew in every chunk, from c.
+//   da_i = (1 - alpha_i) (sum_{j < i <= s} W_sj + sum_{s >= i} A_s + sum_{j < i} B_j + e^{G_last} <dS, S>),
+//   W_sj = dP_sj q_s.k_j + N_sj k_s.k_j,   B_j = k_j.(e^{G_last - G_j} u_j dS^T),
+//   A_s = q_s.(scale e^G dO S^T)_s - k_s.(beta e^G du S^T)_s.
+// da's sum is over every decay factor that token i has a part in: between two
+// tokens, from the state to a later token, from an earlier token or the state
+// to the chunk's end.  Each has the factor alpha_i, so that a gate that forgets
+// keeps the digits of its gradient.  (The same sum as the differences of
+// q.dq - beta v.du of later tokens cancels to alpha of its terms: with float16
+// operands da was off by 0.3% at logits near 0, 8% at -4, 50% at -6.)  The
+// rectangles of W are summed in blocks of 16 by shuffles: a diagonal block its
+// 16 rectangles, another its rows from each token on and its columns up to
+// each.  <dS, S> is the diagonal of dS S^T, 16 rows at a time, on the tensor
+// cores too.
 //
 // These are outputs in 16 bits: S, dS, U, du, dP and N are operands in one
 // float16 term each (2^-12 of a value on average, against 2^-9 for a bfloat16
@@ -43,17 +49,9 @@ struct GradShape {
   static constexpr int hdr = ChunkRecord<D>::k + 512 + 128;   // per-token factors, running sums, slice scales
   static constexpr int k = 0, q = row, s = 2 * row, ds = s + mat, dp = ds + mat, n = dp + 8192, buf = n + 8192,
                        u = 0, r = row, o = 2 * row, h = 3 * row, stage = 3 * row + hdr, vec = buf + 2 * stage,
-                       total = vec + (64 + 64 + 3 * CW * 64 + 64) * 4;
+                       total = vec + (64 + 64 + 2 * CW * 64 + 9 * 64 + 64) * 4;
 };
 
-__device__ __forceinline__ void scale_unit(unsigned char *p, float f) {
-  uint4 v = *reinterpret_cast<uint4 *>(p);
-  __half2 *h = reinterpret_cast<__half2 *>(&v);
-  const __half2 s = __float2half2_rn(f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __hmul2(h[i], s);
-  *reinterpret_cast<uint4 *>(p) = v;
-}
 __device__ __forceinline__ void scale_frag(uint32_t (&a)[4], float f) {
   const __half2 s = __float2half2_rn(f);
 #pragma unroll
@@ -76,8 +74,78 @@ __device__ __forceinline__ void store_pair(T *o, long long ld, int col, const fl
   if (on1) *reinterpret_cast<uint2 *>(o + 8 * ld + col) = odd ? make_uint2(x1, b1) : make_uint2(a1, x1);
 }
 
+// Sum over a row's four threads; over the eight rows of a half of a block, of
+// this row and those behind it.
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+__device__ __forceinline__ float rows_from(float x, int g) {
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const float y = __shfl_down_sync(0xffffffffu, x, 4 * o);
+    if (g + o < 8) x += y;
+  }
+  return x;
+}
+
+// A 16 x 16 block of W (rows s, columns j), as an accumulator pair.  On the
+// diagonal: diag[r] = sum of s >= r, j < r.  Else rows[r] = sum of s >= r over
+// all j, cols[r] = sum of j < r over all s.
+__device__ __forceinline__ void diagonal_sums(const float (&w)[2][4], float *diag, int lane) {
+  const int g = lane >> 2, t4 = lane & 3;
+  float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int col = 8 * nt + 2 * t4 + e;
+      const float b = rows_from(w[nt][e + 2], g), a = rows_from(w[nt][e], g) + __shfl_sync(0xffffffffu, b, t4);
+      if (col < g) lo += a;
+      if (col < g + 8) hi += b;
+    }
+  lo = quad_sum(lo);
+  hi = quad_sum(hi);
+  if (t4 == 0) {
+    diag[g] = lo;
+    diag[g + 8] = hi;
+  }
+}
+__device__ __forceinline__ void edge_sums(const float (&w)[2][4], float *rows, float *cols, int lane) {
+  const int g = lane >> 2, t4 = lane & 3;
+  const float hi = rows_from(quad_sum((w[0][2] + w[0][3]) + (w[1][2] + w[1][3])), g);
+  const float lo = rows_from(quad_sum((w[0][0] + w[0][1]) + (w[1][0] + w[1][1])), g) + __shfl_sync(0xffffffffu, hi, t4);
+  if (t4 == 0) {
+    rows[g] = lo;
+    rows[g + 8] = hi;
+  }
+  float before = 0.0f;   // columns of the first half, then of both
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt) {
+    float c0 = w[nt][0] + w[nt][2], c1 = w[nt][1] + w[nt][3];
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      c0 += __shfl_xor_sync(0xffffffffu, c0, o);
+      c1 += __shfl_xor_sync(0xffffffffu, c1, o);
+    }
+    float to = c0 + c1;   // up to this pair
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const float y = __shfl_up_sync(0xffffffffu, to, o, 4);
+      if (t4 >= o) to += y;
+    }
+    float from = __shfl_up_sync(0xffffffffu, to, 1, 4);
+    from = before + (t4 > 0 ? from : 0.0f);
+    if (g == 0) {
+      cols[8 * nt + 2 * t4] = from;
+      cols[8 * nt + 2 * t4 + 1] = from + c0;
+    }
+    before += __shfl_sync(0xffffffffu, to, 3, 4);
+  }
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(ChunkArgs p, int chunks) {
+__global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta_grad_kernel(ChunkArgs p, int chunks) {
   using L = GradShape<D>;
   using R = ChunkRecord<D>;
   constexpr int kThreads = L::threads, CW = L::CW;
@@ -86,7 +154,9 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
   constexpr int KS = D / 16;
   extern __shared__ __align__(128) unsigned char smem[];
   float *vec = reinterpret_cast<float *>(smem + L::vec);
-  float *oinv = vec, *udu = vec + 64, *qdq = vec + 128, *wk = qdq + CW * 64, *zk = wk + CW * 64, *red = zk + CW * 64;
+  // per token: scale of dO, u.du, A, B; rows[4][64], cols[4][64], diag[64] of W's blocks; maxima and <dS, S>
+  float *oinv = vec, *udu = vec + 64, *as = vec + 128, *bs = as + CW * 64, *wrows = bs + CW * 64, *wcols = wrows + 256,
+        *wdiag = wcols + 256, *red = wdiag + 64;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int m = warp & 3, cw = warp >> 2;
   const long long ldc = static_cast<long long>(p.s.H) * D;
@@ -208,18 +278,8 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
       sinv = __shfl_sync(0xffffffffu, t, kSliceS);
       dsinv = __shfl_sync(0xffffffffu, t, kSliceDs);
     }
-    float ktop, qtop;
-    bool flatk;
-    {
-      const float k0 = tok[kTokK * 64 + lane], k1 = tok[kTokK * 64 + 32 + lane];
-      const float q0 = tok[kTokQ * 64 + lane], q1 = tok[kTokQ * 64 + 32 + lane];
-      ktop = warp_max(fmaxf(k0, k1));
-      qtop = warp_max(fmaxf(q0, q1));
-      if (!(ktop > 0.0f)) ktop = 1.0f;
-      if (!(qtop > 0.0f)) qtop = 1.0f;
-      flatk = __all_sync(0xffffffffu, (k0 == ktop || k0 == 0.0f) && (k1 == ktop || k1 == 0.0f) &&
-                                          (q0 == qtop || q0 == 0.0f) && (q1 == qtop || q1 == 0.0f));
-    }
+    const float *fac = reinterpret_cast<const float *>(sb + L::h + R::fac);
+    const float last = fac[kFacLast], kinv = fac[kFacK], qinv = fac[kFacQ];
     __syncthreads();
 
     const float be0 = tok[kTokBeta * 64 + i0], be1 = tok[kTokBeta * 64 + i0 + 8];
@@ -285,7 +345,40 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
         red[warp] = topp;
         red[32 + warp] = topn;
       }
+      sweep::cp_async_wait<1>();   // S, dS, K and Q
       __syncthreads();
+#pragma unroll
+      for (int np = 0; np < NPA; ++np) {   // W, from Q K^T and K K^T
+        const int blk = NPA * cw + np;
+        if (blk > m) continue;
+        float w[2][4], z[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[i][e] = z[i][e] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t aq[4], ak[4], bk[4];
+          ldsm4(aq, ofd.at(0, ks) + L::q + 16 * m * D * 2);
+          ldsm4(ak, ofd.at(0, ks) + L::k + 16 * m * D * 2);
+          ldsm4(bk, ofb.at(np, ks) + L::k + 16 * NPA * cw * D * 2);
+          mma_f16(w[0], aq, bk[0], bk[1]);
+          mma_f16(w[1], aq, bk[2], bk[3]);
+          mma_f16(z[0], ak, bk[0], bk[1]);
+          mma_f16(z[1], ak, bk[2], bk[3]);
+        }
+        const float qk = qinv * kinv, kk = kinv * kinv;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p = w[i][e] * qk * P[2 * np + i][e];
+            w[i][e] = fmaf(z[i][e] * kk, N[2 * np + i][e], p);
+            if (blk == m && 8 * i + 2 * t4 + (e & 1) >= g + (e >> 1) * 8) w[i][e] = 0.0f;
+          }
+        if (blk == m) diagonal_sums(w, wdiag + 16 * m, lane);
+        else edge_sums(w, wrows + 64 * blk + 16 * m, wcols + 64 * m + 16 * blk, lane);
+      }
       topp = warp_max(red[lane & (kThreads / 32 - 1)]);
       topn = warp_max(red[32 + (lane & (kThreads / 32 - 1))]);
       const Pow2 pp = pow2_scale(topp), pn = pow2_scale(topn);
@@ -294,7 +387,7 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
       // kLeastShare).  Fragments of a smaller unit are brought to it as they are read.
       const float omax = warp_max(fmaxf(oinv[lane], oinv[32 + lane]));
       const float bmax = warp_max(fmaxf(tok[kTokBeta * 64 + lane], tok[kTokBeta * 64 + 32 + lane]));
-      const float pk = topp > 0.0f ? pp.inv * ktop : 0.0f, pq = topp > 0.0f ? pp.inv * qtop : 0.0f, nk = topn > 0.0f ? pn.inv * ktop : 0.0f;
+      const float pk = topp > 0.0f ? pp.inv * kinv : 0.0f, pq = topp > 0.0f ? pp.inv * qinv : 0.0f, nk = topn > 0.0f ? pn.inv * kinv : 0.0f;
       uq = fmaxf(fmaxf(pk, kLeastUnit), fabsf(p.s.scale) * omax * sunit * (1024.0f * kLeastShare));
       uk = fmaxf(fmaxf(fmaxf(nk, pq), kLeastUnit), rinv * bmax * sunit * (1024.0f * kLeastShare));
       fpk = pk / uq;
@@ -309,7 +402,6 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
           *reinterpret_cast<uint32_t *>(smem + L::n + o) = pack_h2(N[nt][e] * pn.s, N[nt][e + 1] * pn.s);
         }
     }
-    sweep::cp_async_wait<2>();   // S and dS
     __syncthreads();
 
     float Q[NH][4], K[NH][4], X[NH][4];
@@ -375,17 +467,6 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
     }
     __syncthreads();             // S and dS have been used
     fetch_states(next);
-    sweep::cp_async_wait<2>();   // K and Q
-    __syncthreads();
-    if (!flatk) {                // one power of two for all rows
-      constexpr int U = D / 8;
-      for (int i = tid; i < 64 * U; i += kThreads) {
-        const uint32_t o = tile_off<D * 2>(i / U, i % U);
-        scale_unit(smem + L::k + o, tok[kTokK * 64 + i / U] / ktop);
-        scale_unit(smem + L::q + o, tok[kTokQ * 64 + i / U] / qtop);
-      }
-      __syncthreads();
-    }
     {   // the sums so far, in the units of what joins them
       const float e0 = expf(G[i0] + Gl[i0]), e1 = expf(G[i0 + 8] + Gl[i0 + 8]);
       const float fs = p.s.scale * sinv, fk = -rinv * sinv, iq = 1.0f / uq, ik = 1.0f / uk;
@@ -397,6 +478,37 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
         set_hi(Q[i], mul2(row_hi(Q[i]), splat(q1)));
         set_lo(K[i], mul2(row_lo(K[i]), splat(k0)));
         set_hi(K[i], mul2(row_hi(K[i]), splat(k1)));
+      }
+    }
+    {   // A and B: dots of the states' share with the key and the query
+      const float l0 = expf((G[63] - G[i0]) + (Gl[63] - Gl[i0])) * uinv * dsinv;
+      const float l1 = expf((G[63] - G[i0 + 8]) + (Gl[63] - Gl[i0 + 8])) * uinv * dsinv;
+      float2 z0 = make_float2(0, 0), z1 = z0, w0 = z0, w1 = z0, y0 = z0, y1 = z0;
+#pragma unroll
+      for (int i = 0; i < NH; ++i) {
+        const uint32_t o = tile_off<D * 2>(i0, cw * NH + i) + 4 * t4;
+        const float2 k0 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::k + o));
+        const float2 k1 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::k + o + 8 * D * 2));
+        const float2 q0 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::q + o));
+        const float2 q1 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::q + o + 8 * D * 2));
+        z0 = fma2(row_lo(K[i]), k0, z0);
+        z1 = fma2(row_hi(K[i]), k1, z1);
+        w0 = fma2(row_lo(X[i]), k0, w0);
+        w1 = fma2(row_hi(X[i]), k1, w1);
+        y0 = fma2(row_lo(Q[i]), q0, y0);
+        y1 = fma2(row_hi(Q[i]), q1, y1);
+        set_lo(X[i], mul2(row_lo(X[i]), splat(l0)));
+        set_hi(X[i], mul2(row_hi(X[i]), splat(l1)));
+      }
+      float r[6] = {z0.x + z0.y, z1.x + z1.y, w0.x + w0.y, w1.x + w1.y, y0.x + y0.y, y1.x + y1.y};
+#pragma unroll
+      for (int i = 0; i < 6; ++i) r[i] = quad_sum(r[i]);
+      if (t4 == 0) {
+        const float qu = uq * qinv, ku = uk * kinv;
+        as[cw * 64 + i0] = fmaf(r[4], qu, r[0] * ku);
+        as[cw * 64 + i0 + 8] = fmaf(r[5], qu, r[1] * ku);
+        bs[cw * 64 + i0] = r[2] * (l0 * kinv);
+        bs[cw * 64 + i0 + 8] = r[3] * (l1 * kinv);
       }
     }
     // Q += dP K, K += N K
@@ -422,43 +534,8 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
     T *dq = static_cast<T *>(p.dq) + (row + i0) * ldc + h * D + col0;
     T *dk = static_cast<T *>(p.dk) + (row + i0) * ldc + h * D + col0;
     const bool on0 = i0 < len, on1 = i0 + 8 < len;
-    {   // dots with the key and the query
-      const float l0 = expf((G[63] - G[i0]) + (Gl[63] - Gl[i0])) * uinv * dsinv;
-      const float l1 = expf((G[63] - G[i0 + 8]) + (Gl[63] - Gl[i0 + 8])) * uinv * dsinv;
-      float2 z0 = make_float2(0, 0), z1 = z0, w0 = z0, w1 = z0, y0 = z0, y1 = z0;
 #pragma unroll
-      for (int i = 0; i < NH; ++i) {
-        const uint32_t o = tile_off<D * 2>(i0, cw * NH + i) + 4 * t4;
-        const float2 k0 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::k + o));
-        const float2 k1 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::k + o + 8 * D * 2));
-        const float2 q0 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::q + o));
-        const float2 q1 = unpack_h2(*reinterpret_cast<const uint32_t *>(smem + L::q + o + 8 * D * 2));
-        z0 = fma2(row_lo(K[i]), k0, z0);
-        z1 = fma2(row_hi(K[i]), k1, z1);
-        w0 = fma2(row_lo(X[i]), k0, w0);
-        w1 = fma2(row_hi(X[i]), k1, w1);
-        y0 = fma2(row_lo(Q[i]), q0, y0);
-        y1 = fma2(row_hi(Q[i]), q1, y1);
-        set_lo(X[i], mul2(row_lo(X[i]), splat(l0)));
-        set_hi(X[i], mul2(row_hi(X[i]), splat(l1)));
-      }
-#pragma unroll
-      for (int i = 0; i < NH; i += 2) store_pair<T>(dq, ldc, 8 * i, Q[i], Q[i + 1], uq, on0, on1, lane);
-      float r[6] = {z0.x + z0.y, z1.x + z1.y, w0.x + w0.y, w1.x + w1.y, y0.x + y0.y, y1.x + y1.y};
-#pragma unroll
-      for (int i = 0; i < 6; ++i) {
-        r[i] += __shfl_xor_sync(0xffffffffu, r[i], 1);
-        r[i] += __shfl_xor_sync(0xffffffffu, r[i], 2);
-      }
-      if (t4 == 0) {
-        zk[cw * 64 + i0] = r[0] * (uk * ktop);
-        zk[cw * 64 + i0 + 8] = r[1] * (uk * ktop);
-        wk[cw * 64 + i0] = r[2] * (l0 * ktop);
-        wk[cw * 64 + i0 + 8] = r[3] * (l1 * ktop);
-        qdq[cw * 64 + i0] = r[4] * (uq * qtop);
-        qdq[cw * 64 + i0 + 8] = r[5] * (uq * qtop);
-      }
-    }
+    for (int i = 0; i < NH; i += 2) store_pair<T>(dq, ldc, 8 * i, Q[i], Q[i + 1], uq, on0, on1, lane);
     // K += N^T K + dP^T Q
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
@@ -490,37 +567,48 @@ __global__ void __launch_bounds__(GradShape<D>::threads) delta_grad_kernel(Chunk
     for (int i = 0; i < NH; i += 2) store_pair<T>(dk, ldc, 8 * i, K[i], K[i + 1], 1.0f, on0, on1, lane);
     __syncthreads();   // K, Q, dP, N have been used, the dots are written
     fetch_keys(next);
-    if (warp == 0) {   // the gates' gradients: two tokens a lane, later tokens first
-      float in = lane < KS ? red[16 + lane] : 0.0f, w = 0.0f, gain[2];
+    if (warp == 0) {   // the gates' gradients, two tokens a lane
+      float A[2], B[2], F[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int i = 2 * lane + e;
-        float x = -udu[i];
+        const int i = 2 * lane + e, blk = i >> 4;
+        A[e] = B[e] = 0.0f;
 #pragma unroll
         for (int j = 0; j < CW; ++j) {
-          w += wk[j * 64 + i];
-          x += qdq[j * 64 + i] + zk[j * 64 + i];
+          A[e] += as[j * 64 + i];
+          B[e] += bs[j * 64 + i];
         }
-        gain[e] = x;
+        F[e] = wdiag[i];   // the rectangle of W: the diagonal block's, the block row's, the block column's, whole blocks
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (j < blk) F[e] += wrows[j * 64 + i];
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+          if (j > blk) F[e] += wcols[j * 64 + i];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int l = 2; l < 4; ++l)
+            if (j < blk && blk < l) F[e] += wrows[j * 64 + 16 * l];
       }
-      const float last = *reinterpret_cast<const float *>(sb + L::h + R::fac);
-      const float cc = head_sum<32>(fmaf(last * sinv * dsinv, in, w));
-      const float own = gain[0] + gain[1];
-      float sum = own;
+      const float cc = last * sinv * dsinv * head_sum<32>(lane < KS ? red[16 + lane] : 0.0f);
+      float later = A[0] + A[1], earlier = B[0] + B[1];   // over this lane's tokens and those behind (before) them
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_down_sync(0xffffffffu, sum, o);
-        if (lane + o < 32) sum += y;
+        const float y = __shfl_down_sync(0xffffffffu, later, o), z = __shfl_up_sync(0xffffffffu, earlier, o);
+        if (lane + o < 32) later += y;
+        if (lane >= o) earlier += z;
       }
-      const float after = cc + (sum - own);
+      const float behind = __shfl_down_sync(0xffffffffu, later, 1), before = __shfl_up_sync(0xffffffffu, earlier, 1);
+      const float b0 = lane > 0 ? before : 0.0f, a1 = (lane < 31 ? behind : 0.0f) + A[1];
+      const float dl[2] = {F[0] + (later + b0 + cc), F[1] + (a1 + (b0 + B[0]) + cc)};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
         if (i < len) {
           const float a = fmaxf(sweep::widen(la[e]), -80.0f);
           const float bb = fmaxf(sweep::widen(lb[e]), -80.0f);
-          const float dl = after + gain[1] + (e == 0 ? gain[0] : 0.0f);
-          static_cast<T *>(p.da)[(row + i) * p.s.H + h] = sweep::narrow<T>(dl / (1.0f + expf(a)));
+          static_cast<T *>(p.da)[(row + i) * p.s.H + h] = sweep::narrow<T>(dl[e] / (1.0f + expf(a)));
           static_cast<T *>(p.db)[(row + i) * p.s.H + h] = sweep::narrow<T>(udu[i] / (1.0f + expf(bb)));
         }
       }

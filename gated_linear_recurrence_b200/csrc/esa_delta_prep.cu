@@ -164,8 +164,6 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
     tok[kTokX * 64 + i] = flag & 1 ? 0.0f : be * into;
     tok[kTokL * 64 + i] = flag & 1 ? 0.0f : out;
     tok[kTokY * 64 + i] = flag & 2 ? nan : into;
-    tok[kTokK * 64 + i] = flag & 1 ? 0.0f : sk.inv;
-    tok[kTokQ * 64 + i] = flag & 2 ? 0.0f : sq.inv;
   }
   // K K^T (warps 0-3) and Q K^T (warps 4-7): 16 rows a warp, tiles on and below the diagonal
   float acc[8][4];
