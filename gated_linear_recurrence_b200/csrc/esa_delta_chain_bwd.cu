@@ -13,6 +13,9 @@
 // second kernel (esa_delta_grad.cu) in float16, one power of two per 16
 // channels.
 //
+// A key or query that is not finite makes du of its chunk NaN, and with it all
+// that the chunk adds to dS.
+//
 // 484 mma a chunk and warp at D = 128, bound as the forward chain is.
 #include <type_traits>
 
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
       }
     }
     // du itself, -beta e^G du into X; the largest of that and of scale e^G dO
-    const float2 rf = mul2(mul2(pr.inv, zf), splat(fac.t));
+    const float2 rf = mul2(mul2(pr.inv, zf), splat(fac.tb));
     top = make_float2(0.0f, 0.0f);
     float2 topx = top, topo = top;
 #pragma unroll

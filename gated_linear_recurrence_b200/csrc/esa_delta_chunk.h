@@ -38,10 +38,11 @@ enum { kTokBeta = 0, kTokX = 1, kTokL = 2, kTokY = 3, kTokRows = 4 };
 // of three scales can leave float32's range where the value itself does not.
 
 // The factors of a chunk: e^{G_last}, 1/scale of T, 1/scale of P, first token
-// whose key is not finite (or 64), 1/scale of the keys, of the queries, scale of P.
+// whose key is not finite (or 64), 1/scale of the keys, of the queries, scale of P,
+// and 1/scale of T again for the backward, NaN where a key or query of the chunk is not finite.
 enum { kFacLast = 0, kFacK = 4, kFacQ = 5 };
 struct Fac {
-  float last, t, p, first, k, q, ps, unused;
+  float last, t, p, first, k, q, ps, tb;
 };
 __device__ __forceinline__ Fac load_fac(const void *at) {
   const float4 a = static_cast<const float4 *>(at)[0], b = static_cast<const float4 *>(at)[1];

@@ -385,11 +385,14 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
     *reinterpret_cast<uint4 *>(smem + R::tl + at) = lo;
   } else if (lane == 0) {
     float first = 64.0f;
-    for (int i = 63; i >= 0; --i)
+    bool any = false;
+    for (int i = 63; i >= 0; --i) {
       if (static_cast<int>(bad[i]) & 1) first = static_cast<float>(i);
+      any = any || bad[i] != 0.0f;
+    }
     float4 *fac = reinterpret_cast<float4 *>(smem + R::fac);
     fac[0] = make_float4(expf(G[63] + Gl[63]), st.inv, sp.inv, first);
-    fac[1] = make_float4(sk.inv, sq.inv, sp.s, 0.0f);
+    fac[1] = make_float4(sk.inv, sq.inv, sp.s, any ? __int_as_float(0x7fc00000) : st.inv);
   }
   fence_proxy_async_smem();
   __syncthreads();

@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
     __syncthreads();
     // 2. du^T = dU^T T for this warp's tokens: all of dU from them on
     const RowPow2 pr = pow2_scale(get_top(tops_ + 64, g));
-    const float2 rf = mul2(mul2(pr.inv, zf), splat(fac.t));
+    const float2 rf = mul2(mul2(pr.inv, zf), splat(fac.tb));
     float Uo[2][4];
     {
       float A[3][2][4];

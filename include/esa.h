@@ -393,10 +393,11 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
  *     dq = scale S_t dy,  db = (du.u)(1 - beta),
  *     da = (<dS, S_t> - beta v.du)(1 - alpha),  dS <- alpha (dS - beta k du^T).
  * Value channels do not mix in dv and dS_init, whatever their sizes; dq, dk, da
- * and db are sums over them.  An entry of dy or dS_final that is not finite
- * makes dv and dS_init of its value channel NaN, and dk, da, db of its head (dy:
- * dq of its token as well), for all earlier tokens, and may for later ones of
- * its chunk of 64; one of v, k or S_init that of its chunk and later ones.
+ * and db are sums over them.  Entries that are not finite make results NaN from
+ * where they have a part in them on, to the bounds of the chunk of 64 tokens:
+ *   q, k           dk, dv, da, db of their head for all earlier tokens, dS_init
+ *   dy, dS_final   the same, but dv and dS_init of their value channel alone
+ *   v, k, S_init   dq, dk, da, db of their head for all later tokens
  */
 int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, long long ld_v, const void *a,
                   const void *b, long long ld_g, const void *dy, const float *dS_final, void *dq, void *dk, void *dv,

@@ -119,3 +119,21 @@ def test_states_that_are_not_finite(cuda_device, value, D, H):
     for n in ("dk", "da", "db"):
         assert not torch.isfinite(bad[n][0, :192, 1]).any(), n
         assert torch.equal(bad[n][:, :, 0], clean[n][:, :, 0]), n
+
+
+@pytest.mark.parametrize("dt,D,H", [("bf16", *s) for s in SPREADS] + [("f16", 64, 2), ("f32", 32, 2), ("f32", 64, 80)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("what", ["q", "k"])
+def test_gradients_of_keys_and_queries_that_are_not_finite(cuda_device, what, value, dt, D, H):
+    """All earlier tokens of the head have a share of such a key's or query's gradient; other heads have none."""
+    x, S0, dS = draw(dt, 1, T, H, D, seed=9)
+    clean = run(x, S0, dS, D ** -0.5)
+    x[what][0, 150, 1, 3] = value
+    bad = run(x, S0, dS, D ** -0.5)
+    for n in ("dk", "dv", "da", "db"):
+        assert not torch.isfinite(bad[n][0, :150, 1]).any(), n
+    assert not torch.isfinite(bad["dS0"][0, 1]).any()
+    other = [h for h in range(H) if h != 1]
+    for n in ("y", "dq", "dk", "dv", "da", "db"):
+        assert torch.equal(bad[n][:, :, other], clean[n][:, :, other]), n
+    assert torch.equal(bad["dq"][0, :128, 1], clean["dq"][0, :128, 1])   # of earlier chunks: S dy of the past alone
