@@ -30,7 +30,7 @@ namespace esa {
 
 constexpr int kChunk = 64;
 enum { kTokBeta = 0, kTokX = 1, kTokL = 2, kTokY = 3, kTokRows = 4 };
-//   kTokBeta  beta (0 where the key is not finite)
+//   kTokBeta  beta (0 where the key or gate is not finite)
 //   kTokX     beta e^G          (what the state's prediction K S is multiplied by; 0 where the key is not finite)
 //   kTokL     e^{G_last - G}    (what u is multiplied by before it is added to the state; the same)
 //   kTokY     e^G               (what the state's output Q S is multiplied by; NaN where the query is not finite)
@@ -38,8 +38,8 @@ enum { kTokBeta = 0, kTokX = 1, kTokL = 2, kTokY = 3, kTokRows = 4 };
 // of three scales can leave float32's range where the value itself does not.
 
 // The factors of a chunk: e^{G_last}, 1/scale of T, 1/scale of P, first token
-// whose key is not finite (or 64), 1/scale of the keys, of the queries, scale of P,
-// and 1/scale of T again for the backward, NaN where a key or query of the chunk is not finite.
+// whose key or gate is not finite (or 64), 1/scale of the keys, of the queries, scale of P,
+// and 1/scale of T again for the backward, NaN where a key, query or gate of the chunk is not finite.
 enum { kFacLast = 0, kFacK = 4, kFacQ = 5 };
 struct Fac {
   float last, t, p, first, k, q, ps, tb;

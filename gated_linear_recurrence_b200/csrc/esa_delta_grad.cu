@@ -606,8 +606,7 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
       for (int e = 0; e < 2; ++e) {
         const int i = 2 * lane + e;
         if (i < len) {
-          const float a = fmaxf(sweep::widen(la[e]), -80.0f);
-          const float bb = fmaxf(sweep::widen(lb[e]), -80.0f);
+          const float a = sweep::clamp(sweep::widen(la[e])), bb = sweep::clamp(sweep::widen(lb[e]));
           static_cast<T *>(p.da)[(row + i) * p.s.H + h] = sweep::narrow<T>(dl[e] / (1.0f + expf(a)));
           static_cast<T *>(p.db)[(row + i) * p.s.H + h] = sweep::narrow<T>(udu[i] / (1.0f + expf(bb)));
         }

@@ -18,7 +18,8 @@
 //
 // G is kept in two float32 terms: its differences are exponentiated, and a
 // token that forgets everything (G falls by 80) must not cost its successors
-// their digits.  Below the diagonal blocks e^{Gi - Gj} is e^{Gi - Gr} e^{Gr - Gj}
+// their digits.  A gate that is NaN is treated as a key that is not finite: the
+// head is NaN from its token on.  Below the diagonal blocks e^{Gi - Gj} is e^{Gi - Gr} e^{Gr - Gj}
 // with r the row block's first token: two factors of at most 1, one
 // exponential per row and one per column instead of one per element.
 //
@@ -64,7 +65,8 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
   float *Md = reinterpret_cast<float *>(smem + L::md), *Dd = reinterpret_cast<float *>(smem + L::dd);
   float *vec = reinterpret_cast<float *>(smem + L::vec), *red = reinterpret_cast<float *>(smem + L::red);
   uint32_t *redu = reinterpret_cast<uint32_t *>(red);
-  float *beta = vec, *bad = vec + 64;   // bad: key (bit 0) and query (bit 1) rows that are not finite
+  // bad: tokens whose key (1), query (2) or gate (4) is not finite
+  float *beta = vec, *bad = vec + 64;
   float *G = reinterpret_cast<float *>(smem + R::g), *Gl = G + 64;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int mw = warp & 3;
@@ -91,13 +93,18 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = 2 * lane + e;
-      float be = 0.0f;
+      float be = 0.0f, lost = 0.0f;
       if (i < len) {
-        la[e] = -log1pf(expf(-fmaxf(sweep::widen(ga[(row + i) * p.s.ld_g + h]), -80.0f)));
-        be = sweep::gate(sweep::widen(gb[(row + i) * p.s.ld_g + h]));
+        const float xa = sweep::widen(ga[(row + i) * p.s.ld_g + h]), xb = sweep::widen(gb[(row + i) * p.s.ld_g + h]);
+        if (xa == xa && xb == xb) {
+          la[e] = -log1pf(expf(-sweep::clamp(xa)));
+          be = sweep::gate(xb);
+        } else {
+          lost = 4.0f;
+        }
       }
       beta[i] = be;
-      bad[i] = 0.0f;
+      bad[i] = lost;
     }
     double x = static_cast<double>(la[0]) + la[1];
     const double own = x;
@@ -160,9 +167,9 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
     const float into = expf(G[i] + Gl[i]), out = expf((G[63] - G[i]) + (Gl[63] - Gl[i]));
     const float nan = __int_as_float(0x7fc00000), be = beta[i];
     float *tok = reinterpret_cast<float *>(smem + R::tok);
-    tok[kTokBeta * 64 + i] = flag & 1 ? 0.0f : be;
-    tok[kTokX * 64 + i] = flag & 1 ? 0.0f : be * into;
-    tok[kTokL * 64 + i] = flag & 1 ? 0.0f : out;
+    tok[kTokBeta * 64 + i] = flag & 5 ? 0.0f : be;
+    tok[kTokX * 64 + i] = flag & 5 ? 0.0f : be * into;
+    tok[kTokL * 64 + i] = flag & 5 ? 0.0f : out;
     tok[kTokY * 64 + i] = flag & 2 ? nan : into;
   }
   // K K^T (warps 0-3) and Q K^T (warps 4-7): 16 rows a warp, tiles on and below the diagonal
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
     float first = 64.0f;
     bool any = false;
     for (int i = 63; i >= 0; --i) {
-      if (static_cast<int>(bad[i]) & 1) first = static_cast<float>(i);
+      if (static_cast<int>(bad[i]) & 5) first = static_cast<float>(i);
       any = any || bad[i] != 0.0f;
     }
     float4 *fac = reinterpret_cast<float4 *>(smem + R::fac);

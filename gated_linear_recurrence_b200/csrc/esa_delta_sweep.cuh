@@ -51,7 +51,9 @@ template <> __device__ __forceinline__ float narrow(float v) { return v; }
 template <> __device__ __forceinline__ __half narrow(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 narrow(float v) { return __float2bfloat16_rn(v); }
 
-__device__ __forceinline__ float gate(float x) { return 1.0f / (1.0f + expf(-fmaxf(x, -80.0f))); }
+// Logits are clamped at -80 below; a NaN stays one, as everything after it.
+__device__ __forceinline__ float clamp(float x) { return x < -80.0f ? -80.0f : x; }
+__device__ __forceinline__ float gate(float x) { return 1.0f / (1.0f + expf(-clamp(x))); }
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(256) delta_finish_kernel(FinishArgs p) {
   g = head_sum<32>(g);
   ub = head_sum<32>(ub);
   if (lane == 0) {
-    const float x = fmaxf(widen(static_cast<const T *>(p.b)[bt * p.s.ld_g + h]), -80.0f);
+    const float x = clamp(widen(static_cast<const T *>(p.b)[bt * p.s.ld_g + h]));
     static_cast<T *>(p.db)[id] = narrow<T>(ub / (1.0f + expf(x)));   // 1 - beta = 1 / (1 + e^b)
     const long long b = bt / p.s.T, t = bt - b * p.s.T;
     p.gain[(b * p.s.H + h) * p.s.T + t] = g;
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(256) delta_da_kernel(FinishArgs p, int slices)
   for (int e = 0; e < 2; ++e)
     if (t + e < p.s.T) {
       const long long bt = static_cast<long long>(b) * p.s.T + t + e;
-      const float a = fmaxf(widen(static_cast<const T *>(p.a)[bt * p.s.ld_g + h]), -80.0f);
+      const float a = clamp(widen(static_cast<const T *>(p.a)[bt * p.s.ld_g + h]));
       static_cast<T *>(p.da)[bt * p.s.H + h] = narrow<T>((later + x1 + (e == 0 ? x0 : 0.0f)) / (1.0f + expf(a)));
     }
 }

@@ -69,19 +69,18 @@ __device__ __forceinline__ void gates_of(const SweepArgs &p, const Place &a, flo
     la[e] = 0.0;
     float be = 0.0f;
     if (i < a.len) {
-      la[e] = -log1pf(expf(-fmaxf(ga[(a.row + i) * p.s.ld_g + a.h], -80.0f)));
+      la[e] = -log1pf(expf(-sweep::clamp(ga[(a.row + i) * p.s.ld_g + a.h])));
       be = sweep::gate(gb[(a.row + i) * p.s.ld_g + a.h]);
     }
     beta[i] = be;
   }
   double x = la[0] + la[1];
-  const double own = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const double y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  const double first = x - own + la[0];
+  const double before = __shfl_up_sync(0xffffffffu, x, 1), first = (lane > 0 ? before : 0.0) + la[0];
   const float f0 = static_cast<float>(first), f1 = static_cast<float>(x);
   G[2 * lane] = make_float2(f0, static_cast<float>(first - f0));
   G[2 * lane + 1] = make_float2(f1, static_cast<float>(x - f1));

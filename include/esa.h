@@ -350,8 +350,8 @@ int esa_step(const void *a_t, const void *v_t, const void *q_t, float *E, void *
  *     S_t = alpha_t S_{t-1} + k_t u_t^T,
  *     y_t = scale S_t^T q_t.
  * Keys are used as given: with |k_t| <= 1 the recurrence never grows (the
- * caller normalises them); logits below -80 count as -80.  No counterpart on
- * the pages.
+ * caller normalises them); logits below -80 count as -80, one that is NaN makes
+ * its head NaN from its token on.  No counterpart on the pages.
  *   q, k      rows of H*D elements, ld_qk elements apart: (b, t) at b T + t.
  *   v         the same with ld_v.  ld >= H*D, and ld times the element size a
  *             multiple of 16 bytes (else ESA_ERR_ARG / ESA_ERR_ALIGN), so that
@@ -395,9 +395,9 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
  * Value channels do not mix in dv and dS_init, whatever their sizes; dq, dk, da
  * and db are sums over them.  Entries that are not finite make results NaN from
  * where they have a part in them on, to the bounds of the chunk of 64 tokens:
- *   q, k           dk, dv, da, db of their head for all earlier tokens, dS_init
+ *   q, k, a, b     dk, dv, da, db of their head for all earlier tokens, dS_init
  *   dy, dS_final   the same, but dv and dS_init of their value channel alone
- *   v, k, S_init   dq, dk, da, db of their head for all later tokens
+ *   k, v, a, b, S_init  dq, dk, da, db of their head for all later tokens
  */
 int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, long long ld_v, const void *a,
                   const void *b, long long ld_g, const void *dy, const float *dS_final, void *dq, void *dk, void *dv,

@@ -6,6 +6,7 @@ outputs three float16 roundings of intermediates.
 import pytest
 import torch
 
+from gated_linear_recurrence_b200 import esa_delta_fwd, esa_delta_step
 from tests._delta_reference import PER_TOKEN, assert_within, delta_reference
 from tests.test_gpu_delta import check, draw, ins, run
 
@@ -137,3 +138,43 @@ def test_gradients_of_keys_and_queries_that_are_not_finite(cuda_device, what, va
     for n in ("y", "dq", "dk", "dv", "da", "db"):
         assert torch.equal(bad[n][:, :, other], clean[n][:, :, other]), n
     assert torch.equal(bad["dq"][0, :128, 1], clean["dq"][0, :128, 1])   # of earlier chunks: S dy of the past alone
+
+
+@pytest.mark.parametrize("dt,T,D,H", [("bf16", T, D, H) for T in (20, 200) for D, H in SPREADS]
+                         + [("f16", 200, 64, 2), ("bf16", 5, 64, 2), ("f32", 5, 64, 2), ("f32", 150, 32, 80), ("f32", 333, 32, 2),
+                            ("f32", 333, 128, 2)])
+@pytest.mark.parametrize("what", ["a", "b"])
+@pytest.mark.parametrize("at", [2, 3, -1])
+def test_gates_that_are_nan(cuda_device, at, what, dt, T, D, H):
+    """A NaN logit makes its head NaN from its token on (and is not a gate of e^-80), in y, S and the gradients."""
+    x, S0, dS = draw(dt, 1, T, H, D, seed=10)
+    clean = run(x, S0, dS, D ** -0.5)
+    at = at % T
+    x[what][0, at, 1] = float("nan")
+    bad = run(x, S0, dS, D ** -0.5)
+    y, S, _ = esa_delta_fwd(*ins(x), S_init=S0, keep=False)
+    for out in (bad["y"], y):
+        assert not torch.isfinite(out[0, at:, 1]).any() and torch.isfinite(out[0, :at, 1]).all()
+    assert torch.equal(bad["y"][0, :at, 1], clean["y"][0, :at, 1])
+    assert not torch.isfinite(bad["S"][0, 1]).any() and not torch.isfinite(S[0, 1]).any()
+    for n in ("dk", "dv", "da", "db"):
+        assert not torch.isfinite(bad[n][0, :at, 1]).any(), n
+    assert not torch.isfinite(bad["dS0"][0, 1]).any()
+    other = [h for h in range(H) if h != 1]
+    for n in ("y", "dq", "dk", "dv", "da", "db"):
+        assert torch.equal(bad[n][:, :, other], clean[n][:, :, other]), n
+
+
+@pytest.mark.parametrize("what", ["a", "b"])
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_one_token_with_a_gate_that_is_nan(cuda_device, D, what):
+    x, S0, _ = draw("bf16", 2, 1, 3, D, seed=11)
+    tok = {n: t[:, 0].contiguous() for n, t in x.items()}
+    want_S = S0.clone()
+    want = esa_delta_step(*ins(tok), want_S)
+    tok[what][1, 2] = float("nan")
+    S = S0.clone()
+    y = esa_delta_step(*ins(tok), S)
+    assert not torch.isfinite(y[1, 2]).any() and not torch.isfinite(S[1, 2]).any()
+    y[1, 2], S[1, 2] = want[1, 2], want_S[1, 2]
+    assert torch.equal(y, want) and torch.equal(S, want_S)
