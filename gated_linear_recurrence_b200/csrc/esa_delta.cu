@@ -274,11 +274,13 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
   FinishArgs f{};
   f.s = s;
   f.nc = lo.nc;
-  f.q = q; f.v = v; f.a = a; f.b = b;
+  f.q = q; f.k = k; f.v = v; f.a = a; f.b = b; f.dy = dy;
   f.u = p.u; f.du = p.du; f.dkf = p.dk; f.dk2 = p.dk2; f.dqf = p.dq; f.end = p.end;
+  f.S_ck = p.S_ck; f.dS_ck = p.dS_ck;
   f.gain = reinterpret_cast<float *>(base + lo.gain);
   f.dq = dq; f.dk = dk; f.dv = dv; f.da = da; f.db = db;
-  return launch_delta_finish(dtype, f, st);
+  if ((rc = launch_delta_finish(dtype, f, st))) return rc;
+  return launch_delta_gate(dtype, f, st);
 }
 
 int esa_delta_step(const void *q_t, const void *k_t, long long ld_qk, const void *v_t, long long ld_v,

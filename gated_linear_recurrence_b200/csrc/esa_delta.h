@@ -41,12 +41,13 @@ int launch_delta_step(int dtype, const SweepArgs &a, cudaStream_t st);   // one 
 
 struct FinishArgs {
   DeltaShape s;
-  const void *q, *v, *a, *b;
-  const float *u, *du, *dkf, *dk2, *dqf, *end;
+  const void *q, *k, *v, *a, *b, *dy;
+  const float *u, *du, *dkf, *dk2, *dqf, *end, *S_ck, *dS_ck;
   int nc;
   float *gain;   // [B,H,T]
   void *dq, *dk, *dv, *da, *db;
 };
-int launch_delta_finish(int dtype, const FinishArgs &a, cudaStream_t st);
+int launch_delta_finish(int dtype, const FinishArgs &a, cudaStream_t st);   // dq, dk, dv, db, gain
+int launch_delta_gate(int dtype, const FinishArgs &a, cudaStream_t st);     // da
 
 }  // namespace esa

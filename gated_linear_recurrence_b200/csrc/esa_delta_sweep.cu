@@ -78,8 +78,6 @@ int finish(const FinishArgs &a, cudaStream_t st) {
     case 128: sweep::delta_finish_kernel<T, 128><<<grid, 256, 0, st>>>(a); break;
     default: return ESA_ERR_UNSUPPORTED;
   }
-  const long long chunks = static_cast<long long>(a.s.B) * a.s.H * a.nc;
-  sweep::delta_da_kernel<T><<<static_cast<unsigned>((chunks + 7) / 8), 256, 0, st>>>(a, a.s.D * a.s.D / 1024);
   return runtime_status(cudaGetLastError());
 }
 

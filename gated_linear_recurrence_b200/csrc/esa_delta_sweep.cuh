@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(D * lanes<D>()) delta_keys_kernel(SweepArgs p)
 }
 
 // One warp per token and head: round dq, dk, dv; db = (u.du)(1 - beta);
-// gain = q.dq - beta v.du, the summand of dlog alpha.
+// gain = q.dq - beta v.du, the summand of dlog alpha (esa_delta_gate.cu).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) delta_finish_kernel(FinishArgs p) {
   const long long id = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -434,35 +434,77 @@ __global__ void __launch_bounds__(256) delta_finish_kernel(FinishArgs p) {
   }
 }
 
-// da_t = (1 - alpha_t) (sum of gain_s over the chunk's later tokens + <dS, S> at
-// its end): one warp per chunk and head, two tokens a lane.  The sums start
-// anew in every chunk, so their roundings do not add up over the sequence.
+// ---- chunk by chunk (esa_delta_wy.cu, esa_delta_gate.cu) ----------------------
+struct Place {
+  int b, h, t0, len;      // batch entry, head, first token, tokens
+  long long row, chunk;   // first token's row, index of the chunk
+};
+// Chunk n of a head.
+__device__ __forceinline__ Place place_of(const DeltaShape &s, int nc, int head, int n) {
+  Place a;
+  a.b = head / s.H;
+  a.h = head - a.b * s.H;
+  a.t0 = n * CHUNK;
+  a.len = min(CHUNK, s.T - a.t0);
+  a.row = static_cast<long long>(a.b) * s.T + a.t0;
+  a.chunk = static_cast<long long>(head) * nc + n;
+  return a;
+}
+
+// G in two terms (differences of sums that may reach thousands are
+// exponentiated) and beta, by the first warp; alpha = 1, beta = 0 behind the end.
 template <typename T>
-__global__ void __launch_bounds__(256) delta_da_kernel(FinishArgs p, int slices) {
-  const long long id = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (id >= static_cast<long long>(p.s.B) * p.s.H * p.nc) return;
-  const int head = static_cast<int>(id / p.nc), t0 = static_cast<int>(id - static_cast<long long>(head) * p.nc) * CHUNK;
-  const int b = head / p.s.H, h = head - b * p.s.H, lane = threadIdx.x & 31;
-  const float *gain = p.gain + static_cast<long long>(head) * p.s.T;
-  float end = 0.0f;
-  for (int i = 0; i < slices; ++i) end += p.end[id * slices + i];
-  const int t = t0 + 2 * lane;
-  const float x0 = t < p.s.T ? gain[t] : 0.0f, x1 = t + 1 < p.s.T ? gain[t + 1] : 0.0f;
-  float sum = x0 + x1;
+__device__ __forceinline__ void gates_of(const DeltaShape &s, const void *a_, const void *b_, const Place &a, float2 *G, float *beta) {
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  const T *ga = static_cast<const T *>(a_), *gb = static_cast<const T *>(b_);
+  double la[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = 2 * lane + e;
+    la[e] = 0.0;
+    float be = 0.0f;
+    if (i < a.len) {
+      la[e] = -log1pf(expf(-clamp(widen(ga[(a.row + i) * s.ld_g + a.h]))));
+      be = gate(widen(gb[(a.row + i) * s.ld_g + a.h]));
+    }
+    beta[i] = be;
+  }
+  double x = la[0] + la[1];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const float y = __shfl_down_sync(0xffffffffu, sum, o);
-    if (lane + o < 32) sum += y;
+    const double y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  const float after = __shfl_down_sync(0xffffffffu, sum, 1);
-  const float later = end + (lane < 31 ? after : 0.0f);
+  const double before = __shfl_up_sync(0xffffffffu, x, 1), first = (lane > 0 ? before : 0.0) + la[0];
+  const float f0 = static_cast<float>(first), f1 = static_cast<float>(x);
+  G[2 * lane] = make_float2(f0, static_cast<float>(first - f0));
+  G[2 * lane + 1] = make_float2(f1, static_cast<float>(x - f1));
+}
+__device__ __forceinline__ float decay(float2 i, float2 j) { return expf((i.x - j.x) + (i.y - j.y)); }
+
+// X Y^T of two [64][D] tiles: rows ti + 16 r, columns tj + 16 c.
+template <int D>
+__device__ __forceinline__ void dots(const float *X, const float *Y, int ti, int tj, float (&acc)[4][4]) {
+  constexpr int P = D + 4;
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-    if (t + e < p.s.T) {
-      const long long bt = static_cast<long long>(b) * p.s.T + t + e;
-      const float a = clamp(widen(static_cast<const T *>(p.a)[bt * p.s.ld_g + h]));
-      static_cast<T *>(p.da)[bt * p.s.H + h] = narrow<T>((later + x1 + (e == 0 ? x0 : 0.0f)) / (1.0f + expf(a)));
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[r][c] = 0.0f;
+#pragma unroll 2
+  for (int d = 0; d < D; d += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      x[r] = *reinterpret_cast<const float4 *>(X + (ti + 16 * r) * P + d);
+      y[r] = *reinterpret_cast<const float4 *>(Y + (tj + 16 * r) * P + d);
     }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        acc[r][c] = fmaf(x[r].x, y[c].x, fmaf(x[r].y, y[c].y, fmaf(x[r].z, y[c].z, fmaf(x[r].w, y[c].w, acc[r][c]))));
+  }
 }
 
 }  // namespace sweep

@@ -27,6 +27,9 @@
 namespace esa {
 namespace {
 
+using sweep::decay;
+using sweep::dots;
+using sweep::Place;
 constexpr int C = sweep::CHUNK, kThreads = 256, kCols = 16;   // tokens, threads, value channels of a state block
 
 __device__ __forceinline__ void copy_or_zero(float *dst, const float *src, bool on) {
@@ -42,75 +45,6 @@ __device__ __forceinline__ void rows_in(float *dst, int pitch, const float *src,
   }
 }
 
-struct Place {
-  int b, h, len;
-  long long row, chunk;   // first token's row, index of the chunk
-};
-__device__ __forceinline__ Place place_of(const SweepArgs &p, int head, int n) {
-  Place a;
-  a.b = head / p.s.H;
-  a.h = head - a.b * p.s.H;
-  a.len = min(C, p.s.T - n * C);
-  a.row = static_cast<long long>(a.b) * p.s.T + n * C;
-  a.chunk = static_cast<long long>(head) * p.nc + n;
-  return a;
-}
-
-// G in two terms (differences of sums that may reach thousands are
-// exponentiated) and beta, by the first warp; alpha = 1, beta = 0 behind the end.
-__device__ __forceinline__ void gates_of(const SweepArgs &p, const Place &a, float2 *G, float *beta) {
-  if (threadIdx.x >= 32) return;
-  const int lane = threadIdx.x;
-  const float *ga = static_cast<const float *>(p.a), *gb = static_cast<const float *>(p.b);
-  double la[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int i = 2 * lane + e;
-    la[e] = 0.0;
-    float be = 0.0f;
-    if (i < a.len) {
-      la[e] = -log1pf(expf(-sweep::clamp(ga[(a.row + i) * p.s.ld_g + a.h])));
-      be = sweep::gate(gb[(a.row + i) * p.s.ld_g + a.h]);
-    }
-    beta[i] = be;
-  }
-  double x = la[0] + la[1];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  const double before = __shfl_up_sync(0xffffffffu, x, 1), first = (lane > 0 ? before : 0.0) + la[0];
-  const float f0 = static_cast<float>(first), f1 = static_cast<float>(x);
-  G[2 * lane] = make_float2(f0, static_cast<float>(first - f0));
-  G[2 * lane + 1] = make_float2(f1, static_cast<float>(x - f1));
-}
-__device__ __forceinline__ float decay(float2 i, float2 j) { return expf((i.x - j.x) + (i.y - j.y)); }
-
-// X Y^T of two [64][D] tiles: rows ti + 16 r, columns tj + 16 c.
-template <int D>
-__device__ __forceinline__ void dots(const float *X, const float *Y, int ti, int tj, float (&acc)[4][4]) {
-  constexpr int P = D + 4;
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[r][c] = 0.0f;
-#pragma unroll 2
-  for (int d = 0; d < D; d += 4) {
-    float4 x[4], y[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      x[r] = *reinterpret_cast<const float4 *>(X + (ti + 16 * r) * P + d);
-      y[r] = *reinterpret_cast<const float4 *>(Y + (tj + 16 * r) * P + d);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        acc[r][c] = fmaf(x[r].x, y[c].x, fmaf(x[r].y, y[c].y, fmaf(x[r].z, y[c].z, fmaf(x[r].w, y[c].w, acc[r][c]))));
-  }
-}
-
 constexpr int kTri = C + 4;   // pitch of a [64][64] matrix
 template <int D> constexpr int wy_floats() { return C * (D + 4) + C * kTri + C * 2 * D + 4 * C; }
 
@@ -120,12 +54,12 @@ __global__ void __launch_bounds__(kThreads) delta_wy_kernel(SweepArgs p) {
   float *K = reinterpret_cast<float *>(smem), *M = K + C * (D + 4), *X = M + C * kTri;
   float2 *G = reinterpret_cast<float2 *>(X + C * 2 * D);
   float *beta = reinterpret_cast<float *>(G + C), *into_beta = beta + C;
-  const Place a = place_of(p, blockIdx.x / p.nc, blockIdx.x % p.nc);
+  const Place a = sweep::place_of(p.s, p.nc, blockIdx.x / p.nc, blockIdx.x % p.nc);
   const int tid = threadIdx.x;
   rows_in(K, D + 4, static_cast<const float *>(p.k) + a.row * p.s.ld_qk + a.h * D, p.s.ld_qk, a.len, D);
   rows_in(X + D, 2 * D, static_cast<const float *>(p.v) + a.row * p.s.ld_v + a.h * D, p.s.ld_v, a.len, D);
   sweep::cp_async_commit();
-  gates_of(p, a, G, beta);
+  sweep::gates_of<float>(p.s, p.a, p.b, a, G, beta);
   sweep::cp_async_wait<0>();
   __syncthreads();
   {
@@ -215,14 +149,14 @@ __global__ void __launch_bounds__(kThreads) delta_wz_kernel(SweepArgs p) {
   float *K = reinterpret_cast<float *>(smem), *Q = K + C * (D + 4), *P = Q + C * (D + 4), *O = P + C * kTri;
   float2 *G = reinterpret_cast<float2 *>(O + C * D);
   float *beta = reinterpret_cast<float *>(G + C);
-  const Place a = place_of(p, blockIdx.x / p.nc, blockIdx.x % p.nc);
+  const Place a = sweep::place_of(p.s, p.nc, blockIdx.x / p.nc, blockIdx.x % p.nc);
   const int tid = threadIdx.x;
   const long long ldc = static_cast<long long>(p.s.H) * D;
   rows_in(K, D + 4, static_cast<const float *>(p.k) + a.row * p.s.ld_qk + a.h * D, p.s.ld_qk, a.len, D);
   rows_in(Q, D + 4, static_cast<const float *>(p.q) + a.row * p.s.ld_qk + a.h * D, p.s.ld_qk, a.len, D);
   rows_in(O, D, static_cast<const float *>(p.dy) + a.row * ldc + a.h * D, ldc, a.len, D);
   sweep::cp_async_commit();
-  gates_of(p, a, G, beta);
+  sweep::gates_of<float>(p.s, p.a, p.b, a, G, beta);
   sweep::cp_async_wait<0>();
   __syncthreads();
   {
@@ -287,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) delta_state_kernel(SweepArgs p) {
   const float *k = static_cast<const float *>(p.k), *q = static_cast<const float *>(p.q), *dy = static_cast<const float *>(p.dy);
   auto fetch = [&](int it, int buf) {
     if (it < p.nc) {
-      const Place a = place_of(p, head, BWD ? p.nc - 1 - it : it);
+      const Place a = sweep::place_of(p.s, p.nc, head, BWD ? p.nc - 1 - it : it);
       float *s = sm + buf * L::stage;
       const float *w = p.wt + a.chunk * (C * D);
       rows_in(s + (BWD ? L::second : L::first), L::pitch, w, D, C, D);

@@ -82,3 +82,51 @@ def test_gate_gradient_of_short_sequences(cuda_device, n):
         x["a"].fill_(-3.0)
     ref = delta_reference(*ins(x), 0.125, S0, x["dy"], dS)
     check_da(run(x, S0, dS, 0.125)["da"], ref["da"], -3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,H", [(32, 2), (64, 2), (64, 65), (128, 2), (128, 17)])
+@pytest.mark.parametrize("n", [1, 17, 64, 65, 200, 333])
+@pytest.mark.parametrize("mean", [30, 3, 0, -4, -9, -30])
+def test_gate_gradient_in_float32(cuda_device, mean, n, D, H):
+    """Token sweeps, from end to end and chunk by chunk.  Where every gate keeps a quarter the terms are at most four times
+    as large as their sum, else none is larger than the sum's own: the bound of two sweeps, four times."""
+    x, S0, dS = draw("f32", 1, n, H, D, seed=n)
+    if n > 1:
+        gates(x, mean)
+    xs, got, ref = two_heads(x, S0, dS, run(x, S0, dS, D ** -0.5))
+    # autograd's 1 - sigmoid(a) in float64 is off by 2^-53 e^a of itself, 0.1% at 30: the same factor without the difference
+    a = xs["a"].cpu().double()
+    want = ref["da"] / (1.0 - torch.sigmoid(a)) / (1.0 + torch.exp(a))
+    extra = 4 * 2 * PER_TOKEN * n ** 0.5
+    assert_within("da", got["da"], want, extra, extra)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [5, 7, 200])
+def test_gate_gradient_of_one_gate_that_forgets(cuda_device, n, dt):
+    """Chunks with one such gate and chunks without; a short 16-bit sequence goes token by token too."""
+    x, S0, dS = draw(dt, 1, n, 2, 64, seed=n)
+    x["a"].fill_(5.0)
+    x["a"][:, [3, n - 1]] = -8.0
+    ref = delta_reference(*ins(x), 0.125, S0, x["dy"], dS)["da"]
+    da = run(x, S0, dS, 0.125)["da"]
+    extra = 4 * 2 * PER_TOKEN * n ** 0.5 if dt == "f32" or n < 8 else HALF_P
+    assert_within("da", da, ref, extra, extra)
+    assert_within("da of the gates that forget", da[:, [3, n - 1]], ref[:, [3, n - 1]], extra, extra)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_gate_gradient_of_strided_rows(cuda_device, dt):
+    n, H, D = 5 if dt == "bf16" else 70, 2, 64
+    x, S0, dS = draw(dt, 2, n, H, D, seed=12)
+    gates(x, -4)
+    want = run(x, S0, dS, 0.125)["da"]
+    P = torch.zeros(2, n, 3 * H * D + 16, dtype=x["q"].dtype, device="cuda")
+    q, k, v = (P[..., i * H * D:(i + 1) * H * D].unflatten(-1, (H, D)) for i in range(3))
+    a, b = P[..., 3 * H * D + 1:3 * H * D + 1 + H], P[..., 3 * H * D + 5:3 * H * D + 5 + H]
+    for dst, name in zip((q, k, v, a, b), "qkvab"):
+        dst.copy_(x[name])
+    assert torch.equal(run(dict(q=q, k=k, v=v, a=a, b=b, dy=x["dy"]), S0, dS, 0.125)["da"], want)
