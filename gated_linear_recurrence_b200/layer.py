@@ -311,7 +311,7 @@ def _wants_grad(*ts):
 class _DeltaRuleFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, a, b, S_init, scale, keep, want_S):
-        S0 = None if S_init is None else S_init.detach().contiguous()
+        S0 = None if S_init is None else _dense(S_init.detach())
         y, S, ws = _delta.esa_delta_fwd(q, k, v, a, b, scale=scale, S_init=S0, keep=keep, want_S_final=want_S)
         ctx.set_materialize_grads(False)
         ctx.scale = scale
@@ -323,8 +323,8 @@ class _DeltaRuleFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, dS):
         q, k, v, a, b, S0, ws = ctx.saved_tensors
-        dy = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if dy is None else dy.contiguous()
-        dS = None if dS is None else dS.contiguous()
+        dy = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if dy is None else _dense(dy)
+        dS = None if dS is None else _dense(dS)
         *grads, dS0 = _delta.esa_delta_bwd(q, k, v, a, b, dy, ws, scale=ctx.scale, S_init=S0, dS_final=dS,
                                            want_dS_init=ctx.needs_input_grad[5])
         return (*(g if need else None for g, need in zip(grads, ctx.needs_input_grad)), dS0, None, None, None)
@@ -339,6 +339,7 @@ def _in_place(t):
 
 
 def _dense(t):
+    """``t`` contiguous and on 16 bytes (a slice of a flat buffer may be the one and not the other)."""
     t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
