@@ -44,16 +44,25 @@ def _stream(device, stream):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _scratch(like, nbytes, stream):
+    """``nbytes`` on ``like``'s device, from the pool of the stream that uses them: once dropped they go to that stream's
+    next allocations alone, which come after the kernels still to run on it."""
+    if stream is None:
+        return like.new_empty(nbytes, dtype=torch.uint8)
+    with torch.cuda.stream(stream):
+        return like.new_empty(nbytes, dtype=torch.uint8)
+
+
 def esa_delta_workspace_size(B: int, T: int, H: int, D: int, dtype, keep: bool = True) -> int:
     code = _esa._DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
     return int(load_library().esa_delta_workspace_size(B, T, H, D, code, int(bool(keep))))
 
 
-def _new_workspace(B, T, H, D, q, keep):
+def _new_workspace(B, T, H, D, q, keep, stream):
     n = load_library().esa_delta_workspace_size(B, T, H, D, _DTYPE_CODE[q.dtype], 1 if keep else 0)
     if n == 0:
         raise ValueError(f"unsupported shape for the delta rule: B={B}, T={T}, H={H}, D={D} (D is 32, 64 or 128)")
-    return q.new_empty(n, dtype=torch.uint8)
+    return _scratch(q, n, stream)
 
 
 def _check_workspace(workspace, device):
@@ -137,7 +146,9 @@ def esa_delta_fwd(q, k, v, a, b, scale=None, S_init=None, y=None, S_final=None, 
     a row stride, a and b another).  ``scale`` defaults to D ** -0.5.
     ``keep`` leaves in the workspace what :func:`esa_delta_bwd` reads (9 times
     ``q``'s bytes with 16-bit tensors); an inference call passes False (3.4
-    times at D = 128, 4.8 at D = 64).
+    times at D = 128, 4.8 at D = 64).  ``stream`` runs the call on that stream
+    instead of the current one; outputs are allocated on the current one, so
+    hold them until that stream is done with them.
     """
     B, T, H, D, ld_qk, ld_v, ld_g = _inputs(q, k, v, a, b)
     y = _like(q) if y is None else _out("y", y, q.shape, q.dtype, q.device)
@@ -147,7 +158,7 @@ def esa_delta_fwd(q, k, v, a, b, scale=None, S_init=None, y=None, S_final=None, 
         S_final = q.new_empty((B, H, D, D), dtype=torch.float32)
     _check_state("S_init", S_init, B, H, D, q.device)
     if workspace is None:
-        workspace = _new_workspace(B, T, H, D, q, keep)
+        workspace = _new_workspace(B, T, H, D, q, keep, stream)
     nbytes = _check_workspace(workspace, q.device)
     with _on(q.device):
         rc = load_library().esa_delta_fwd(

@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import torch
 
-from .delta import _like, _ptr, _stream
+from .delta import _check_workspace, _like, _ptr, _scratch, _stream
 from .esa import EsaError, _on, load_library
 
 _DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
@@ -115,6 +115,7 @@ def esa_norm_bwd(dy, h, weight, stats, dh=None, dx=None, dweight=None, dbias=Non
     ``h`` through the residual stream and is added to ``dx``, which is the
     gradient of ``x`` and of ``residual`` alike.  ``dweight`` and ``dbias``
     have the weight's dtype (``wdtype``, or ``h``'s, without a weight).
+    ``stream`` is :func:`~.delta.esa_delta_fwd`'s.
     """
     rows, N = _check_x(h, "h")
     ld_h, ld_dy = _rows("h", h), _rows("dy", dy, h)
@@ -137,12 +138,8 @@ def esa_norm_bwd(dy, h, weight, stats, dh=None, dx=None, dweight=None, dbias=Non
     lib = load_library()
     codes = (_DTYPE_CODE[h.dtype], _DTYPE_CODE[wdt])
     if workspace is None and (dweight is not None or dbias is not None):
-        workspace = h.new_empty(lib.esa_norm_workspace_size(rows, N, *codes), dtype=torch.uint8)
-    nbytes = 0
-    if workspace is not None:
-        if not workspace.is_cuda or workspace.device != h.device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous CUDA tensor on {h.device}")
-        nbytes = workspace.numel() * workspace.element_size()
+        workspace = _scratch(h, lib.esa_norm_workspace_size(rows, N, *codes), stream)
+    nbytes = 0 if workspace is None else _check_workspace(workspace, h.device)
     with _on(h.device):
         rc = lib.esa_norm_bwd(_ptr(dy), ld_dy, _ptr(h), ld_h, _ptr(weight), _ptr(stats), _ptr(dh), ld_dh, _ptr(dx),
                               _ptr(dweight), _ptr(dbias), rows, N, *codes, _ptr(workspace), nbytes,
