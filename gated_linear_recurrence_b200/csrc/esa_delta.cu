@@ -113,6 +113,7 @@ int elem(int dtype) { return dtype == ESA_F32 ? 4 : 2; }
 
 int check_shape(int B, int T, int H, int D, int dtype) {
   if (B < 0 || T < 0 || H < 1 || D < 1) return ESA_ERR_ARG;
+  if (T > INT_MAX - 64) return ESA_ERR_ARG;                                    // tokens up to a chunk's end
   if (dtype < ESA_F32 || dtype > ESA_E4M3) return ESA_ERR_ARG;
   if (dtype == ESA_E4M3 || (D != 32 && D != 64 && D != 128)) return ESA_ERR_UNSUPPORTED;
   if (static_cast<long long>(H) * D > INT_MAX / 2) return ESA_ERR_ARG;
