@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     if constexpr (KEEP) {
       const float all = warp_max(fmaxf(tops.x * sinv.x, tops.y * sinv.y));
       const Pow2 pss = store_scale(all);
-      sf = mul2(splat(pss.s), sunit);
+      sf = mul2(splat(pss.s), xinv);
       if (lane == 0)
         p.w.slice[c * 32 + kSliceS + (dvw >> 4)] = cut ? __int_as_float(0x7fc00000) : slice_unit(all, pss);
     }

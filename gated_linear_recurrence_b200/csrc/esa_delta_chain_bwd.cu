@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     const float2 sunit = mul2(ps.inv, sinv), xinv = unit_or_zero(tops, sunit);
     const float alls = warp_max(fmaxf(tops.x * sinv.x, tops.y * sinv.y));
     const Pow2 pss = store_scale(alls);
-    const float2 sf = mul2(splat(pss.s), sunit);
+    const float2 sf = mul2(splat(pss.s), xinv);
     if (lane == 0) p.w.slice[c * 32 + kSliceDs + (dvw >> 4)] = slice_unit(alls, pss);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {

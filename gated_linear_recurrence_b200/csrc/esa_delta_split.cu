@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
     if constexpr (KEEP) {
       const float all = warp_max(fmaxf(tops.x * sinv.x, tops.y * sinv.y));
       const Pow2 pss = store_scale(all);
-      sf = mul2(splat(pss.s), sunit);
+      sf = mul2(splat(pss.s), xinv);
       if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceS + slice] = slice_unit(all, pss);
     }
     {
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
     const float2 sunit = mul2(ps.inv, sinv), xinv = unit_or_zero(tops, sunit);
     const float alls = warp_max(fmaxf(tops.x * sinv.x, tops.y * sinv.y));
     const Pow2 pss = store_scale(alls);
-    const float2 sf = mul2(splat(pss.s), sunit);
+    const float2 sf = mul2(splat(pss.s), xinv);
     if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceDs + slice] = slice_unit(alls, pss);
     {
       float X[8][4];

@@ -178,3 +178,23 @@ def test_one_token_with_a_gate_that_is_nan(cuda_device, D, what):
     assert not torch.isfinite(y[1, 2]).any() and not torch.isfinite(S[1, 2]).any()
     y[1, 2], S[1, 2] = want[1, 2], want_S[1, 2]
     assert torch.equal(y, want) and torch.equal(S, want_S)
+
+
+@pytest.mark.parametrize("D,H", SPREADS)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_value_channels_of_zeros(cuda_device, dt, D, H):
+    """Channels that are zero throughout beside small ones: zeros times any scale."""
+    x, _, _ = draw(dt, 1, T, H, D, seed=13, state=False)
+    x["v"] = (x["v"].float() * 1e-4).to(x["v"].dtype)
+    x["v"][..., 3] = 0
+    x["v"][..., 16:32] = 0
+    x["dy"] = (x["dy"].float() * 1e-3).to(x["dy"].dtype)
+    x["dy"][..., 5] = 0
+    xs, got, ref = two_heads(x, None, None, run(x, None, None, 1.0))
+    for n in ("y", "S"):
+        assert not got[n][..., [3, *range(16, 32)]].any()
+    assert not got["dv"][..., 5].any()
+    ref = delta_reference(*ins(xs), 1.0, None, xs["dy"], None)
+    # da is some 1e-7: in float16 a whole multiple of 2^-24, off by 2^-25, which assert_within counts
+    assert_within("da", got["da"], ref["da"], HALF_P, HALF_P)
+    check(xs, got | {"da": ref["da"].float()}, ref, T, D, half_p=HALF_P)
