@@ -164,9 +164,9 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     const float zp = p.s.scale * fac.p;
     const bool with = zp != 0.0f;
     const float2 xk = mul2(xinv, splat(fac.k));
-    RowPow2 pd = pow2_scale(quad_max(top));
-    if (with) pd = least_unit(pd, xk, iscale * fac.ps);
-    const float2 zf = with ? mul2(pd.inv, splat(zp)) : splat(1.0f), yd = mul2(pd.inv, splat(p.s.scale));
+    const RowPow2 pd = pow2_scale(quad_max(top)), pz = with ? least_unit(pd, xk, iscale * fac.ps) : pd;
+    const float2 low = mul2(pd.inv, pz.s);   // what the product with P takes of dO: 1 unless its unit is too small
+    const float2 zf = with ? mul2(pz.inv, splat(zp)) : splat(1.0f), yd = mul2(pd.inv, splat(p.s.scale));
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
@@ -183,19 +183,21 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
     if (with) {
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
+        uint32_t o[4] = {od[kb][0], od[kb][1], od[kb][2], od[kb][3]};
+        if (low.x != 1.0f || low.y != 1.0f) scale_h2(o, low);
 #pragma unroll
         for (int np = 0; np <= kb; ++np) {
           uint32_t bh[4];
           ldsm4t(bh, tri0 + tri(kb, np) + R::ph);
-          mma_f16(X[2 * np], od[kb], bh[0], bh[1]);
-          mma_f16(X[2 * np + 1], od[kb], bh[2], bh[3]);
+          mma_f16(X[2 * np], o, bh[0], bh[1]);
+          mma_f16(X[2 * np + 1], o, bh[2], bh[3]);
         }
 #pragma unroll
         for (int np = 0; np <= kb; ++np) {
           uint32_t bl[4];
           ldsm4t(bl, tri0 + tri(kb, np) + R::pl);
-          mma_f16(X[2 * np], od[kb], bl[0], bl[1]);
-          mma_f16(X[2 * np + 1], od[kb], bl[2], bl[3]);
+          mma_f16(X[2 * np], o, bl[0], bl[1]);
+          mma_f16(X[2 * np + 1], o, bl[2], bl[3]);
         }
       }
     }

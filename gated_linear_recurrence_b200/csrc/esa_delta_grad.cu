@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
       }
     }
     // slice scales: the largest of each kind, and what each slice has of it (1 almost always)
-    float part, uinv, rinv, sinv, dsinv, sunit;   // sunit: sinv, or 0 for a state of zeros
+    float part, uinv, rinv, sinv, dsinv;   // 0 for zeros
     bool flat;
     {
       float v = (lane & 7) < KS ? reinterpret_cast<const float *>(sb + L::h + R::k + 512)[lane] : 0.0f;
@@ -269,8 +269,6 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
       if (__any_sync(0xffffffffu, v != v)) t = v = __int_as_float(0x7fc00000);   // a channel of the chunk is not finite
-      sunit = __shfl_sync(0xffffffffu, t, kSliceS);
-      if (t == 0.0f) t = 1.0f;
       part = v > 0.0f && v != t ? v / t : 1.0f;
       flat = __all_sync(0xffffffffu, part == 1.0f);
       uinv = __shfl_sync(0xffffffffu, t, kSliceU);
@@ -367,13 +365,12 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
           mma_f16(z[0], ak, bk[0], bk[1]);
           mma_f16(z[1], ak, bk[2], bk[3]);
         }
-        const float qk = qinv * kinv, kk = kinv * kinv;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float p = w[i][e] * qk * P[2 * np + i][e];
-            w[i][e] = fmaf(z[i][e] * kk, N[2 * np + i][e], p);
+            const float p = w[i][e] * qinv * (kinv * P[2 * np + i][e]);
+            w[i][e] = fmaf(z[i][e] * kinv, kinv * N[2 * np + i][e], p);
             if (blk == m && 8 * i + 2 * t4 + (e & 1) >= g + (e >> 1) * 8) w[i][e] = 0.0f;
           }
         if (blk == m) diagonal_sums(w, wdiag + 16 * m, lane);
@@ -388,8 +385,8 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
       const float omax = warp_max(fmaxf(oinv[lane], oinv[32 + lane]));
       const float bmax = warp_max(fmaxf(tok[kTokBeta * 64 + lane], tok[kTokBeta * 64 + 32 + lane]));
       const float pk = topp > 0.0f ? pp.inv * kinv : 0.0f, pq = topp > 0.0f ? pp.inv * qinv : 0.0f, nk = topn > 0.0f ? pn.inv * kinv : 0.0f;
-      uq = fmaxf(fmaxf(pk, kLeastUnit), fabsf(p.s.scale) * omax * sunit * (1024.0f * kLeastShare));
-      uk = fmaxf(fmaxf(fmaxf(nk, pq), kLeastUnit), rinv * bmax * sunit * (1024.0f * kLeastShare));
+      uq = fmaxf(fmaxf(pk, kLeastUnit), fabsf(p.s.scale) * omax * sinv * (1024.0f * kLeastShare));
+      uk = fmaxf(fmaxf(fmaxf(nk, pq), kLeastUnit), rinv * bmax * sinv * (1024.0f * kLeastShare));
       fpk = pk / uq;
       fpq = pq / uk;
       fnk = nk / uk;
@@ -504,11 +501,11 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
 #pragma unroll
       for (int i = 0; i < 6; ++i) r[i] = quad_sum(r[i]);
       if (t4 == 0) {
-        const float qu = uq * qinv, ku = uk * kinv;
-        as[cw * 64 + i0] = fmaf(r[4], qu, r[0] * ku);
-        as[cw * 64 + i0 + 8] = fmaf(r[5], qu, r[1] * ku);
-        bs[cw * 64 + i0] = r[2] * (l0 * kinv);
-        bs[cw * 64 + i0 + 8] = r[3] * (l1 * kinv);
+        // unit by unit: a product of two may be below float32's range
+        as[cw * 64 + i0] = fmaf(r[4] * uq, qinv, r[0] * uk * kinv);
+        as[cw * 64 + i0 + 8] = fmaf(r[5] * uq, qinv, r[1] * uk * kinv);
+        bs[cw * 64 + i0] = r[2] * l0 * kinv;
+        bs[cw * 64 + i0 + 8] = r[3] * l1 * kinv;
       }
     }
     // Q += dP K, K += N K
@@ -591,7 +588,7 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
           for (int l = 2; l < 4; ++l)
             if (j < blk && blk < l) F[e] += wrows[j * 64 + 16 * l];
       }
-      const float cc = last * sinv * dsinv * head_sum<32>(lane < KS ? red[16 + lane] : 0.0f);
+      const float cc = head_sum<32>(lane < KS ? red[16 + lane] : 0.0f) * sinv * (last * dsinv);
       float later = A[0] + A[1], earlier = B[0] + B[1];   // over this lane's tokens and those behind (before) them
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {

@@ -527,9 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
     const float zp = p.s.scale * fac.p;
     const bool with = zp != 0.0f;
     const float2 xk = mul2(xinv, splat(fac.k));
-    RowPow2 pd = pow2_scale(quad_max(topd));
-    if (with) pd = least_unit(pd, xk, iscale * fac.ps);
-    const float2 zf = with ? mul2(pd.inv, splat(zp)) : splat(1.0f), yd = mul2(pd.inv, splat(p.s.scale));
+    const RowPow2 pd = pow2_scale(quad_max(topd)), pz = with ? least_unit(pd, xk, iscale * fac.ps) : pd;
+    const float2 low = mul2(pd.inv, pz.s);   // what the product with P takes of dO: 1 unless its unit is too small
+    const float2 zf = with ? mul2(pz.inv, splat(zp)) : splat(1.0f), yd = mul2(pd.inv, splat(p.s.scale));
     float2 topo = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)
@@ -567,10 +567,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
           const uint32_t at = tri0 + kb * (kb + 1) / 2 * 512 + w * 512;
           ldsm4t(bh, at + R::ph);
           ldsm4t(bl, at + R::pl);
-          mma_f16(X[0], od[kb], bh[0], bh[1]);
-          mma_f16(X[1], od[kb], bh[2], bh[3]);
-          mma_f16(Z[0], od[kb], bl[0], bl[1]);
-          mma_f16(Z[1], od[kb], bl[2], bl[3]);
+          uint32_t o[4] = {od[kb][0], od[kb][1], od[kb][2], od[kb][3]};
+          if (low.x != 1.0f || low.y != 1.0f) scale_h2(o, low);
+          mma_f16(X[0], o, bh[0], bh[1]);
+          mma_f16(X[1], o, bh[2], bh[3]);
+          mma_f16(Z[0], o, bl[0], bl[1]);
+          mma_f16(Z[1], o, bl[2], bl[3]);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

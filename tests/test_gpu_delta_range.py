@@ -198,3 +198,43 @@ def test_value_channels_of_zeros(cuda_device, dt, D, H):
     # da is some 1e-7: in float16 a whole multiple of 2^-24, off by 2^-25, which assert_within counts
     assert_within("da", got["da"], ref["da"], HALF_P, HALF_P)
     check(xs, got | {"da": ref["da"].float()}, ref, T, D, half_p=HALF_P)
+
+
+FAR = {   # factors of the inputs; closed: no token writes; steep: gates of about e^-10
+    "dy_far_below_its_share_of_dk": (dict(dy=2e-24, k=7e-17, S=0), False, False),
+    "closed_and_large_dy": (dict(q=2e-8, dy=8e5, scale=4e4, k=4e-5, S=0), True, False),
+    "steep_and_tiny_scale": (dict(S=6e-19, scale=3e-18, k=5e-18), False, True),
+    "tiny_keys_queries_and_dS": (dict(q=9e-30, v=6, k=2e-23, dS=4e-29), False, False),
+}
+
+
+@pytest.mark.parametrize("D,H", SPREADS)
+@pytest.mark.parametrize("n", [8, 64, 130])
+@pytest.mark.parametrize("which", FAR)
+def test_factors_far_apart(cuda_device, which, n, D, H):
+    """Inputs of sizes so different that products of two of their scales are outside float32: no infinity, and every
+    gradient within the bounds of its largest value."""
+    fac, closed, steep = FAR[which]
+    x, S0, dS = draw("bf16", 1, n, H, D, seed=n, state=fac.get("S") != 0)
+    for m in ("q", "k", "v", "dy"):
+        x[m] = (x[m].float() * fac.get(m, 1)).to(x[m].dtype)
+    if S0 is not None:
+        S0, dS = S0 * fac.get("S", 1), dS * fac.get("dS", 1)
+    if closed:
+        x["b"].fill_(float("-inf"))
+    if steep:
+        x["a"] = x["a"] - 13
+    scale = D ** -0.5 * fac.get("scale", 1)
+    out = run(x, S0, dS, scale)
+    xs, got, _ = two_heads(x, S0, dS, out)
+    ref = delta_reference(*ins(xs), scale, None if S0 is None else S0[:, :2], xs["dy"], None if dS is None else dS[:, :2])
+    for name, t in got.items():
+        r = ref[name]
+        assert torch.isfinite(t).all(), name
+        # Steep gates leave db to the last token alone: db = (1 - beta) sum_c du_c u_c is off by 2^-11 sum_c |du_c u_c|,
+        # which is any multiple of one token's |db| (of a tensor's largest, a small one).
+        if steep and name == "db":
+            continue
+        if float(r.abs().max()) > 1e-33:   # else of some few digits itself
+            extra = HALF_P if t.dtype != torch.float32 else 2 * PER_TOKEN * n
+            assert_within(name, t, r, extra, extra)
