@@ -390,16 +390,16 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
     const uint32_t at = (blk * (blk + 1) / 2 + blk) * 512 + tile_off<32>(i, u);
     *reinterpret_cast<uint4 *>(smem + R::th + at) = hi;
     *reinterpret_cast<uint4 *>(smem + R::tl + at) = lo;
-  } else if (lane == 0) {
-    float first = 64.0f;
-    bool any = false;
-    for (int i = 63; i >= 0; --i) {
-      if (static_cast<int>(bad[i]) & 5) first = static_cast<float>(i);
-      any = any || bad[i] != 0.0f;
+  } else {   // warp 3
+    const int f0 = static_cast<int>(bad[lane]), f1 = static_cast<int>(bad[32 + lane]);
+    const unsigned lost0 = __ballot_sync(0xffffffffu, f0 & 5), lost1 = __ballot_sync(0xffffffffu, f1 & 5);
+    const bool any = __any_sync(0xffffffffu, f0 | f1);
+    if (lane == 0) {
+      const int first = lost0 ? __ffs(lost0) - 1 : lost1 ? 31 + __ffs(lost1) : 64;
+      float4 *fac = reinterpret_cast<float4 *>(smem + R::fac);
+      fac[0] = make_float4(expf(G[63] + Gl[63]), st.inv, sp.inv, static_cast<float>(first));
+      fac[1] = make_float4(sk.inv, sq.inv, sp.s, any ? __int_as_float(0x7fc00000) : st.inv);
     }
-    float4 *fac = reinterpret_cast<float4 *>(smem + R::fac);
-    fac[0] = make_float4(expf(G[63] + Gl[63]), st.inv, sp.inv, first);
-    fac[1] = make_float4(sk.inv, sq.inv, sp.s, any ? __int_as_float(0x7fc00000) : st.inv);
   }
   fence_proxy_async_smem();
   __syncthreads();
