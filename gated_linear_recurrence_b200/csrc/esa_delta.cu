@@ -196,6 +196,7 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
     c.S_in = S_init;
     c.S_out = S_final;
     c.keep = keep != 0;
+    c.least = least_output_unit(scale);
     if ((rc = launch_chunk_prep(dtype, c, st))) return rc;
     return launch_chunk_fwd(dtype, c, st);
   }
@@ -248,6 +249,7 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
     c.S_in = dS_final;
     c.S_out = dS_init;
     c.keep = true;
+    c.iscale = 1.0f / scale;   // not used where the scale is zero
     if ((rc = launch_chunk_bwd(dtype, c, st))) return rc;
     return launch_chunk_grad(dtype, c, st);
   }

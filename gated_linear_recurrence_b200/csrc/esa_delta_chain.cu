@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
     }
     // Y = scale (e^G S^T Q^T + U P^T); the first product joins the second's
     // sum, in its unit zu (see kLeastShare)
-    const OutputUnit ou0 = output_unit(xinv.x * fac.q, pu.inv.x, fac.p, fac.ps), ou1 = output_unit(xinv.y * fac.q, pu.inv.y, fac.p, fac.ps);
+    const OutputUnit ou0 = output_unit(xinv.x * fac.q, pu.inv.x, fac.p, fac.ps, p.least),
+                     ou1 = output_unit(xinv.y * fac.q, pu.inv.y, fac.p, fac.ps, p.least);
     const float2 us = make_float2(ou0.us, ou1.us), yf = mul2(make_float2(ou0.unit, ou1.unit), splat(p.s.scale));
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {

@@ -86,7 +86,6 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
       for (int e = 0; e < 4; ++e) S[nt][e] = 0.0f;
   }
 
-  const float iscale = 1.0f / fabsf(p.s.scale);
   fetch(nc - 1, 0);
 #pragma unroll 1
   for (int it = 0; it < nc; ++it) {
@@ -161,18 +160,19 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
       }
     }
     // dU^T = zf (X r + dO^T P) (see kLeastShare); without an output gradient's share (scale 0) P is left out
-    const float zp = p.s.scale * fac.p;
-    const bool with = zp != 0.0f;
+    const bool with = p.s.scale != 0.0f;
     const float2 xk = mul2(xinv, splat(fac.k));
-    const RowPow2 pd = pow2_scale(quad_max(top)), pz = with ? least_unit(pd, xk, iscale * fac.ps) : pd;
+    const RowPow2 pd = pow2_scale(quad_max(top)), pz = with ? least_unit(pd, xk, fabsf(p.iscale), fac.ps) : pd;
     const float2 low = mul2(pd.inv, pz.s);   // what the product with P takes of dO: 1 unless its unit is too small
-    const float2 zf = with ? mul2(pz.inv, splat(zp)) : splat(1.0f), yd = mul2(pd.inv, splat(p.s.scale));
+    const float2 zf = with ? make_float2(mul_pow2(p.s.scale, fac.p, pz.inv.x), mul_pow2(p.s.scale, fac.p, pz.inv.y)) : splat(1.0f);
+    const float2 yd = mul2(pd.inv, splat(p.s.scale));
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
       for (int e = 0; e < 4; ++e) od[kb][e] = pack2(mul2(unpack_io<T>(od[kb][e]), splat(e & 1 ? pd.s.y : pd.s.x)));
     {
-      const float2 r = make_float2(xk.x / zf.x, xk.y / zf.y);
+      // xk / zf; 1 / zf is at most 2^120
+      const float2 r = with ? mul2(xk, make_float2(mul_pow2(p.iscale, pz.s.x, fac.ps), mul_pow2(p.iscale, pz.s.y, fac.ps))) : xk;
 #pragma unroll
       for (int nt = 0; nt < 8; ++nt) {
         const float2 tl = *reinterpret_cast<const float2 *>(tok + kTokL * 64 + 8 * nt);

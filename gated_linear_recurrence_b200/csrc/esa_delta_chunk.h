@@ -22,6 +22,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstddef>
 
 #include "esa_delta.h"
@@ -75,7 +76,15 @@ struct ChunkArgs {
   const float *S_in;   // S_init, or dS_final for the backward chain
   float *S_out;        // S_final, or dS_init
   bool keep;
+  float least, iscale;   // of the scale: the least unit of an output (see output_unit), its inverse
 };
+
+// A power of two of 2^-120 / min(|scale|, 1) to twice that, 1 at most: its product with the scale keeps its digits too.
+inline float least_output_unit(float scale) {
+  int e = 0;
+  if (scale != 0.0f && fabsf(scale) < 1.0f) frexpf(scale, &e);   // 2^(e - 1) <= |scale| < 2^e
+  return ldexpf(1.0f, e > -119 ? -119 - e : 0);
+}
 
 int launch_chunk_prep(int dtype, const ChunkArgs &a, cudaStream_t st);
 int launch_chunk_fwd(int dtype, const ChunkArgs &a, cudaStream_t st);

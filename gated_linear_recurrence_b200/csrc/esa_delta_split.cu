@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
       sinv = make_float2(pow2_inverse(asc.x), pow2_inverse(asc.y));
     }
     const float2 xs = mul2(asc, splat(fac.k));
-    const OutputUnit ou0 = output_unit(xinv.x * fac.q, pu.inv.x, fac.p, fac.ps), ou1 = output_unit(xinv.y * fac.q, pu.inv.y, fac.p, fac.ps);
+    const OutputUnit ou0 = output_unit(xinv.x * fac.q, pu.inv.x, fac.p, fac.ps, p.least),
+                     ou1 = output_unit(xinv.y * fac.q, pu.inv.y, fac.p, fac.ps, p.least);
     const float2 us = make_float2(ou0.us, ou1.us), yf = mul2(make_float2(ou0.unit, ou1.unit), splat(p.s.scale));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -438,7 +439,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
   float S[NQ][4];
   float2 sinv = splat(1.0f);
   load_state<D>(S, p.S_in ? p.S_in + static_cast<long long>(head) * D * D : nullptr, dvw, w * (D / 4), g, t4);
-  const float iscale = 1.0f / fabsf(p.s.scale);
   fetch(nc - 1, 0);
 #pragma unroll 1
   for (int it = 0; it < nc; ++it) {
@@ -524,12 +524,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
       }
     }
     // the unit of the output gradient's share of dU^T (see kLeastShare); without a share (scale 0) P is left out
-    const float zp = p.s.scale * fac.p;
-    const bool with = zp != 0.0f;
+    const bool with = p.s.scale != 0.0f;
     const float2 xk = mul2(xinv, splat(fac.k));
-    const RowPow2 pd = pow2_scale(quad_max(topd)), pz = with ? least_unit(pd, xk, iscale * fac.ps) : pd;
+    const RowPow2 pd = pow2_scale(quad_max(topd)), pz = with ? least_unit(pd, xk, fabsf(p.iscale), fac.ps) : pd;
     const float2 low = mul2(pd.inv, pz.s);   // what the product with P takes of dO: 1 unless its unit is too small
-    const float2 zf = with ? mul2(pz.inv, splat(zp)) : splat(1.0f), yd = mul2(pd.inv, splat(p.s.scale));
+    const float2 zf = with ? make_float2(mul_pow2(p.s.scale, fac.p, pz.inv.x), mul_pow2(p.s.scale, fac.p, pz.inv.y)) : splat(1.0f);
+    const float2 yd = mul2(pd.inv, splat(p.s.scale));
+    // xk / zf; 1 / zf is at most 2^120
+    const float2 xr = with ? mul2(xk, make_float2(mul_pow2(p.iscale, pz.s.x, fac.ps), mul_pow2(p.iscale, pz.s.y, fac.ps))) : xk;
     float2 topo = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)
@@ -554,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float2 tl = *reinterpret_cast<const float2 *>(tok + kTokL * 64 + 16 * w + 8 * i);
-        set_lo(X[i], mul2(row_lo(X[i]), mul2(tl, splat(xk.x / zf.x))));
-        set_hi(X[i], mul2(row_hi(X[i]), mul2(tl, splat(xk.y / zf.y))));
+        set_lo(X[i], mul2(row_lo(X[i]), mul2(tl, splat(xr.x))));
+        set_hi(X[i], mul2(row_hi(X[i]), mul2(tl, splat(xr.y))));
       }
       if (with) {
         float Z[2][4];

@@ -139,23 +139,29 @@ __device__ __forceinline__ float2 update_scale(float2 upd, float2 top, float2 un
 }
 
 // The scale of an output gradient, `own`, such that the unit of its product, its
-// inverse times a factor of inverse `ishare`, is no smaller than kLeastShare
-// allows beside a product of unit `other`; a power of two.
-__device__ __forceinline__ Pow2 least_unit(Pow2 own, float other, float ishare) {
-  const float least = fminf(fmaxf(other * kLeastShare, kLeastUnit) * ishare, 2.5961484292674138e33f);   // 2^111
+// inverse times 1 / (a b), is no smaller than kLeastShare allows beside a product
+// of unit `other`; a power of two.
+__device__ __forceinline__ Pow2 least_unit(Pow2 own, float other, float a, float b) {
+  const float least = fminf(fmaxf(other * kLeastShare, kLeastUnit) * a * b, 2.5961484292674138e33f);   // 2^111
   if (!(least > own.inv)) return own;
   const float inv = __uint_as_float((__float_as_uint(least) & 0x7f800000u) + 0x00800000u);   // the next power of two
   return {pow2_inverse(inv), inv};
 }
 
+// x a b for powers of two a and b whose product alone may leave float32's range.
+__device__ __forceinline__ float mul_pow2(float x, float a, float b) {
+  const int e = static_cast<int>(__float_as_uint(a) >> 23) + static_cast<int>(__float_as_uint(b) >> 23) - 254, h = e >> 1;
+  return x * __uint_as_float(static_cast<uint32_t>(127 + h) << 23) * __uint_as_float(static_cast<uint32_t>(127 + e - h) << 23);
+}
+
 // Y = scale (e^G S^T Q^T + U P^T), formed as unit scale (r e^G (S^T Q^T) + (us U) P^T):
 // `xq` is the unit of S^T Q^T, `uinv` that of U by its own size, `p` that of P
-// (`ps` its inverse).
+// (`ps` its inverse), `least` the least of `unit` (ChunkArgs::least).
 struct OutputUnit {
   float us, unit, r;
 };
-__device__ __forceinline__ OutputUnit output_unit(float xq, float uinv, float p, float ps) {
-  uinv = fmaxf(uinv, fmaxf(xq * kLeastShare, kLeastUnit) * ps);
+__device__ __forceinline__ OutputUnit output_unit(float xq, float uinv, float p, float ps, float least) {
+  uinv = fmaxf(uinv, fmaxf(xq * kLeastShare, least) * ps);
   const float unit = p * uinv;
   return {pow2_inverse(uinv), unit, xq * pow2_inverse(unit)};
 }
@@ -170,9 +176,9 @@ __device__ __forceinline__ RowPow2 pow2_scale(float2 top) {
   const Pow2 a = pow2_scale(top.x), b = pow2_scale(top.y);
   return {make_float2(a.s, b.s), make_float2(a.inv, b.inv)};
 }
-__device__ __forceinline__ RowPow2 least_unit(RowPow2 own, float2 other, float ishare) {
-  const Pow2 a = least_unit(Pow2{own.s.x, own.inv.x}, other.x, ishare), b = least_unit(Pow2{own.s.y, own.inv.y}, other.y, ishare);
-  return {make_float2(a.s, b.s), make_float2(a.inv, b.inv)};
+__device__ __forceinline__ RowPow2 least_unit(RowPow2 own, float2 other, float a, float b) {
+  const Pow2 x = least_unit(Pow2{own.s.x, own.inv.x}, other.x, a, b), y = least_unit(Pow2{own.s.y, own.inv.y}, other.y, a, b);
+  return {make_float2(x.s, y.s), make_float2(x.inv, y.inv)};
 }
 // A state's unit, zero for a state of zeros (see kLeastShare).
 __device__ __forceinline__ float2 unit_or_zero(float2 top, float2 unit) {

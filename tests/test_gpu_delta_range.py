@@ -204,6 +204,8 @@ FAR = {   # factors of the inputs; closed: no token writes; steep: gates of abou
     "dy_far_below_its_share_of_dk": (dict(dy=2e-24, k=7e-17, S=0), False, False),
     "closed_and_large_dy": (dict(q=2e-8, dy=8e5, scale=4e4, k=4e-5, S=0), True, False),
     "steep_and_tiny_scale": (dict(S=6e-19, scale=3e-18, k=5e-18), False, True),
+    "tiny_keys_and_scale": (dict(scale=2e-12, k=1e-29), False, False),
+    "tiny_scale": (dict(scale=1e-25), False, False),
     "tiny_keys_queries_and_dS": (dict(q=9e-30, v=6, k=2e-23, dS=4e-29), False, False),
 }
 
