@@ -17,16 +17,17 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // Sequences of 16-bit types of at least this many tokens go through the
 // chunked kernels, shorter ones and float32 token by token.  A chunk costs the
 // same however few its tokens, a sweep goes by the token, and the gradients
-// have four sweeps.  Forward alone (us, chunked / token by token): 8 heads
-// 9.5 / 7.1 at T = 32 and D = 32, 10.2 / 8.8 at D = 64, 11.6 / 13.9 at D = 128;
-// 512 heads of D = 64 22 / 16 at T = 24, 22 / 20 at 32, 23 / 30 at 48.  With
-// the backward: 8 heads of D = 64 21 / 21 at T = 4, 21 / 25 at 8; 512 heads of
-// D = 64 54 / 47 at T = 8, 55 / 69 at 16; of D = 128 132 / 127 at T = 4, 133 /
-// 178 at 8.
-constexpr int kChunkMinT = 32, kChunkMinKeptT = 8;
-bool chunked(const DeltaShape &s, int dtype, bool keep) {
-  return dtype != ESA_F32 && s.T >= (keep ? kChunkMinKeptT : kChunkMinT);
-}
+// have four sweeps.  Forward alone (us, chunked / token by token):
+//             8 heads                         64 heads             512 heads
+//   D =  32   9.9 / 7.8 at T = 32, 9.9 / 9.9 at 40   10.2 / 9.9 at 40     16.2 / 10.4 at 40, 26.9 / 27.3 at 128
+//   D =  64   10.5 / 8.9 at 32, 10.4 / 11.3 at 40    11.4 / 11.4 at 40    21.7 / 20.8 at 32, 21.9 / 26.0 at 40
+//   D = 128   11.8 / 10.8 at 24, 11.9 / 13.3 at 32   13.8 / 14.0 at 24    48.2 / 55.6 at 16, 49.6 / 80.6 at 24
+// and with the backward:
+//   D =  32   21.0 / 19.4 at 12, 20.9 / 21.4 at 16   21.7 / 22.0 at 16    39.8 / 30.5 at 16, 40.0 / 37.7 at 24
+//   D =  64   22.6 / 19.2 at 8, 22.5 / 21.9 at 12    25.3 / 27.1 at 12    55.8 / 41.9 at 8, 56.0 / 50.7 at 12
+//   D = 128   28.0 / 23.4 at 8, 28.1 / 26.6 at 12    33.5 / 34.2 at 8     133 / 114 at 4, 134 / 162 at 8
+int chunk_min(int D, bool keep) { return keep ? (D == 32 ? 16 : D == 64 ? 12 : 8) : D == 128 ? 24 : 40; }
+bool chunked(const DeltaShape &s, int dtype, bool keep) { return dtype != ESA_F32 && s.T >= chunk_min(s.D, keep); }
 
 // Long float32 sequences of few heads: the states between chunks first, then
 // the sweeps of all chunks at once.  Forward (us, states first / one sweep): 8

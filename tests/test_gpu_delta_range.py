@@ -240,3 +240,14 @@ def test_factors_far_apart(cuda_device, which, n, D, H):
         if float(r.abs().max()) > 1e-33:   # else of some few digits itself
             extra = HALF_P if t.dtype != torch.float32 else 2 * PER_TOKEN * n
             assert_within(name, t, r, extra, extra)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("D,lengths", [(32, (15, 16, 39, 40)), (64, (11, 12, 39, 40)), (128, (7, 8, 23, 24))])
+def test_lengths_around_the_chunks_use(cuda_device, D, lengths, dt):
+    for n in lengths:
+        x, S0, dS = draw(dt, 2, n, 3, D, seed=n)
+        ref = delta_reference(*ins(x), D ** -0.5, S0, x["dy"], dS)
+        check(x, run(x, S0, dS, None), ref, n, D, half_p=HALF_P)
+        y, S, _ = esa_delta_fwd(*ins(x), S_init=S0, keep=False)
+        check(x, {"y": y, "S": S}, ref, n, D, gradients=False, half_p=HALF_P)
