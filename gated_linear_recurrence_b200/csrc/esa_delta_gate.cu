@@ -13,8 +13,8 @@
 // with S the state entering the chunk and dS the gradient of the one leaving
 // it: seven products of 64 rows in float32 multiply-adds, by a block a chunk.
 // Training with long memory does not pay for them: 8 heads of D = 64, T = 4096,
-// 645 us with the backward at logits around 4 and 724 around 0; 256 heads of
-// D = 32, T = 512, 399 and 509.
+// 646 us with the backward at logits around 4 and 698 around 0; 256 heads of
+// D = 32, T = 512, 393 and 528.
 #include "esa_delta_sweep.cuh"
 
 #include "esa.h"
@@ -85,100 +85,117 @@ __device__ __forceinline__ void state_dots(float *out, const float *f, const flo
   __syncthreads();
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) delta_gate_kernel(FinishArgs p) {
-  using L = GateSmem<D>;
-  constexpr int kParts = D * D / 1024;   // of <dS, S> at the chunk's end
-  extern __shared__ __align__(16) float sm[];
-  const int tid = threadIdx.x, lane = tid & 31, head = blockIdx.x / p.nc;
-  const Place a = sweep::place_of(p.s, p.nc, head, blockIdx.x - head * p.nc);
+// Two tokens a lane: the logits, and whether a gate of the chunk forgets.
+template <typename T>
+__device__ __forceinline__ bool read_logits(const FinishArgs &p, const Place &a, float (&logit)[2]) {
   const T *ga = static_cast<const T *>(p.a) + a.row * p.s.ld_g + a.h;
-  float logit[2];   // of tokens 2 lane and 2 lane + 1: every warp has all gates of the chunk
   bool forgets = false;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int i = 2 * lane + e;
+    const int i = 2 * (threadIdx.x & 31) + e;
     logit[e] = i < a.len ? sweep::clamp(sweep::widen(ga[i * p.s.ld_g])) : 80.0f;
     forgets = forgets || !(sweep::gate(logit[e]) >= kForgets);
   }
-  float f[2];
-  if (!__any_sync(0xffffffffu, forgets)) {
-    if (tid >= 32) return;
-    const float *gain = p.gain + static_cast<long long>(head) * p.s.T + a.t0;
-    float end = 0.0f;
-    for (int i = 0; i < kParts; ++i) end += p.end[a.chunk * kParts + i];
-    const float x0 = 2 * lane < a.len ? gain[2 * lane] : 0.0f, x1 = 2 * lane + 1 < a.len ? gain[2 * lane + 1] : 0.0f;
-    float sum = x0 + x1;
+  return __any_sync(0xffffffffu, forgets);
+}
+
+template <typename T>
+__device__ __forceinline__ void write_da(const FinishArgs &p, const Place &a, const float (&f)[2], const float (&logit)[2]) {
+  T *da = static_cast<T *>(p.da) + a.row * p.s.H + a.h;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float y = __shfl_down_sync(0xffffffffu, sum, o);
-      if (lane + o < 32) sum += y;
+  for (int e = 0; e < 2; ++e) {
+    const int i = 2 * (threadIdx.x & 31) + e;
+    if (i < a.len) da[static_cast<long long>(i) * p.s.H] = sweep::narrow<T>(f[e] / (1.0f + expf(logit[e])));   // 1 - alpha = 1 / (1 + e^a)
+  }
+}
+
+// The running sums, by one warp.
+template <typename T, int D>
+__device__ __forceinline__ void light_chunk(const FinishArgs &p, const Place &a, const float (&logit)[2]) {
+  constexpr int kParts = D * D / 1024;   // of <dS, S> at the chunk's end
+  const int lane = threadIdx.x & 31;
+  const float *gain = p.gain + (static_cast<long long>(a.b) * p.s.H + a.h) * p.s.T + a.t0;
+  float end = 0.0f, f[2];
+  for (int i = 0; i < kParts; ++i) end += p.end[a.chunk * kParts + i];
+  const float x0 = 2 * lane < a.len ? gain[2 * lane] : 0.0f, x1 = 2 * lane + 1 < a.len ? gain[2 * lane + 1] : 0.0f;
+  float sum = x0 + x1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float y = __shfl_down_sync(0xffffffffu, sum, o);
+    if (lane + o < 32) sum += y;
+  }
+  const float after = __shfl_down_sync(0xffffffffu, sum, 1);
+  f[1] = end + (lane < 31 ? after : 0.0f) + x1;
+  f[0] = f[1] + x0;
+  write_da<T>(p, a, f, logit);
+}
+
+// The terms that have the factor alpha, by the block.
+template <typename T, int D>
+__device__ __forceinline__ void heavy_chunk(const FinishArgs &p, const Place &a, float *sm) {
+  using L = GateSmem<D>;
+  const int tid = threadIdx.x, lane = tid & 31;
+  float *X = sm + L::x, *Y = sm + L::y, *W = sm + L::w, *beta = sm + L::beta, *as = sm + L::as, *bs = sm + L::bs,
+        *fq = sm + L::fq, *fk = sm + L::fk, *fb = sm + L::fb, *part = sm + L::part;
+  float2 *G = reinterpret_cast<float2 *>(sm + L::g);
+  const long long ldc = static_cast<long long>(p.s.H) * D, own = a.row * ldc + a.h * D;
+  const T *q = static_cast<const T *>(p.q) + a.row * p.s.ld_qk + a.h * D, *k = static_cast<const T *>(p.k) + a.row * p.s.ld_qk + a.h * D;
+  const T *dy = static_cast<const T *>(p.dy) + own;
+  const float *S = p.S_ck + a.chunk * (D * D), *dS = p.dS_ck + a.chunk * (D * D);
+  const int ti = tid >> 4, tj = tid & 15;
+  sweep::gates_of<T>(p.s, p.a, p.b, a, G, beta);
+  rows_in<T, D>(X, q, p.s.ld_qk, a.len);
+  rows_in<T, D>(Y, k, p.s.ld_qk, a.len);
+  __syncthreads();
+  if (tid < C) {
+    const float2 zero = make_float2(0.0f, 0.0f);
+    const float into = decay(G[tid], zero);
+    as[tid] = bs[tid] = 0.0f;
+    fq[tid] = p.s.scale * into;
+    fk[tid] = -beta[tid] * into;
+    fb[tid] = decay(G[C - 1], G[tid]);
+  }
+  float qk[4][4], kk[4][4], z[4][4];
+  sweep::dots<D>(X, Y, ti, tj, qk);
+  sweep::dots<D>(Y, Y, ti, tj, kk);
+  __syncthreads();
+  rows_in<T, D>(X, dy, ldc, a.len);
+  rows_in<float, D>(Y, p.u + own, ldc, a.len);
+  __syncthreads();
+  sweep::dots<D>(X, Y, ti, tj, z);
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) qk[r][c] *= p.s.scale * z[r][c];
+  __syncthreads();
+  rows_in<float, D>(X, p.du + own, ldc, a.len);
+  __syncthreads();
+  sweep::dots<D>(X, Y, ti, tj, z);
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int i = ti + 16 * r, j = tj + 16 * c;
+      W[i * kTri + j] = j < i ? decay(G[i], G[j]) * fmaf(-beta[i] * kk[r][c], z[r][c], qk[r][c]) : 0.0f;
     }
-    const float after = __shfl_down_sync(0xffffffffu, sum, 1);
-    f[1] = end + (lane < 31 ? after : 0.0f) + x1;
-    f[0] = f[1] + x0;
-  } else {
-    float *X = sm + L::x, *Y = sm + L::y, *W = sm + L::w, *beta = sm + L::beta, *as = sm + L::as, *bs = sm + L::bs,
-          *fq = sm + L::fq, *fk = sm + L::fk, *fb = sm + L::fb, *part = sm + L::part;
-    float2 *G = reinterpret_cast<float2 *>(sm + L::g);
-    const long long ldc = static_cast<long long>(p.s.H) * D, own = a.row * ldc + a.h * D;
-    const T *q = static_cast<const T *>(p.q) + a.row * p.s.ld_qk + a.h * D, *k = static_cast<const T *>(p.k) + a.row * p.s.ld_qk + a.h * D;
-    const T *dy = static_cast<const T *>(p.dy) + own;
-    const float *S = p.S_ck + a.chunk * (D * D), *dS = p.dS_ck + a.chunk * (D * D);
-    const int ti = tid >> 4, tj = tid & 15;
-    sweep::gates_of<T>(p.s, p.a, p.b, a, G, beta);
-    rows_in<T, D>(X, q, p.s.ld_qk, a.len);
-    rows_in<T, D>(Y, k, p.s.ld_qk, a.len);
-    __syncthreads();
-    if (tid < C) {
-      const float2 zero = make_float2(0.0f, 0.0f);
-      const float into = decay(G[tid], zero);
-      as[tid] = bs[tid] = 0.0f;
-      fq[tid] = p.s.scale * into;
-      fk[tid] = -beta[tid] * into;
-      fb[tid] = decay(G[C - 1], G[tid]);
-    }
-    float qk[4][4], kk[4][4], z[4][4];
-    sweep::dots<D>(X, Y, ti, tj, qk);
-    sweep::dots<D>(Y, Y, ti, tj, kk);
-    __syncthreads();
-    rows_in<T, D>(X, dy, ldc, a.len);
-    rows_in<float, D>(Y, p.u + own, ldc, a.len);
-    __syncthreads();
-    sweep::dots<D>(X, Y, ti, tj, z);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) qk[r][c] *= p.s.scale * z[r][c];
-    __syncthreads();
-    rows_in<float, D>(X, p.du + own, ldc, a.len);
-    __syncthreads();
-    sweep::dots<D>(X, Y, ti, tj, z);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int i = ti + 16 * r, j = tj + 16 * c;
-        W[i * kTri + j] = j < i ? decay(G[i], G[j]) * fmaf(-beta[i] * kk[r][c], z[r][c], qk[r][c]) : 0.0f;
-      }
-    state_dots<T, D>(as, fk, X, Y, S, k, p.s.ld_qk, a.len);   // X: du
-    rows_in<T, D>(X, dy, ldc, a.len);
-    state_dots<T, D>(as, fq, X, Y, S, q, p.s.ld_qk, a.len);
-    rows_in<float, D>(X, p.u + own, ldc, a.len);
-    state_dots<T, D>(bs, fb, X, Y, dS, k, p.s.ld_qk, a.len);
-    float c = 0.0f;
-    for (int i = tid * 4; i < D * D; i += kThreads * 4) {
-      const float4 s4 = *reinterpret_cast<const float4 *>(S + i), d4 = *reinterpret_cast<const float4 *>(dS + i);
-      c = fmaf(s4.x, d4.x, fmaf(s4.y, d4.y, fmaf(s4.z, d4.z, fmaf(s4.w, d4.w, c))));
-    }
-    c = head_sum<32>(c);
-    if (lane == 0) part[tid >> 5] = c;
-    if (tid < C) {   // column j of W: the sum over s >= i in the place of row i, for the rectangles with j < i
-      float x = 0.0f;
-      for (int i = C - 1; i > tid; --i) W[i * kTri + tid] = x += W[i * kTri + tid];
-    }
-    __syncthreads();
-    if (tid >= 32) return;
+  state_dots<T, D>(as, fk, X, Y, S, k, p.s.ld_qk, a.len);   // X: du
+  rows_in<T, D>(X, dy, ldc, a.len);
+  state_dots<T, D>(as, fq, X, Y, S, q, p.s.ld_qk, a.len);
+  rows_in<float, D>(X, p.u + own, ldc, a.len);
+  state_dots<T, D>(bs, fb, X, Y, dS, k, p.s.ld_qk, a.len);
+  float c = 0.0f;
+  for (int i = tid * 4; i < D * D; i += kThreads * 4) {
+    const float4 s4 = *reinterpret_cast<const float4 *>(S + i), d4 = *reinterpret_cast<const float4 *>(dS + i);
+    c = fmaf(s4.x, d4.x, fmaf(s4.y, d4.y, fmaf(s4.z, d4.z, fmaf(s4.w, d4.w, c))));
+  }
+  c = head_sum<32>(c);
+  if (lane == 0) part[tid >> 5] = c;
+  if (tid < C) {   // column j of W: the sum over s >= i in the place of row i, for the rectangles with j < i
+    float x = 0.0f;
+    for (int i = C - 1; i > tid; --i) W[i * kTri + tid] = x += W[i * kTri + tid];
+  }
+  __syncthreads();
+  if (tid < 32) {
     float A[2], B[2], F[2], cc = 0.0f;
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) cc += part[i];
@@ -205,14 +222,35 @@ __global__ void __launch_bounds__(kThreads) delta_gate_kernel(FinishArgs p) {
     }
     const float behind = __shfl_down_sync(0xffffffffu, later, 1), before = __shfl_up_sync(0xffffffffu, earlier, 1);
     const float b0 = lane > 0 ? before : 0.0f, a1 = (lane < 31 ? behind : 0.0f) + A[1];
-    f[0] = F[0] + (later + b0 + cc);
-    f[1] = F[1] + (a1 + (b0 + B[0]) + cc);
+    float logit[2];
+    read_logits<T>(p, a, logit);
+    const float f[2] = {F[0] + (later + b0 + cc), F[1] + (a1 + (b0 + B[0]) + cc)};
+    write_da<T>(p, a, f, logit);
   }
-  T *da = static_cast<T *>(p.da) + a.row * p.s.H + a.h;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int i = 2 * lane + e;
-    if (i < a.len) da[static_cast<long long>(i) * p.s.H] = sweep::narrow<T>(f[e] / (1.0f + expf(logit[e])));   // 1 - alpha = 1 / (1 + e^a)
+}
+
+// Each warp looks at one of the block's `group` chunks; those with a gate that
+// forgets are left to the whole block, one after another.  4096 chunks of long
+// memory take 7.5 us so, 25 with a block a chunk; 2048 that forget 136 and 122.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) delta_gate_kernel(FinishArgs p, int chunks, int group) {
+  extern __shared__ __align__(16) float sm[];
+  __shared__ unsigned heavy;
+  const int warp = threadIdx.x >> 5, first = blockIdx.x * group;
+  if (threadIdx.x == 0) heavy = 0;
+  __syncthreads();
+  if (warp < group && first + warp < chunks) {
+    const int head = (first + warp) / p.nc;
+    const Place a = sweep::place_of(p.s, p.nc, head, first + warp - head * p.nc);
+    float logit[2];
+    if (!read_logits<T>(p, a, logit)) light_chunk<T, D>(p, a, logit);
+    else if ((threadIdx.x & 31) == 0) atomicOr(&heavy, 1u << warp);
+  }
+  __syncthreads();
+  for (unsigned left = heavy; left != 0; left &= left - 1) {
+    const int c = first + __ffs(left) - 1, head = c / p.nc;
+    heavy_chunk<T, D>(p, sweep::place_of(p.s, p.nc, head, c - head * p.nc), sm);
+    __syncthreads();
   }
 }
 
@@ -220,11 +258,14 @@ template <typename T, int D>
 int run(const FinishArgs &a, cudaStream_t st) {
   auto kern = delta_gate_kernel<T, D>;
   constexpr int bytes = GateSmem<D>::total * 4;
-  if (bytes > 48 * 1024) {
+  if (bytes > 47 * 1024) {   // 48 KB with the static part
     const int rc = runtime_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
     if (rc) return rc;
   }
-  kern<<<static_cast<unsigned>(a.s.B) * a.s.H * a.nc, kThreads, bytes, st>>>(a);
+  const int chunks = a.s.B * a.s.H * a.nc;
+  int group = chunks / (4 * sm_count());   // four blocks an SM at least, where there are as many chunks
+  group = group < 1 ? 1 : group > kThreads / 32 ? kThreads / 32 : group;
+  kern<<<(chunks + group - 1) / group, kThreads, bytes, st>>>(a, chunks, group);
   return runtime_status(cudaGetLastError());
 }
 
