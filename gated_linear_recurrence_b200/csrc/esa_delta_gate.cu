@@ -231,7 +231,8 @@ __device__ __forceinline__ void heavy_chunk(const FinishArgs &p, const Place &a,
 
 // Each warp looks at one of the block's `group` chunks; those with a gate that
 // forgets are left to the whole block, one after another.  4096 chunks of long
-// memory take 7.5 us so, 25 with a block a chunk; 2048 that forget 136 and 122.
+// memory take 7.5 us so, 25 with a block a chunk; with 2048 that all forget a
+// whole pass takes 528 us, 509 with a block a chunk.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) delta_gate_kernel(FinishArgs p, int chunks, int group) {
   extern __shared__ __align__(16) float sm[];

@@ -22,8 +22,8 @@ _DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 def _rows(name, t, like=None):
     """Elements between consecutive rows of a tensor [..., N] whose rows are
     contiguous and evenly spaced."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor (the ESA library has no CPU path)")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() < 1:
+        raise TypeError(f"{name} must be a CUDA tensor [..., N] (the ESA library has no CPU path)")
     if like is not None and (t.shape != like.shape or t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must have shape {tuple(like.shape)}, dtype {like.dtype}, {like.device}")
     N = int(t.shape[-1])

@@ -389,7 +389,8 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
 /*
  * Backward: gradients of sum(dy . y) + sum(dS_final . S_final) with respect to
  * q, k, v, a, b and S_init.  The inputs and the workspace are those of the
- * matching esa_delta_fwd with keep = 1, unchanged since.  With dS the gradient
+ * matching esa_delta_fwd with keep = 1, unchanged since; outputs overlap no
+ * input, but dS_init may be dS_final.  With dS the gradient
  * of S_t from later tokens, dS += scale q_t dy_t^T, then
  *     du = dS^T k,  dv = beta du,  dk = dS u - alpha beta S_{t-1} du,
  *     dq = scale S_t dy,  db = (du.u)(1 - beta),
@@ -408,8 +409,8 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
 
 /* One token: q_t, k_t, v_t [B,H,D] with rows ld_qk and ld_v elements apart,
  * a_t, b_t [B,H] ld_g apart (strides and alignment as above), y_t [B,H,D]
- * contiguous; S [B,H,D,D] float32 is read and overwritten.  Needs no
- * workspace. */
+ * contiguous and apart from the inputs; S [B,H,D,D] float32 is read and
+ * overwritten.  Needs no workspace. */
 int esa_delta_step(const void *q_t, const void *k_t, long long ld_qk, const void *v_t, long long ld_v,
                    const void *a_t, const void *b_t, long long ld_g, float *S, void *y_t, int B, int H, int D,
                    float scale, int dtype, void *stream);

@@ -6,7 +6,7 @@ outputs three float16 roundings of intermediates.
 import pytest
 import torch
 
-from gated_linear_recurrence_b200 import esa_delta_fwd, esa_delta_step
+from gated_linear_recurrence_b200 import esa_delta_bwd, esa_delta_fwd, esa_delta_step
 from tests._delta_reference import PER_TOKEN, assert_within, delta_reference
 from tests.test_gpu_delta import check, draw, ins, run
 
@@ -251,3 +251,27 @@ def test_lengths_around_the_chunks_use(cuda_device, D, lengths, dt):
         check(x, run(x, S0, dS, None), ref, n, D, half_p=HALF_P)
         y, S, _ = esa_delta_fwd(*ins(x), S_init=S0, keep=False)
         check(x, {"y": y, "S": S}, ref, n, D, gradients=False, half_p=HALF_P)
+
+
+@pytest.mark.parametrize("dt,D,H", [("bf16", *s) for s in SPREADS] + [("f32", 64, 2), ("f32", 32, 80)])
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_scales_of_zero_and_below(cuda_device, scale, dt, D, H):
+    x, S0, dS = draw(dt, 1, T, H, D, seed=14)
+    out = run(x, S0, dS, scale)
+    xs, got, _ = two_heads(x, S0, dS, out)
+    ref = delta_reference(*ins(xs), scale, S0[:, :2], xs["dy"], dS[:, :2])
+    if scale == 0.0:
+        assert not got["y"].any() and not got["dq"].any()
+    check(xs, got, ref, T, D, half_p=HALF_P)
+
+
+@pytest.mark.parametrize("dt,D,H,n", [("bf16", 128, 2, 150), ("bf16", 64, 80, 70), ("bf16", 32, 2, 9), ("f32", 64, 2, 40),
+                                      ("f32", 64, 2, 300)])
+def test_state_gradient_over_the_final_one(cuda_device, dt, D, H, n):
+    x, S0, dS = draw(dt, 1, n, H, D, seed=15)
+    _, _, ws = esa_delta_fwd(*ins(x), S_init=S0)
+    want = esa_delta_bwd(*ins(x), x["dy"], ws, S_init=S0, dS_final=dS)
+    got = esa_delta_bwd(*ins(x), x["dy"], ws, S_init=S0, dS_final=dS, dS_init=dS)   # the workspace is read again
+    assert got[5] is dS
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
