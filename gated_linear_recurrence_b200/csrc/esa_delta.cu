@@ -50,7 +50,7 @@ struct DeltaLayout {
   size_t u = 0, S_ck = 0, dS_ck = 0, du = 0, dk = 0, dq = 0, gain = 0, end = 0, dk2 = 0, wt = 0, u0 = 0, fac = 0, total = 0;
 };
 // The chunk arrays, laid out from `base`; `*total` gets their size.
-ChunkArrays chunk_arrays(unsigned char *base, const DeltaShape &s, bool keep, size_t *total) {
+ChunkArrays chunk_arrays(unsigned char *base, const DeltaShape &s, int dtype, bool keep, size_t *total) {
   ChunkArrays w{};
   w.nc = (s.T + kChunk - 1) / kChunk;
   const size_t n = static_cast<size_t>(s.B) * s.H * w.nc;
@@ -66,6 +66,10 @@ ChunkArrays chunk_arrays(unsigned char *base, const DeltaShape &s, bool keep, si
     const size_t D = s.D;
     w.u16 = reinterpret_cast<__half *>(take(n * 64 * D * 2));
     w.r16 = reinterpret_cast<__half *>(take(n * 64 * D * 2));
+    if (dtype == ESA_F16) {
+      w.u16l = reinterpret_cast<__half *>(take(n * 64 * D * 2));
+      w.r16l = reinterpret_cast<__half *>(take(n * 64 * D * 2));
+    }
     w.s16 = reinterpret_cast<__half *>(take(n * D * D * 2));
     w.ds16 = reinterpret_cast<__half *>(take(n * D * D * 2));
     w.slice = reinterpret_cast<float *>(take(n * 32 * sizeof(float)));
@@ -165,7 +169,7 @@ size_t esa_delta_workspace_size(int B, int T, int H, int D, int dtype, int keep)
   const DeltaShape s{B, T, H, D, 0, 0, 0, 1.0f};
   size_t total = 0;
   if (chunked(s, dtype, keep != 0)) {
-    chunk_arrays(nullptr, s, keep != 0, &total);
+    chunk_arrays(nullptr, s, dtype, keep != 0, &total);
     return total + 256;
   }
   return delta_layout(s, dtype, keep != 0).total + 256;
@@ -191,7 +195,7 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
     ChunkArgs c{};
     size_t total;
     c.s = s;
-    c.w = chunk_arrays(static_cast<unsigned char *>(workspace), s, keep != 0, &total);
+    c.w = chunk_arrays(static_cast<unsigned char *>(workspace), s, dtype, keep != 0, &total);
     c.q = q; c.k = k; c.v = v; c.a = a; c.b = b;
     c.y = y;
     c.S_in = S_init;
@@ -244,7 +248,7 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
     ChunkArgs c{};
     size_t total;
     c.s = s;
-    c.w = chunk_arrays(base, s, true, &total);
+    c.w = chunk_arrays(base, s, dtype, true, &total);
     c.q = q; c.k = k; c.v = v; c.a = a; c.b = b; c.dy = dy;
     c.dq = dq; c.dk = dk; c.dv = dv; c.da = da; c.db = db;
     c.S_in = dS_final;

@@ -383,10 +383,24 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
         stsm4t(vw + 16 * kb * L::kRow, o);
       }
       __syncwarp();
-      __half *ur = p.w.u16 + (c * 64 + (lane >> 1)) * D + dvw + 8 * (lane & 1);
+      const long long ur = (c * 64 + (lane >> 1)) * D + dvw + 8 * (lane & 1);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4 *>(ur + 16 * i * D) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
+        *reinterpret_cast<uint4 *>(p.w.u16 + ur + 16 * i * D) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
+      if constexpr (kTwo) {   // and the second term
+        __syncwarp();
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          uint32_t hi[4], lo[4];
+          split_rows(U[2 * kb], U[2 * kb + 1], splat(pus.s), hi, lo);
+          const uint32_t o[4] = {lo[0], lo[2], lo[1], lo[3]};
+          stsm4t(vw + 16 * kb * L::kRow, o);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4 *>(p.w.u16l + ur + 16 * i * D) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
+      }
     }
     __syncthreads();   // the next turn's copies overwrite this buffer
   }

@@ -11,7 +11,7 @@
 // and dv = beta du.  What enters dS keeps float32 accuracy (two float16 terms,
 // K, Q and dO exact), because dS_init is float32.  dS and du are left for the
 // second kernel (esa_delta_grad.cu) in float16, one power of two per 16
-// channels.
+// channels; du of float16 tensors in two terms.
 //
 // A key or query that is not finite makes du of its chunk NaN, and with it all
 // that the chunk adds to dS.
@@ -330,10 +330,24 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_bwd_kernel(ChunkArgs p)
       stsm4t(vw + 16 * np * L::kRow, o);
     }
     __syncwarp();
-    __half *ur = p.w.r16 + (c * 64 + (lane >> 1)) * D + dvw + 8 * (lane & 1);
+    const long long ur = (c * 64 + (lane >> 1)) * D + dvw + 8 * (lane & 1);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4 *>(ur + 16 * i * D) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
+      *reinterpret_cast<uint4 *>(p.w.r16 + ur + 16 * i * D) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
+    if constexpr (std::is_same<T, __half>::value) {   // and the second term
+      __syncwarp();
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t hi[4], lo[4];
+        split_rows(U[2 * np], U[2 * np + 1], splat(pus.s), hi, lo);
+        const uint32_t o[4] = {lo[0], lo[2], lo[1], lo[3]};
+        stsm4t(vw + 16 * np * L::kRow, o);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(p.w.r16l + ur + 16 * i * D) = *reinterpret_cast<const uint4 *>(vr + 16 * i * L::kRow);
+    }
     if (lane == 0) p.w.slice[c * 32 + kSliceR + (dvw >> 4)] = slice_unit(allu, pus);
     __syncthreads();
   }

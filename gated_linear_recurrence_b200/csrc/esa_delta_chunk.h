@@ -14,6 +14,7 @@
 //   g      [2][64] float32         running sums of log alpha, two terms
 // and, kept for the backward or written by it,
 //   u16, r16   [64][D] float16     u and du (token rows), one power of two per 16 channels
+//   u16l, r16l [64][D] float16     their second terms (float16 tensors)
 //   s16, ds16  [D][D] float16      state entering the chunk and gradient of the state leaving it
 //                                  (row: value channel), one power of two per 16 rows
 //   slice      [4][8] float32      inverses of those powers of two (0 for a group of zeros, NaN for one that is not finite)
@@ -63,7 +64,7 @@ enum { kSliceU = 0, kSliceR = 8, kSliceS = 16, kSliceDs = 24 };   // rows of `sl
 
 struct ChunkArrays {
   unsigned char *rec;
-  __half *u16, *r16, *s16, *ds16;
+  __half *u16, *r16, *u16l, *r16l, *s16, *ds16;
   float *slice;
   int nc;
 };

@@ -23,14 +23,20 @@
 // cores too.
 //
 // These are outputs in 16 bits: S, dS, U, du, dP and N are operands in one
-// float16 term each (2^-12 of a value on average, against 2^-9 for a bfloat16
-// output and 2^-12 for a float16 one).
+// float16 term each (2^-12 of a value on average) where the output is bfloat16
+// (2^-9).  For a float16 output (2^-12) U, du, dP and N are in two, so that of
+// each product's operands one is rounded, S or dS, at most: with one term each
+// dq, dk and db were 3.7e-4 off in the 2-norm, where the output's rounding alone
+// is 2.1e-4; now dq and dk are at 2.4e-4 and db at 2.1e-4, for 25% more time of
+// this kernel.  (S and dS in two as well would be 64 KB more a chunk at D = 128.)
 //
 // A persistent block takes chunk after chunk.  Warp (m, cw) has 16 tokens and
 // a share of the channels.  U, du and dO of the next chunk are copied while
 // this one is computed (two buffers), its S and dS as soon as this one's have
 // been used, then its K and Q; so copies of 190 KB a chunk (D = 128) run under
 // 2,500 mma.
+#include <type_traits>
+
 #include "esa_delta_chunk.h"
 #include "esa_delta_sweep.cuh"
 #include "esa_mma.cuh"
@@ -41,15 +47,20 @@
 namespace esa {
 namespace {
 
-template <int D>
+// TWO: U, du, dP and N in two terms.  Then a chunk's rows have one buffer where
+// two of them do not fit (D = 128) or keep a second block off the SM (D = 64).
+template <int D, bool TWO>
 struct GradShape {
   static constexpr int threads = D == 128 ? 512 : 256;
   static constexpr int CW = threads / 128;          // shares of the channels
   static constexpr int row = 64 * D * 2, mat = D * D * 2;
   static constexpr int hdr = ChunkRecord<D>::k + 512 + 128;   // per-token factors, running sums, slice scales
-  static constexpr int k = 0, q = row, s = 2 * row, ds = s + mat, dp = ds + mat, n = dp + 8192, buf = n + 8192,
-                       u = 0, r = row, o = 2 * row, h = 3 * row, stage = 3 * row + hdr, vec = buf + 2 * stage,
+  static constexpr int stages = TWO && D >= 64 ? 1 : 2;
+  static constexpr int k = 0, q = row, s = 2 * row, ds = s + mat, dp = ds + mat, n = dp + 8192, lo = 16384,   // lo: from a tile to its second term
+                       h = n + 8192 + (TWO ? lo : 0), buf = h + 2 * hdr,
+                       u = 0, r = row, o = 2 * row, ul = 3 * row, rl = 4 * row, stage = (TWO ? 5 : 3) * row, vec = buf + stages * stage,
                        total = vec + (64 + 64 + 2 * CW * 64 + 9 * 64 + 64) * 4;
+  static_assert(hdr % 128 == 0 && total <= 227 * 1024, "headers between tiles; a block's shared memory");
 };
 
 __device__ __forceinline__ void scale_frag(uint32_t (&a)[4], float f) {
@@ -144,9 +155,13 @@ __device__ __forceinline__ void edge_sums(const float (&w)[2][4], float *rows, f
   }
 }
 
+template <typename T>
+constexpr bool two_terms() { return std::is_same<T, __half>::value; }
+
 template <typename T, int D>
-__global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta_grad_kernel(ChunkArgs p, int chunks) {
-  using L = GradShape<D>;
+__global__ void __launch_bounds__(GradShape<D, two_terms<T>()>::threads, D == 128 ? 1 : 2) delta_grad_kernel(ChunkArgs p, int chunks) {
+  constexpr bool kTwo = two_terms<T>();
+  using L = GradShape<D, kTwo>;
   using R = ChunkRecord<D>;
   constexpr int kThreads = L::threads, CW = L::CW;
   constexpr int NH = D / (8 * CW);   // accumulator tiles of a share of the channels
@@ -171,7 +186,11 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
   int nb = 0, nh = 0, nt0 = 0;              // place of the chunk whose rows were fetched last
   auto fetch_rows = [&](int c, int buf) {   // U, du, dO and the header
     if (c < chunks) {
-      const uint32_t st = s0 + L::buf + buf * L::stage;
+      const uint32_t st = s0 + L::buf + (L::stages == 2 ? buf : 0) * L::stage, hd = s0 + L::h + buf * L::hdr;
+      if constexpr (kTwo) {
+        copy_rows<D * 2, 64, kThreads>(st + L::ul, p.w.u16l + static_cast<long long>(c) * (64 * D));
+        copy_rows<D * 2, 64, kThreads>(st + L::rl, p.w.r16l + static_cast<long long>(c) * (64 * D));
+      }
       copy_rows<D * 2, 64, kThreads>(st + L::u, p.w.u16 + static_cast<long long>(c) * (64 * D));
       copy_rows<D * 2, 64, kThreads>(st + L::r, p.w.r16 + static_cast<long long>(c) * (64 * D));
       place(c, nb, nh, nt0);
@@ -186,10 +205,10 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
           cp_async16_zfill(st + L::o + tile_off<D * 2>(rr, u), rr < len ? dy + rr * ldc : static_cast<const T *>(p.dy), rr < len);
       }
       const unsigned char *rec = p.w.rec + static_cast<long long>(c) * R::bytes;
-      if (tid < R::k / 16) cp_async16_s(st + L::h + tid * 16, rec + tid * 16);
-      else if (tid >= 128 && tid < 160) cp_async16_s(st + L::h + R::k + (tid - 128) * 16, rec + R::g + (tid - 128) * 16);
+      if (tid < R::k / 16) cp_async16_s(hd + tid * 16, rec + tid * 16);
+      else if (tid >= 128 && tid < 160) cp_async16_s(hd + R::k + (tid - 128) * 16, rec + R::g + (tid - 128) * 16);
       else if (tid >= 160 && tid < 168)
-        cp_async16_s(st + L::h + R::k + 512 + (tid - 160) * 16, p.w.slice + static_cast<long long>(c) * 32 + (tid - 160) * 4);
+        cp_async16_s(hd + R::k + 512 + (tid - 160) * 16, p.w.slice + static_cast<long long>(c) * 32 + (tid - 160) * 4);
     }
     sweep::cp_async_commit();
   };
@@ -219,13 +238,14 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
     const int b = nb, h = nh, t0 = nt0;
     const int len = min(kChunk, p.s.T - t0);
     const long long row = static_cast<long long>(b) * p.s.T + t0;
-    const uint32_t bo = L::buf + buf * L::stage;
+    const uint32_t bo = L::buf + (L::stages == 2 ? buf : 0) * L::stage;
     unsigned char *sb = smem + bo;
-    const float *tok = reinterpret_cast<const float *>(sb + L::h);
-    const float *G = reinterpret_cast<const float *>(sb + L::h + R::k), *Gl = G + 64;
+    const unsigned char *hd = smem + L::h + buf * L::hdr;
+    const float *tok = reinterpret_cast<const float *>(hd);
+    const float *G = reinterpret_cast<const float *>(hd + R::k), *Gl = G + 64;
     sweep::cp_async_wait<2>();   // rows of this chunk
     __syncthreads();
-    fetch_rows(next, buf ^ 1);
+    if constexpr (L::stages == 2) fetch_rows(next, buf ^ 1);
     T la[2], lb[2];              // warp 0: the gates' logits, for the end
     la[0] = la[1] = lb[0] = lb[1] = sweep::narrow<T>(0.0f);
     if (warp == 0) {
@@ -264,7 +284,7 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
     float part, uinv, rinv, sinv, dsinv;   // 0 for zeros
     bool flat;
     {
-      float v = (lane & 7) < KS ? reinterpret_cast<const float *>(sb + L::h + R::k + 512)[lane] : 0.0f;
+      float v = (lane & 7) < KS ? reinterpret_cast<const float *>(hd + R::k + 512)[lane] : 0.0f;
       float t = v;
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
@@ -276,7 +296,7 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
       sinv = __shfl_sync(0xffffffffu, t, kSliceS);
       dsinv = __shfl_sync(0xffffffffu, t, kSliceDs);
     }
-    const float *fac = reinterpret_cast<const float *>(sb + L::h + R::fac);
+    const float *fac = reinterpret_cast<const float *>(hd + R::fac);
     const float last = fac[kFacLast], kinv = fac[kFacK], qinv = fac[kFacQ];
     __syncthreads();
 
@@ -291,13 +311,15 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
       if (NPA * cw <= m) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          uint32_t ao[4], ar[4];
+          uint32_t ao[4], ar[4], al[4];
           ldsm4(ao, ofd.at(0, ks) + bo + L::o + 16 * m * D * 2);
           ldsm4(ar, ofd.at(0, ks) + bo + L::r + 16 * m * D * 2);
+          if constexpr (kTwo) ldsm4(al, ofd.at(0, ks) + bo + L::rl + 16 * m * D * 2);
           if (!flat) {
-            const float fu = __shfl_sync(0xffffffffu, part, kSliceU + ks);
+            const float fu = __shfl_sync(0xffffffffu, part, kSliceU + ks), fr = fu * __shfl_sync(0xffffffffu, part, kSliceR + ks);
             scale_frag(ao, fu);
-            scale_frag(ar, fu * __shfl_sync(0xffffffffu, part, kSliceR + ks));
+            scale_frag(ar, fr);
+            if constexpr (kTwo) scale_frag(al, fr);
           }
 #pragma unroll
           for (int np = 0; np < NPA; ++np) {
@@ -308,6 +330,15 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
             mma_f16(P[2 * np + 1], ao, bu[2], bu[3]);
             mma_f16(N[2 * np], ar, bu[0], bu[1]);
             mma_f16(N[2 * np + 1], ar, bu[2], bu[3]);
+            if constexpr (kTwo) {
+              mma_f16(N[2 * np], al, bu[0], bu[1]);
+              mma_f16(N[2 * np + 1], al, bu[2], bu[3]);
+              ldsm4(bu, ofb.at(np, ks) + bo + L::ul + 16 * NPA * cw * D * 2);
+              mma_f16(P[2 * np], ao, bu[0], bu[1]);
+              mma_f16(P[2 * np + 1], ao, bu[2], bu[3]);
+              mma_f16(N[2 * np], ar, bu[0], bu[1]);
+              mma_f16(N[2 * np + 1], ar, bu[2], bu[3]);
+            }
           }
         }
       }
@@ -343,7 +374,7 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
         red[warp] = topp;
         red[32 + warp] = topn;
       }
-      sweep::cp_async_wait<1>();   // S, dS, K and Q
+      sweep::cp_async_wait<L::stages - 1>();   // S, dS, K and Q
       __syncthreads();
 #pragma unroll
       for (int np = 0; np < NPA; ++np) {   // W, from Q K^T and K K^T
@@ -395,8 +426,14 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const uint32_t o = tile_off<128>(i0 + (e >> 1) * 8, 2 * NPA * cw + nt) + 4 * t4;
-          *reinterpret_cast<uint32_t *>(smem + L::dp + o) = pack_h2(P[nt][e] * pp.s, P[nt][e + 1] * pp.s);
-          *reinterpret_cast<uint32_t *>(smem + L::n + o) = pack_h2(N[nt][e] * pn.s, N[nt][e + 1] * pn.s);
+          const float2 x = mul2(make_float2(P[nt][e], P[nt][e + 1]), splat(pp.s)), y = mul2(make_float2(N[nt][e], N[nt][e + 1]), splat(pn.s));
+          if constexpr (kTwo) {
+            split2(x, *reinterpret_cast<uint32_t *>(smem + L::dp + o), *reinterpret_cast<uint32_t *>(smem + L::dp + L::lo + o));
+            split2(y, *reinterpret_cast<uint32_t *>(smem + L::n + o), *reinterpret_cast<uint32_t *>(smem + L::n + L::lo + o));
+          } else {
+            *reinterpret_cast<uint32_t *>(smem + L::dp + o) = pack2(x);
+            *reinterpret_cast<uint32_t *>(smem + L::n + o) = pack2(y);
+          }
         }
     }
     __syncthreads();
@@ -418,15 +455,24 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
     // dO S^T, du S^T and U dS^T; S and dS are stored [value channel][key channel]
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      uint32_t ao[4], ar[4], au[4];
+      uint32_t ao[4], ar[4], au[4], rl[4], ul[4];
       ldsm4(ao, ofd.at(0, ks) + bo + L::o + 16 * m * D * 2);
       ldsm4(ar, ofd.at(0, ks) + bo + L::r + 16 * m * D * 2);
       ldsm4(au, ofd.at(0, ks) + bo + L::u + 16 * m * D * 2);
+      if constexpr (kTwo) {
+        ldsm4(rl, ofd.at(0, ks) + bo + L::rl + 16 * m * D * 2);
+        ldsm4(ul, ofd.at(0, ks) + bo + L::ul + 16 * m * D * 2);
+      }
       if (!flat) {
-        const float fs = __shfl_sync(0xffffffffu, part, kSliceS + ks);
+        const float fs = __shfl_sync(0xffffffffu, part, kSliceS + ks), fr = fs * __shfl_sync(0xffffffffu, part, kSliceR + ks);
+        const float fu = __shfl_sync(0xffffffffu, part, kSliceU + ks) * __shfl_sync(0xffffffffu, part, kSliceDs + ks);
         scale_frag(ao, fs);
-        scale_frag(ar, fs * __shfl_sync(0xffffffffu, part, kSliceR + ks));
-        scale_frag(au, __shfl_sync(0xffffffffu, part, kSliceU + ks) * __shfl_sync(0xffffffffu, part, kSliceDs + ks));
+        scale_frag(ar, fr);
+        scale_frag(au, fu);
+        if constexpr (kTwo) {
+          scale_frag(rl, fr);
+          scale_frag(ul, fu);
+        }
       }
 #pragma unroll
       for (int np = 0; np < NH / 2; ++np) {
@@ -439,6 +485,12 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
         mma_f16(K[2 * np + 1], ar, bs[2], bs[3]);
         mma_f16(X[2 * np], au, bd[0], bd[1]);
         mma_f16(X[2 * np + 1], au, bd[2], bd[3]);
+        if constexpr (kTwo) {
+          mma_f16(K[2 * np], rl, bs[0], bs[1]);
+          mma_f16(K[2 * np + 1], rl, bs[2], bs[3]);
+          mma_f16(X[2 * np], ul, bd[0], bd[1]);
+          mma_f16(X[2 * np + 1], ul, bd[2], bd[3]);
+        }
       }
     }
     if (warp < KS) {   // <dS, S> of 16 rows: the diagonal of dS S^T
@@ -462,7 +514,8 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
       if (!flat) x *= __shfl_sync(0xffffffffu, part, kSliceS + warp) * __shfl_sync(0xffffffffu, part, kSliceDs + warp);
       if (lane == 0) red[16 + warp] = x;
     }
-    __syncthreads();             // S and dS have been used
+    __syncthreads();             // S and dS have been used, and U, du and dO
+    if constexpr (L::stages == 1) fetch_rows(next, buf ^ 1);
     fetch_states(next);
     {   // the sums so far, in the units of what joins them
       const float e0 = expf(G[i0] + Gl[i0]), e1 = expf(G[i0 + 8] + Gl[i0 + 8]);
@@ -517,6 +570,13 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
       ldsm4(an, of64.at(0, kb) + L::n + 16 * m * 128);
       if (fpk != 1.0f) scale_frag(ap, fpk);
       if (fnk != 1.0f) scale_frag(an, fnk);
+      uint32_t pl[4], nl[4];
+      if constexpr (kTwo) {
+        ldsm4(pl, of64.at(0, kb) + L::dp + L::lo + 16 * m * 128);
+        ldsm4(nl, of64.at(0, kb) + L::n + L::lo + 16 * m * 128);
+        if (fpk != 1.0f) scale_frag(pl, fpk);
+        if (fnk != 1.0f) scale_frag(nl, fnk);
+      }
 #pragma unroll
       for (int np = 0; np < NH / 2; ++np) {
         uint32_t bk[4];
@@ -525,6 +585,12 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
         mma_f16(Q[2 * np + 1], ap, bk[2], bk[3]);
         mma_f16(K[2 * np], an, bk[0], bk[1]);
         mma_f16(K[2 * np + 1], an, bk[2], bk[3]);
+        if constexpr (kTwo) {
+          mma_f16(Q[2 * np], pl, bk[0], bk[1]);
+          mma_f16(Q[2 * np + 1], pl, bk[2], bk[3]);
+          mma_f16(K[2 * np], nl, bk[0], bk[1]);
+          mma_f16(K[2 * np + 1], nl, bk[2], bk[3]);
+        }
       }
     }
     const int col0 = cw * NH * 8 + (lane & 1 ? 8 : 0) + 2 * (t4 & 2);   // this thread's first channel in a pair of tiles
@@ -537,22 +603,30 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
       if (kb < m) continue;
-      uint32_t rp[4], rn[4];
       const uint32_t at = s0 + tile_off<128>(16 * kb + (lane & 15), 2 * m + (lane >> 4));
-      ldsm4t(rp, at + L::dp);
-      ldsm4t(rn, at + L::n);
-      uint32_t ap[4] = {rp[0], rp[2], rp[1], rp[3]}, an[4] = {rn[0], rn[2], rn[1], rn[3]};
-      if (fpq != 1.0f) scale_frag(ap, fpq);
-      if (fnk != 1.0f) scale_frag(an, fnk);
+      uint32_t ap[2][4], an[2][4];   // terms
+#pragma unroll
+      for (int x = 0; x < (kTwo ? 2 : 1); ++x) {
+        uint32_t rp[4], rn[4];
+        ldsm4t(rp, at + L::dp + x * L::lo);
+        ldsm4t(rn, at + L::n + x * L::lo);
+        ap[x][0] = rp[0]; ap[x][1] = rp[2]; ap[x][2] = rp[1]; ap[x][3] = rp[3];
+        an[x][0] = rn[0]; an[x][1] = rn[2]; an[x][2] = rn[1]; an[x][3] = rn[3];
+        if (fpq != 1.0f) scale_frag(ap[x], fpq);
+        if (fnk != 1.0f) scale_frag(an[x], fnk);
+      }
 #pragma unroll
       for (int np = 0; np < NH / 2; ++np) {
         uint32_t bk[4], bq[4];
         ldsm4t(bk, cols(kb, np) + L::k);
         ldsm4t(bq, cols(kb, np) + L::q);
-        mma_f16(K[2 * np], an, bk[0], bk[1]);
-        mma_f16(K[2 * np + 1], an, bk[2], bk[3]);
-        mma_f16(K[2 * np], ap, bq[0], bq[1]);
-        mma_f16(K[2 * np + 1], ap, bq[2], bq[3]);
+#pragma unroll
+        for (int x = 0; x < (kTwo ? 2 : 1); ++x) {
+          mma_f16(K[2 * np], an[x], bk[0], bk[1]);
+          mma_f16(K[2 * np + 1], an[x], bk[2], bk[3]);
+          mma_f16(K[2 * np], ap[x], bq[0], bq[1]);
+          mma_f16(K[2 * np + 1], ap[x], bq[2], bq[3]);
+        }
       }
     }
 #pragma unroll
@@ -615,7 +689,7 @@ __global__ void __launch_bounds__(GradShape<D>::threads, D == 128 ? 1 : 2) delta
 
 template <typename T, int D>
 int run(const ChunkArgs &a, cudaStream_t st) {
-  using L = GradShape<D>;
+  using L = GradShape<D, two_terms<T>()>;
   auto kern = delta_grad_kernel<T, D>;
   int rc = runtime_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total));
   if (rc) return rc;

@@ -403,6 +403,15 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
         stsm4t(vw, u);
         __syncwarp();
         *reinterpret_cast<uint4 *>(p.w.u16 + (c * 64 + r) * D + dvw + 8 * (lane & 1)) = *reinterpret_cast<const uint4 *>(vr);
+        if constexpr (kTwo) {   // and the second term
+          uint32_t hi[4], lo[4];
+          split_rows(Uo[0], Uo[1], splat(pus.s), hi, lo);
+          const uint32_t ul[4] = {lo[0], lo[2], lo[1], lo[3]};
+          __syncwarp();
+          stsm4t(vw, ul);
+          __syncwarp();
+          *reinterpret_cast<uint4 *>(p.w.u16l + (c * 64 + r) * D + dvw + 8 * (lane & 1)) = *reinterpret_cast<const uint4 *>(vr);
+        }
         if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceU + slice] = cut ? __int_as_float(0x7fc00000) : slice_unit(all, pus);
       }
     }
@@ -697,6 +706,15 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs 
       stsm4t(vw, u);
       __syncwarp();
       *reinterpret_cast<uint4 *>(p.w.r16 + (c * 64 + r) * D + dvw + 8 * (lane & 1)) = *reinterpret_cast<const uint4 *>(vr);
+      if constexpr (std::is_same<T, __half>::value) {   // and the second term
+        uint32_t hi[4], lo[4];
+        split_rows(Uo[0], Uo[1], splat(pus.s), hi, lo);
+        const uint32_t ul[4] = {lo[0], lo[2], lo[1], lo[3]};
+        __syncwarp();
+        stsm4t(vw, ul);
+        __syncwarp();
+        *reinterpret_cast<uint4 *>(p.w.r16l + (c * 64 + r) * D + dvw + 8 * (lane & 1)) = *reinterpret_cast<const uint4 *>(vr);
+      }
       if (threadIdx.x == 0) p.w.slice[c * 32 + kSliceR + slice] = slice_unit(allu, pus);
     }
     __syncthreads();

@@ -369,8 +369,8 @@ int esa_step(const void *a_t, const void *v_t, const void *q_t, float *E, void *
  * what esa_delta_bwd reads and its scratch).  0 on a bad argument.  Sequences
  * of 16-bit types go in chunks of 64 tokens, from 8 (D = 128), 12 or 16 (D = 32)
  * tokens on with keep, from 24 (D = 128) or 40 without, whose operands and states
- * are kept there: at D = 128 3.4 times the bytes of q without keep and 9.4 with,
- * at D = 64 4.8 and 8.8.  Between those lengths calls with and without keep differ
+ * are kept there: at D = 128 3.4 times the bytes of q without keep and 9.4 with
+ * (float16 11.4), at D = 64 4.7 and 8.7 (10.7).  Between those lengths calls with and without keep differ
  * by their roundings, in y (16-bit) and S_final.  float32
  * sequences of few heads keep their chunks' states from 192 tokens on.  The
  * workspace needs no initialisation and can be reused by any later call; two
