@@ -16,8 +16,9 @@
 // Rounding.  What enters the state keeps float32 accuracy: S, R, U and T are
 // operands in two float16 terms each (22 bits, esa_mma.cuh), K is exact, sums
 // are float32.  The output's own product takes S, U and P in one float16 term
-// (2^-12 of a value on average) when the output is bfloat16 (2^-9), and S and
-// U in two when it is float16, P in one.
+// (2^-12 of a value on average) when the output is bfloat16 (2^-9), and in two
+// when it is float16 (y 2.1e-4 off in the 2-norm, as its rounding alone; with P
+// in one term 2.8e-4).
 //
 // A chunk costs a warp 400 mma at D = 128 (130 of them off the chain).  The
 // issue rate of mma.sync (8 clocks per m16n8k16 and SM quarter, measured 550
@@ -38,11 +39,11 @@
 namespace esa {
 namespace {
 
-template <int D, int W>
+template <int D, int W, bool TWO>   // TWO: with the second term of P
 struct ChainSmem {
   using R = ChunkRecord<D>;
   static constexpr int kRow = 32 * W;   // bytes of a value row of the block
-  static constexpr int v = R::pl, stage = v + 64 * kRow;
+  static constexpr int v = TWO ? R::g : R::pl, stage = v + 64 * kRow;
   static constexpr int total = 2 * stage;
 };
 
@@ -85,10 +86,10 @@ __device__ __noinline__ void poison_rows(unsigned char *tile, int unit, int firs
 
 template <typename T, int D, int W, bool KEEP>
 __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p) {
-  using L = ChainSmem<D, W>;
+  constexpr bool kTwo = std::is_same<T, __half>::value;    // two terms in the output's product
+  using L = ChainSmem<D, W, kTwo>;
   using R = ChunkRecord<D>;
   constexpr int NT = D / 8;                                // accumulator tiles of the state
-  constexpr bool kTwo = std::is_same<T, __half>::value;    // two terms in the output's product
   extern __shared__ __align__(128) unsigned char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
   constexpr int SL = D / (16 * W);
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
 
   auto fetch = [&](int n, int buf) {
     const uint32_t s = s0 + buf * L::stage;
-    copy_linear<R::pl, W * 32>(s, p.w.rec + (c0 + n) * R::bytes);
+    copy_linear<L::v, W * 32>(s, p.w.rec + (c0 + n) * R::bytes);
     const int len = min(kChunk, p.s.T - n * kChunk);
     const T *src = v + (row0 + n * kChunk) * p.s.ld_v;
 #pragma unroll
@@ -352,6 +353,9 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
         if constexpr (kTwo) {
           mma_f16(Y[2 * np], ul, bp[0], bp[1]);
           mma_f16(Y[2 * np + 1], ul, bp[2], bp[3]);
+          ldsm4(bp, tri0 + tri(np, kb) + R::pl);
+          mma_f16(Y[2 * np], uh[kb], bp[0], bp[1]);
+          mma_f16(Y[2 * np + 1], uh[kb], bp[2], bp[3]);
         }
       }
     }
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(W * 32, 1) delta_chain_fwd_kernel(ChunkArgs p)
 
 template <typename T, int D, int W, bool KEEP>
 int run(const ChunkArgs &a, cudaStream_t st) {
-  using L = ChainSmem<D, W>;
+  using L = ChainSmem<D, W, std::is_same<T, __half>::value>;
   auto kern = delta_chain_fwd_kernel<T, D, W, KEEP>;
   const int rc = runtime_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total));
   if (rc) return rc;

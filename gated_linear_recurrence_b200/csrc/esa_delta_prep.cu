@@ -30,6 +30,8 @@
 //
 // The record (esa_delta_chunk.h) is put together in shared memory and leaves
 // in one bulk copy.
+#include <type_traits>
+
 #include "esa_delta_chunk.h"
 #include "esa_delta_sweep.cuh"
 #include "esa_mma.cuh"
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(ChunkArgs p) {
   __syncthreads();
   if (tid == 0) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p.w.rec + c * R::bytes),
-                 "r"(smem_u32(smem)), "r"(p.keep ? R::bytes : R::pl)
+                 "r"(smem_u32(smem)), "r"(p.keep ? R::bytes : std::is_same<T, __half>::value ? R::g : R::pl)   // what the forward reads
                  : "memory");
     bulk_commit();
     bulk_wait_read0();

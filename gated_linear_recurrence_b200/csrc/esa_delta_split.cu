@@ -31,10 +31,10 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kTileF = 32 * 16;   // bytes of an accumulator tile of a warp: a float4 a lane
 
-template <int D, bool BWD>
+template <int D, bool BWD, bool TWO>   // TWO: the forward's with the second term of P
 struct SplitSmem {
   using R = ChunkRecord<D>;
-  static constexpr int rows = BWD ? R::bytes : R::pl;           // v (dy) rows, 32 bytes each
+  static constexpr int rows = BWD ? R::bytes : TWO ? R::g : R::pl;   // v (dy) rows, 32 bytes each
   static constexpr int stage = rows + 64 * 32;
   static constexpr int part = 2 * stage;                        // [warp][tile] partial sums
   static constexpr int party = part + 32 * kTileF;              // the output's (forward)
@@ -94,10 +94,10 @@ __device__ __forceinline__ void store_state(const float (&S)[D / 32][4], float2 
 
 template <typename T, int D, bool KEEP>
 __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs p) {
-  using L = SplitSmem<D, false>;
+  constexpr bool kTwo = std::is_same<T, __half>::value;
+  using L = SplitSmem<D, false, kTwo>;
   using R = ChunkRecord<D>;
   constexpr int KQ = D / 64, NQ = D / 32;   // k-steps and accumulator tiles of a quarter of the key channels
-  constexpr bool kTwo = std::is_same<T, __half>::value;
   extern __shared__ __align__(128) unsigned char smem[];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
   const int head = blockIdx.x / (D / 16), slice = blockIdx.x % (D / 16), dvw = 16 * slice;
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
 
   auto fetch = [&](int n, int buf) {
     const uint32_t s = s0 + buf * L::stage;
-    copy_linear<R::pl, kThreads>(s, p.w.rec + (c0 + n) * R::bytes);
+    copy_linear<L::rows, kThreads>(s, p.w.rec + (c0 + n) * R::bytes);
     const int len = min(kChunk, p.s.T - n * kChunk), r = threadIdx.x >> 1;   // 64 rows of two units
     cp_async16_zfill(s + L::rows + tile_off<32>(r, threadIdx.x & 1),
                      r < len ? v + (row0 + n * kChunk + r) * p.s.ld_v : v, r < len);
@@ -366,6 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
         if constexpr (kTwo) {
           mma_f16(Yo[0], ul, bp[0], bp[1]);
           mma_f16(Yo[1], ul, bp[2], bp[3]);
+          ldsm4(bp, tri0 + (w * (w + 1) / 2 + kb) * 512 + R::pl);
+          mma_f16(Yo[0], uh, bp[0], bp[1]);
+          mma_f16(Yo[1], uh, bp[2], bp[3]);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) own[e] = uh[e];   // the last one is this warp's own tokens
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_split_fwd_kernel(ChunkArgs 
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) delta_split_bwd_kernel(ChunkArgs p) {
-  using L = SplitSmem<D, true>;
+  using L = SplitSmem<D, true, false>;
   using R = ChunkRecord<D>;
   constexpr int KQ = D / 64, NQ = D / 32;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -732,12 +735,12 @@ int launch(K kern, int smem, const ChunkArgs &a, cudaStream_t st) {
 
 template <typename T, int D>
 int fwd(const ChunkArgs &a, cudaStream_t st) {
-  return a.keep ? launch(delta_split_fwd_kernel<T, D, true>, SplitSmem<D, false>::total, a, st)
-                : launch(delta_split_fwd_kernel<T, D, false>, SplitSmem<D, false>::total, a, st);
+  constexpr int smem = SplitSmem<D, false, std::is_same<T, __half>::value>::total;
+  return a.keep ? launch(delta_split_fwd_kernel<T, D, true>, smem, a, st) : launch(delta_split_fwd_kernel<T, D, false>, smem, a, st);
 }
 template <typename T, int D>
 int bwd(const ChunkArgs &a, cudaStream_t st) {
-  return launch(delta_split_bwd_kernel<T, D>, SplitSmem<D, true>::total, a, st);
+  return launch(delta_split_bwd_kernel<T, D>, SplitSmem<D, true, false>::total, a, st);
 }
 
 }  // namespace

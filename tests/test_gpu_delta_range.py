@@ -279,13 +279,13 @@ def test_state_gradient_over_the_final_one(cuda_device, dt, D, H, n):
 
 @pytest.mark.parametrize("D,H", SPREADS)
 @pytest.mark.parametrize("n", [64, 300])
-def test_float16_gradients_near_their_rounding(cuda_device, n, D, H):
+def test_float16_results_near_their_rounding(cuda_device, n, D, H):
     """Of each product's operands one is rounded to float16, S or dS, so a gradient's error is at most sqrt(2) times that
     of its own rounding in the 2-norm.  (Not da's: its sum's parts, <dS, S> and those of earlier and later tokens, are each
     off by so much of their own size and may cancel; it is held in test_delta_gate_gradient.)"""
     x, S0, dS = draw("f16", 1, n, H, D, seed=16, a_mean=4.0)
     xs, got, ref = two_heads(x, S0, dS, run(x, S0, dS, D ** -0.5))
-    for name, times in (("dv", 1.1), ("dq", 1.5), ("dk", 1.5), ("db", 1.5)):
+    for name, times in (("y", 1.1), ("dv", 1.1), ("dq", 1.5), ("dk", 1.5), ("db", 1.5)):
         r = ref[name]
         own = float((r.half().double() - r).norm())
         off = float((got[name].cpu().double() - r).norm())
