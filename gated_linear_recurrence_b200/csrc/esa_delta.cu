@@ -4,6 +4,7 @@
 #include "esa_delta_chunk.h"
 
 #include <climits>
+#include <cmath>
 
 #include "esa.h"
 #include "esa_host.h"
@@ -132,6 +133,9 @@ int check_rows(long long ld, long long least, int dtype) {
   return (ld * elem(dtype)) % 16 ? ESA_ERR_ALIGN : ESA_OK;
 }
 
+// A scale below the normal range has no inverse in float32: it counts as zero.
+float normal(float s) { return fabsf(s) < 1.17549435e-38f ? 0.0f : s; }
+
 int check_scale(float s) { return s == s && s < 3.0e38f && s > -3.0e38f ? ESA_OK : ESA_ERR_ARG; }
 
 // Shape, strides and the five inputs of a sequence call.
@@ -178,7 +182,7 @@ size_t esa_delta_workspace_size(int B, int T, int H, int D, int dtype, int keep)
 int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, long long ld_v, const void *a,
                   const void *b, long long ld_g, void *y, float *S_final, int B, int T, int H, int D, float scale,
                   const float *S_init, int dtype, int keep, void *workspace, size_t workspace_bytes, void *stream) {
-  const DeltaShape s{B, T, H, D, ld_qk, ld_v, ld_g, scale};
+  const DeltaShape s{B, T, H, D, ld_qk, ld_v, ld_g, normal(scale)};
   int rc = check_inputs(s, dtype, q, k, v, a, b);
   if (rc) return rc;
   if (keep != 0 && keep != 1) return ESA_ERR_ARG;
@@ -201,7 +205,7 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
     c.S_in = S_init;
     c.S_out = S_final;
     c.keep = keep != 0;
-    c.least = least_output_unit(scale);
+    c.least = least_output_unit(s.scale);
     if ((rc = launch_chunk_prep(dtype, c, st))) return rc;
     return launch_chunk_fwd(dtype, c, st);
   }
@@ -227,7 +231,7 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
                   const void *b, long long ld_g, const void *dy, const float *dS_final, void *dq, void *dk, void *dv,
                   void *da, void *db, float *dS_init, int B, int T, int H, int D, float scale, const float *S_init,
                   int dtype, void *workspace, size_t workspace_bytes, void *stream) {
-  const DeltaShape s{B, T, H, D, ld_qk, ld_v, ld_g, scale};
+  const DeltaShape s{B, T, H, D, ld_qk, ld_v, ld_g, normal(scale)};
   int rc = check_inputs(s, dtype, q, k, v, a, b);
   if (rc) return rc;
   if (B > 0 && T > 0 && (!dy || !dq || !dk || !dv || !da || !db)) return ESA_ERR_ARG;
@@ -254,7 +258,7 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
     c.S_in = dS_final;
     c.S_out = dS_init;
     c.keep = true;
-    c.iscale = 1.0f / scale;   // not used where the scale is zero
+    c.iscale = 1.0f / s.scale;   // not used where the scale is zero
     if ((rc = launch_chunk_bwd(dtype, c, st))) return rc;
     return launch_chunk_grad(dtype, c, st);
   }
@@ -294,7 +298,7 @@ int esa_delta_bwd(const void *q, const void *k, long long ld_qk, const void *v, 
 int esa_delta_step(const void *q_t, const void *k_t, long long ld_qk, const void *v_t, long long ld_v,
                    const void *a_t, const void *b_t, long long ld_g, float *S, void *y_t, int B, int H, int D,
                    float scale, int dtype, void *stream) {
-  const DeltaShape s{B, 1, H, D, ld_qk, ld_v, ld_g, scale};
+  const DeltaShape s{B, 1, H, D, ld_qk, ld_v, ld_g, normal(scale)};
   int rc = check_inputs(s, dtype, q_t, k_t, v_t, a_t, b_t);
   if (rc) return rc;
   if (B > 0 && (!S || !y_t)) return ESA_ERR_ARG;

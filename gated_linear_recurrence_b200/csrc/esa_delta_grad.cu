@@ -72,6 +72,12 @@ __device__ __forceinline__ void scale_frag(uint32_t (&a)[4], float f) {
   }
 }
 
+// x a b of two units, whose product may leave float32's range where that with x does not.
+__device__ __forceinline__ float mul3(float x, float a, float b) {
+  const float ab = a * b;
+  return ab >= 1.17549435e-38f && ab <= 8.507059173023462e37f ? x * ab : x * a * b;   // 2^-126, 2^126
+}
+
 // Two neighbouring accumulator tiles times f, rounded, as 8-byte stores: lanes
 // exchange as in store_block.  `o` is the thread's first element of a pair.
 template <typename T>
@@ -347,8 +353,8 @@ __global__ void __launch_bounds__(GradShape<D, two_terms<T>()>::threads, D == 12
       float fp[2], fn[2], gi[2], gli[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        fp[e] = p.s.scale * oinv[i0 + 8 * e] * uinv;
-        fn[e] = -(e ? be1 : be0) * ru;
+        fp[e] = mul3(p.s.scale, oinv[i0 + 8 * e], uinv);
+        fn[e] = -mul3(e ? be1 : be0, rinv, uinv);
         gi[e] = G[i0 + 8 * e];
         gli[e] = Gl[i0 + 8 * e];
       }
@@ -416,8 +422,8 @@ __global__ void __launch_bounds__(GradShape<D, two_terms<T>()>::threads, D == 12
       const float omax = warp_max(fmaxf(oinv[lane], oinv[32 + lane]));
       const float bmax = warp_max(fmaxf(tok[kTokBeta * 64 + lane], tok[kTokBeta * 64 + 32 + lane]));
       const float pk = topp > 0.0f ? pp.inv * kinv : 0.0f, pq = topp > 0.0f ? pp.inv * qinv : 0.0f, nk = topn > 0.0f ? pn.inv * kinv : 0.0f;
-      uq = fmaxf(fmaxf(pk, kLeastUnit), fabsf(p.s.scale) * omax * sinv * (1024.0f * kLeastShare));
-      uk = fmaxf(fmaxf(fmaxf(nk, pq), kLeastUnit), rinv * bmax * sinv * (1024.0f * kLeastShare));
+      uq = fmaxf(fmaxf(pk, kLeastUnit), mul3(fabsf(p.s.scale), omax, sinv) * (1024.0f * kLeastShare));
+      uk = fmaxf(fmaxf(fmaxf(nk, pq), kLeastUnit), mul3(bmax, rinv, sinv) * (1024.0f * kLeastShare));
       fpk = pk / uq;
       fpq = pq / uk;
       fnk = nk / uk;
@@ -519,9 +525,9 @@ __global__ void __launch_bounds__(GradShape<D, two_terms<T>()>::threads, D == 12
     fetch_states(next);
     {   // the sums so far, in the units of what joins them
       const float e0 = expf(G[i0] + Gl[i0]), e1 = expf(G[i0 + 8] + Gl[i0 + 8]);
-      const float fs = p.s.scale * sinv, fk = -rinv * sinv, iq = 1.0f / uq, ik = 1.0f / uk;
-      const float q0 = fs * oinv[i0] * iq * e0, q1 = fs * oinv[i0 + 8] * iq * e1;
-      const float k0 = fk * be0 * ik * e0, k1 = fk * be1 * ik * e1;
+      const float iq = 1.0f / uq, ik = 1.0f / uk;
+      const float q0 = mul3(p.s.scale, oinv[i0], sinv) * iq * e0, q1 = mul3(p.s.scale, oinv[i0 + 8], sinv) * iq * e1;
+      const float k0 = -mul3(be0, rinv, sinv) * ik * e0, k1 = -mul3(be1, rinv, sinv) * ik * e1;
 #pragma unroll
       for (int i = 0; i < NH; ++i) {
         set_lo(Q[i], mul2(row_lo(Q[i]), splat(q0)));

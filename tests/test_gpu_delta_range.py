@@ -204,6 +204,8 @@ FAR = {   # factors of the inputs; closed: no token writes; steep: gates of abou
     "dy_far_below_its_share_of_dk": (dict(dy=2e-24, k=7e-17, S=0), False, False),
     "closed_and_large_dy": (dict(q=2e-8, dy=8e5, scale=4e4, k=4e-5, S=0), True, False),
     "steep_and_tiny_scale": (dict(S=6e-19, scale=3e-18, k=5e-18), False, True),
+    "tiny_dy_and_scale_and_large_v": (dict(q=1e-4, v=1e17, dy=7e-26, scale=4e-23, S=0), False, False),
+    "closed_and_large_states": (dict(q=3e-10, v=7e-11, S=9e15, dS=1e22), True, False),
     "tiny_keys_and_scale": (dict(scale=2e-12, k=1e-29), False, False),
     "tiny_scale": (dict(scale=1e-25), False, False),
     "tiny_keys_queries_and_dS": (dict(q=9e-30, v=6, k=2e-23, dS=4e-29), False, False),
@@ -232,6 +234,9 @@ def test_factors_far_apart(cuda_device, which, n, D, H):
     ref = delta_reference(*ins(xs), scale, None if S0 is None else S0[:, :2], xs["dy"], None if dS is None else dS[:, :2])
     for name, t in got.items():
         r = ref[name]
+        # da = (1 - alpha) f with f of about <dS, S>: 1e22 x 0.1 x 9e15 x 0.3 x 128 = 3.5e38, past float32's 3.4e38
+        if name == "da" and float((r * (1 + torch.exp(xs["a"].cpu().double()))).abs().max()) > 8e37:
+            continue
         assert torch.isfinite(t).all(), name
         # Steep gates leave db to the last token alone: db = (1 - beta) sum_c du_c u_c is off by 2^-11 sum_c |du_c u_c|,
         # which is any multiple of one token's |db| (of a tensor's largest, a small one).
@@ -254,11 +259,13 @@ def test_lengths_around_the_chunks_use(cuda_device, D, lengths, dt):
 
 
 @pytest.mark.parametrize("dt,D,H", [("bf16", *s) for s in SPREADS] + [("f32", 64, 2), ("f32", 32, 80)])
-@pytest.mark.parametrize("scale", [0.0, -0.3])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-40])
 def test_scales_of_zero_and_below(cuda_device, scale, dt, D, H):
     x, S0, dS = draw(dt, 1, T, H, D, seed=14)
     out = run(x, S0, dS, scale)
     xs, got, _ = two_heads(x, S0, dS, out)
+    if scale == 1e-40:   # below float32's normal range: zero
+        scale = 0.0
     ref = delta_reference(*ins(xs), scale, S0[:, :2], xs["dy"], dS[:, :2])
     if scale == 0.0:
         assert not got["y"].any() and not got["dq"].any()
