@@ -20,13 +20,16 @@
 // when it is float16 (y 2.1e-4 off in the 2-norm, as its rounding alone; with P
 // in one term 2.8e-4).
 //
+// Scales.  A row, a value channel, has its own powers of two (RowPow2): what is
+// kept of an entry depends on its own channel alone, within the chunk.
+//
 // A chunk costs a warp 400 mma at D = 128 (130 of them off the chain).  The
 // issue rate of mma.sync (8 clocks per m16n8k16 and SM quarter, measured 550
 // TFLOP/s) bounds it with two warps per quarter, the latency of the dependent
-// steps with one.  tcgen05 would have four times the rate but takes 128 rows:
-// the whole head in one SM, with the state converted through tensor memory
-// three times a chunk; with few heads (the usual case of a long prompt) that
-// leaves most SMs idle, where 16-row warps spread a head over eight.
+// steps with one.  With few heads (the usual case of a long prompt) 16-row warps
+// spread a head over eight SMs.  tcgen05 takes 128 rows, a whole head at D = 128:
+// where heads fill their blocks anyway its rate would pay, at the price of the
+// state's conversion through tensor memory three times a chunk; not tried.
 #include <type_traits>
 
 #include "esa_delta_chunk.h"
@@ -455,8 +458,9 @@ int by_d(const ChunkArgs &a, cudaStream_t st) {
 
 // Four warps a slice while every slice's block has an SM to itself; else whole
 // heads, of which a block takes eight warps at D = 128 once four warps a block
-// would put more than one block on an SM (16 heads: 129 us a pass of 32 chunks
-// in halves against 205 whole; 128 heads: 263 against 215).
+// would put more than one block on an SM (32 chunks with what the backward
+// reads, in halves and whole: 16 heads 157 and 221 us, backward 155 and 248; 128
+// heads 236 and 232, 311 and 252).
 ChainPlan chain_plan(int heads, int D) {
   if (D >= 64 && static_cast<long long>(heads) * (D / 16) <= sm_count()) return kChainSplit;
   return D == 128 && 2ll * heads <= sm_count() ? kChainHalves : kChainWhole;

@@ -14,8 +14,9 @@
 //   2. all of R meets in shared memory; each warp solves for its tokens' U;
 //   3. all of U meets; each warp adds to its quarter of the state, and
 //      finishes the outputs of its tokens.
-// Four barriers a chunk.  At 16 heads of D = 128, forward, a chunk takes
-// 2.4 us against 4.0 with a warp a slice (2.6 against 4.5 backward).
+// Four barriers a chunk.  At 16 heads of D = 128 a chunk takes 2.5 us forward
+// (with what the backward reads) against 4.9 with a warp a slice, 2.7 against
+// 4.8 backward.
 #include <type_traits>
 
 #include "esa_delta_chunk.h"

@@ -362,7 +362,10 @@ int esa_step(const void *a_t, const void *v_t, const void *q_t, float *E, void *
  *   S_init, S_final, dS_final, dS_init  [B,H,D,D] contiguous float32, each
  *             NULL when absent (zeros) or not wanted.
  * dtype ESA_F32, ESA_F16 or ESA_BF16, D of 32, 64 or 128 (else
- * ESA_ERR_UNSUPPORTED).  scale is finite (else ESA_ERR_ARG); below 2^-126 it
+ * ESA_ERR_UNSUPPORTED).  Sequences of 16-bit types that go in chunks (below)
+ * keep 22 bits of the largest value that a value channel takes in its chunk of
+ * 64 tokens: an entry may be off by 2^-28 of that, also of one forgotten since.
+ * scale is finite (else ESA_ERR_ARG); below 2^-126 it
  * counts as zero.  The state and all sums are float32.
  */
 
