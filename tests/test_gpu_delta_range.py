@@ -297,3 +297,23 @@ def test_float16_results_near_their_rounding(cuda_device, n, D, H):
         own = float((r.half().double() - r).norm())
         off = float((got[name].cpu().double() - r).norm())
         assert off <= times * own, f"{name}: {off / float(r.norm()):.2e}, rounding {own / float(r.norm()):.2e}"
+
+
+@pytest.mark.parametrize("dt,D,H", [("bf16", *s) for s in SPREADS] + [("f16", 128, 2), ("f32", 64, 2), ("f32", 32, 80)])
+@pytest.mark.parametrize("what", ["k", "v", "a", "b", "S"])
+def test_later_gradients_of_entries_that_are_not_finite(cuda_device, what, dt, D, H):
+    """What makes the state NaN makes all later gradients that read it NaN; other heads keep theirs."""
+    x, S0, dS = draw(dt, 1, T, H, D, seed=17)
+    clean = run(x, S0, dS, D ** -0.5)
+    if what == "S":
+        S0[0, 1, 3, 5] = float("nan")
+    elif what in "ab":
+        x[what][0, 70, 1] = float("nan")
+    else:
+        x[what][0, 70, 1, 5] = float("nan")
+    bad = run(x, S0, dS, D ** -0.5)
+    for n in ("dq", "dk", "da", "db"):
+        assert not torch.isfinite(bad[n][0, 70:, 1]).any(), n
+    other = [h for h in range(H) if h != 1]
+    for n in ("y", "dq", "dk", "dv", "da", "db"):
+        assert torch.equal(bad[n][:, :, other], clean[n][:, :, other]), n
