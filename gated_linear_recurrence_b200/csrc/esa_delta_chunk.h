@@ -7,7 +7,7 @@
 // kernel in the order and with the swizzle in which later kernels hold it in
 // shared memory, so that a copy of it is linear:
 //   tok    [kTokRows][64] float32  per-token factors (rows below)
-//   fac    [8] float32             rows of `Fac` below
+//   fac    [8] float32             the chunk's factors, `Fac` below
 //   k, q   [64][D] float16         keys and queries, each tile scaled by a power of two (exact)
 //   th, tl 10 blocks 16 x 16       two float16 terms of T = (1 + M)^-1 (lower triangle), scaled likewise
 //   ph, pl 10 blocks 16 x 16       two float16 terms of P_ij = e^{Gi-Gj} q_i.k_j (j <= i), scaled likewise

@@ -362,11 +362,11 @@ int esa_step(const void *a_t, const void *v_t, const void *q_t, float *E, void *
  *   S_init, S_final, dS_final, dS_init  [B,H,D,D] contiguous float32, each
  *             NULL when absent (zeros) or not wanted.
  * dtype ESA_F32, ESA_F16 or ESA_BF16, D of 32, 64 or 128 (else
- * ESA_ERR_UNSUPPORTED).  Sequences of 16-bit types that go in chunks (below)
- * keep 22 bits of the largest value that a value channel takes in its chunk of
- * 64 tokens: an entry may be off by 2^-28 of that, also of one forgotten since.
- * scale is finite (else ESA_ERR_ARG); below 2^-126 it
- * counts as zero.  The state and all sums are float32.
+ * ESA_ERR_UNSUPPORTED).  scale is finite (else ESA_ERR_ARG); below 2^-126 it
+ * counts as zero.  The state and all sums are float32; in sequences of 16-bit
+ * types that go in chunks of 64 tokens (below) a product's operands keep 22
+ * bits, and 2^-30 of the largest value that their value channel takes in the
+ * chunk, one forgotten since included.
  */
 
 /* Bytes of workspace for esa_delta_fwd (keep = 0: the forward alone; 1: also
@@ -374,11 +374,11 @@ int esa_step(const void *a_t, const void *v_t, const void *q_t, float *E, void *
  * of 16-bit types go in chunks of 64 tokens, from 8 (D = 128), 12 or 16 (D = 32)
  * tokens on with keep, from 24 (D = 128) or 40 without, whose operands and states
  * are kept there: at D = 128 3.4 times the bytes of q without keep and 9.4 with
- * (float16 11.4), at D = 64 4.7 and 8.7 (10.7).  Between those lengths calls with and without keep differ
- * by their roundings, in y (16-bit) and S_final.  float32
- * sequences of few heads keep their chunks' states from 192 tokens on.  The
- * workspace needs no initialisation and can be reused by any later call; two
- * calls that may overlap need two. */
+ * (float16 11.4), at D = 64 4.7 and 8.7 (10.7).  Between those lengths calls
+ * with and without keep differ by their roundings.  float32 sequences of few
+ * heads keep their chunks' states from 192 tokens on.  The workspace needs no
+ * initialisation and can be reused by any later call; two calls that may
+ * overlap need two. */
 size_t esa_delta_workspace_size(int B, int T, int H, int D, int dtype, int keep);
 
 /* Forward over a whole sequence.  keep = 1 leaves what the backward needs in
@@ -394,8 +394,8 @@ int esa_delta_fwd(const void *q, const void *k, long long ld_qk, const void *v, 
  * Backward: gradients of sum(dy . y) + sum(dS_final . S_final) with respect to
  * q, k, v, a, b and S_init.  The inputs and the workspace are those of the
  * matching esa_delta_fwd with keep = 1, unchanged since; outputs overlap no
- * input, but dS_init may be dS_final.  With dS the gradient
- * of S_t from later tokens, dS += scale q_t dy_t^T, then
+ * input, but dS_init may be dS_final.  With dS the gradient of S_t from later
+ * tokens, dS += scale q_t dy_t^T, then
  *     du = dS^T k,  dv = beta du,  dk = dS u - alpha beta S_{t-1} du,
  *     dq = scale S_t dy,  db = (du.u)(1 - beta),
  *     da = (<dS, S_t> - beta v.du)(1 - alpha),  dS <- alpha (dS - beta k du^T).
